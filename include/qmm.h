@@ -186,6 +186,121 @@ typedef enum { QMM_MXFP4 = 0, QMM_MXFP8 = 1, QMM_NVFP4 = 2 } qmm_mx_format;
 qmm_status qmm_small_m_mx(const void* X, const uint32_t* Wq, const uint8_t* scales, int M, int N, int K, int format,
                           void* Y, int out_dtype, int variant, int splits, void* stream);
 
+/* Quantisation into the microscaling formats: row r of X [R, K] (bf16 or fp32
+ * by x_dtype, rows ldx >= K elements apart) is cut into groups of g = 32
+ * (QMM_NVFP4: 16) along K; with a the largest |x| of a group
+ *   QMM_MXFP4, QMM_MXFP8: scale byte E = clamp(floor(log2 a) - e + 127, 0, 254),
+ *              e = 2 (E2M1) or 8 (E4M3), E = 0 for a = 0; s = 2^(E - 127);
+ *   QMM_NVFP4: s = a / 6 (one fp32 division) rounded to E4M3, at most 448;
+ * and every code is x / s rounded to the nearest value of the format, ties to
+ * the even code, beyond the largest value to the largest; the sign of x stays.
+ * s = 0 gives codes 0 (with x's signs).  A group that holds a NaN or an
+ * infinity gets a NaN scale (255; nvfp4 0x7F) and codes +0.
+ * Wq [R, K*bits/32] and scales [R, K/g] have the layout qmm_small_m_mx reads.
+ * values: null, or bf16 [R, K]: what the codes stand for, s * value(code) (to
+ * nearest even where bf16 cannot hold it: mxfp8 below 2^-130 only).
+ * K must be a multiple of 32 (QMM_ERR_SHAPE); X and values are aligned to
+ * their element, Wq to 4 bytes.  R == 0 or K == 0 launches nothing.  X must
+ * not overlap the outputs.                                                    */
+qmm_status qmm_quantize_mx(const void* X, int x_dtype, int64_t R, int64_t K, int64_t ldx, int format, uint32_t* Wq,
+                           uint8_t* scales, void* values, void* stream);
+
+/* Product of two microscaled 4-bit matrices, any number of rows:
+ *     Y[M,N] = Xv[M,K] . Wv[N,K]^T
+ * Xq, Wq: E2M1 codes [M, K/8] and [N, K/8] words; x_scales, w_scales
+ * [M, K/g] and [N, K/g]; format QMM_MXFP4 or QMM_NVFP4 (QMM_MXFP8:
+ * QMM_ERR_UNSUPPORTED); as qmm_quantize_mx writes them.  Products of codes and
+ * scales are exact, sums fp32; Y is bf16 (round to nearest even) or fp32.  NaN
+ * scales give NaN outputs.  K must be a multiple of 32; Xq and Wq are 16-byte
+ * aligned.  M == 0 or N == 0 launches nothing, K == 0 fills Y with zeros.     */
+qmm_status qmm_matmul_mx(const uint32_t* Xq, const uint8_t* x_scales, const uint32_t* Wq, const uint8_t* w_scales,
+                         int M, int N, int K, int format, void* Y, int out_dtype, void* stream);
+
+/* A paged key-value cache.  Token j of sequence b lives in page
+ * block_table[b][j / page_size] at slot j mod page_size; its key for head h
+ * starts at k + page * k_page + slot * k_token + h * k_head (strides in
+ * elements; the D elements of a head are contiguous), its value likewise.
+ * QMM_KV_E4M3 elements stand for k_scale (v_scale) times their E4M3 value;
+ * QMM_KV_BF16 ignores the scales.
+ * lengths[b] counts the tokens of sequence b including its new rows.
+ * A page number outside 0..num_pages-1 or a length outside
+ * 0..max_pages*page_size sets bit 5 of qmm_device_status(): tokens of such a
+ * page are neither written nor seen, and the length is clamped.
+ * All device arrays; page_size >= 1.                                          */
+typedef enum { QMM_KV_BF16 = 0, QMM_KV_E4M3 = 1 } qmm_kv_dtype;
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page, k_token, k_head;
+  int64_t v_page, v_token, v_head;
+  const int32_t* block_table; /* [B][table_stride], the first max_pages of each row are read */
+  const int32_t* lengths;     /* [B] */
+  int64_t table_stride;
+  int64_t num_pages;
+  int32_t max_pages;
+  int32_t page_size;
+  int32_t heads;              /* key-value heads */
+  int32_t head_dim;           /* D: 64, 128 or 256 */
+  int32_t dtype;              /* qmm_kv_dtype */
+  float k_scale, v_scale;
+} qmm_paged_cache;
+
+/* Writes the new rows' keys and values into the cache: row i < m_b of
+ * sequence b goes to position lengths[b] - m_b + i (rows whose position is
+ * negative are dropped).  k_new, v_new: bf16, row b*M + i starts k_ld (v_ld)
+ * elements after row 0 times that index, its heads * D elements contiguous (so
+ * both may be slices of one projection's output).  m_b = q_lens[b] clamped to
+ * 0..M, or M if q_lens is null.  E4M3 elements are x / scale (one fp32
+ * division), nearest even, at most 448 in magnitude; NaN stays NaN.
+ * k, v, k_new, v_new 16-byte aligned, strides multiples of 16 bytes (else
+ * QMM_ERR_ALIGN).  Two rows of one call must not name the same slot.          */
+qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
+                         int B, int M, const int32_t* q_lens, void* stream);
+
+/* Attention of M = 1..16 new rows of each of B sequences over the cache.  Row
+ * i < m_b of sequence b stands at position p = lengths[b] - m_b + i and sees
+ * the tokens j <= p with window == 0, or j > p - window, or j < sinks:
+ *     out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k[j,h / G]) v[j,h / G],
+ * G = q_heads / cache heads (a whole number).  q: bf16, row b*M + i q_ld
+ * elements apart, q_heads * D contiguous; out: bf16 [B, M, q_heads, D]; lse:
+ * null or fp32 [B, M, q_heads], log sum_j exp(scale * q . k_j).  A row that
+ * sees no token, and rows i >= m_b: out 0, lse -inf.  What a row does not see
+ * never reaches it, whatever is stored there.  Scores, softmax statistics and
+ * sums are fp32; probabilities enter the second product as bf16 (fp16 for an
+ * E4M3 cache).
+ * workspace: qmm_paged_attention_workspace() bytes, 16-byte aligned, not shared
+ * by calls that may run at the same time; contents need no initialisation.
+ * Alignment as qmm_kv_append (q and out too).                                 */
+qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
+                               const int32_t* q_lens, float scale, int window, int sinks, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim);
+
+/* Verification of drafted tokens against the target's logits [B, k+1, V] (bf16
+ * or fp32; row i is the target's distribution after i accepted drafts, rows
+ * row_stride, sequences batch_stride elements apart), from given random
+ * numbers.  With p_i = softmax(logits_i / temperature[b]) and q_i =
+ * draft_probs[b, i] (fp32 [B, k, V], what the draft drew token d_i from; null:
+ * the drafts were certain, q_i(d_i) = 1), draft i is accepted while
+ *     uniform[b, i] * q_i(d_i) < p_i(d_i).
+ * After n accepted drafts the next token is the v with the largest
+ * w(v) / noise[b, v] (noise fp32 [B, V], exponentially distributed, > 0;
+ * the lowest v of equals): w = max(p_n - q_n, 0) where draft n was refused
+ * (w = p_n if that is 0 everywhere), w = p_n where all were accepted.
+ * temperature[b] <= 0 or NaN is greedy: a draft is accepted if it is the lowest
+ * argmax of its row, and the next token is the argmax of row n.
+ * draft_lens (null: k everywhere): sequence b has draft_lens[b] drafts, clamped
+ * to 0..k.  A draft outside 0..V-1 is refused (with draft_probs null, q_n is
+ * then 0 everywhere).  A NaN logit counts as -inf, which has probability 0.  A
+ * row whose largest logit is not finite (-inf everywhere, or a +inf) has no
+ * softmax: no draft is accepted on it and its token is its lowest argmax.
+ * tokens int32 [B, k+1]: the accepted drafts, the next token, then -1;
+ * accepted int32 [B]: n.  0 <= k <= 31, V >= 1.                                */
+qmm_status qmm_verify_draft(const void* logits, int logits_dtype, int64_t batch_stride, int64_t row_stride,
+                            const int32_t* draft_tokens, const float* draft_probs, const float* uniform,
+                            const float* noise, const float* temperature, const int32_t* draft_lens, int B, int k,
+                            int V, int32_t* tokens, int32_t* accepted, void* stream);
+
 /* Number of uint32 words of a packed [N, K] matrix: N * K * bits / 32
  * (0 if bits is unsupported or K*bits is not a multiple of 32).                 */
 size_t qmm_packed_words(int64_t N, int64_t K, int bits);
@@ -229,7 +344,8 @@ int qmm_last_cuda_error(void);                 /* cudaError_t of the last failur
  * consumer gave up waiting for a weight tile, bit 1 = the producer gave up
  * waiting for a free stage, bit 2 = copies still in flight at exit gave up,
  * bit 3 = a gathered call had an invalid index list (see qmm_gather_small_m),
- * bit 4 = qmm_from_ggml met a block outside its exact range.
+ * bit 4 = qmm_from_ggml met a block outside its exact range, bit 5 = a paged
+ * cache call met an invalid page number or length (see qmm_paged_cache).
  * Every wait is bounded (about 2 s), so a fault shows up here instead of as a
  * hang.  Synchronizes with the device; clears the word when `clear` != 0.
  * 0xFFFFFFFF if the word could not be read.                                    */

@@ -27,7 +27,7 @@ OUT_BF16 = 0
 OUT_F32 = 1
 
 # Every function the header declares, with its ctypes signature.
-_vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "qmm_small_m": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp]),
     "qmm_small_m_ex": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _vp]),
@@ -37,6 +37,13 @@ SIGNATURES = {
                                   _i32, _i32, _i32, _vp]),
     "qmm_from_ggml": (_i32, [_i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "qmm_small_m_mx": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _vp]),
+    "qmm_quantize_mx": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "qmm_matmul_mx": (_i32, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp]),
+    "qmm_kv_append": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp]),
+    "qmm_paged_attention": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _f32, _i32, _i32, _vp, _vp, _vp,
+                                   ctypes.c_size_t, _vp]),
+    "qmm_paged_attention_workspace": (ctypes.c_size_t, [_i32, _i32, _i32, _i32, _i32]),
+    "qmm_verify_draft": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "qmm_packed_words": (ctypes.c_size_t, [_i64, _i64, _i32]),
     "qmm_pack": (_i32, [_vp, _i64, _i64, _i32, _vp]),
     "qmm_unpack": (_i32, [_vp, _i64, _i64, _i32, _vp]),
@@ -50,6 +57,16 @@ SIGNATURES = {
     "qmm_device_status": (ctypes.c_uint, [_i32]),
     "qmm_version": (ctypes.c_char_p, []),
 }
+
+
+class PagedCacheStruct(ctypes.Structure):
+    """``qmm_paged_cache`` of the header."""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("k_page", _i64), ("k_token", _i64), ("k_head", _i64), ("v_page", _i64),
+                ("v_token", _i64), ("v_head", _i64), ("block_table", _vp), ("lengths", _vp), ("table_stride", _i64),
+                ("num_pages", _i64), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", _f32),
+                ("v_scale", _f32)]
 
 
 class QmmError(RuntimeError):
@@ -301,3 +318,268 @@ def small_m(x, wq, scales, biases, bits: int, group_size: int, out=None, out_dty
     small_m_residual_ptr(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), residual.data_ptr(),
                          M, N, K, bits, group_size, out.data_ptr(), od, variant, splits, handle)
     return out
+
+
+# ------------------------------------------------- the operators around the product
+def _launch_on(stream, device):
+    """(cudaStream_t as int, the stream to record new tensors on or None) of a
+    call.  Outputs and workspaces are allocated on the current stream; a call
+    that runs on another one has them recorded there, so that their memory is
+    not handed out again before the call is done."""
+    import torch
+
+    current = torch.cuda.current_stream(device)
+    if stream is None:
+        return current.cuda_stream, None
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == current.cuda_stream:
+        return handle, None
+    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+
+
+def _new(shape, dtype, device, record):
+    import torch
+
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if record is not None:
+        # the caching allocator may have handed out memory that the current
+        # stream still works on: the call's stream waits for it
+        record.wait_stream(torch.cuda.current_stream(device))
+        t.record_stream(record)
+    return t
+
+
+def _cuda(device, **tensors):
+    """All given tensors live on ``device``."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if device.type != "cuda":
+        raise ValueError("CUDA tensors are needed")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def quantize_mx(x, fmt: str, values=None, out=None, stream=None):
+    """Microscaled codes and scale bytes of ``x`` [R, K] (bf16 or fp32; rows may
+    be strided), formats as :func:`small_m_mx`: returns (codes int32
+    [R, K*bits/32], scales uint8 [R, K/g]), into ``out`` if given.  ``values``:
+    an optional bf16 [R, K] tensor that receives what the codes stand for."""
+    import torch
+
+    f, bits, g = MX_FORMATS[fmt]
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("x must be a bfloat16 or float32 matrix")
+    R, K = x.shape
+    dev = x.device
+    _cuda(dev, values=values)
+    if K % 32 != 0:
+        raise ValueError("K must be a multiple of 32")
+    if K > 1 and x.stride(1) != 1 or R > 1 and x.stride(0) < K:
+        raise ValueError("the elements of a row of x must be contiguous, and its rows apart")
+    if values is not None and (values.dtype != torch.bfloat16 or values.shape != x.shape or not values.is_contiguous()):
+        raise ValueError("values must be a contiguous bfloat16 tensor of x's shape")
+    handle, record = _launch_on(stream, dev)
+    if out is None:
+        out = _new((R, K * bits // 32), torch.int32, dev, record), _new((R, K // g), torch.uint8, dev, record)
+    codes, scales = out
+    _cuda(dev, codes=codes, scales=scales)
+    if (tuple(codes.shape) != (R, K * bits // 32) or codes.dtype != torch.int32 or not codes.is_contiguous()
+            or tuple(scales.shape) != (R, K // g) or scales.dtype != torch.uint8 or not scales.is_contiguous()):
+        raise ValueError("out must be contiguous (int32 [R, K*bits/32], uint8 [R, K/g])")
+    _check(lib().qmm_quantize_mx(x.data_ptr(), OUT_F32 if x.dtype == torch.float32 else OUT_BF16, R, K,
+                                 x.stride(0) if R > 1 else K, f, codes.data_ptr(), scales.data_ptr(), _ptr(values),
+                                 handle), "qmm_quantize_mx")
+    return codes, scales
+
+
+def matmul_mx(xq, x_scales, wq, w_scales, fmt: str, out=None, out_dtype=None, stream=None):
+    """Y = X . W^T of two microscaled 4-bit matrices (``"mxfp4"`` or ``"nvfp4"``)
+    as :func:`quantize_mx` gives them, any number of rows; Y bf16 or fp32 [M, N]."""
+    import torch
+
+    f, bits, g = MX_FORMATS[fmt]
+    if bits != 4:
+        raise ValueError("matmul_mx takes the 4-bit formats")
+    dev = xq.device
+    _cuda(dev, x_scales=x_scales, wq=wq, w_scales=w_scales, out=out)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out dtype must be bfloat16 or float32")
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("codes must be matrices")
+    (M, words), N = xq.shape, wq.shape[0]
+    K = words * 8
+    for name, t, dtype, shape in (("xq", xq, torch.int32, (M, words)), ("wq", wq, torch.int32, (N, words)),
+                                  ("x_scales", x_scales, torch.uint8, (M, K // g)),
+                                  ("w_scales", w_scales, torch.uint8, (N, K // g))):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    handle, record = _launch_on(stream, dev)
+    if out is None:
+        out = _new((M, N), out_dtype, dev, record)
+    elif tuple(out.shape) != (M, N) or out.dtype != out_dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
+    _check(lib().qmm_matmul_mx(xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), M, N, K, f,
+                               out.data_ptr(), OUT_F32 if out_dtype == torch.float32 else OUT_BF16, handle),
+           "qmm_matmul_mx")
+    return out
+
+
+def _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B):
+    import torch
+
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, heads, D] of one shape and dtype")
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError("the cache must be bfloat16 or float8_e4m3fn")
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise ValueError("the D elements of a head must be contiguous")
+    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
+    if tuple(lengths.shape) != (B,) or lengths.dtype != torch.int32 or not lengths.is_contiguous():
+        raise ValueError("lengths must be int32 [B]")
+    pages, page_size, heads, D = k_cache.shape
+    ks, vs = k_cache.stride(), v_cache.stride()
+    width = block_table.shape[1]
+    return PagedCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                            block_table.data_ptr(), lengths.data_ptr(), block_table.stride(0) if B > 1 else width, pages,
+                            width, page_size, heads, D, 0 if k_cache.dtype == torch.bfloat16 else 1, k_scale, v_scale)
+
+
+def _rows(t, B, M, name):
+    """Distance of the [B, M] rows of ``t`` [B, M, heads, D] (one distance for
+    all; a row's elements are contiguous)."""
+    import torch
+
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    heads, D = t.shape[2], t.shape[3]
+    s = t.stride()
+    ld = s[1] if M > 1 else s[0] if B > 1 else heads * D
+    if ((D > 1 and s[3] != 1) or (heads > 1 and s[2] != D) or (B > 1 and M > 1 and s[0] != M * ld)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous and its rows evenly apart")
+    return ld
+
+
+def _q_lens(q_lens, B):
+    import torch
+
+    if q_lens is not None and (tuple(q_lens.shape) != (B,) or q_lens.dtype != torch.int32 or not q_lens.is_contiguous()):
+        raise ValueError("q_lens must be int32 [B]")
+
+
+def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None, k_scale: float = 1.0,
+              v_scale: float = 1.0, stream=None):
+    """Write the new rows' keys and values into a paged cache.
+
+    ``k_new``, ``v_new``: bf16 [B, M, heads, D] (rows may be strided, e.g.
+    slices of a fused projection); ``k_cache``, ``v_cache``: bf16 or
+    float8_e4m3fn [pages, page_size, heads, D], any strides with D contiguous;
+    ``block_table``: int32 [B, max_pages]; ``lengths``: int32 [B], tokens of
+    each sequence with its new rows; ``q_lens``: int32 [B], new rows of each
+    sequence (None: M).  Row i of sequence b goes to position
+    lengths[b] - q_lens[b] + i.  E4M3 elements hold x / scale."""
+    if k_new.dim() != 4 or k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must be [B, M, heads, D] of one shape")
+    B, M = k_new.shape[:2]
+    dev = k_new.device
+    _cuda(dev, v_new=v_new, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths, q_lens=q_lens)
+    cache = _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B)
+    if tuple(k_new.shape[2:]) != tuple(k_cache.shape[2:]):
+        raise ValueError("k_new and the cache must have the same heads and D")
+    _q_lens(q_lens, B)
+    k_ld, v_ld = _rows(k_new, B, M, "k_new"), _rows(v_new, B, M, "v_new")
+    handle, _ = _launch_on(stream, dev)
+    _check(lib().qmm_kv_append(ctypes.byref(cache), k_new.data_ptr(), k_ld, v_new.data_ptr(), v_ld, B, M, _ptr(q_lens),
+                               handle), "qmm_kv_append")
+
+
+def paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens=None, scale: float | None = None, window: int = 0,
+                    sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, return_lse: bool = False,
+                    workspace=None, stream=None):
+    """Attention of M = 1..16 new rows per sequence over a paged cache.
+
+    ``q``: bf16 [B, M, q_heads, D] (rows may be strided); the cache as in
+    :func:`kv_append`, already holding the new rows.  Row i of sequence b sees
+    the tokens up to its own position; with ``window`` > 0 only the last
+    ``window`` of them and the first ``sinks`` of the sequence.  ``scale``
+    defaults to 1/sqrt(D).  Returns ``out`` bf16 [B, M, q_heads, D], with
+    ``return_lse`` also the fp32 [B, M, q_heads] log-sum-exp of the scaled
+    scores (-inf, and 0 in ``out``, for rows that see nothing).  ``workspace``:
+    a uint8 tensor of ``lib().qmm_paged_attention_workspace`` bytes to reuse."""
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("q must be [B, M, q_heads, D]")
+    B, M, Hq, D = q.shape
+    dev = q.device
+    _cuda(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths, q_lens=q_lens, out=out,
+          workspace=workspace)
+    cache = _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B)
+    if D != cache.head_dim:
+        raise ValueError("q and the cache must have the same D")
+    _q_lens(q_lens, B)
+    q_ld = _rows(q, B, M, "q")
+    handle, record = _launch_on(stream, dev)
+    if out is None:
+        out = _new((B, M, Hq, D), torch.bfloat16, dev, record)
+    elif tuple(out.shape) != (B, M, Hq, D) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
+    lse = _new((B, M, Hq), torch.float32, dev, record) if return_lse else None
+    need = lib().qmm_paged_attention_workspace(B, M, Hq, cache.heads, D)
+    if workspace is None:
+        workspace = _new((need,), torch.uint8, dev, record)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _check(lib().qmm_paged_attention(ctypes.byref(cache), q.data_ptr(), q_ld, B, M, Hq, _ptr(q_lens),
+                                     D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(lse),
+                                     workspace.data_ptr(), workspace.numel(), handle), "qmm_paged_attention")
+    return (out, lse) if return_lse else out
+
+
+def verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens=None, stream=None):
+    """Accept or refuse drafted tokens against the target's logits.
+
+    ``logits``: bf16 or fp32 [B, k+1, V] (a row's elements contiguous);
+    ``draft_tokens``: int32 [B, k]; ``draft_probs``: fp32 [B, k, V] the drafts
+    were drawn from, or None if they were certain; ``uniform``: fp32 [B, k] in
+    [0, 1); ``noise``: fp32 [B, V], exponentially distributed;
+    ``temperature``: fp32 [B], 0 for greedy; ``draft_lens``: int32 [B] or None.
+    Returns (tokens int32 [B, k+1]: the accepted drafts, the next token, then
+    -1; accepted int32 [B])."""
+    import torch
+
+    if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
+        raise ValueError("logits must be [B, k+1, V]")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("logits must be bfloat16 or float32")
+    B, rows, V = logits.shape
+    k = rows - 1
+    dev = logits.device
+    if V > 1 and logits.stride(2) != 1:
+        raise ValueError("the elements of a row of logits must be contiguous")
+    for name, t, dtype, shape in (("draft_tokens", draft_tokens, torch.int32, (B, k)),
+                                  ("draft_probs", draft_probs, torch.float32, (B, k, V)),
+                                  ("uniform", uniform, torch.float32, (B, k)), ("noise", noise, torch.float32, (B, V)),
+                                  ("temperature", temperature, torch.float32, (B,)),
+                                  ("draft_lens", draft_lens, torch.int32, (B,))):
+        if t is None and name in ("draft_probs", "draft_lens"):
+            continue
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    _cuda(dev, draft_tokens=draft_tokens, draft_probs=draft_probs, uniform=uniform, noise=noise, temperature=temperature,
+          draft_lens=draft_lens)
+    handle, record = _launch_on(stream, dev)
+    tokens = _new((B, rows), torch.int32, dev, record)
+    accepted = _new((B,), torch.int32, dev, record)
+    _check(lib().qmm_verify_draft(logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16,
+                                  logits.stride(0) if B > 1 else rows * V, logits.stride(1) if rows > 1 else V,
+                                  draft_tokens.data_ptr(), _ptr(draft_probs), uniform.data_ptr(), noise.data_ptr(),
+                                  temperature.data_ptr(), _ptr(draft_lens), B, k, V, tokens.data_ptr(),
+                                  accepted.data_ptr(), handle), "qmm_verify_draft")
+    return tokens, accepted

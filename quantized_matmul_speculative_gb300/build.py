@@ -25,6 +25,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               f"-I{INCLUDE}", f"-I{CSRC}"]
 
+# the C ABI, and the operators around the small-M product
+PLAIN_UNITS = ["qmm_api", "qmm_quantize", "qmm_mx_matmul", "qmm_paged", "qmm_verify"]
 MMA_INSTANCES = [(4, 32), (4, 64), (4, 128), (2, 32), (2, 64), (2, 128), (8, 32), (8, 64), (8, 128)]
 
 
@@ -37,7 +39,7 @@ def nvcc() -> str:
 
 def units():
     """(source, object, extra flags) for every translation unit."""
-    out = [(CSRC / "qmm_api.cu", BUILD / "qmm_api.o", [])]
+    out = [(CSRC / f"{name}.cu", BUILD / f"{name}.o", []) for name in PLAIN_UNITS]
     for bits, gs in MMA_INSTANCES:
         out.append((CSRC / "qmm_mma_inst.cu", BUILD / f"qmm_mma_b{bits}_g{gs}.o",
                     [f"-DQMM_BITS={bits}", f"-DQMM_GS={gs}"]))

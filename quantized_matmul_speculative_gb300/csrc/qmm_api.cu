@@ -339,6 +339,13 @@ qmm_status fail_cuda(cudaError_t e) {
 
 }  // namespace
 
+int finish_call(cudaError_t e) { return e == cudaSuccess ? QMM_OK : fail_cuda(e); }
+
+bool injected_launch_failure() {
+  const char* inject = std::getenv("QMM_TEST_INJECT");
+  return inject != nullptr && std::strcmp(inject, "launch_fail") == 0;
+}
+
 const VariantDesc* variant_desc(int v) { return (v >= 0 && v < kNumVariants) ? &kVariants[v] : nullptr; }
 int variant_count() { return kNumVariants; }
 int variant_rows_per_cta(const VariantDesc& d) { return d.family == kFamilyMma ? 16 * d.R * d.WN : 16; }
@@ -485,6 +492,8 @@ unsigned int qmm_device_status(int clear) {
   v |= read_device_status<8, 32>(clear);
   v |= read_device_status<8, 64>(clear);
   v |= read_device_status<8, 128>(clear);
+  v |= read_paged_status(clear);
+  v |= read_mx_matmul_status(clear);
   unsigned int g = 0;
   if (cudaMemcpyFromSymbol(&g, qmm::g_qmm_ggml_status, sizeof(g)) != cudaSuccess) return 0xFFFFFFFFu;
   if (clear && g) {

@@ -82,4 +82,36 @@ bool tma_supported(const CallArgs& a, int csize, const VariantDesc& d);
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 
+// Remember `e` for qmm_last_cuda_error() and return QMM_OK or QMM_ERR_CUDA.
+int finish_call(cudaError_t e);
+
+// Host-side fault injection of the error-path tests: launches report an error.
+bool injected_launch_failure();
+
+// Device status word of the paged-cache unit (bit 5: invalid page or length).
+constexpr unsigned int kStatusBadPage = 32u;
+unsigned int read_paged_status(int clear);
+// Device status word of the microscaled product's unit (bounded waits).
+unsigned int read_mx_matmul_status(int clear);
+
+// Launch with programmatic stream serialization: the kernel may start while its
+// predecessor finishes and calls griddepcontrol.wait before it touches memory
+// that an earlier kernel may write or still read.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const A&... args) {
+  if (injected_launch_failure()) return cudaErrorLaunchFailure;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 }  // namespace qmm

@@ -1,0 +1,253 @@
+// Paged key-value cache: append of new rows and attention over it
+// (qmm_kv_append, qmm_paged_attention; definitions in include/qmm.h).
+#include "../../include/qmm.h"
+#include "qmm_device.cuh"
+#include "qmm_internal.h"
+
+namespace qmm {
+namespace {
+
+__device__ __forceinline__ uint32_t cvt_e4m3(float x) {  // nearest even, saturating; NaN stays NaN
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  return r & 0xFFu;
+}
+
+// Tokens of sequence b, clamped to what its block table can hold.
+__device__ __forceinline__ int64_t seq_length(const qmm_paged_cache& c, int b) {
+  const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
+  int64_t n = c.lengths[b];
+  if (n < 0 || n > cap) {
+    atomicOr(&g_qmm_status, kStatusBadPage);
+    n = n < 0 ? 0 : cap;
+  }
+  return n;
+}
+__device__ __forceinline__ int new_rows(const int32_t* q_lens, int b, int M) {
+  const int m = q_lens != nullptr ? q_lens[b] : M;
+  return m < 0 ? 0 : m > M ? M : m;
+}
+// Page of token j, or -1 (and the status bit) if the table names none.
+__device__ __forceinline__ int64_t token_page(const qmm_paged_cache& c, int b, int64_t j) {
+  const int64_t p = c.block_table[b * c.table_stride + j / c.page_size];
+  if (p < 0 || p >= c.num_pages) {
+    atomicOr(&g_qmm_status, kStatusBadPage);
+    return -1;
+  }
+  return p;
+}
+
+// One thread per 8 elements of one row's key or value.
+__global__ void __launch_bounds__(256)
+kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, const uint16_t* vn, int64_t v_ld, int B, int M,
+                 const int32_t* q_lens) {
+  griddep_wait();
+  const int per_row = c.heads * (c.head_dim / 8);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= static_cast<int64_t>(B) * M * per_row) return;
+  const int64_t row = t / per_row;
+  const int chunk = static_cast<int>(t - row * per_row);
+  const int b = static_cast<int>(row / M), i = static_cast<int>(row - static_cast<int64_t>(b) * M);
+  const int m = new_rows(q_lens, b, M);
+  const int64_t pos = seq_length(c, b) - m + i;
+  if (i >= m || pos < 0) return;
+  const int64_t page = token_page(c, b, pos);
+  if (page < 0) return;
+  const int h = chunk / (c.head_dim / 8), d = (chunk - h * (c.head_dim / 8)) * 8;
+  const int64_t slot = pos % c.page_size;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint4 x = *reinterpret_cast<const uint4*>((kv ? vn + row * v_ld : kn + row * k_ld) + h * c.head_dim + d);
+    const int64_t at = page * (kv ? c.v_page : c.k_page) + slot * (kv ? c.v_token : c.k_token) +
+                       h * (kv ? c.v_head : c.k_head) + d;
+    if (c.dtype == QMM_KV_BF16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(kv ? c.v : c.k) + at) = x;
+    } else {
+      const float s = kv ? c.v_scale : c.k_scale;
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t o[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[j / 2] |= cvt_e4m3(__fdiv_rn(bf16_lo(w[j]), s)) << (16 * (j & 1));
+        o[j / 2] |= cvt_e4m3(__fdiv_rn(bf16_hi(w[j]), s)) << (16 * (j & 1) + 8);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kv ? c.v : c.k) + at) = make_uint2(o[0], o[1]);
+    }
+  }
+}
+
+struct AttentionArgs {
+  qmm_paged_cache c;
+  const uint16_t* q;
+  int64_t q_ld;
+  int M, Hq;
+  const int32_t* q_lens;
+  float scale;
+  int window, sinks;
+  __nv_bfloat16* out;
+  float* lse;
+};
+
+// One CTA of four warps per (new row, head, sequence); a warp takes every
+// fourth token, a lane D/32 elements; the warps' partial softmaxes are joined
+// in shared memory.
+template <int D, bool E8>
+__global__ void __launch_bounds__(128) attention_kernel(const AttentionArgs a) {
+  constexpr int E = D / 32;
+  griddep_wait();
+  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int hk = h / (a.Hq / a.c.heads);
+  const int m = new_rows(a.q_lens, b, a.M);
+  const int64_t pos = i < m ? seq_length(a.c, b) - m + i : -1;
+  float q[E], o[E] = {};
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    q[e] = bf16_lo(a.q[(static_cast<int64_t>(b) * a.M + i) * a.q_ld + static_cast<int64_t>(h) * D + e * 32 + lane]) * a.scale;
+  float top = -INFINITY, sum = 0.f;
+  for (int64_t j = warp; j <= pos; j += 4) {
+    if (a.window != 0 && j <= pos - a.window && j >= a.sinks) continue;
+    const int64_t page = token_page(a.c, b, j);
+    if (page < 0) continue;
+    const int64_t slot = j % a.c.page_size;
+    const int64_t ka = page * a.c.k_page + slot * a.c.k_token + hk * a.c.k_head;
+    const int64_t va = page * a.c.v_page + slot * a.c.v_token + hk * a.c.v_head;
+    auto load = [&](const void* p, int64_t at, float s) {
+      return E8 ? e4m3_to_float(static_cast<const uint8_t*>(p)[at]) * s : bf16_lo(static_cast<const uint16_t*>(p)[at]);
+    };
+    float x = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x += q[e] * load(a.c.k, ka + e * 32 + lane, a.c.k_scale);
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) x += __shfl_xor_sync(0xffffffffu, x, s);
+    if (x == -INFINITY) continue;  // weight 0
+    const float t = fmaxf(top, x);
+    const float c = expf(top - t), p = expf(x - t);
+    sum = sum * c + p;
+    top = t;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * load(a.c.v, va + e * 32 + lane, a.c.v_scale);
+  }
+  __shared__ float so[4][D], st[4], ss[4];
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
+  if (lane == 0) {
+    st[warp] = top;
+    ss[warp] = sum;
+  }
+  __syncthreads();
+  const float t = fmaxf(fmaxf(st[0], st[1]), fmaxf(st[2], st[3]));
+  const float base = t == -INFINITY ? 0.f : t;
+  float f[4], total = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = expf(st[w] - base);
+    total += f[w] * ss[w];
+  }
+  const int64_t row = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h;
+  for (int d = threadIdx.x; d < D; d += 128) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += f[w] * so[w][d];
+    a.out[row * D + d] = __float2bfloat16_rn(total != 0.f ? v / total : 0.f);
+  }
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = logf(total) + base;
+}
+
+bool misaligned(int64_t a, int64_t m) { return (a % m) != 0; }
+
+// Checks that append and attention share; QMM_OK if there is work to launch.
+qmm_status check_cache(const qmm_paged_cache* c, int B, int M) {
+  if (c == nullptr) return QMM_ERR_NULL;
+  if (c->dtype != QMM_KV_BF16 && c->dtype != QMM_KV_E4M3) return QMM_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMM_ERR_UNSUPPORTED;
+  if (B < 0 || B > 65535 || M < 0 || M > 16 || c->heads < 1 || c->heads > 4096 || c->page_size < 1 || c->max_pages < 0 ||
+      c->num_pages < 0 || c->num_pages > 0x7fffffff || static_cast<int64_t>(c->max_pages) * c->page_size > 0x7fffffff)
+    return QMM_ERR_SHAPE;
+  if (c->table_stride < c->max_pages) return QMM_ERR_SHAPE;
+  if (c->dtype == QMM_KV_E4M3 && !(c->k_scale > 0.f && c->v_scale > 0.f && c->k_scale < INFINITY && c->v_scale < INFINITY))
+    return QMM_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0) return QMM_OK;
+  if (c->lengths == nullptr) return QMM_ERR_NULL;
+  if (c->max_pages > 0 && (c->k == nullptr || c->v == nullptr || c->block_table == nullptr)) return QMM_ERR_NULL;
+  const int64_t per16 = c->dtype == QMM_KV_BF16 ? 8 : 16;
+  if (misaligned(reinterpret_cast<intptr_t>(c->k), 16) || misaligned(reinterpret_cast<intptr_t>(c->v), 16) ||
+      misaligned(c->k_page, per16) || misaligned(c->k_token, per16) || misaligned(c->k_head, per16) ||
+      misaligned(c->v_page, per16) || misaligned(c->v_token, per16) || misaligned(c->v_head, per16) ||
+      misaligned(reinterpret_cast<intptr_t>(c->lengths), 4) || misaligned(reinterpret_cast<intptr_t>(c->block_table), 4))
+    return QMM_ERR_ALIGN;
+  return QMM_OK;
+}
+
+}  // namespace
+
+unsigned int read_paged_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_qmm_status, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  if (clear && v != 0) {
+    const unsigned int zero = 0;
+    cudaMemcpyToSymbol(g_qmm_status, &zero, sizeof(zero));
+  }
+  return v;
+}
+
+}  // namespace qmm
+
+extern "C" {
+
+using namespace qmm;
+
+qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
+                         int B, int M, const int32_t* q_lens, void* stream) {
+  const qmm_status rc = check_cache(cache, B, M);
+  if (rc != QMM_OK) return rc;
+  const int64_t width = static_cast<int64_t>(cache->heads) * cache->head_dim;
+  if (k_ld < width || v_ld < width) return QMM_ERR_SHAPE;
+  if (B == 0 || M == 0) return QMM_OK;
+  if (k_new == nullptr || v_new == nullptr) return QMM_ERR_NULL;
+  if (misaligned(reinterpret_cast<intptr_t>(k_new), 16) || misaligned(reinterpret_cast<intptr_t>(v_new), 16) ||
+      misaligned(k_ld, 8) || misaligned(v_ld, 8) || misaligned(reinterpret_cast<intptr_t>(q_lens), 4))
+    return QMM_ERR_ALIGN;
+  const int64_t threads = static_cast<int64_t>(B) * M * (width / 8);
+  return static_cast<qmm_status>(finish_call(launch_dependent(
+      kv_append_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), 256, 0, static_cast<cudaStream_t>(stream),
+      *cache, static_cast<const uint16_t*>(k_new), k_ld, static_cast<const uint16_t*>(v_new), v_ld, B, M, q_lens)));
+}
+
+size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim) {
+  (void)B, (void)M, (void)q_heads, (void)heads, (void)head_dim;
+  return 0;
+}
+
+qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
+                               const int32_t* q_lens, float scale, int window, int sinks, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  const qmm_status rc = check_cache(cache, B, M);
+  if (rc != QMM_OK) return rc;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || window < 0 || sinks < 0 ||
+      q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)
+    return QMM_ERR_SHAPE;
+  if (B == 0 || M == 0) return QMM_OK;
+  if (q == nullptr || out == nullptr) return QMM_ERR_NULL;
+  if (misaligned(reinterpret_cast<intptr_t>(q), 16) || misaligned(reinterpret_cast<intptr_t>(out), 16) ||
+      misaligned(q_ld, 8) || misaligned(reinterpret_cast<intptr_t>(lse), 4) ||
+      misaligned(reinterpret_cast<intptr_t>(q_lens), 4))
+    return QMM_ERR_ALIGN;
+  const AttentionArgs a{*cache, static_cast<const uint16_t*>(q), q_ld, M, q_heads, q_lens, scale, window, sinks,
+                        static_cast<__nv_bfloat16*>(out), lse};
+  const dim3 grid(M, q_heads, B);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool e8 = cache->dtype == QMM_KV_E4M3;
+  cudaError_t e;
+  switch (cache->head_dim) {
+    case 64: e = e8 ? launch_dependent(attention_kernel<64, true>, grid, 128, 0, st, a)
+                    : launch_dependent(attention_kernel<64, false>, grid, 128, 0, st, a); break;
+    case 128: e = e8 ? launch_dependent(attention_kernel<128, true>, grid, 128, 0, st, a)
+                     : launch_dependent(attention_kernel<128, false>, grid, 128, 0, st, a); break;
+    default: e = e8 ? launch_dependent(attention_kernel<256, true>, grid, 128, 0, st, a)
+                    : launch_dependent(attention_kernel<256, false>, grid, 128, 0, st, a); break;
+  }
+  return static_cast<qmm_status>(finish_call(e));
+}
+
+}  // extern "C"
