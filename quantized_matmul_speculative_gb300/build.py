@@ -27,6 +27,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 # the C ABI, and the operators around the small-M product
 PLAIN_UNITS = ["qmm_api", "qmm_quantize", "qmm_mx_matmul", "qmm_paged", "qmm_verify"]
+HEAD_DIMS = [64, 128, 256]
 MMA_INSTANCES = [(4, 32), (4, 64), (4, 128), (2, 32), (2, 64), (2, 128), (8, 32), (8, 64), (8, 128)]
 
 
@@ -40,6 +41,8 @@ def nvcc() -> str:
 def units():
     """(source, object, extra flags) for every translation unit."""
     out = [(CSRC / f"{name}.cu", BUILD / f"{name}.o", []) for name in PLAIN_UNITS]
+    for d in HEAD_DIMS:
+        out.append((CSRC / "qmm_paged_inst.cu", BUILD / f"qmm_paged_d{d}.o", [f"-DQMM_HEAD_DIM={d}"]))
     for bits, gs in MMA_INSTANCES:
         out.append((CSRC / "qmm_mma_inst.cu", BUILD / f"qmm_mma_b{bits}_g{gs}.o",
                     [f"-DQMM_BITS={bits}", f"-DQMM_GS={gs}"]))

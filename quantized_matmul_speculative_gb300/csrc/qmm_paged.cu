@@ -1,8 +1,6 @@
 // Paged key-value cache: append of new rows and attention over it
 // (qmm_kv_append, qmm_paged_attention; definitions in include/qmm.h).
-#include "../../include/qmm.h"
-#include "qmm_device.cuh"
-#include "qmm_internal.h"
+#include "qmm_paged.cuh"
 
 namespace qmm {
 namespace {
@@ -13,20 +11,6 @@ __device__ __forceinline__ uint32_t cvt_e4m3(float x) {  // nearest even, satura
   return r & 0xFFu;
 }
 
-// Tokens of sequence b, clamped to what its block table can hold.
-__device__ __forceinline__ int64_t seq_length(const qmm_paged_cache& c, int b) {
-  const int64_t cap = static_cast<int64_t>(c.max_pages) * c.page_size;
-  int64_t n = c.lengths[b];
-  if (n < 0 || n > cap) {
-    atomicOr(&g_qmm_status, kStatusBadPage);
-    n = n < 0 ? 0 : cap;
-  }
-  return n;
-}
-__device__ __forceinline__ int new_rows(const int32_t* q_lens, int b, int M) {
-  const int m = q_lens != nullptr ? q_lens[b] : M;
-  return m < 0 ? 0 : m > M ? M : m;
-}
 // Page of token j, or -1 (and the status bit) if the table names none.
 __device__ __forceinline__ int64_t token_page(const qmm_paged_cache& c, int b, int64_t j) {
   const int64_t p = c.block_table[b * c.table_stride + j / c.page_size];
@@ -49,7 +33,7 @@ kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, cons
   const int chunk = static_cast<int>(t - row * per_row);
   const int b = static_cast<int>(row / M), i = static_cast<int>(row - static_cast<int64_t>(b) * M);
   const int m = new_rows(q_lens, b, M);
-  const int64_t pos = seq_length(c, b) - m + i;
+  const int pos = seq_length(c, b) - m + i;
   if (i >= m || pos < 0) return;
   const int64_t page = token_page(c, b, pos);
   if (page < 0) return;
@@ -74,84 +58,6 @@ kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, cons
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(kv ? c.v : c.k) + at) = make_uint2(o[0], o[1]);
     }
   }
-}
-
-struct AttentionArgs {
-  qmm_paged_cache c;
-  const uint16_t* q;
-  int64_t q_ld;
-  int M, Hq;
-  const int32_t* q_lens;
-  float scale;
-  int window, sinks;
-  __nv_bfloat16* out;
-  float* lse;
-};
-
-// One CTA of four warps per (new row, head, sequence); a warp takes every
-// fourth token, a lane D/32 elements; the warps' partial softmaxes are joined
-// in shared memory.
-template <int D, bool E8>
-__global__ void __launch_bounds__(128) attention_kernel(const AttentionArgs a) {
-  constexpr int E = D / 32;
-  griddep_wait();
-  const int i = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = h / (a.Hq / a.c.heads);
-  const int m = new_rows(a.q_lens, b, a.M);
-  const int64_t pos = i < m ? seq_length(a.c, b) - m + i : -1;
-  float q[E], o[E] = {};
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    q[e] = bf16_lo(a.q[(static_cast<int64_t>(b) * a.M + i) * a.q_ld + static_cast<int64_t>(h) * D + e * 32 + lane]) * a.scale;
-  float top = -INFINITY, sum = 0.f;
-  for (int64_t j = warp; j <= pos; j += 4) {
-    if (a.window != 0 && j <= pos - a.window && j >= a.sinks) continue;
-    const int64_t page = token_page(a.c, b, j);
-    if (page < 0) continue;
-    const int64_t slot = j % a.c.page_size;
-    const int64_t ka = page * a.c.k_page + slot * a.c.k_token + hk * a.c.k_head;
-    const int64_t va = page * a.c.v_page + slot * a.c.v_token + hk * a.c.v_head;
-    auto load = [&](const void* p, int64_t at, float s) {
-      return E8 ? e4m3_to_float(static_cast<const uint8_t*>(p)[at]) * s : bf16_lo(static_cast<const uint16_t*>(p)[at]);
-    };
-    float x = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) x += q[e] * load(a.c.k, ka + e * 32 + lane, a.c.k_scale);
-#pragma unroll
-    for (int s = 16; s > 0; s /= 2) x += __shfl_xor_sync(0xffffffffu, x, s);
-    if (x == -INFINITY) continue;  // weight 0
-    const float t = fmaxf(top, x);
-    const float c = expf(top - t), p = expf(x - t);
-    sum = sum * c + p;
-    top = t;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * c + p * load(a.c.v, va + e * 32 + lane, a.c.v_scale);
-  }
-  __shared__ float so[4][D], st[4], ss[4];
-#pragma unroll
-  for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
-  if (lane == 0) {
-    st[warp] = top;
-    ss[warp] = sum;
-  }
-  __syncthreads();
-  const float t = fmaxf(fmaxf(st[0], st[1]), fmaxf(st[2], st[3]));
-  const float base = t == -INFINITY ? 0.f : t;
-  float f[4], total = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = expf(st[w] - base);
-    total += f[w] * ss[w];
-  }
-  const int64_t row = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h;
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) v += f[w] * so[w][d];
-    a.out[row * D + d] = __float2bfloat16_rn(total != 0.f ? v / total : 0.f);
-  }
-  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = logf(total) + base;
 }
 
 bool misaligned(int64_t a, int64_t m) { return (a % m) != 0; }
@@ -181,6 +87,13 @@ qmm_status check_cache(const qmm_paged_cache* c, int B, int M) {
 
 }  // namespace
 
+extern template cudaError_t launch_attention<64>(AttentionArgs, bool, cudaStream_t);
+extern template cudaError_t launch_attention<128>(AttentionArgs, bool, cudaStream_t);
+extern template cudaError_t launch_attention<256>(AttentionArgs, bool, cudaStream_t);
+extern template unsigned int read_attention_status<64>(int);
+extern template unsigned int read_attention_status<128>(int);
+extern template unsigned int read_attention_status<256>(int);
+
 unsigned int read_paged_status(int clear) {
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, g_qmm_status, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
@@ -188,7 +101,7 @@ unsigned int read_paged_status(int clear) {
     const unsigned int zero = 0;
     cudaMemcpyToSymbol(g_qmm_status, &zero, sizeof(zero));
   }
-  return v;
+  return v | read_attention_status<64>(clear) | read_attention_status<128>(clear) | read_attention_status<256>(clear);
 }
 
 }  // namespace qmm
@@ -215,8 +128,9 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
 }
 
 size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim) {
-  (void)B, (void)M, (void)q_heads, (void)heads, (void)head_dim;
-  return 0;
+  if (B <= 0 || M <= 0 || M > 16 || heads <= 0 || q_heads <= 0 || q_heads % heads != 0 || q_heads > 65535 || head_dim <= 0)
+    return 0;
+  return attention_workspace(attention_ctas_per_sm(head_dim) * device_sm_count(), attention_row_block(M * (q_heads / heads)), head_dim);
 }
 
 qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
@@ -233,20 +147,39 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
       misaligned(q_ld, 8) || misaligned(reinterpret_cast<intptr_t>(lse), 4) ||
       misaligned(reinterpret_cast<intptr_t>(q_lens), 4))
     return QMM_ERR_ALIGN;
-  const AttentionArgs a{*cache, static_cast<const uint16_t*>(q), q_ld, M, q_heads, q_lens, scale, window, sinks,
-                        static_cast<__nv_bfloat16*>(out), lse};
-  const dim3 grid(M, q_heads, B);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (workspace == nullptr) return QMM_ERR_NULL;
+  if (misaligned(reinterpret_cast<intptr_t>(workspace), 16)) return QMM_ERR_ALIGN;
   const bool e8 = cache->dtype == QMM_KV_E4M3;
-  cudaError_t e;
-  switch (cache->head_dim) {
-    case 64: e = e8 ? launch_dependent(attention_kernel<64, true>, grid, 128, 0, st, a)
-                    : launch_dependent(attention_kernel<64, false>, grid, 128, 0, st, a); break;
-    case 128: e = e8 ? launch_dependent(attention_kernel<128, true>, grid, 128, 0, st, a)
-                     : launch_dependent(attention_kernel<128, false>, grid, 128, 0, st, a); break;
-    default: e = e8 ? launch_dependent(attention_kernel<256, true>, grid, 128, 0, st, a)
-                    : launch_dependent(attention_kernel<256, false>, grid, 128, 0, st, a); break;
-  }
+  AttentionArgs a = {};
+  a.c = *cache;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_ld = q_ld;
+  a.B = B;
+  a.M = M;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->heads;
+  a.q_lens = q_lens;
+  a.scale_log2 = scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f);
+  a.v_scale = e8 ? cache->v_scale : 1.f;
+  a.window = window;
+  a.sinks = window != 0 ? sinks : 0;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.RB = attention_row_block(M * a.G);
+  a.RT = (M * a.G + a.RB - 1) / a.RB;
+  // as many CTAs as the SMs hold, at most one a tile
+  const int64_t tiles = static_cast<int64_t>(B) * cache->heads * a.RT *
+                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + kKvTile - 1) / kKvTile);
+  const int64_t fit = attention_ctas_per_sm(cache->head_dim) * static_cast<int64_t>(device_sm_count());
+  a.parts = static_cast<int>(tiles < 1 ? 1 : tiles < fit ? tiles : fit);
+  if (static_cast<int64_t>(B) * cache->heads * a.RT * (a.RB / 4) > 0x7fffffff) return QMM_ERR_SHAPE;
+  if (workspace_bytes < attention_workspace(a.parts, a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.parts) * 2 * a.RB * cache->head_dim);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = cache->head_dim == 64    ? launch_attention<64>(a, e8, st)
+                        : cache->head_dim == 128 ? launch_attention<128>(a, e8, st)
+                                                 : launch_attention<256>(a, e8, st);
   return static_cast<qmm_status>(finish_call(e));
 }
 
