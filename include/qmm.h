@@ -225,7 +225,7 @@ qmm_status qmm_matmul_mx(const uint32_t* Xq, const uint8_t* x_scales, const uint
  * lengths[b] counts the tokens of sequence b including its new rows.
  * A page number outside 0..num_pages-1 or a length outside
  * 0..max_pages*page_size sets bit 5 of qmm_device_status(): tokens of such a
- * page are neither written nor seen, and the length is clamped.
+ * page are not written and read as zeros, and the length is clamped.
  * All device arrays; page_size >= 1.                                          */
 typedef enum { QMM_KV_BF16 = 0, QMM_KV_E4M3 = 1 } qmm_kv_dtype;
 typedef struct {

@@ -1,5 +1,7 @@
 // Paged key-value cache: append of new rows and attention over it
 // (qmm_kv_append, qmm_paged_attention; definitions in include/qmm.h).
+#include <cmath>
+
 #include "qmm_paged.cuh"
 
 namespace qmm {
@@ -130,7 +132,7 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
 size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim) {
   if (B <= 0 || M <= 0 || M > 16 || heads <= 0 || q_heads <= 0 || q_heads % heads != 0 || q_heads > 65535 || head_dim <= 0)
     return 0;
-  return attention_workspace(attention_ctas_per_sm(head_dim) * device_sm_count(), attention_row_block(M * (q_heads / heads)), head_dim);
+  return attention_workspace(device_sm_count(), attention_row_block(M * (q_heads / heads)), head_dim);
 }
 
 qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
@@ -159,7 +161,9 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.Hq = q_heads;
   a.G = q_heads / cache->heads;
   a.q_lens = q_lens;
-  a.scale_log2 = scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f);
+  // at least 1e-30: a masked score of -inf stays -inf, and no finite score of use is told from 0 by less
+  a.scale_log2 = std::fmax(std::fabs(scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f)), 1e-30f);
+  a.negate = scale < 0.f;
   a.v_scale = e8 ? cache->v_scale : 1.f;
   a.window = window;
   a.sinks = window != 0 ? sinks : 0;
@@ -167,15 +171,16 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.lse = lse;
   a.RB = attention_row_block(M * a.G);
   a.RT = (M * a.G + a.RB - 1) / a.RB;
-  // as many CTAs as the SMs hold, at most one a tile
+  a.TN = attention_tile(cache->head_dim);
+  // one CTA an SM, at most one a tile
   const int64_t tiles = static_cast<int64_t>(B) * cache->heads * a.RT *
-                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + kKvTile - 1) / kKvTile);
-  const int64_t fit = attention_ctas_per_sm(cache->head_dim) * static_cast<int64_t>(device_sm_count());
+                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + a.TN - 1) / a.TN);
+  const int64_t fit = device_sm_count();
   a.parts = static_cast<int>(tiles < 1 ? 1 : tiles < fit ? tiles : fit);
-  if (static_cast<int64_t>(B) * cache->heads * a.RT * (a.RB / 4) > 0x7fffffff) return QMM_ERR_SHAPE;
   if (workspace_bytes < attention_workspace(a.parts, a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.parts) * 2 * a.RB * cache->head_dim);
+  a.part_seg = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(a.parts) * 2 * a.RB);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->head_dim == 64    ? launch_attention<64>(a, e8, st)
                         : cache->head_dim == 128 ? launch_attention<128>(a, e8, st)

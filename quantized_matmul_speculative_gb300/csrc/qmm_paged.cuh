@@ -4,7 +4,7 @@
 // The work.  A segment is one (sequence, key-value head, block of query rows):
 // its rows are the new rows x the G query heads of the key-value head, so one
 // pass over the keys and values serves them all.  A segment's visible tokens
-// are cut into tiles of 64; the tiles of all segments form one list (sequence,
+// are cut into tiles of 32 or 64; the tiles of all segments form one list (sequence,
 // head, row block, tile order), and CTA c of the grid takes the c-th equal
 // share of it, whatever the lengths: a single long sequence is split over all
 // SMs, a batch of ragged ones is balanced.  A segment that one CTA finishes is
@@ -16,6 +16,8 @@
 // p v, l likewise; o / l and (m + log2 l) ln 2 at the end.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include <climits>
 #include <type_traits>
 
@@ -25,8 +27,15 @@
 
 namespace qmm {
 
-constexpr int kKvTile = 64;       // tokens of a tile
-constexpr int kAttnThreads = 128;
+// Tokens of a tile: as many as leave the accumulators their registers and every
+// team of warps a stage of its own.
+__host__ __device__ constexpr int attention_tile(int D) { return D >= 256 ? 16 : D >= 128 ? 32 : 64; }
+constexpr int kComputeWarps = 8;
+// Two computing warpgroups and one that loads; the registers a thread is
+// launched with (168 of 384 threads: 64512) move to the computing ones.
+constexpr int kAttnThreads = 32 * (kComputeWarps + 4);
+constexpr int kLaunchRegs = 168;
+constexpr int kJoinThreads = 128;
 
 struct AttentionArgs {
   qmm_paged_cache c;
@@ -34,20 +43,24 @@ struct AttentionArgs {
   int64_t q_ld;
   int B, M, Hq, G;  // G = Hq / c.heads
   const int32_t* q_lens;
-  float scale_log2;  // scale * log2(e), times k_scale for an E4M3 cache
+  float scale_log2;  // |scale| log2(e), times k_scale for an E4M3 cache; > 0
+  int negate;        // the queries' signs are flipped (a negative scale)
   float v_scale;
   int window, sinks;
   __nv_bfloat16* out;
   float* lse;
+  int box;        // tokens of a TMA box (8 or 16); 0: copied row by row
   int RB, RT;     // rows of a row block, row blocks of a segment's M * G rows
+  int TN;         // attention_tile()
   int parts;      // CTAs of the attention kernel
   float* part_o;  // [parts][2][RB][D]
   float2* part_ml;  // [parts][2][RB]
+  int4* part_seg;   // [parts] the segment that begins in a CTA's share and goes on: (b, h, rt, parts), parts 0: none
 };
 
 // Bytes of the parts that `ctas` CTAs can leave.
 inline size_t attention_workspace(int ctas, int RB, int D) {
-  return static_cast<size_t>(ctas) * 2 * RB * (static_cast<size_t>(D) * 4 + 8);
+  return static_cast<size_t>(ctas) * (2 * RB * (static_cast<size_t>(D) * 4 + 8) + 16);
 }
 inline int attention_row_block(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
@@ -89,9 +102,9 @@ __device__ __forceinline__ Visible visible(const AttentionArgs& a, int L, int m,
   v.win_tile = 0;
   v.tiles = 0;
   if (i0 > i1 || v.hi <= 0) return v;
-  const int all = (v.hi + kKvTile - 1) / kKvTile;
-  const int ns = a.window ? (min(a.sinks, v.hi) + kKvTile - 1) / kKvTile : 0;
-  const int w0 = v.first / kKvTile;
+  const int all = (v.hi + a.TN - 1) / a.TN;
+  const int ns = a.window ? (min(a.sinks, v.hi) + a.TN - 1) / a.TN : 0;
+  const int w0 = v.first / a.TN;
   if (ns >= w0) {
     v.tiles = all;
   } else {
@@ -121,23 +134,6 @@ __device__ __forceinline__ long long warp_scan(long long v, long long& inc) {
   return __shfl_sync(0xffffffffu, inc, 31);
 }
 
-// Tiles of all sequences, and of those before sequence `b` (every lane calls).
-__device__ __forceinline__ long long total_tiles(const AttentionArgs& a, int b, long long* before) {
-  long long total = 0, pre = 0;
-  for (int base = 0; base < a.B; base += 32) {
-    const int s = base + (threadIdx.x & 31);
-    const long long n = s < a.B ? static_cast<long long>(head_tiles(a, s)) * a.c.heads : 0;
-    long long inc;
-    total += warp_scan(n, inc);
-    long long mine = s < b ? n : 0;
-#pragma unroll
-    for (int x = 16; x > 0; x /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, x);
-    pre += mine;
-  }
-  if (before != nullptr) *before = pre;
-  return total;
-}
-
 // CTAs that work: no more than there are tiles, so that every share holds one.
 __device__ __forceinline__ int working(const AttentionArgs& a, long long T) {
   return T < a.parts ? static_cast<int>(T) : a.parts;
@@ -152,9 +148,12 @@ __device__ __forceinline__ int share_of(long long T, int P, long long t) {
   return c;
 }
 
-// A place in the list of tiles.
+// A CTA's share of the list, segment by segment.
 struct Cursor {
-  int b, h, rt, k;
+  int left;    // tiles of the share from this segment on
+  int it;      // the share's tiles before this segment
+  int b, h, rt;
+  int kb, ke;  // tiles of the segment in this share
   int L, m;
   Visible v;
 
@@ -162,77 +161,99 @@ struct Cursor {
     L = seq_length(a.c, b);
     m = new_rows(a.q_lens, b, a.M);
   }
-  // The place of tile t < T (every lane of the warp calls).
-  __device__ __forceinline__ void seek(const AttentionArgs& a, long long t) {
+  // The share of this CTA (every lane of the warp calls); false: none.
+  // `parts`: CTAs that share the list; T: its tiles; t0: the share's first.
+  __device__ __forceinline__ bool begin(const AttentionArgs& a, int& parts, long long& T, long long& t0) {
+    const int lane = threadIdx.x & 31;
+    T = 0;
+    long long n = 0;  // tiles of sequence (last base) + lane
+    for (int base = 0; base < a.B; base += 32) {
+      n = base + lane < a.B ? static_cast<long long>(head_tiles(a, base + lane)) * a.c.heads : 0;
+      long long inc;
+      T += warp_scan(n, inc);
+    }
+    parts = working(a, T);
+    if (static_cast<int>(blockIdx.x) >= parts) return false;
+    t0 = share_begin(T, parts, blockIdx.x);
+    left = static_cast<int>(share_begin(T, parts, blockIdx.x + 1) - t0);
+    it = 0;
     long long before = 0;
     b = 0;
     for (int base = 0; base < a.B; base += 32) {
-      const int s = base + (threadIdx.x & 31);
-      const long long n = s < a.B ? static_cast<long long>(head_tiles(a, s)) * a.c.heads : 0;
+      if (a.B > 32) n = base + lane < a.B ? static_cast<long long>(head_tiles(a, base + lane)) * a.c.heads : 0;
       long long inc;
       const long long sum = warp_scan(n, inc);
-      if (before + sum > t) {
-        const unsigned who = __ballot_sync(0xffffffffu, before + inc > t);
-        const int lane = __ffs(who) - 1;
-        b = base + lane;
-        before += __shfl_sync(0xffffffffu, inc - n, lane);
+      if (before + sum > t0) {
+        const unsigned who = __ballot_sync(0xffffffffu, before + inc > t0);
+        const int l = __ffs(who) - 1;
+        b = base + l;
+        before += __shfl_sync(0xffffffffu, inc - n, l);
         break;
       }
       before += sum;
     }
     load(a);
     const int per_head = max(head_tiles(a, b), 1);
-    h = static_cast<int>((t - before) / per_head);
-    int r = static_cast<int>(t - before - static_cast<long long>(h) * per_head);
-    for (rt = 0; rt < a.RT; ++rt) {
+    h = static_cast<int>((t0 - before) / per_head);
+    int r = static_cast<int>(t0 - before - static_cast<long long>(h) * per_head);
+    for (rt = 0; rt < a.RT - 1; ++rt) {
       v = visible(a, L, m, rt);
       if (r < v.tiles) break;
       r -= v.tiles;
     }
-    k = r;
+    v = visible(a, L, m, rt);
+    kb = r;
+    ke = min(v.tiles, kb + left);
+    return true;
   }
-  // The next tile; past the last one nothing is valid.
-  __device__ __forceinline__ void next(const AttentionArgs& a) {
-    if (++k < v.tiles) return;
-    k = 0;
+  // The next segment; false past the last one.
+  __device__ __forceinline__ bool next(const AttentionArgs& a) {
+    it += ke - kb;
+    left -= ke - kb;
+    if (left <= 0) return false;
     do {
       if (++rt == a.RT) {
         rt = 0;
         if (++h == a.c.heads) {
           h = 0;
-          if (++b >= a.B) return;
+          if (++b >= a.B) return false;
           load(a);
         }
       }
       v = visible(a, L, m, rt);
     } while (v.tiles == 0);
+    kb = 0;
+    ke = min(v.tiles, left);
+    return true;
   }
-  __device__ __forceinline__ int token0() const {
-    return (k < v.sink_tiles ? k : k - v.sink_tiles + v.win_tile) * kKvTile;
-  }
+  __device__ __forceinline__ int tile(int k) const { return k < v.sink_tiles ? k : k - v.sink_tiles + v.win_tile; }
 };
 
 // ---------------------------------------------------------------------------
-// Shared-memory tiles: rows of RB bytes (64, 128, 256 or 512), 16-byte chunks
-// permuted so that the eight rows one ldmatrix phase reads lie in different
-// banks.  Rows of 64 bytes share a 128-byte line in pairs.
+// Shared-memory tiles: groups of 16 tokens, each as slices of 128 bytes of the
+// tokens' rows ([slice][16 tokens][128 bytes]; rows of 64 bytes: [16][64]), the
+// 16-byte chunks permuted as the TMA's 128-byte (64-byte) swizzle leaves them:
+// the eight rows of one ldmatrix phase lie in different banks.
 // ---------------------------------------------------------------------------
 template <int ROWB>
-__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
-  if constexpr (ROWB >= 128) {
-    return row * ROWB + ((chunk ^ (row & 7)) << 4);
-  } else {
-    return (row >> 1) * 128 + (((((row & 1) << 2) | chunk) ^ ((row >> 1) & 7)) << 4);
-  }
+__device__ __forceinline__ uint32_t tile_at(int token, int chunk) {
+  const int r = token & 15, g = (token >> 4) * 16 * ROWB;
+  if constexpr (ROWB >= 128) return g + (chunk >> 3) * 2048 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+  else return g + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool fill) {
+__device__ __forceinline__ void cp_async_16(uint32_t dst, unsigned long long src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives on `bar` when this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -247,10 +268,36 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b with a zero accumulator input.
+__device__ __forceinline__ void mma_f16_16816_z(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// (x0, x1) = (x0, x1) * f, and s += (x0, x1), as packed pairs.
+__device__ __forceinline__ void fmul2(float& x0, float& x1, float f) {
+  asm("{\n .reg .b64 a, c;\n mov.b64 a, {%0, %1};\n mov.b64 c, {%2, %2};\n mul.rn.f32x2 a, a, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(f));
+}
+__device__ __forceinline__ void fadd2(float& s0, float& s1, float x0, float x1) {
+  asm("{\n .reg .b64 a, c;\n mov.b64 a, {%0, %1};\n mov.b64 c, {%2, %3};\n add.rn.f32x2 a, a, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
+}
+// (x0, x1) = (x0, x1) * f - c.
+__device__ __forceinline__ void fms2(float& x0, float& x1, float f, float c) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 d, {%3, %3};\n"
+      " fma.rn.f32x2 a, a, b, d;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(f), "f"(-c));
+}
 // Two E4M3 codes (low 16 bits) to two fp16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
   uint32_t r;
   asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -276,27 +323,35 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
             : (((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xFFFFu);
 }
 
-template <int D, bool E8, int RG>
+// RPW 16-row tiles a warp, RG warps a team (RG * RPW * 16 rows a row block).
+template <int D, bool E8, int RG, int RPW>
 struct AttnCfg {
+  static constexpr int TN = attention_tile(D);
   static constexpr int ROWB = D * (E8 ? 1 : 2);
-  static constexpr int TILEB = kKvTile * ROWB;  // bytes of a key (or value) tile
-  // two CTAs an SM (113 KB each); one for D = 256, whose accumulators and stages fill it
-  static constexpr int CTAS = D == 256 ? 1 : 2;
-  static constexpr int STAGES = D == 256 ? (E8 ? 5 : 3) : TILEB >= 16384 ? 3 : TILEB >= 8192 ? 6 : 8;
-  static constexpr int WT = 4 / RG;     // warps that share a row group, each with its tokens of the tile
-  static constexpr int NT = kKvTile / WT;  // tokens of a warp
-  static constexpr int DS = 32;         // output columns joined at a time
-  static constexpr bool QREG = D <= 128;  // query fragments stay in registers
-  static constexpr int OFF_ADDR = STAGES * 2 * TILEB;            // [STAGES][64] key and value addresses
-  static constexpr int OFF_JOIN = OFF_ADDR + STAGES * kKvTile * 16;  // [4][16][DS + 4] floats
-  static constexpr int OFF_ML = OFF_JOIN + (WT > 1 ? 4 * 16 * (DS + 4) * 4 : 0);  // [4][16] (m, l)
-  static constexpr int OFF_Q = OFF_ML + (WT > 1 ? 4 * 16 * 8 : 0);  // [RG][D / 16][32] query fragments, if not in registers
-  static constexpr int SMEM = OFF_Q + (QREG ? 0 : RG * 16 * D * 2);
-  static_assert(CTAS * (SMEM + 1024) <= 233472 && SMEM <= 232448, "shared memory of an SM");
+  static constexpr int TILEB = TN * ROWB;  // bytes of a key (or value) tile
+  static constexpr int TEAMS = kComputeWarps / RG;
+  static constexpr int DS = RPW == 1 ? 64 : 32;   // output columns joined at a time
+  static constexpr bool QREG = D * RPW <= 128;    // query fragments stay in registers
+  static constexpr int JOINB = TEAMS > 1 ? kComputeWarps * 16 * RPW * (DS + 4) * 4 : 0;  // [8][16 RPW][DS + 4] floats
+  static constexpr int MLB = TEAMS > 1 ? kComputeWarps * 16 * RPW * 8 : 0;               // [8][16 RPW] (m, l)
+  static constexpr int QB = QREG ? 0 : RG * RPW * 16 * D * 2;  // [RG][D / 16][RPW][32] query fragments
+  // A multiple of the teams and of the loading warps of a kind: a stage always
+  // belongs to one team and one loader, which see its phases in order (a
+  // barrier's parity tells a phase from its neighbour only).
+  static constexpr int MULT = TEAMS > 2 ? TEAMS : 2;
+  static constexpr int STAGES = (232448 - 1024 - JOINB - MLB - QB) / (2 * TILEB + 32) / MULT * MULT;
+  // registers of a computing and of a loading thread: the outputs of 32 rows of
+  // 128 columns (or 16 of 256) need most of them
+  static constexpr int COMPUTE_REGS = D * RPW > 128 ? 224 : 208, LOAD_REGS = D * RPW > 128 ? 56 : 88;
+  static_assert(256 * COMPUTE_REGS + 128 * LOAD_REGS <= kAttnThreads * kLaunchRegs, "setmaxnreg would wait forever");
+  // Barriers: keys full, values full, keys empty, values empty, [STAGES] each
+  static constexpr int OFF_BAR = STAGES * 2 * TILEB;
+  static constexpr int OFF_JOIN = OFF_BAR + STAGES * 32;
+  static constexpr int OFF_ML = OFF_JOIN + JOINB;
+  static constexpr int OFF_Q = OFF_ML + MLB;
+  static constexpr int SMEM = OFF_Q + QB + 1024;  // and the alignment of its start
+  static_assert(TILEB % 1024 == 0 && SMEM <= 232448 && STAGES >= 2, "shared memory of an SM");
 };
-
-// CTAs an SM holds (AttnCfg::CTAS).
-inline int attention_ctas_per_sm(int D) { return D == 256 ? 1 : 2; }
 
 // Query fragments of one warp: rows r0 = lane / 4 and r0 + 8 of its row group.
 // bf16: as the MMA lays them out.  E4M3 cache: fp16, each row scaled by a power
@@ -313,14 +368,15 @@ struct Query {
 template <int D, int N, bool E8>
 __device__ __forceinline__ void load_query(const AttentionArgs& a, Query<N, E8>& f, const uint16_t* const (&row)[2]) {
   const int c = threadIdx.x & 3;
+  const uint32_t flip = a.negate ? 0x80008000u : 0u;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     f.scale[r] = a.scale_log2;
     if constexpr (!E8) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        f.a[kk][r] = row[r] ? *reinterpret_cast<const uint32_t*>(row[r] + kk * 16 + 2 * c) : 0u;
-        f.a[kk][r + 2] = row[r] ? *reinterpret_cast<const uint32_t*>(row[r] + kk * 16 + 8 + 2 * c) : 0u;
+        f.a[kk][r] = row[r] ? *reinterpret_cast<const uint32_t*>(row[r] + kk * 16 + 2 * c) ^ flip : 0u;
+        f.a[kk][r + 2] = row[r] ? *reinterpret_cast<const uint32_t*>(row[r] + kk * 16 + 8 + 2 * c) ^ flip : 0u;
       }
     } else {
       uint2 x[D / 16];
@@ -328,6 +384,8 @@ __device__ __forceinline__ void load_query(const AttentionArgs& a, Query<N, E8>&
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         x[kk] = row[r] ? *reinterpret_cast<const uint2*>(row[r] + kk * 16 + 4 * c) : make_uint2(0, 0);
+        x[kk].x ^= flip;
+        x[kk].y ^= flip;
         top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(x[kk].x)), fabsf(bf16_hi(x[kk].x))),
                                fmaxf(fabsf(bf16_lo(x[kk].y)), fabsf(bf16_hi(x[kk].y)))));
       }
@@ -354,349 +412,465 @@ __device__ __forceinline__ int out_col(int ot, int e) {
   return E8 ? (ot >> 1) * 16 + 4 * c + 2 * e + (ot & 1) : ot * 8 + 2 * c + e;
 }
 
-template <int D, bool E8, int RG>
-__global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, E8, RG>::CTAS) attention_kernel(const AttentionArgs a) {
-  using Cfg = AttnCfg<D, E8, RG>;
-  constexpr int ST = Cfg::STAGES, NT = Cfg::NT, ROWB = Cfg::ROWB, CPR = ROWB / 16;
-  extern __shared__ __align__(128) unsigned char smem[];
-  const uint32_t sbase = smem_addr(smem);
-  ulonglong2* const addr = reinterpret_cast<ulonglong2*>(smem + Cfg::OFF_ADDR);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rg = warp / Cfg::WT, wt = warp % Cfg::WT;  // row group, token part
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("barrier.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
+}
 
-  griddep_wait();
-  griddep_launch_dependents();
-  const long long T = total_tiles(a, 0, nullptr);
-  const int P = working(a, T);
-  if (static_cast<int>(blockIdx.x) >= P) return;
-  const long long t0 = share_begin(T, P, blockIdx.x);
-  const int n = static_cast<int>(share_begin(T, P, blockIdx.x + 1) - t0);
+// Whether some row of queries sees one of the tokens j .. j + count - 1.
+__device__ __forceinline__ bool seen(const AttentionArgs& a, const Cursor& p, int j, int count) {
+  return j < p.v.hi && (j + count > p.v.first || j < a.sinks);
+}
 
-  Cursor pc;  // runs ahead: the tile whose addresses are made next
-  pc.seek(a, t0);
-  Cursor cc = pc;  // the tile that is computed
-
-  // Key and value address of token `r` of the cursor's tile: its page (loaded
-  // here), then the sums in finish.  -1: not seen by any row.
-  struct Place {
-    int page, slot;
-  };
-  auto find = [&](int r) {
-    Place p{-1, 0};
-    const int j = pc.token0() + r;
-    if (pc.b < a.B && j < pc.v.hi && (j >= pc.v.first || j < a.sinks)) {
-      const int block = j / a.c.page_size;
-      p.slot = j - block * a.c.page_size;
-      p.page = a.c.block_table[pc.b * a.c.table_stride + block];
-      if (p.page < 0 || p.page >= a.c.num_pages) {
-        bad_page();
-        p.page = -1;
+// A loading warp: of four, two load keys and two values, every second tile
+// each, so that one's chain of page number, free stage and copies overlaps the
+// others', and a stage's keys are refilled while its values are still in use.
+//
+// Where pages divide into boxes of 8 or 16 tokens (a.box), TMA copies boxes of
+// [tokens][128 bytes] (16 tokens: all slices at once); coordinates are (byte
+// column, token of the page, slice, head, page).  A page outside the cache is
+// outside the tensor too and reads as zeros; boxes that nobody sees are left
+// out, and what tokens past the length hold is dealt with where the values are
+// used.  Any other page size: 16-byte asynchronous copies of the tokens' rows;
+// tokens that nobody sees and those of pages outside the cache become zeros.
+template <class Cfg, bool E8>
+__device__ __forceinline__ void load_tiles(const AttentionArgs& a, uint32_t sbase, Cursor pc, int part, bool values,
+                                           const void* map) {
+  constexpr int ST = Cfg::STAGES, SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
+  constexpr int CPR = Cfg::ROWB / 16, RPL = (Cfg::TN + 31) / 32, ES = E8 ? 1 : 2, RPI = 32 / CPR;
+  const int lane = threadIdx.x & 31;
+  const uint32_t full0 = sbase + Cfg::OFF_BAR + (values ? ST * 8 : 0), empty0 = full0 + 2 * ST * 8;
+  const uint32_t tile0 = sbase + (values ? Cfg::TILEB : 0);
+  const unsigned long long cache = reinterpret_cast<unsigned long long>(values ? a.c.v : a.c.k);
+  const int64_t s_page = values ? a.c.v_page : a.c.k_page, s_token = values ? a.c.v_token : a.c.k_token,
+                s_head = values ? a.c.v_head : a.c.k_head;
+  const int step = a.box ? a.box : 1;                                        // tokens a lane finds the page of
+  const int finders = a.box ? Cfg::TN / a.box : Cfg::TN < 32 ? Cfg::TN : 32;  // lanes that do
+  const int per = a.box == 16 ? 1 : SL;                                      // copies of a box
+  int k = pc.kb + part;  // the tile; past ke: in a later segment
+  int page[RPL], slot[RPL], head = 0;
+  bool more = true;
+  auto find = [&]() {
+    while (k >= pc.ke) {
+      const int over = k - pc.ke;
+      if (!pc.next(a)) {
+        more = false;
+        return;
+      }
+      k = pc.kb + over;
+    }
+    head = pc.h;
+#pragma unroll
+    for (int x = 0; x < RPL; ++x) {
+      const int j = pc.tile(k) * Cfg::TN + lane * step + 32 * x;
+      slot[x] = -1;
+      page[x] = 0;
+      if (lane < finders && (x == 0 || !a.box) && seen(a, pc, j, step)) {
+        const int block = j / a.c.page_size;
+        slot[x] = j - block * a.c.page_size;
+        page[x] = a.c.block_table[pc.b * a.c.table_stride + block];
       }
     }
-    return p;
+    k += 2;
   };
-  auto finish = [&](const Place& p, int h, int stage, int r) {
-    ulonglong2 o = make_ulonglong2(0, 0);
-    if (p.page >= 0) {
-      constexpr int ES = E8 ? 1 : 2;
-      o.x = reinterpret_cast<unsigned long long>(a.c.k) +
-            (p.page * a.c.k_page + p.slot * a.c.k_token + h * a.c.k_head) * ES;
-      o.y = reinterpret_cast<unsigned long long>(a.c.v) +
-            (p.page * a.c.v_page + p.slot * a.c.v_token + h * a.c.v_head) * ES;
-    }
-    addr[stage * kKvTile + r] = o;
-  };
-  auto issue = [&](int stage) {
-    const int ch = tid % CPR;
-#pragma unroll
-    for (int p = 0; p < CPR / 2; ++p) {
-      const int row = p * (kAttnThreads / CPR) + tid / CPR;
-      const ulonglong2 o = addr[stage * kKvTile + row];
-      const uint32_t d = sbase + stage * 2 * Cfg::TILEB + tile_at<ROWB>(row, ch);
-      // nothing is read where the size is 0; the address is the cache's own start
-      cp_async_16(d, reinterpret_cast<const char*>(o.x ? o.x : reinterpret_cast<unsigned long long>(a.c.k)) + ch * 16,
-                  o.x != 0);
-      cp_async_16(d + Cfg::TILEB,
-                  reinterpret_cast<const char*>(o.y ? o.y : reinterpret_cast<unsigned long long>(a.c.v)) + ch * 16,
-                  o.y != 0);
-    }
-  };
-
-  {
-    // Addresses of the first ST tiles: all page numbers are loaded before the first is used.
-    Place pl[(ST + 1) / 2];
-    int ph[(ST + 1) / 2];
-#pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      if ((tid >> 6) == (s & 1)) {
-        pl[s / 2] = s < n ? find(tid & 63) : Place{-1, 0};
-        ph[s / 2] = pc.h;
-      }
-      if (s < n) pc.next(a);
-    }
-#pragma unroll
-    for (int s = 0; s < ST; ++s)
-      if ((tid >> 6) == (s & 1)) finish(pl[s / 2], ph[s / 2], s, tid & 63);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) {
-    if (s < n) issue(s);
-    cp_async_commit();
-  }
-
-  float o[D / 8][4];
-  float mx[2], sum[2];
-  Query<Cfg::QREG ? D : 16, E8> qf;  // the query fragments, or
-  uint4* const q_frag = reinterpret_cast<uint4*>(smem + Cfg::OFF_Q) + rg * (D / 16) * 32 + lane;  // where they are
-  float (&q_scale)[2] = qf.scale;
-  int pos[2];       // positions of this thread's two rows; INT_MIN / 2 for rows that do not exist
-  bool fresh = true;
-  int k_first = 0;  // first tile of the current segment in this CTA
-
-  for (int it = 0; it < n; ++it) {
+  find();
+  for (int it = part; more; it += 2) {
     const int stage = it % ST;
-    cp_async_wait<ST - 2>();
-    __syncthreads();
-    if (it + ST - 1 < n) issue((it + ST - 1) % ST);
-    cp_async_commit();
-    const bool more = it + ST < n;
-    Place np{-1, 0};
-    int nh = 0;
-    if (more) {
-      nh = pc.h;
-      if (tid < kKvTile) np = find(tid);
+    const uint32_t full = full0 + stage * 8, base = tile0 + stage * 2 * Cfg::TILEB;
+    int pg[RPL], st[RPL];
+    const int hd = head;
+#pragma unroll
+    for (int x = 0; x < RPL; ++x) {
+      if (slot[x] >= 0 && (page[x] < 0 || page[x] >= a.c.num_pages)) {
+        bad_page();
+        page[x] = -1;
+      }
+      pg[x] = page[x];
+      st[x] = slot[x];
     }
-
-    if (fresh) {
-      fresh = false;
-      k_first = cc.k;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      const uint16_t* row[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        mx[r] = -INFINITY;
-        sum[r] = 0.f;
-        const int gr = cc.rt * a.RB + rg * 16 + (lane >> 2) + 8 * r;
-        const int i = gr / a.G;
-        const bool ok = gr < a.M * a.G && i < cc.m;
-        pos[r] = ok ? cc.L - cc.m + i : INT_MIN / 2;
-        row[r] = ok ? a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld +
-                          static_cast<int64_t>(cc.h * a.G + gr - i * a.G) * D
-                    : nullptr;
-      }
-      if constexpr (Cfg::QREG) {
-        load_query<Cfg::QREG ? D : 16>(a, qf, row);
-      } else {
-        Query<D, E8> f;
-        load_query<D>(a, f, row);
-        q_scale[0] = f.scale[0];
-        q_scale[1] = f.scale[1];
-        if (wt == 0)
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) q_frag[kk * 32] = make_uint4(f.a[kk][0], f.a[kk][1], f.a[kk][2], f.a[kk][3]);
-        if (Cfg::WT > 1) __syncthreads();
-        else __syncwarp();
-      }
-    }
-
-    const int j0 = cc.token0() + wt * NT;  // this warp's first token
-    const bool full = cc.token0() + kKvTile - 1 <= cc.v.pos_lo &&
-                      (a.window == 0 || cc.token0() > cc.v.pos_hi - a.window || cc.token0() + kKvTile <= a.sinks);
-    const uint32_t kt = sbase + stage * 2 * Cfg::TILEB, vt = kt + Cfg::TILEB;
-
-    // scores
-    float s[NT / 8][4];
-#pragma unroll
-    for (int i = 0; i < NT / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-    auto query = [&](int kk, uint32_t (&f)[4]) {
-      if constexpr (Cfg::QREG) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) f[x] = qf.a[kk][x];
-      } else {
-        const uint4 w = q_frag[kk * 32];
-        f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
-      }
-    };
-    if constexpr (!E8) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t f[4];
-        query(kk, f);
-#pragma unroll
-        for (int t = 0; t < NT / 16; ++t) {
-          uint32_t b[4];
-          ldsm_x4(b, kt + tile_at<ROWB>(wt * NT + t * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
-          mma_bf16_16816(s[2 * t], f, b[0], b[1]);
-          mma_bf16_16816(s[2 * t + 1], f, b[2], b[3]);
-        }
+    find();  // the page numbers of the tile after this one
+    if (it >= ST && __any_sync(0xffffffffu, !mbar_wait(empty0 + stage * 8, ((it / ST) & 1) ^ 1, kStatusTimeoutEmpty))) break;
+    if (a.box) {
+      const uint32_t loaded = __ballot_sync(0xffffffffu, st[0] >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(loaded) * a.box * Cfg::ROWB);
+      __syncwarp();
+      const int copies = finders * per;  // at most 32
+      const int box = lane / per, sl = lane - box * per;
+      const int p = __shfl_sync(0xffffffffu, pg[0], box & 31), s = __shfl_sync(0xffffffffu, st[0], box & 31);
+      if (lane < copies && s >= 0) {
+        const int token = box * a.box;
+        tma_load_5d(base + (token >> 4) * 16 * Cfg::ROWB + sl * 2048 + (token & 15) * ROW, map, 0, s, sl, hd, p, full);
       }
     } else {
+      // byte offsets of this lane's tokens from the cache's start, -1: zeros;
+      // they reach the lanes that copy the rows by shuffles
+      long long at[RPL];
 #pragma unroll
-      for (int kk = 0; kk < D / 16; kk += 2) {
-        uint32_t f[2][4];
-        query(kk, f[0]);
-        query(kk + 1, f[1]);
+      for (int x = 0; x < RPL; ++x)
+        at[x] = st[x] >= 0 && pg[x] >= 0 ? (pg[x] * s_page + st[x] * s_token + hd * s_head) * ES : -1;
+      const int ch = lane % CPR;
+#pragma unroll 8
+      for (int g = 0; g < Cfg::TN / RPI; ++g) {
+        const int row = g * RPI + lane / CPR;
+        long long r = __shfl_sync(0xffffffffu, at[0], row & 31);
+        if constexpr (RPL == 2) {
+          const long long r2 = __shfl_sync(0xffffffffu, at[1], row & 31);
+          r = row < 32 ? r : r2;
+        }
+        // nothing is read where zeros are filled in
+        cp_async_16(base + tile_at<Cfg::ROWB>(row, ch), cache + (r < 0 ? 0 : r) + ch * 16, r >= 0);
+      }
+      cp_async_mbar_arrive_noinc(full);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Computing warps in teams of RG (RPW 16-row tiles a warp); team t takes the
+// CTA's tiles t, t + TEAMS, ..., each warp with a running softmax of its own,
+// so that no warp waits for another before the end of a segment.
+template <int D, bool E8, int RG, int RPW>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using Cfg = AttnCfg<D, E8, RG, RPW>;
+  constexpr int ST = Cfg::STAGES, NT = Cfg::TN, ROWB = Cfg::ROWB, CPR = ROWB / 16, TEAMS = Cfg::TEAMS;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t bars = sbase + Cfg::OFF_BAR;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bars + s * 8, a.box ? 1 : 32);
+      mbar_init(bars + (ST + s) * 8, a.box ? 1 : 32);
+      mbar_init(bars + (2 * ST + s) * 8, RG);
+      mbar_init(bars + (3 * ST + s) * 8, RG);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  // rows of segments without tiles: the CTA of the sequence's number writes them
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
+    for (int rt = 0; rt < a.RT; ++rt) {
+      if (visible(a, L, m, rt).tiles != 0) continue;
+      const int r0 = rt * a.RB, rows = min(a.RB, a.M * a.G - r0), per_head = rows * (D / 8);
+      for (int x = tid; x < per_head * a.c.heads; x += kAttnThreads) {
+        const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = gr / a.G;
+        const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
+        *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
+        if (col == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
+      }
+    }
+  }
+  Cursor cc;
+  int P;
+  long long T, t0;
+  if (!cc.begin(a, P, T, t0)) {
+    if (tid == 0) a.part_seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  if (warp >= kComputeWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::LOAD_REGS));
+    load_tiles<Cfg, E8>(a, sbase, cc, warp & 1, (warp & 2) != 0, (warp & 2) != 0 ? &vmap : &kmap);
+    return;
+  }
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::COMPUTE_REGS));
+  const int rg = warp % RG, team = warp / RG;
+
+  float o[RPW][D / 8][4];
+  float mx[RPW][2], sum[RPW][2][2];  // running maximum; sum of the even and of the odd columns
+  Query<Cfg::QREG ? D : 16, E8> qf[RPW];  // the query fragments, or where they are
+  uint4* const q_frag = reinterpret_cast<uint4*>(smem + Cfg::OFF_Q) + rg * (D / 16) * RPW * 32 + lane;
+  int pos[RPW][2];  // positions of this thread's rows; INT_MIN / 2 for rows that do not exist
+  bool lost = false;
+
+  do {  // segment by segment
+    {
 #pragma unroll
-        for (int t = 0; t < NT / 16; ++t) {
-          uint32_t b[4];
-          ldsm_x4(b, kt + tile_at<ROWB>(wt * NT + t * 16 + (lane & 7) + (((lane >> 3) & 1) << 3), kk + (lane >> 4)));
+      for (int w = 0; w < RPW; ++w) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)  // (token octet, k16 step) = (x & 1, x >> 1)
-            mma_f16_16816(s[2 * t + (x & 1)], f[x >> 1], e4m3x2_to_f16x2(b[x]), e4m3x2_to_f16x2(b[x] >> 16));
+        for (int i = 0; i < D / 8; ++i) o[w][i][0] = o[w][i][1] = o[w][i][2] = o[w][i][3] = 0.f;
+        const uint16_t* row[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mx[w][r] = -INFINITY;
+          sum[w][r][0] = sum[w][r][1] = 0.f;
+          const int gr = cc.rt * a.RB + (rg * RPW + w) * 16 + (lane >> 2) + 8 * r;
+          const int i = gr / a.G;
+          const bool ok = gr < a.M * a.G && i < cc.m;
+          pos[w][r] = ok ? cc.L - cc.m + i : INT_MIN / 2;
+          row[r] = ok ? a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld +
+                            static_cast<int64_t>(cc.h * a.G + gr - i * a.G) * D
+                      : nullptr;
+        }
+        if constexpr (Cfg::QREG) {
+          load_query<Cfg::QREG ? D : 16>(a, qf[w], row);
+        } else {
+          Query<D, E8> f;
+          load_query<D>(a, f, row);
+          qf[w].scale[0] = f.scale[0];
+          qf[w].scale[1] = f.scale[1];
+          if (team == 0)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              q_frag[(kk * RPW + w) * 32] = make_uint4(f.a[kk][0], f.a[kk][1], f.a[kk][2], f.a[kk][3]);
         }
       }
+      if (!Cfg::QREG) compute_sync();
     }
+    // this team's tiles
+    for (int k = cc.kb + (team + TEAMS - cc.it % TEAMS) % TEAMS; k < cc.ke; k += TEAMS) {
+      const int it = cc.it + k - cc.kb, stage = it % ST;
+      // a wait that gave up (status bit 0) leaves wrong results, never a hang: later waits are skipped
+      if (!lost) lost = !mbar_wait(bars + stage * 8, (it / ST) & 1, kStatusTimeoutFull);
+      const int j0 = cc.tile(k) * NT;
+      const bool full = j0 + NT - 1 <= cc.v.pos_lo &&
+                        (a.window == 0 || j0 > cc.v.pos_hi - a.window || j0 + NT <= a.sinks);
+      const int koff = stage * 2 * Cfg::TILEB, voff = koff + Cfg::TILEB;
+      const uint32_t kt = sbase + koff, vt = sbase + voff;
 
-    // scale, mask, running maximum
-    float top[2] = {mx[0], mx[1]};
+      // scores
+      float s[RPW][NT / 8][4];
+      auto query = [&](int kk, int w, uint32_t (&f)[4]) {
+        if constexpr (Cfg::QREG) {
 #pragma unroll
-    for (int i = 0; i < NT / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x = s[i][e] * q_scale[e >> 1];
-        if (!full) {
-          const int j = j0 + i * 8 + 2 * (lane & 3) + (e & 1), p = pos[e >> 1];
-          const bool see = j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
-          x = see ? x : -INFINITY;
+          for (int x = 0; x < 4; ++x) f[x] = qf[w].a[kk][x];
+        } else {
+          const uint4 u = q_frag[(kk * RPW + w) * 32];
+          f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
         }
-        s[i][e] = x;
-        top[e >> 1] = fmaxf(top[e >> 1], x);
-      }
-    float corr[2];
+      };
+      if constexpr (!E8) {
+        const int kr = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      const float base = top[r] == -INFINITY ? 0.f : top[r];
-      corr[r] = ex2(mx[r] - base);
-      mx[r] = top[r];
-      top[r] = base;
-      sum[r] *= corr[r];
-    }
-    if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t f[RPW][4];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][0] *= corr[0];
-        o[i][1] *= corr[0];
-        o[i][2] *= corr[1];
-        o[i][3] *= corr[1];
-      }
-    }
+          for (int w = 0; w < RPW; ++w) query(kk, w, f[w]);
 #pragma unroll
-    for (int i = 0; i < NT / 8; ++i)
+          for (int t = 0; t < NT / 16; ++t) {
+            uint32_t b[4];
+            ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk * 2 + ((lane >> 3) & 1)));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[i][e] = ex2(s[i][e] - top[e >> 1]);
-        sum[e >> 1] += s[i][e];
-      }
-
-    // A token that only some rows see meets the others with weight 0, and 0
-    // times its value must be 0.  Where such a value is not finite, the product
-    // is taken with 0 in the place of every value that is not, and those are
-    // added element by element to the rows that see them.
-    bool bad = false;
-    if (!full && cc.v.pos_lo != cc.v.pos_hi) {
-      for (int t = 0; t < NT; ++t) {
-        const int j = j0 + t;
-        if (j >= cc.v.hi) break;
-        if (j > cc.v.pos_lo || (a.window != 0 && j <= cc.v.pos_hi - a.window && j >= a.sinks)) {
-          for (int ch = lane; ch < CPR; ch += 32) {
-            const uint4 w = *reinterpret_cast<const uint4*>(smem + (vt - sbase) + tile_at<ROWB>(wt * NT + t, ch));
-            bad |= (not_finite<E8>(w.x) | not_finite<E8>(w.y) | not_finite<E8>(w.z) | not_finite<E8>(w.w)) != 0;
+            for (int w = 0; w < RPW; ++w) {
+              if (kk == 0) {
+                mma_bf16_16816_z(s[w][2 * t], f[w], b[0], b[1]);
+                mma_bf16_16816_z(s[w][2 * t + 1], f[w], b[2], b[3]);
+              } else {
+                mma_bf16_16816(s[w][2 * t], f[w], b[0], b[1]);
+                mma_bf16_16816(s[w][2 * t + 1], f[w], b[2], b[3]);
+              }
+            }
           }
         }
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    auto values = [&](auto clean) {
-      constexpr bool kClean = decltype(clean)::value;
+      } else {
+        const int kr = lane & 15;
 #pragma unroll
-      for (int t = 0; t < NT / 16; ++t) {
-        // fp16 holds a probability to 11 bits; bf16 to 8 only, so its rest goes in as a second operand
-        uint32_t p[4], rest[4];
+        for (int kk = 0; kk < D / 16; kk += 2) {
+          uint32_t f[RPW][2][4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float lo = s[2 * t + (x >> 1)][2 * (x & 1)], hi = s[2 * t + (x >> 1)][2 * (x & 1) + 1];
-          p[x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-          rest[x] = E8 ? 0u : pack_bf16(lo - bf16_lo(p[x]), hi - bf16_hi(p[x]));
-        }
+          for (int w = 0; w < RPW; ++w) {
+            query(kk, w, f[w][0]);
+            query(kk + 1, w, f[w][1]);
+          }
 #pragma unroll
-        for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
-          uint32_t b[4];
-          ldsm_x4_t(b, vt + tile_at<ROWB>(wt * NT + t * 16 + (lane & 15), (E8 ? d : d * 2) + (lane >> 4)));
-          if constexpr (kClean)
+          for (int t = 0; t < NT / 16; ++t) {
+            uint32_t b[4];
+            ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk + (lane >> 4)));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) b[x] &= ~not_finite<E8>(b[x]);
-          if constexpr (!E8) {
-            mma_bf16_16816(o[2 * d], p, b[0], b[1]);
-            mma_bf16_16816(o[2 * d + 1], p, b[2], b[3]);
-            mma_bf16_16816(o[2 * d], rest, b[0], b[1]);
-            mma_bf16_16816(o[2 * d + 1], rest, b[2], b[3]);
-          } else {
-            // a chunk's 16 dims come in pairs: even and odd dims become one tile each
+            for (int x = 0; x < 4; ++x) {  // (token octet, k16 step) = (x & 1, x >> 1)
+              const uint32_t b0 = e4m3x2_to_f16x2(b[x]), b1 = e4m3x2_to_f16x2(b[x] >> 16);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // chunk d + x
-              mma_f16_16816(o[2 * (d + x)], p, e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4420)),
-                            e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4420)));
-              mma_f16_16816(o[2 * (d + x) + 1], p, e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4431)),
-                            e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4431)));
+              for (int w = 0; w < RPW; ++w) {
+                if (kk + (x >> 1) == 0) mma_f16_16816_z(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
+                else mma_f16_16816(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
+              }
             }
           }
         }
       }
-    };
-    if (!bad) {
-      values(std::false_type{});
-    } else {
-      values(std::true_type{});
+
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + (2 * ST + stage) * 8);
+
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int src = (lane & 28) | ((t & 7) >> 1);
-        const float p0 = __shfl_sync(0xffffffffu, s[t / 8][t & 1], src);
-        const float p1 = __shfl_sync(0xffffffffu, s[t / 8][2 + (t & 1)], src);
-        const int j = j0 + t;
-        const bool see0 = j <= pos[0] && (a.window == 0 || j > pos[0] - a.window || j < a.sinks);
-        const bool see1 = j <= pos[1] && (a.window == 0 || j > pos[1] - a.window || j < a.sinks);
-        bool some = false;
-        for (int ch = lane; ch < CPR; ch += 32) {
-          const uint4 w = *reinterpret_cast<const uint4*>(smem + (vt - sbase) + tile_at<ROWB>(wt * NT + t, ch));
-          some |= (not_finite<E8>(w.x) | not_finite<E8>(w.y) | not_finite<E8>(w.z) | not_finite<E8>(w.w)) != 0;
+      for (int w = 0; w < RPW; ++w) {
+        // mask, running maximum, weights 2^(s scale - m)
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = j0 + i * 8 + 2 * (lane & 3) + (e & 1), p = pos[w][e >> 1];
+              const bool see = j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+              s[w][i][e] = see ? s[w][i][e] : -INFINITY;
+            }
         }
-        if (!__any_sync(0xffffffffu, some)) continue;
+        float corr[2], base[2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int r = 0; r < 2; ++r) {
+          float top = fmaxf(s[w][0][2 * r], s[w][0][2 * r + 1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int col = out_col<E8>(i, e) * (E8 ? 1 : 2);
-            const unsigned char* w = smem + (vt - sbase) + tile_at<ROWB>(wt * NT + t, col / 16) + col % 16;
-            const float v = E8 ? e4m3_to_float(*w) : bf16_lo(*reinterpret_cast<const uint16_t*>(w));
-            if (fabsf(v) <= 3.4028235e38f) continue;
-            if (see0) o[i][e] += p0 * v;
-            if (see1) o[i][2 + e] += p1 * v;
+          for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          top = fmaxf(top * qf[w].scale[r], mx[w][r]);
+          base[r] = top == -INFINITY ? 0.f : top;
+          corr[r] = ex2(mx[w][r] - base[r]);
+          mx[w][r] = top;
+          sum[w][r][0] *= corr[r];
+          sum[w][r][1] *= corr[r];
+        }
+        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            fmul2(o[w][i][0], o[w][i][1], corr[0]);
+            fmul2(o[w][i][2], o[w][i][3], corr[1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            fms2(s[w][i][2 * r], s[w][i][2 * r + 1], qf[w].scale[r], base[r]);
+            s[w][i][2 * r] = ex2(s[w][i][2 * r]);
+            s[w][i][2 * r + 1] = ex2(s[w][i][2 * r + 1]);
+            fadd2(sum[w][r][0], sum[w][r][1], s[w][i][2 * r], s[w][i][2 * r + 1]);
           }
       }
+
+      if (!lost) lost = !mbar_wait(bars + (ST + stage) * 8, (it / ST) & 1, kStatusTimeoutFull);
+      // A token that a row does not see meets it with weight 0, and 0 times its
+      // value must be 0.  Where such a value is not finite (a later draft row's, or
+      // what lies past the length), the product is taken with 0 in the place of
+      // every value that is not, and those are added element by element to the
+      // rows that see them.
+      auto row_bad = [&](int t) {  // some element of token t's value is not finite (this lane's chunks)
+        uint32_t x = 0;
+        for (int ch = lane; ch < CPR; ch += 32) {
+          const uint4 u = *reinterpret_cast<const uint4*>(smem + voff + tile_at<ROWB>(t, ch));
+          x |= not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w);
+        }
+        return x != 0;
+      };
+      bool bad = false;
+      if (!full) {
+        auto scan = [&](int from, int to) {
+          for (int j = max(from, j0); j < min(to, j0 + NT); ++j) bad |= row_bad(j - j0);
+        };
+        scan(max(cc.v.pos_lo + 1, 0), INT_MAX);
+        if (a.window != 0) scan(a.sinks, min(cc.v.pos_hi - a.window, cc.v.pos_lo) + 1);
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      auto values = [&](auto clean) {
+        constexpr bool kClean = decltype(clean)::value;
+#pragma unroll
+        for (int t = 0; t < NT / 16; ++t) {
+          // fp16 holds a probability to 11 bits; bf16 to 8 only, so its rest goes in as a second operand
+          uint32_t p[RPW][4], rest[RPW][4];
+#pragma unroll
+          for (int w = 0; w < RPW; ++w)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float lo = s[w][2 * t + (x >> 1)][2 * (x & 1)], hi = s[w][2 * t + (x >> 1)][2 * (x & 1) + 1];
+              p[w][x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+              rest[w][x] = E8 ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
+            }
+#pragma unroll
+          for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
+            uint32_t b[4];
+            ldsm_x4_t(b, vt + tile_at<ROWB>(t * 16 + (lane & 15), (E8 ? d : 2 * d) + (lane >> 4)));
+            if constexpr (kClean)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) b[x] &= ~not_finite<E8>(b[x]);
+            if constexpr (!E8) {
+#pragma unroll
+              for (int w = 0; w < RPW; ++w) {
+                mma_bf16_16816(o[w][2 * d], p[w], b[0], b[1]);
+                mma_bf16_16816(o[w][2 * d + 1], p[w], b[2], b[3]);
+                mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
+                mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
+              }
+            } else {
+              // a chunk's 16 dims come in pairs: even and odd dims become one tile each
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {  // chunk d + x
+                const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4420));
+                const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4420));
+                const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4431));
+                const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4431));
+#pragma unroll
+                for (int w = 0; w < RPW; ++w) {
+                  mma_f16_16816(o[w][2 * (d + x)], p[w], e0, e1);
+                  mma_f16_16816(o[w][2 * (d + x) + 1], p[w], f0, f1);
+                }
+              }
+            }
+          }
+        }
+      };
+      if (!bad) {
+        values(std::false_type{});
+      } else {
+        values(std::true_type{});
+#pragma unroll 1
+        for (int t = 0; t < NT; ++t) {
+          if (!__any_sync(0xffffffffu, row_bad(t))) continue;
+          const int src = (lane & 28) | ((t & 7) >> 1), j = j0 + t;
+#pragma unroll
+          for (int w = 0; w < RPW; ++w) {
+            float p[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if (i == t >> 3) p[r] = (t & 1) ? s[w][i][2 * r + 1] : s[w][i][2 * r];
+            bool see[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              p[r] = __shfl_sync(0xffffffffu, p[r], src);
+              see[r] = j <= pos[w][r] && (a.window == 0 || j > pos[w][r] - a.window || j < a.sinks);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = out_col<E8>(i, e) * (E8 ? 1 : 2);
+                const unsigned char* u = smem + voff + tile_at<ROWB>(t, col / 16) + col % 16;
+                const float v = E8 ? e4m3_to_float(*u) : bf16_lo(*reinterpret_cast<const uint16_t*>(u));
+                const bool odd = !(fabsf(v) <= 3.4028235e38f);
+                if (odd && see[0]) o[w][i][e] += p[0] * v;
+                if (odd && see[1]) o[w][i][2 + e] += p[1] * v;
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + (3 * ST + stage) * 8);
     }
 
-    // the end of a segment, or of this CTA's share of it
-    if (cc.k + 1 == cc.v.tiles || it + 1 == n) {
-      const bool whole = k_first == 0 && cc.k + 1 == cc.v.tiles;
-      const int slot = blockIdx.x * 2 + (k_first == 0 ? 1 : 0);
+    {
+      // the end of the segment, or of this CTA's share of it
+      const bool whole = cc.kb == 0 && cc.ke == cc.v.tiles;
+      const int slot = blockIdx.x * 2 + (cc.kb == 0 ? 1 : 0);
+      if (cc.left == cc.ke - cc.kb && tid == 0) {  // the last segment of the share: how many CTAs hold it
+        const long long end = t0 + cc.it + cc.v.tiles - 1;  // its last tile, if it begins here
+        a.part_seg[blockIdx.x] = whole || cc.kb != 0 ? make_int4(0, 0, 0, 0)
+                                                     : make_int4(cc.b, cc.h, cc.rt, share_of(T, P, end) - blockIdx.x + 1);
+      }
+      float l[RPW][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-      }
-      float2* const ml = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
-      float* const join = reinterpret_cast<float*>(smem + Cfg::OFF_JOIN);
-      if (Cfg::WT > 1 && (lane & 3) == 0) {
-        ml[warp * 16 + (lane >> 2)] = make_float2(mx[0], sum[0]);
-        ml[warp * 16 + (lane >> 2) + 8] = make_float2(mx[1], sum[1]);
-      }
-      // Rows in slices of DS columns through shared memory: the warps of a row
-      // group are added, and a thread then holds four columns of a row.
-      constexpr int DS = Cfg::DS;
+      for (int w = 0; w < RPW; ++w)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          l[w][r] = sum[w][r][0] + sum[w][r][1];
+          l[w][r] += __shfl_xor_sync(0xffffffffu, l[w][r], 1);
+          l[w][r] += __shfl_xor_sync(0xffffffffu, l[w][r], 2);
+        }
+      // Four columns of a row: to the outputs, or to this CTA's part.
       const int rows = a.M * a.G - cc.rt * a.RB;  // rows of this block that exist
       auto put = [&](int row, int col, float4 v, float m_all, float l_all) {
         if (row >= rows) return;
@@ -705,119 +879,114 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, E8, RG>::CTAS) attent
           const bool some = i < cc.m && l_all != 0.f;  // NaN sums count
           const float f = some ? a.v_scale / l_all : 0.f;
           const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
-          uint2 w = make_uint2(0u, 0u);
-          if (some) w = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
-          *reinterpret_cast<uint2*>(a.out + at * D + col) = w;
+          uint2 u = make_uint2(0u, 0u);
+          if (some) u = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+          *reinterpret_cast<uint2*>(a.out + at * D + col) = u;
           if (col == 0 && a.lse != nullptr) a.lse[at] = some ? (m_all + log2f(l_all)) * 0.6931471805599453f : -INFINITY;
         } else {
           *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * a.RB + row) * D + col) = v;
           if (col == 0) a.part_ml[static_cast<int64_t>(slot) * a.RB + row] = make_float2(m_all, l_all);
         }
       };
-      if constexpr (Cfg::WT > 1) {
+      // Rows in slices of DS columns through shared memory: the teams are added
+      // there, and a thread then holds four columns of a row.
+      constexpr int DS = Cfg::DS, WR = 16 * RPW;  // rows of a warp
+      float2* const ml = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
+      float* const join = reinterpret_cast<float*>(smem + Cfg::OFF_JOIN);
+      if ((lane & 3) == 0) {
 #pragma unroll
-        for (int d0 = 0; d0 < D; d0 += DS) {
-          __syncthreads();
+        for (int w = 0; w < RPW; ++w)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            ml[warp * WR + w * 16 + r * 8 + (lane >> 2)] = make_float2(mx[w][r], l[w][r]);
+      }
+#pragma unroll
+      for (int d0 = 0; d0 < D; d0 += DS) {
+        compute_sync();
+#pragma unroll
+        for (int w = 0; w < RPW; ++w)
 #pragma unroll
           for (int i = d0 / 8; i < (d0 + DS) / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              join[(warp * 16 + (lane >> 2) + 8 * (e >> 1)) * (DS + 4) + out_col<E8>(i, e & 1) - d0] = o[i][e];
-          __syncthreads();
+              join[(warp * WR + w * 16 + (lane >> 2) + 8 * (e >> 1)) * (DS + 4) + out_col<E8>(i, e & 1) - d0] = o[w][i][e];
+        compute_sync();
+        for (int x = tid; x < RG * WR * (DS / 4); x += 32 * kComputeWarps) {
+          const int row = x / (DS / 4), col = (x % (DS / 4)) * 4, w0 = row / WR;  // the row's warp in each team
+          float m_all = -INFINITY, l_all = 0.f;
 #pragma unroll
-          for (int x = tid; x < RG * 16 * (DS / 4); x += kAttnThreads) {
-            const int row = x / (DS / 4), col = (x % (DS / 4)) * 4, w0 = (row / 16) * Cfg::WT;
-            float m_all = -INFINITY, l_all = 0.f;
+          for (int t = 0; t < TEAMS; ++t) m_all = fmaxf(m_all, ml[(w0 + t * RG) * WR + row % WR].x);
+          const float base = m_all == -INFINITY ? 0.f : m_all;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < Cfg::WT; ++w) m_all = fmaxf(m_all, ml[(w0 + w) * 16 + row % 16].x);
-            const float base = m_all == -INFINITY ? 0.f : m_all;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < Cfg::WT; ++w) {
-              const float2 p = ml[(w0 + w) * 16 + row % 16];
-              const float f = ex2(p.x - base);
-              const float4 u = *reinterpret_cast<const float4*>(join + ((w0 + w) * 16 + row % 16) * (DS + 4) + col);
-              l_all += f * p.y;
-              v.x += f * u.x;
-              v.y += f * u.y;
-              v.z += f * u.z;
-              v.w += f * u.w;
-            }
-            put(row, d0 + col, v, m_all, l_all);
+          for (int t = 0; t < TEAMS; ++t) {
+            const float2 p = ml[(w0 + t * RG) * WR + row % WR];
+            const float f = ex2(p.x - base);
+            const float4 u = *reinterpret_cast<const float4*>(join + ((w0 + t * RG) * WR + row % WR) * (DS + 4) + col);
+            l_all += f * p.y;
+            v.x += f * u.x;
+            v.y += f * u.y;
+            v.z += f * u.z;
+            v.w += f * u.w;
           }
-        }
-        __syncthreads();
-      } else {
-        // four columns of a row from two lanes: even lanes take the upper row, odd ones the lower
-#pragma unroll
-        for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
-          const int odd = lane & 1;
-          if constexpr (E8) {
-            put(rg * 16 + (lane >> 2), out_col<true>(i, 0), make_float4(o[i][0], o[i + 1][0], o[i][1], o[i + 1][1]), mx[0], sum[0]);
-            put(rg * 16 + (lane >> 2) + 8, out_col<true>(i, 0), make_float4(o[i][2], o[i + 1][2], o[i][3], o[i + 1][3]), mx[1], sum[1]);
-          } else {
-            const float x0 = __shfl_xor_sync(0xffffffffu, odd ? o[i][0] : o[i][2], 1);
-            const float x1 = __shfl_xor_sync(0xffffffffu, odd ? o[i][1] : o[i][3], 1);
-            const int col = i * 8 + ((lane & 2) << 1);
-            if (!odd) put(rg * 16 + (lane >> 2), col, make_float4(o[i][0], o[i][1], x0, x1), mx[0], sum[0]);
-            else put(rg * 16 + (lane >> 2) + 8, col, make_float4(x0, x1, o[i][2], o[i][3]), mx[1], sum[1]);
-          }
+          put(row, d0 + col, v, m_all, l_all);
         }
       }
-      fresh = true;
+      compute_sync();
     }
-    if (it + 1 < n) cc.next(a);
-    if (more) {
-      if (tid < kKvTile) finish(np, nh, stage, tid);
-      pc.next(a);
-    }
-  }
+  } while (cc.next(a));
 }
 
-// Combines the parts of segments that several CTAs share, and writes the rows
-// of segments without tiles.  One warp per row, D / 32 columns a lane.
+// Combines the parts of segments that several CTAs share: the CTA a segment
+// begins in left its place and the number of parts.  One warp per row, D / 32
+// columns a lane; the parts' statistics are loaded by one lane each.
 template <int D>
-__global__ void __launch_bounds__(kAttnThreads) join_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_seg = a.RB / 4;
-  const int seg = blockIdx.x / per_seg;
+  const int per_seg = a.RB / 4, c0 = blockIdx.x / per_seg;
+  const int4 seg = a.part_seg[c0];
   const int row = (blockIdx.x % per_seg) * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int rt = seg % a.RT, h = (seg / a.RT) % a.c.heads, b = seg / a.RT / a.c.heads;
-  const int gr = rt * a.RB + row;
-  if (gr >= a.M * a.G) return;
-  long long begin;
-  const long long T = total_tiles(a, b, &begin);
-  const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
-  begin += static_cast<long long>(head_tiles(a, b)) * h;
-  for (int r = 0; r < rt; ++r) begin += visible(a, L, m, r).tiles;
-  const int n = visible(a, L, m, rt).tiles;
-  const int i = gr / a.G;
+  const int gr = seg.z * a.RB + row;
+  if (seg.w < 2 || gr >= a.M * a.G) return;
+  const int b = seg.x, h = seg.y, i = gr / a.G;
+  const bool valid = i < new_rows(a.q_lens, b, a.M);
   const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
   constexpr int E = D / 32;  // 2, 4 or 8 columns
   float v[E] = {};
   float top = -INFINITY, sum = 0.f;
-  if (n > 0) {
-    const int P = working(a, T), c0 = share_of(T, P, begin), c1 = share_of(T, P, begin + n - 1);
-    if (c0 == c1) return;
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.part_ml[static_cast<int64_t>(c * 2 + (c == c0)) * a.RB + row].x);
-    const float base = top == -INFINITY ? 0.f : top;
+  for (int base = 0; base < seg.w; base += 32) {
+    // the first part is its CTA's second slot, the others the first
+    const int n = min(32, seg.w - base);
+    const int64_t mine = static_cast<int64_t>((c0 + base + lane) * 2 + (base + lane == 0)) * a.RB + row;
+    const float2 ml = lane < n ? a.part_ml[mine] : make_float2(-INFINITY, 0.f);
+    float t = ml.x;
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
+    t = fmaxf(t, top);
+    const float ref = t == -INFINITY ? 0.f : t, old = ex2(top - ref);
+    const float f = ex2(ml.x - ref);
+    float l = f * ml.y;
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
+    sum = sum * old + l;
+    top = t;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= old;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t p = static_cast<int64_t>(c * 2 + (c == c0)) * a.RB + row;
-      const float2 ml = a.part_ml[p];
-      const float f = ex2(ml.x - base);
-      sum += f * ml.y;
+    for (int c = 0; c < n; ++c) {
+      const float g = __shfl_sync(0xffffffffu, f, c);
+      const int64_t p = static_cast<int64_t>((c0 + base + c) * 2 + (base + c == 0)) * a.RB + row;
       const float2* src = reinterpret_cast<const float2*>(a.part_o + p * D + lane * E);
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
         const float2 u = src[e];
-        v[2 * e] += f * u.x;
-        v[2 * e + 1] += f * u.y;
+        v[2 * e] += g * u.x;
+        v[2 * e + 1] += g * u.y;
       }
     }
   }
-  const bool some = i < m && n > 0 && sum != 0.f;
+  const bool some = valid && sum != 0.f;
   const float f = some ? a.v_scale / sum : 0.f;
 #pragma unroll
   for (int e = 0; e < E / 2; ++e)

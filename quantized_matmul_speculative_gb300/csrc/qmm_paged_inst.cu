@@ -1,4 +1,6 @@
 // The attention kernels of one head size, chosen by -DQMM_HEAD_DIM.
+#include <mutex>
+
 #include "qmm_paged.cuh"
 
 #ifndef QMM_HEAD_DIM
@@ -7,23 +9,79 @@
 
 namespace qmm {
 
-template <int D, bool E8, int RG>
-cudaError_t launch_rows(const AttentionArgs& a, cudaStream_t stream) {
-  using Cfg = AttnCfg<D, E8, RG>;
-  auto kern = attention_kernel<D, E8, RG>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
+static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// The cache as (byte column of a slice, token of a page, slice, head, page),
+// boxes of a.box tokens; false where the driver does not take it.
+static bool cache_map(CUtensorMap* map, const AttentionArgs& a, int D, bool e8, void* base, int64_t page, int64_t token,
+                      int64_t head) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = map_encoder();
+  if (encode == nullptr) return false;
+  const int es = e8 ? 1 : 2, rowb = D * es, slice = rowb < 128 ? rowb : 128, slices = rowb / slice;
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(slice), static_cast<cuuint64_t>(a.c.page_size),
+                              static_cast<cuuint64_t>(slices), static_cast<cuuint64_t>(a.c.heads),
+                              static_cast<cuuint64_t>(a.c.num_pages)};
+  // strides of dimensions of one entry are never used: any valid value does
+  auto stride = [&](int64_t elements, int64_t extent) {
+    return static_cast<cuuint64_t>(extent > 1 ? elements * es : 16);
+  };
+  const cuuint64_t strides[4] = {stride(token, a.c.page_size), static_cast<cuuint64_t>(slice), stride(head, a.c.heads),
+                                 stride(page, a.c.num_pages)};
+  for (cuuint64_t s : strides)
+    if (static_cast<int64_t>(s) <= 0 || s >= (1ull << 40)) return false;
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(slice), static_cast<cuuint32_t>(a.box),
+                             static_cast<cuuint32_t>(a.box == 16 ? slices : 1), 1, 1};
+  const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                slice == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E8, int RG, int RPW>
+cudaError_t launch_rows(const AttentionArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  using Cfg = AttnCfg<D, E8, RG, RPW>;
+  auto kern = attention_kernel<D, E8, RG, RPW>;
+  // the register split needs what the kernel was built with: never launched with less
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(a.parts), kAttnThreads, Cfg::SMEM, stream, a);
+  if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(a.parts), kAttnThreads, Cfg::SMEM, stream, a, kmap, vmap);
 }
 
 template <int D>
 cudaError_t launch_attention(AttentionArgs a, bool e8, cudaStream_t stream) {
-  const cudaError_t e = a.RB == 16   ? (e8 ? launch_rows<D, true, 1>(a, stream) : launch_rows<D, false, 1>(a, stream))
-                        : a.RB == 32 ? (e8 ? launch_rows<D, true, 2>(a, stream) : launch_rows<D, false, 2>(a, stream))
-                                     : (e8 ? launch_rows<D, true, 4>(a, stream) : launch_rows<D, false, 4>(a, stream));
+  // TMA boxes where they divide a page; else, and for strides the TMA cannot
+  // take, row by row.
+  CUtensorMap kmap = {}, vmap = {};
+  a.box = a.c.page_size % 16 == 0 ? 16 : a.c.page_size % 8 == 0 ? 8 : 0;
+  if (a.c.num_pages < 1) a.box = 0;
+  if (a.box != 0 && (!cache_map(&kmap, a, D, e8, a.c.k, a.c.k_page, a.c.k_token, a.c.k_head) ||
+                     !cache_map(&vmap, a, D, e8, a.c.v, a.c.v_page, a.c.v_token, a.c.v_head)))
+    a.box = 0;
+  // Two row tiles a warp share its key and value fragments (and an E4M3
+  // cache's conversions); D = 256 has registers for the outputs of one only.
+  constexpr int W = D == 256 ? 1 : 2;
+  const cudaError_t e =
+      a.RB == 16   ? (e8 ? launch_rows<D, true, 1, 1>(a, kmap, vmap, stream) : launch_rows<D, false, 1, 1>(a, kmap, vmap, stream))
+      : a.RB == 32 ? (e8 ? launch_rows<D, true, 2 / W, W>(a, kmap, vmap, stream) : launch_rows<D, false, 2 / W, W>(a, kmap, vmap, stream))
+                   : (e8 ? launch_rows<D, true, 4 / W, W>(a, kmap, vmap, stream) : launch_rows<D, false, 4 / W, W>(a, kmap, vmap, stream));
   if (e != cudaSuccess) return e;
-  const int64_t blocks = static_cast<int64_t>(a.B) * a.c.heads * a.RT * (a.RB / 4);
-  return launch_dependent(join_kernel<D>, dim3(static_cast<unsigned>(blocks)), kAttnThreads, 0, stream, a);
+  return launch_dependent(join_kernel<D>, dim3(a.parts * (a.RB / 4)), kJoinThreads, 0, stream, a);
 }
 
 template <int D>

@@ -135,6 +135,15 @@ def test_lengths(lens):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("page", [16, 12])
+@pytest.mark.parametrize("M,Hq,D", [(1, 16, 128), (2, 32, 128), (4, 64, 64), (16, 16, 64), (1, 8, 256), (4, 32, 256)])
+def test_many_tiles_per_sm(M, Hq, D, page, dtype):
+    """Long lists: every stage of an SM's ring is refilled many times, and queues of unequal speed run beside each other."""
+    c = Cache([40000, 9000, 31000], 8, D, page, dtype, seed=M, k_scale=0.5, v_scale=0.5)
+    check(c, queries(3, M, Hq, D), rows=[M, 1, M])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (16, 4), (63, 0), (64, 64), (65, 1), (100, 130),
                                           (300, 5), (5000, 4), (1000000, 7)])
 def test_window_and_sinks(window, sinks, dtype):
