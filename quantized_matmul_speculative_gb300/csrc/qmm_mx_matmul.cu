@@ -9,12 +9,15 @@
 // One CTA computes a tile of 128 columns x BN rows over K, or, where there are
 // few tiles, a cluster of C CTAs a share of K each, added in rank order through
 // distributed shared memory.  Warp 0 copies code tiles (256 codes = 128 bytes a
-// row, TMA with the 128-byte swizzle), warps 2..5 the scale bytes, and one
-// thread of warp 1 issues, per stage, the copies of the scales into tensor
-// memory and four MMAs of 64 codes each.  The scale bytes come from the
-// canonical [rows, K/g] layout; a stage holds them as the tensor memory copy
-// wants them: per 4 bytes of K (64 codes of nvfp4, 128 of mxfp4) and 128 rows
-// 512 bytes, row r's at (r mod 32) * 16 + (r / 32) * 4.
+// row, TMA with the 128-byte swizzle), one thread of warp 1 issues four MMAs of
+// 64 codes a stage, and warps 2..5 move the scale bytes from the canonical
+// [rows, K/g] layout into tensor memory, where an MMA wants, for 4 bytes of K
+// (64 codes of nvfp4, 128 of mxfp4) and rows 32 c + l, lane l of each of the
+// four lane quarters, column c: a thread loads its own rows' bytes, they pass
+// through shared memory, and every warp stores the words of all rows to its
+// quarter.  (With the tensor core's own copies from shared memory instead, 12
+// of 50 ns a stage at BN = 256 beside 260 ns of MMAs, the 1000 x 34816 x 5120
+// product took 201 us.)
 //
 // Arithmetic: codes and scales are exact, their products too; the accumulator
 // is fp32.
@@ -23,6 +26,7 @@
 #include <algorithm>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -47,20 +51,20 @@ struct MxMatmulArgs {
   int split;    // CTAs of a cluster
   int stages;
   int pitch;    // scale bytes of a row
-  int words;    // scale bytes can be copied 4 at a time
+  int aligned;  // rows of scales are whole, aligned stages
   uint32_t tmem_cols;
 };
 
 // Shared-memory layout (offsets from a 1024-byte aligned start).
 struct GemmSmem {
-  int x, sfw, sfx, stage;  // within a stage: weight codes, activation codes, scales
+  int x, stage;  // a stage: weight codes, activation codes
+  int scales;    // [2][blocks of 128 rows][128] rows' words on their way
   int bars, total;
   __host__ __device__ GemmSmem(int BN, int stages, int sf_words) {
     x = kCodesW;
-    sfw = x + ((BN * (kTileK / 2) + 1023) & ~1023);
-    sfx = sfw + 512 * sf_words;
-    stage = (sfx + ((BN + 127) / 128) * 512 * sf_words + 1023) & ~1023;
-    bars = stages * stage;
+    stage = x + ((BN * (kTileK / 2) + 1023) & ~1023);
+    scales = stages * stage;
+    bars = scales + 2 * (1 + (BN + 127) / 128) * 128 * 4 * sf_words;
     total = bars + (2 * stages + 1) * 8 + 16;
   }
 };
@@ -71,10 +75,21 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t stride_byt
   return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (static_cast<uint64_t>(stride_bytes >> 4) << 32) |
          (1ull << 46) | (static_cast<uint64_t>(layout) << 61);
 }
-constexpr uint32_t kSwizzle128 = 2, kSwizzleNone = 0;
+constexpr uint32_t kSwizzle128 = 2;
 
-__device__ __forceinline__ void tmem_copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// N columns of this warp's lane quarter.
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* v) {
+  if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+  } else {
+    static_assert(N == 8, "8 or 16 columns");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+  }
 }
 template <bool NV>
 __device__ __forceinline__ void mma_block_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -102,15 +117,181 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 4 scale bytes of row `row` from byte `at` on; those past the row's end, and
-// rows past the matrix, are 0 (their codes are 0 too).
-__device__ __forceinline__ uint32_t scale_bytes(const uint8_t* s, int64_t row, int rows, int pitch, int at) {
-  uint32_t w = 0;
-  if (row < rows)
+// The scale bytes of one row, a stage's worth (4 SFW bytes) at a time: aligned
+// chunks, four loaded ahead, in a ring whose places are compile-time numbers (u).
+// ALIGNED: every row starts on a chunk, and chunks are whole stages.  Else a
+// stage's bytes lie in two chunks and are shifted together; chunks that reach
+// out of the matrix are loaded byte by byte, and bytes past the row's end are 0
+// (the codes there are 0, and 0 times a foreign NaN would not be).  Rows past
+// the matrix read its last row: their codes are 0 and their outputs not stored.
+template <int SFW, bool ALIGNED>
+struct ScaleRow {
+  const uint8_t* next;  // the chunk to load next
+  const uint8_t* begin;
+  const uint8_t* end;   // of the matrix
+  uint32_t c[4][SFW];
+  int shift;            // the stage's first byte in its first chunk
+
+  __device__ __forceinline__ void load(uint32_t (&w)[SFW], bool wanted) {
+    if (ALIGNED ? wanted : (next >= begin && next + 4 * SFW <= end)) {
+      if constexpr (SFW == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(next));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(next));
+        w[0] = v.x, w[1] = v.y;
+      }
+    } else if (!ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (at + i < pitch) w |= static_cast<uint32_t>(s[row * pitch + at + i]) << (8 * i);
-  return w;
+      for (int i = 0; i < SFW; ++i) w[i] = 0;
+#pragma unroll 1
+      for (int i = 0; i < 4 * SFW; ++i)
+        if (next + i >= begin && next + i < end) {
+          const uint32_t byte = static_cast<uint32_t>(__ldg(next + i)) << (8 * (i & 3));
+#pragma unroll
+          for (int x = 0; x < SFW; ++x)
+            if (x == i >> 2) w[x] |= byte;
+        }
+    }
+    next += 4 * SFW;
+  }
+  // Row `row` (the last one if there is none), stages `stage` .. stage_end - 1.
+  __device__ __forceinline__ void start(const uint8_t* s, int row, int rows, int pitch, int stage, int stage_end) {
+    const uint8_t* at = s + static_cast<int64_t>(min(row, rows - 1)) * pitch + stage * (4 * SFW);
+    shift = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(at) & (4 * SFW - 1));
+    next = at - shift;
+    begin = s;
+    end = s + static_cast<int64_t>(rows) * pitch;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(c[i], stage + i < stage_end);
+  }
+  // The stage's words, of which `valid` bytes are the row's; chunk u is then
+  // replaced by the one four on, if it is wanted.
+  template <int U>
+  __device__ __forceinline__ void take(uint32_t (&w)[SFW], int valid, bool wanted) {
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < SFW; ++i) w[i] = c[U][i];
+    } else {
+      uint32_t x[2 * SFW];
+#pragma unroll
+      for (int i = 0; i < SFW; ++i) x[i] = c[U][i], x[SFW + i] = c[(U + 1) & 3][i];
+      if (SFW == 4 && (shift & 8)) {
+#pragma unroll
+        for (int i = 0; i < 2 * SFW - 2; ++i) x[i] = x[i + 2];
+      }
+      if (shift & 4) {
+#pragma unroll
+        for (int i = 0; i < 2 * SFW - 1; ++i) x[i] = x[i + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < SFW; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], 8 * (shift & 3));
+      if (valid < 4 * SFW) {
+#pragma unroll
+        for (int i = 0; i < SFW; ++i) {
+          const int left = valid - 4 * i;
+          w[i] = left >= 4 ? w[i] : left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+        }
+      }
+    }
+    load(c[U], wanted);
+  }
+};
+
+// The scale warps.  Measured at 1000 x 34816 x 5120: with the loads' bounds and
+// shifts decided per stage (580 instructions a stage and warp) this alone was
+// the bound, 250 us.
+template <int SFW, bool ALIGNED, int XB>
+__device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSmem& L, unsigned char* smem, uint32_t full,
+                                             uint32_t empty, uint32_t tmem, int m0, int n0, int k_begin, int k_end) {
+  using Words = typename std::conditional<SFW == 4, uint4, uint2>::type;
+  const int r = threadIdx.x & 127, lane = r & 31;
+  Words* const pass = reinterpret_cast<Words*>(smem + L.scales);  // [2][1 + XB][128]
+  const uint32_t columns = tmem + a.BN + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
+  ScaleRow<SFW, ALIGNED> sw, sx[XB];
+  sw.start(a.ws, n0 + r, a.N, a.pitch, k_begin, k_end);
+#pragma unroll
+  for (int b = 0; b < XB; ++b) sx[b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, k_begin, k_end);
+  int s = 0;
+  uint32_t phase = 1;  // of the empty barriers: the first round passes at once
+  auto stage = [&](auto u, int k) {
+    constexpr int U = decltype(u)::value;
+    const int valid = a.pitch - k * (4 * SFW);
+    const bool wanted = k + 4 < k_end;
+    // (two places in turn: a thread that passed the barrier of stage k + 1 has read stage k's)
+    Words* const rows = pass + (U & 1) * (1 + XB) * 128;
+#pragma unroll
+    for (int b = 0; b <= XB; ++b) {
+      uint32_t w[SFW];
+      if (b == 0) sw.template take<U>(w, valid, wanted);
+      else sx[b > 0 ? b - 1 : 0].template take<U>(w, valid, wanted);
+      if constexpr (SFW == 4) rows[b * 128 + r] = make_uint4(w[0], w[1], w[2], w[3]);
+      else rows[b * 128 + r] = make_uint2(w[0], w[1]);
+    }
+    asm volatile("barrier.sync 1, 128;" ::: "memory");
+    // columns: word w of the weights' rows (4), then word w of the activations' (4 XB)
+    uint32_t v[(1 + XB) * 4 * SFW];
+#pragma unroll
+    for (int b = 0; b <= XB; ++b)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const Words x = rows[b * 128 + c * 32 + lane];
+        uint32_t w[4] = {x.x, x.y, 0, 0};
+        if constexpr (SFW == 4) w[2] = x.z, w[3] = x.w;
+#pragma unroll
+        for (int i = 0; i < SFW; ++i)
+          v[b == 0 ? i * 4 + c : SFW * 4 + i * XB * 4 + (b - 1) * 4 + c] = w[i];
+      }
+    if (__any_sync(0xffffffffu, !mbar_wait(empty + s * 8, phase, kStatusTimeoutEmpty))) return false;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    constexpr int kCols = (1 + XB) * 4 * SFW;  // 16, 24, 32 or 48
+    const uint32_t at = columns + s * kCols;
+#pragma unroll
+    for (int c = 0; c + 16 <= kCols; c += 16) tmem_store<16>(at + c, v + c);
+    if constexpr (kCols % 16 != 0) tmem_store<8>(at + kCols - 8, v + kCols - 8);
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    mbar_arrive(full + s * 8);
+    if (++s == a.stages) {
+      s = 0;
+      phase ^= 1;
+    }
+    return true;
+  };
+  // A stage given up (after its wait ran out) gives up the rest: every warp
+  // still meets the others at the barrier of each stage.
+  bool ok = true;
+  auto tick = [&](auto u, int k) {
+    if (k >= k_end) return;
+    if (ok) ok = stage(u, k);
+    else asm volatile("barrier.sync 1, 128;" ::: "memory");
+  };
+  for (int k = k_begin; k < k_end; k += 4) {
+    tick(std::integral_constant<int, 0>{}, k);
+    tick(std::integral_constant<int, 1>{}, k + 1);
+    tick(std::integral_constant<int, 2>{}, k + 2);
+    tick(std::integral_constant<int, 3>{}, k + 3);
+  }
+}
+
+// A warp's 32 accumulator lanes (columns of Y) to `rows` rows of Y, from its
+// lane's element of the first one on.  Whole groups of 16 rows need no test.
+template <class T>
+__device__ __forceinline__ void store_tile(uint32_t acc, T* y, int64_t ld, int rows, bool inside) {
+  for (int c = 0; c < rows; c += 16, y += 16 * ld) {
+    uint32_t v[16];
+    tmem_load16(v, acc + c);
+    tmem_wait_load();
+    if (!inside) continue;
+    if (c + 16 <= rows) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i * ld] = static_cast<T>(__uint_as_float(v[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < rows) y[i * ld] = static_cast<T>(__uint_as_float(v[i]));
+    }
+  }
 }
 
 template <bool NV>
@@ -175,15 +356,8 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
         const int it = k - k_begin, s = it % a.stages;
         if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scales were written by threads
         const uint32_t base = sbase + s * L.stage;
         const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + xb)), sfx = sfw + SFW * 4;
-#pragma unroll
-        for (int w = 0; w < SFW; ++w) {
-          tmem_copy_scales(sfw + w * 4, smem_desc(base + L.sfw + w * 512, 128, kSwizzleNone));
-          for (int b = 0; b < xb; ++b)
-            tmem_copy_scales(sfx + (w * xb + b) * 4, smem_desc(base + L.sfx + (w * xb + b) * 512, 128, kSwizzleNone));
-        }
         const uint64_t da = smem_desc(base, 1024, kSwizzle128), db = smem_desc(base + L.x, 1024, kSwizzle128);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -198,56 +372,32 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
       mma_commit(done);
     }
   } else {
-    // scale bytes of weight row r and of activation rows r, r + 128
-    const int r = threadIdx.x - 64;
-    const int at_r = (r & 31) * 16 + (r >> 5) * 4;
-    bool lost = false;
-    const int xb = (a.BN + 127) / 128;
-    for (int k = k_begin; k < k_end; ++k) {
-      const int it = k - k_begin, s = it % a.stages;
-      if (it >= a.stages && !lost) lost = !mbar_wait(empty + s * 8, ((it / a.stages) & 1) ^ 1, kStatusTimeoutEmpty);
-      if (lost) break;
-      const uint32_t base = sbase + s * L.stage;
-      for (int b = 0; b <= xb; ++b) {  // the weights' block, then the activations'
-        const bool isx = b > 0;
-        const int64_t row = isx ? static_cast<int64_t>(m0) + (b - 1) * 128 + r : static_cast<int64_t>(n0) + r;
-        const int rows = isx ? min(a.M, m0 + a.BN) : a.N;
-        const uint8_t* src = isx ? a.xs : a.ws;
-#pragma unroll
-        for (int w = 0; w < SFW; ++w) {
-          const uint32_t dst = base + (isx ? L.sfx + (w * xb + b - 1) * 512 : L.sfw + w * 512) + at_r;
-          const int at = (k * SFW + w) * 4;
-          if (a.words) {
-            const bool ok = row < rows && at < a.pitch;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src + (ok ? row * a.pitch + at : 0)),
-                         "r"(ok ? 4 : 0) : "memory");
-          } else {
-            *reinterpret_cast<uint32_t*>(smem + (dst - sbase)) = scale_bytes(src, row, rows, a.pitch, at);
-          }
-        }
-      }
-      if (a.words) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + s * 8) : "memory");
-      else mbar_arrive(full + s * 8);
+    if (a.BN > 128) {
+      if (a.aligned) stage_scales<SFW, true, 2>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
+      else stage_scales<SFW, false, 2>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
+    } else {
+      if (a.aligned) stage_scales<SFW, true, 1>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
+      else stage_scales<SFW, false, 1>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     mbar_wait(done, 0, kStatusTimeoutDrain);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const int q = warp & 3;
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int n = n0 + q * 32 + lane;
-    float* const part = reinterpret_cast<float*>(smem);  // [BN][128], over the stages
-    for (int c = 0; c < a.BN; c += 16) {
-      uint32_t v[16];
-      tmem_load16(v, acc + c);
-      tmem_wait_load();
-      if (a.split > 1) {
+    if (a.split > 1) {
+      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;  // [BN][128], over the stages
+      for (int c = 0; c < a.BN; c += 16, part += 16 * kTileN) {
+        uint32_t v[16];
+        tmem_load16(v, acc + c);
+        tmem_wait_load();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kTileN + q * 32 + lane] = __uint_as_float(v[i]);
-      } else if (n < a.N) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (m0 + c + i < a.M) store_y(a.Y, nullptr, static_cast<int64_t>(m0 + c + i) * a.N + n, __uint_as_float(v[i]), a.out_f32);
+        for (int i = 0; i < 16; ++i) part[i * kTileN] = __uint_as_float(v[i]);
       }
+    } else if (a.out_f32) {
+      store_tile<float>(acc, static_cast<float*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N, min(a.BN, a.M - m0), n < a.N);
+    } else {
+      store_tile<__nv_bfloat16>(acc, static_cast<__nv_bfloat16*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N,
+                                min(a.BN, a.M - m0), n < a.N);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
@@ -330,7 +480,8 @@ cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cud
   constexpr int SFW = NV ? 4 : 2;
   a.ktiles = (a.K + kTileK - 1) / kTileK;
   a.pitch = a.K / (NV ? 16 : 32);
-  a.words = a.pitch % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & 3) == 0;
+  a.aligned = a.pitch % (4 * SFW) == 0 &&
+              ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & (4 * SFW - 1)) == 0;
   plan(a, device_sm_count());
   a.tiles_m = (a.M + a.BN - 1) / a.BN;
   const int64_t ctas = static_cast<int64_t>((a.N + kTileN - 1) / kTileN) * a.tiles_m * a.split;
