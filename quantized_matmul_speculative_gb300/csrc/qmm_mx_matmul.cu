@@ -10,7 +10,7 @@
 // few tiles, a cluster of C CTAs a share of K each, added in rank order through
 // distributed shared memory.  Warp 0 copies code tiles (256 codes = 128 bytes a
 // row, TMA with the 128-byte swizzle), one thread of warp 1 issues four MMAs of
-// 64 codes a stage, and warps 2..5 move the scale bytes from the canonical
+// 64 codes a stage, and warps 2..9 move the scale bytes from the canonical
 // [rows, K/g] layout into tensor memory, where an MMA wants, for 4 bytes of K
 // (64 codes of nvfp4, 128 of mxfp4) and rows 32 c + l, lane l of each of the
 // four lane quarters, column c: a thread loads its own rows' bytes, they pass
@@ -37,7 +37,8 @@ namespace {
 
 constexpr int kTileN = 128;   // columns of Y (rows of W) of a tile: the MMA's M
 constexpr int kTileK = 256;   // codes of a stage: 128 bytes a row
-constexpr int kGemmThreads = 192;
+constexpr int kScaleGroups = 2;  // of four warps, each with every second stage's scales
+constexpr int kGemmThreads = 64 + 128 * kScaleGroups;
 constexpr int kCodesW = kTileN * kTileK / 2;  // bytes of a stage's weight codes
 
 struct MxMatmulArgs {
@@ -58,13 +59,13 @@ struct MxMatmulArgs {
 // Shared-memory layout (offsets from a 1024-byte aligned start).
 struct GemmSmem {
   int x, stage;  // a stage: weight codes, activation codes
-  int scales;    // [2][blocks of 128 rows][128] rows' words on their way
+  int scales;    // [groups][2][blocks of 128 rows][128] rows' words on their way
   int bars, total;
   __host__ __device__ GemmSmem(int BN, int stages, int sf_words) {
     x = kCodesW;
     stage = x + ((BN * (kTileK / 2) + 1023) & ~1023);
     scales = stages * stage;
-    bars = scales + 2 * (1 + (BN + 127) / 128) * 128 * 4 * sf_words;
+    bars = scales + kScaleGroups * 2 * (1 + (BN + 127) / 128) * 128 * 4 * sf_words;
     total = bars + (2 * stages + 1) * 8 + 16;
   }
 };
@@ -117,45 +118,53 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
 }
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The scale bytes of one row, a stage's worth (4 SFW bytes) at a time: aligned
-// chunks, four loaded ahead, in a ring whose places are compile-time numbers (u).
-// ALIGNED: every row starts on a chunk, and chunks are whole stages.  Else a
-// stage's bytes lie in two chunks and are shifted together; chunks that reach
-// out of the matrix are loaded byte by byte, and bytes past the row's end are 0
-// (the codes there are 0, and 0 times a foreign NaN would not be).  Rows past
-// the matrix read its last row: their codes are 0 and their outputs not stored.
+// The scale bytes of one row, every second stage's (4 SFW bytes each), loaded
+// kAhead of them ahead into a ring whose places are compile-time numbers (u).
+// ALIGNED: every row starts on a multiple of a stage's bytes and holds whole
+// stages.  Else a stage's bytes lie in two aligned chunks and are shifted
+// together; chunks that reach out of the matrix are loaded byte by byte, and
+// bytes past the row's end are 0 (the codes there are 0, and 0 times a foreign
+// NaN would not be).  Rows past the matrix read its last row: their codes are
+// 0 and their outputs not stored.
 template <int SFW, bool ALIGNED>
 struct ScaleRow {
+  static constexpr int kAhead = ALIGNED ? 4 : 2, kChunks = ALIGNED ? 1 : 2;
   const uint8_t* next;  // the chunk to load next
   const uint8_t* begin;
   const uint8_t* end;   // of the matrix
-  uint32_t c[4][SFW];
+  uint32_t c[kAhead][kChunks * SFW];
   int shift;            // the stage's first byte in its first chunk
 
-  __device__ __forceinline__ void load(uint32_t (&w)[SFW], bool wanted) {
-    if (ALIGNED ? wanted : (next >= begin && next + 4 * SFW <= end)) {
-      if constexpr (SFW == 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(next));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(next));
-        w[0] = v.x, w[1] = v.y;
-      }
-    } else if (!ALIGNED) {
+  __device__ __forceinline__ void load(uint32_t (&w)[kChunks * SFW], bool wanted) {
+    if (wanted) {
 #pragma unroll
-      for (int i = 0; i < SFW; ++i) w[i] = 0;
+      for (int h = 0; h < kChunks; ++h) {
+        const uint8_t* const p = next + h * 4 * SFW;
+        if (ALIGNED || (p >= begin && p + 4 * SFW <= end)) {
+          if constexpr (SFW == 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            w[2 * h] = v.x, w[2 * h + 1] = v.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < SFW; ++i) w[h * SFW + i] = 0;
 #pragma unroll 1
-      for (int i = 0; i < 4 * SFW; ++i)
-        if (next + i >= begin && next + i < end) {
-          const uint32_t byte = static_cast<uint32_t>(__ldg(next + i)) << (8 * (i & 3));
+          for (int i = 0; i < 4 * SFW; ++i)
+            if (p + i >= begin && p + i < end) {
+              const uint32_t byte = static_cast<uint32_t>(__ldg(p + i)) << (8 * (i & 3));
 #pragma unroll
-          for (int x = 0; x < SFW; ++x)
-            if (x == i >> 2) w[x] |= byte;
+              for (int x = 0; x < SFW; ++x)
+                if (x == i >> 2) w[h * SFW + x] |= byte;
+            }
         }
+      }
     }
-    next += 4 * SFW;
+    next += kScaleGroups * 4 * SFW;
   }
-  // Row `row` (the last one if there is none), stages `stage` .. stage_end - 1.
+  // Row `row` (the last one if there is none), stages `stage`, stage + 2, .. before stage_end.
   __device__ __forceinline__ void start(const uint8_t* s, int row, int rows, int pitch, int stage, int stage_end) {
     const uint8_t* at = s + static_cast<int64_t>(min(row, rows - 1)) * pitch + stage * (4 * SFW);
     shift = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(at) & (4 * SFW - 1));
@@ -163,10 +172,10 @@ struct ScaleRow {
     begin = s;
     end = s + static_cast<int64_t>(rows) * pitch;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load(c[i], stage + i < stage_end);
+    for (int i = 0; i < kAhead; ++i) load(c[i], stage + kScaleGroups * i < stage_end);
   }
-  // The stage's words, of which `valid` bytes are the row's; chunk u is then
-  // replaced by the one four on, if it is wanted.
+  // The stage's words, of which `valid` bytes are the row's; place u is then
+  // refilled, if that stage is wanted.
   template <int U>
   __device__ __forceinline__ void take(uint32_t (&w)[SFW], int valid, bool wanted) {
     if constexpr (ALIGNED) {
@@ -175,7 +184,7 @@ struct ScaleRow {
     } else {
       uint32_t x[2 * SFW];
 #pragma unroll
-      for (int i = 0; i < SFW; ++i) x[i] = c[U][i], x[SFW + i] = c[(U + 1) & 3][i];
+      for (int i = 0; i < 2 * SFW; ++i) x[i] = c[U][i];
       if (SFW == 4 && (shift & 8)) {
 #pragma unroll
         for (int i = 0; i < 2 * SFW - 2; ++i) x[i] = x[i + 2];
@@ -198,27 +207,30 @@ struct ScaleRow {
   }
 };
 
-// The scale warps.  Measured at 1000 x 34816 x 5120: with the loads' bounds and
-// shifts decided per stage (580 instructions a stage and warp) this alone was
-// the bound, 250 us.
+// The scale warps, in two groups.  Measured at 1000 x 34816 x 5120: with the
+// loads' bounds and shifts decided per stage (580 instructions a stage and warp)
+// this alone was the bound, 250 us; with one group, whose chain of load, pass,
+// store and wait takes longer than a stage's MMAs, 149 us.
 template <int SFW, bool ALIGNED, int XB>
 __device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSmem& L, unsigned char* smem, uint32_t full,
                                              uint32_t empty, uint32_t tmem, int m0, int n0, int k_begin, int k_end) {
   using Words = typename std::conditional<SFW == 4, uint4, uint2>::type;
-  const int r = threadIdx.x & 127, lane = r & 31;
-  Words* const pass = reinterpret_cast<Words*>(smem + L.scales);  // [2][1 + XB][128]
+  using Row = ScaleRow<SFW, ALIGNED>;
+  const int r = threadIdx.x & 127, lane = r & 31, group = (threadIdx.x - 64) >> 7;
+  Words* const pass = reinterpret_cast<Words*>(smem + L.scales) + group * 2 * (1 + XB) * 128;  // [2][1 + XB][128]
   const uint32_t columns = tmem + a.BN + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
-  ScaleRow<SFW, ALIGNED> sw, sx[XB];
-  sw.start(a.ws, n0 + r, a.N, a.pitch, k_begin, k_end);
+  Row sw, sx[XB];
+  sw.start(a.ws, n0 + r, a.N, a.pitch, k_begin + group, k_end);
 #pragma unroll
-  for (int b = 0; b < XB; ++b) sx[b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, k_begin, k_end);
-  int s = 0;
-  uint32_t phase = 1;  // of the empty barriers: the first round passes at once
+  for (int b = 0; b < XB; ++b) sx[b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, k_begin + group, k_end);
+  bool ok = true;
   auto stage = [&](auto u, int k) {
     constexpr int U = decltype(u)::value;
+    if (k >= k_end) return;
+    const int it = k - k_begin, s = it % a.stages;
     const int valid = a.pitch - k * (4 * SFW);
-    const bool wanted = k + 4 < k_end;
-    // (two places in turn: a thread that passed the barrier of stage k + 1 has read stage k's)
+    const bool wanted = k + kScaleGroups * Row::kAhead < k_end;
+    // (two places in turn: a thread that passed the barrier of its next stage has read this one's)
     Words* const rows = pass + (U & 1) * (1 + XB) * 128;
 #pragma unroll
     for (int b = 0; b <= XB; ++b) {
@@ -228,7 +240,7 @@ __device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSm
       if constexpr (SFW == 4) rows[b * 128 + r] = make_uint4(w[0], w[1], w[2], w[3]);
       else rows[b * 128 + r] = make_uint2(w[0], w[1]);
     }
-    asm volatile("barrier.sync 1, 128;" ::: "memory");
+    asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
     // columns: word w of the weights' rows (4), then word w of the activations' (4 XB)
     uint32_t v[(1 + XB) * 4 * SFW];
 #pragma unroll
@@ -242,7 +254,10 @@ __device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSm
         for (int i = 0; i < SFW; ++i)
           v[b == 0 ? i * 4 + c : SFW * 4 + i * XB * 4 + (b - 1) * 4 + c] = w[i];
       }
-    if (__any_sync(0xffffffffu, !mbar_wait(empty + s * 8, phase, kStatusTimeoutEmpty))) return false;
+    // after a wait that ran out the rest is left out (a status bit); the warps still meet at every barrier above
+    if (ok && it >= a.stages)
+      ok = !__any_sync(0xffffffffu, !mbar_wait(empty + s * 8, ((it / a.stages) & 1) ^ 1, kStatusTimeoutEmpty));
+    if (!ok) return;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     constexpr int kCols = (1 + XB) * 4 * SFW;  // 16, 24, 32 or 48
     const uint32_t at = columns + s * kCols;
@@ -252,33 +267,24 @@ __device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSm
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     mbar_arrive(full + s * 8);
-    if (++s == a.stages) {
-      s = 0;
-      phase ^= 1;
+  };
+  for (int k = k_begin + group; k < k_end; k += kScaleGroups * Row::kAhead) {
+    stage(std::integral_constant<int, 0>{}, k);
+    stage(std::integral_constant<int, 1>{}, k + kScaleGroups);
+    if constexpr (Row::kAhead == 4) {
+      stage(std::integral_constant<int, 2>{}, k + 2 * kScaleGroups);
+      stage(std::integral_constant<int, 3>{}, k + 3 * kScaleGroups);
     }
-    return true;
-  };
-  // A stage given up (after its wait ran out) gives up the rest: every warp
-  // still meets the others at the barrier of each stage.
-  bool ok = true;
-  auto tick = [&](auto u, int k) {
-    if (k >= k_end) return;
-    if (ok) ok = stage(u, k);
-    else asm volatile("barrier.sync 1, 128;" ::: "memory");
-  };
-  for (int k = k_begin; k < k_end; k += 4) {
-    tick(std::integral_constant<int, 0>{}, k);
-    tick(std::integral_constant<int, 1>{}, k + 1);
-    tick(std::integral_constant<int, 2>{}, k + 2);
-    tick(std::integral_constant<int, 3>{}, k + 3);
   }
 }
 
-// A warp's 32 accumulator lanes (columns of Y) to `rows` rows of Y, from its
-// lane's element of the first one on.  Whole groups of 16 rows need no test.
+// A warp's 32 accumulator lanes (columns of Y) to the rows `first` .. rows - 1
+// of Y, every second 16 of them; `y` is its lane's element of row 0.  Whole
+// groups of 16 rows need no test.
 template <class T>
-__device__ __forceinline__ void store_tile(uint32_t acc, T* y, int64_t ld, int rows, bool inside) {
-  for (int c = 0; c < rows; c += 16, y += 16 * ld) {
+__device__ __forceinline__ void store_tile(uint32_t acc, T* y, int64_t ld, int first, int rows, bool inside) {
+  y += first * ld;
+  for (int c = first; c < rows; c += 16 * kScaleGroups, y += 16 * kScaleGroups * ld) {
     uint32_t v[16];
     tmem_load16(v, acc + c);
     tmem_wait_load();
@@ -294,8 +300,8 @@ __device__ __forceinline__ void store_tile(uint32_t acc, T* y, int64_t ld, int r
   }
 }
 
-template <bool NV>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+template <bool NV, int XB>  // XB blocks of 128 activation rows
+__global__ void __launch_bounds__(kGemmThreads, 3 - XB)
 mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   constexpr int SFW = NV ? 4 : 2;  // 4-byte scale words of a row in a stage
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -351,20 +357,19 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
       bool lost = false;
       const uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a.BN >> 3) << 17) | (NV ? 0u : 1u << 23) |
                              (static_cast<uint32_t>(kTileN >> 4) << 24);
-      const int xb = (a.BN + 127) / 128;  // 128-row blocks of activation scales
       for (int k = k_begin; k < k_end; ++k) {
         const int it = k - k_begin, s = it % a.stages;
         if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t base = sbase + s * L.stage;
-        const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + xb)), sfx = sfw + SFW * 4;
+        const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + XB)), sfx = sfw + SFW * 4;
         const uint64_t da = smem_desc(base, 1024, kSwizzle128), db = smem_desc(base + L.x, 1024, kSwizzle128);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // nvfp4: a word of scales for 64 codes; mxfp4: its lower, then its upper half
           const int w = NV ? j : j >> 1;
           const uint32_t id = NV ? 0u : (j & 1) * 2u;
-          mma_block_scaled<NV>(tmem, da + j * 2, db + j * 2, idesc | (id << 4) | (id << 29), sfw + w * 4, sfx + w * xb * 4,
+          mma_block_scaled<NV>(tmem, da + j * 2, db + j * 2, idesc | (id << 4) | (id << 29), sfw + w * 4, sfx + w * XB * 4,
                                it > 0 || j > 0);
         }
         mma_commit(empty + s * 8);
@@ -372,21 +377,17 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
       mma_commit(done);
     }
   } else {
-    if (a.BN > 128) {
-      if (a.aligned) stage_scales<SFW, true, 2>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-      else stage_scales<SFW, false, 2>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-    } else {
-      if (a.aligned) stage_scales<SFW, true, 1>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-      else stage_scales<SFW, false, 1>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-    }
+    if (a.aligned) stage_scales<SFW, true, XB>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
+    else stage_scales<SFW, false, XB>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
     mbar_wait(done, 0, kStatusTimeoutDrain);
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const int q = warp & 3;
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int n = n0 + q * 32 + lane;
+    const int first = 16 * ((threadIdx.x - 64) >> 7);  // the groups take 16 rows in turn
     if (a.split > 1) {
-      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;  // [BN][128], over the stages
-      for (int c = 0; c < a.BN; c += 16, part += 16 * kTileN) {
+      float* part = reinterpret_cast<float*>(smem) + first * kTileN + q * 32 + lane;  // [BN][128], over the stages
+      for (int c = first; c < a.BN; c += 16 * kScaleGroups, part += 16 * kScaleGroups * kTileN) {
         uint32_t v[16];
         tmem_load16(v, acc + c);
         tmem_wait_load();
@@ -394,10 +395,11 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
         for (int i = 0; i < 16; ++i) part[i * kTileN] = __uint_as_float(v[i]);
       }
     } else if (a.out_f32) {
-      store_tile<float>(acc, static_cast<float*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N, min(a.BN, a.M - m0), n < a.N);
+      store_tile<float>(acc, static_cast<float*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N, first,
+                        min(a.BN, a.M - m0), n < a.N);
     } else {
       store_tile<__nv_bfloat16>(acc, static_cast<__nv_bfloat16*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N,
-                                min(a.BN, a.M - m0), n < a.N);
+                                first, min(a.BN, a.M - m0), n < a.N);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
@@ -461,7 +463,7 @@ void plan(MxMatmulArgs& a, int sms) {
     const int64_t tiles = static_cast<int64_t>((a.N + kTileN - 1) / kTileN) * ((a.M + bn - 1) / bn);
     for (int c : {1, 2, 4, 8}) {
       if (c > 1 && (c > a.ktiles / 2 || tiles * c > 2 * sms || bn > 128)) break;
-      const int per_sm = bn <= 64 ? 2 : 1;
+      const int per_sm = bn <= 32 ? 2 : 1;
       const double waves = static_cast<double>((tiles * c + sms * per_sm - 1) / (sms * per_sm));
       const double stage = per_sm * std::max(bn * 1.5, 790.0 / ((a.M + bn - 1) / bn));
       const double cost = waves * ((a.ktiles + c - 1) / c * stage + 2500.0 + bn * 8.0 + (c > 1 ? 1500.0 : 0.0));
@@ -486,18 +488,19 @@ cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cud
   a.tiles_m = (a.M + a.BN - 1) / a.BN;
   const int64_t ctas = static_cast<int64_t>((a.N + kTileN - 1) / kTileN) * a.tiles_m * a.split;
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
-  // Two CTAs an SM up to 64 rows, else one; stages as shared memory and the
+  // Two CTAs an SM up to 32 rows, else one; stages as shared memory and the
   // tensor memory's columns (accumulators, then each stage's scales) allow.
-  const int budget = a.BN <= 64 ? 113 * 1024 : 227 * 1024, cols = a.BN <= 64 ? 256 : 512;
+  const int budget = a.BN <= 32 ? 113 * 1024 : 227 * 1024, cols = a.BN <= 32 ? 256 : 512;
   const int sf_cols = SFW * 4 * (1 + (a.BN + 127) / 128);
-  a.stages = 1;
-  while (a.stages < 8 && GemmSmem(a.BN, a.stages + 1, SFW).total + 1024 <= budget && a.BN + (a.stages + 1) * sf_cols <= cols)
-    ++a.stages;
+  // (an even number: a stage's scales always come from one group)
+  a.stages = 2;
+  while (a.stages < 8 && GemmSmem(a.BN, a.stages + 2, SFW).total + 1024 <= budget && a.BN + (a.stages + 2) * sf_cols <= cols)
+    a.stages += 2;
   a.tmem_cols = cols;
   const int smem = GemmSmem(a.BN, a.stages, SFW).total + 1024;
   CUtensorMap wmap, xmap;
   if (!codes_map(&wmap, Wq, a.N, a.K, kTileN) || !codes_map(&xmap, Xq, a.M, a.K, a.BN)) return cudaErrorNotSupported;
-  auto kern = mx_matmul_kernel<NV>;
+  auto kern = a.BN > 128 ? mx_matmul_kernel<NV, 2> : mx_matmul_kernel<NV, 1>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
