@@ -1,5 +1,7 @@
 // Verification of drafted tokens (qmm_verify_draft, include/qmm.h).
+#include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -20,6 +22,8 @@ struct VerifyArgs {
   int B, k, V;
   int32_t* tokens;
   int32_t* accepted;
+  int cluster;  // CTAs of a sequence
+  int round;    // rows between two exchanges
 };
 
 // (value, index) with the larger value, the lower index of equals.
@@ -29,88 +33,326 @@ __device__ __forceinline__ void best_of(float& v, int& i, float v2, int i2) {
     i = i2;
   }
 }
-
-constexpr int kThreads = 512;
-
-// The CTA's best (value, index); every thread gets it.
-__device__ __forceinline__ void block_best(float& v, int& i, float* sv, int* si) {
+__device__ __forceinline__ void warp_best(float& v, int& i) {
 #pragma unroll
-  for (int s = 16; s > 0; s /= 2)
-    best_of(v, i, __shfl_xor_sync(0xffffffffu, v, s), __shfl_xor_sync(0xffffffffu, i, s));
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) {
-    sv[threadIdx.x / 32] = v;
-    si[threadIdx.x / 32] = i;
-  }
-  __syncthreads();
-  v = sv[0];
-  i = si[0];
-  for (int w = 1; w < kThreads / 32; ++w) best_of(v, i, sv[w], si[w]);
+  for (int s = 16; s > 0; s /= 2) best_of(v, i, __shfl_xor_sync(0xffffffffu, v, s), __shfl_xor_sync(0xffffffffu, i, s));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// (m, s) and (m2, s2): maxima and sums of 2^((x - max) c); joined.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
+  const float t = fmaxf(m, m2), b = base_of(t);
+  s = s * ex2((m - b) * c) + s2 * ex2((m2 - b) * c);
+  m = t;
 }
 
-// One CTA per sequence: row by row the largest logit (with its lowest index)
-// and the sum of exponentials, until a draft is refused.
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxRows = 32, kMaxCluster = 16;
+
+struct Partial {
+  float m;  // largest logit of this CTA's part of a row
+  float s;  // sum of exponentials relative to it (greedy: unused)
+  int at;   // its lowest index (greedy)
+};
+
+__device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
+  return __float_as_int(ld_dsmem_f32(reinterpret_cast<const float*>(p), rank));
+}
+
+// One cluster per sequence; a CTA of it takes a share of the vocabulary of
+// every row.  Rounds of a.round rows: each CTA's maximum and sum of
+// exponentials of its share (one pass, running maximum per thread), exchanged
+// through distributed shared memory; every CTA then finds the same first
+// refusal.  Rows past the round of the first refusal are never read.  Then one
+// pass over the refused (or last) row, its draft probabilities and the noise
+// for the next token.  Sums are added in a fixed order: results do not depend
+// on timing.
+//
+// What bounds it: the bytes of the rows read, where there are many sequences
+// (rounds of one row, several clusters an SM so that one's exchange overlaps
+// another's reads); the latency of its two exchanges, where there are few (all
+// rows in one round).
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a) {
-  __shared__ float sv[kThreads / 32];
-  __shared__ int si[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
+  using T = typename std::conditional<F32, float, uint16_t>::type;
+  constexpr int VEC = F32 ? 4 : 8;  // logits of a 16-byte load
+  __shared__ Partial warp_part[kMaxRows][kWarps];
+  __shared__ Partial part[2][kMaxRows];  // this CTA's, by the round's parity
+  __shared__ float s_xd[kMaxRows], s_qd[kMaxRows], s_u[kMaxRows];
+  __shared__ int s_d[kMaxRows];
+  __shared__ float s_top[kMaxRows], s_sum[kMaxRows];
+  __shared__ int s_at[kMaxRows], s_yes[kMaxRows];
+  __shared__ float best_v[2][kWarps], cta_v[2];
+  __shared__ int best_i[2][kWarps], cta_i[2];
   griddep_wait();
-  const int b = blockIdx.x;
-  const float T = a.temperature[b];
-  const bool greedy = !(T > 0.f);
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int b = blockIdx.x / C;
+  const T* const rows = static_cast<const T*>(a.logits) + b * a.batch_stride;
+  auto value = [](T x) { return fmaxf(F32 ? static_cast<float>(x) : bf16_lo(x), -INFINITY); };  // NaN: -inf
+  const float temp = a.temperature[b];
+  const bool greedy = !(temp > 0.f);
+  const float c = greedy ? 1.f : fmaxf(1.4426950408889634f / temp, 1e-30f);
   int drafts = a.draft_lens != nullptr ? a.draft_lens[b] : a.k;
   drafts = drafts < 0 ? 0 : drafts > a.k ? a.k : drafts;
-  int n = 0, token = 0;
-  for (;; ++n) {
-    const int64_t off = b * a.batch_stride + n * a.row_stride;
-    auto logit = [&](int v) {
-      const float x = F32 ? static_cast<const float*>(a.logits)[off + v]
-                          : bf16_lo(static_cast<const uint16_t*>(a.logits)[off + v]);
-      return x == x ? x : -INFINITY;
-    };
-    float top = -INFINITY;
-    int at = 0x7fffffff;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) best_of(top, at, logit(v), v);
-    block_best(top, at, sv, si);
-    token = at;
-    const int d = n < drafts ? a.draft[b * a.k + n] : -1;
-    const bool usable = fabsf(top) <= 3.4028235e38f;
-    if (greedy || !usable) {
-      if (n < drafts && usable && d == at) continue;
-      break;
-    }
-    float sum = 0.f;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) sum += expf((logit(v) - top) / T);
-#pragma unroll
-    for (int s = 16; s > 0; s /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sv[threadIdx.x / 32] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < kThreads / 32; ++w) sum += sv[w];
-    const float* q = a.q != nullptr && n < drafts ? a.q + (static_cast<int64_t>(b) * a.k + n) * a.V : nullptr;
+  if (tid < drafts) {
+    const int d = a.draft[static_cast<int64_t>(b) * a.k + tid];
     const bool valid = d >= 0 && d < a.V;
-    if (n < drafts && valid) {
-      const float qd = a.q != nullptr ? q[d] : 1.f;
-      if (a.u[b * a.k + n] * qd < expf((logit(d) - top) / T) / sum) continue;
-    }
-    float best = -1.f, plain = -1.f;
-    int besti = 0x7fffffff, plaini = 0x7fffffff;
-    const float* e = a.noise + static_cast<int64_t>(b) * a.V;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) {
-      const float p = expf((logit(v) - top) / T) / sum;
-      const float w = n >= drafts ? p : q != nullptr ? p - q[v] : v == d ? 0.f : p;
-      if (w > 0.f) best_of(best, besti, w / e[v], v);
-      best_of(plain, plaini, p > 0.f ? p / e[v] : 0.f, v);
-    }
-    block_best(best, besti, sv, si);
-    block_best(plain, plaini, sv, si);
-    token = best > 0.f ? besti : plaini;
-    break;
+    s_d[tid] = valid ? d : -1;
+    s_u[tid] = a.u[static_cast<int64_t>(b) * a.k + tid];
+    s_xd[tid] = valid ? value(rows[tid * a.row_stride + d]) : 0.f;
+    s_qd[tid] = valid && a.q != nullptr ? a.q[(static_cast<int64_t>(b) * a.k + tid) * a.V + d] : 1.f;
   }
-  for (int j = threadIdx.x; j <= a.k; j += kThreads)
-    a.tokens[b * (a.k + 1) + j] = j < n ? a.draft[b * a.k + j] : j == n ? token : -1;
-  if (threadIdx.x == 0) a.accepted[b] = n;
+
+  int n = 0;  // accepted drafts
+  for (int r0 = 0, parity = 0;; r0 += a.round, parity ^= 1) {
+    const int r1 = min(r0 + a.round, drafts + 1);
+    for (int r = r0; r < r1; ++r) {
+      const T* const x = rows + r * a.row_stride;
+      // elements before the first 16-byte boundary and after the last go to CTA 0
+      const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
+      const int vecs = (a.V - head) / VEC, tail = head + vecs * VEC;
+      const int v0 = static_cast<int>(static_cast<int64_t>(vecs) * rank / C), v1 = static_cast<int>(static_cast<int64_t>(vecs) * (rank + 1) / C);
+      const uint4* const xv = reinterpret_cast<const uint4*>(x + head);
+      float m = -INFINITY, s = 0.f;
+      int at = INT_MAX;
+      auto unpack = [&](const uint4& w, float (&f)[VEC]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (F32) {
+            f[i] = fmaxf(__uint_as_float(u[i]), -INFINITY);
+          } else {
+            f[2 * i] = fmaxf(bf16_lo(u[i]), -INFINITY);
+            f[2 * i + 1] = fmaxf(bf16_hi(u[i]), -INFINITY);
+          }
+        }
+      };
+      // U vectors at a time: their maximum first, so that a thread's sum is rescaled at most once for all
+      auto take = [&](const uint4* w, int count, int first) {
+        float f[4][VEC];
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < count) unpack(w[j], f[j]);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            if (j >= count) f[j][i] = -INFINITY;
+            if (greedy) best_of(m, at, f[j][i], head + (first + j * kThreads) * VEC + i);
+            else top = fmaxf(top, f[j][i]);
+          }
+        }
+        if (greedy) return;
+        const float base = base_of(top);
+        s *= ex2((m - base) * c);
+        m = top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s += ex2((f[j][i] - base) * c);
+      };
+      int v = v0 + tid;
+      for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(xv + v + j * kThreads);
+        take(w, 4, v);
+      }
+      if (v < v1) {
+        uint4 w[4];
+        int count = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (v + j * kThreads < v1) {
+            w[j] = __ldg(xv + v + j * kThreads);
+            count = j + 1;
+          }
+        take(w, count, v);
+      }
+      if (rank == 0) {
+        auto one = [&](int i) {
+          const float f = value(x[i]);
+          if (greedy) {
+            best_of(m, at, f, i);
+          } else {
+            const float t = fmaxf(m, f), base = base_of(t);
+            s = s * ex2((m - base) * c) + ex2((f - base) * c);
+            m = t;
+          }
+        };
+        if (tid < head) one(tid);
+        if (tail + tid < a.V && tid < VEC) one(tail + tid);
+      }
+      if (greedy) {
+        warp_best(m, at);
+      } else {
+        const float t = [&] {
+          float u = m;
+#pragma unroll
+          for (int d = 16; d > 0; d /= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
+          return u;
+        }();
+        s *= ex2((m - base_of(t)) * c);
+        m = t;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+      }
+      if (lane == 0) warp_part[r - r0][warp] = Partial{m, s, at};
+    }
+    __syncthreads();
+    // a warp joins a row's warps, in order
+    for (int r = r0 + warp; r < r1; r += kWarps) {
+      if (lane == 0) {
+        Partial p = warp_part[r - r0][0];
+#pragma unroll 4
+        for (int w = 1; w < kWarps; ++w) {
+          const Partial o = warp_part[r - r0][w];
+          if (greedy) best_of(p.m, p.at, o.m, o.at);
+          else join(p.m, p.s, o.m, o.s, c);
+        }
+        part[parity][r - r0] = p;
+      }
+    }
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    // and a thread a row's CTAs: every CTA finds the same
+    if (tid < r1 - r0) {
+      const int r = r0 + tid;
+      Partial p = part[parity][tid];
+      if (C > 1) {
+        const Partial* const at = &part[parity][tid];
+        Partial o[kMaxCluster];
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (q < C) o[q] = Partial{ld_dsmem_f32(&at->m, q), ld_dsmem_f32(&at->s, q), ld_dsmem_i32(&at->at, q)};
+        p = o[0];
+#pragma unroll
+        for (int q = 1; q < kMaxCluster; ++q)
+          if (q < C) {
+            if (greedy) best_of(p.m, p.at, o[q].m, o[q].at);
+            else join(p.m, p.s, o[q].m, o[q].s, c);
+          }
+      }
+      const bool usable = fabsf(p.m) <= 3.4028235e38f;
+      s_top[r] = p.m;
+      s_sum[r] = p.s;
+      s_at[r] = p.at;
+      bool yes = false;
+      if (r < drafts && usable) {
+        if (greedy) yes = s_d[r] == p.at;
+        else if (s_d[r] >= 0) yes = s_u[r] * s_qd[r] < ex2((s_xd[r] - p.m) * c) / p.s;
+      }
+      s_yes[r] = yes;
+    }
+    __syncthreads();
+    while (n < r1 && s_yes[n]) ++n;
+    if (n < r1) break;  // the last row (n == drafts) never says yes
+  }
+
+  // The next token, from row n.
+  const bool usable = fabsf(s_top[n]) <= 3.4028235e38f;
+  int token = s_at[n];
+  if (!greedy) {
+    const T* const x = rows + n * a.row_stride;
+    const bool refused = n < drafts;
+    const float top = base_of(s_top[n]), inv = 1.f / s_sum[n];
+    const float* const q = refused && a.q != nullptr && usable ? a.q + (static_cast<int64_t>(b) * a.k + n) * a.V : nullptr;
+    const int d = refused && a.q == nullptr ? s_d[n] : -1;
+    const float* const e = a.noise + static_cast<int64_t>(b) * a.V;
+    // largest w / noise, and largest p / noise, which stands in where w is 0 everywhere; of a row without a
+    // softmax the largest logit
+    float v[2] = {-INFINITY, -INFINITY};
+    int at[2] = {INT_MAX, INT_MAX};
+    const int i0 = static_cast<int>(static_cast<int64_t>(a.V) * rank / C), i1 = static_cast<int>(static_cast<int64_t>(a.V) * (rank + 1) / C);
+    auto look = [&](int i, float f, float qi, float ei) {
+      if (!usable) {
+        best_of(v[1], at[1], f, i);
+        return;
+      }
+      const float p = ex2((f - top) * c) * inv;
+      const float w = q != nullptr ? p - qi : i == d ? 0.f : p;
+      if (w > 0.f) best_of(v[0], at[0], __fdiv_rn(w, ei), i);
+      if (q != nullptr || d >= 0) best_of(v[1], at[1], p > 0.f ? __fdiv_rn(p, ei) : 0.f, i);
+    };
+    int i = i0 + tid;
+    for (; i + 7 * kThreads < i1; i += 8 * kThreads) {
+      float f[8], qi[8], ei[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[j] = value(x[i + j * kThreads]);
+        qi[j] = q != nullptr ? __ldg(q + i + j * kThreads) : 0.f;
+        ei[j] = __ldg(e + i + j * kThreads);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) look(i + j * kThreads, f[j], qi[j], ei[j]);
+    }
+    for (; i < i1; i += kThreads) look(i, value(x[i]), q != nullptr ? __ldg(q + i) : 0.f, __ldg(e + i));
+    if (usable && q == nullptr && d < 0) v[1] = v[0], at[1] = at[0];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      warp_best(v[h], at[h]);
+      if (lane == 0) best_v[h][warp] = v[h], best_i[h][warp] = at[h];
+    }
+    __syncthreads();
+    if (warp < 2) {
+      float bv = lane < kWarps ? best_v[warp][lane] : -INFINITY;
+      int bi = lane < kWarps ? best_i[warp][lane] : INT_MAX;
+      warp_best(bv, bi);
+      if (lane == 0) cta_v[warp] = bv, cta_i[warp] = bi;
+    }
+    if (C > 1) cluster_sync_all();
+    else __syncthreads();
+    if (rank == 0 && warp == 0) {
+      float bv[2];
+      int bi[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bv[h] = lane < C ? (C > 1 ? ld_dsmem_f32(&cta_v[h], lane) : cta_v[h]) : -INFINITY;
+        bi[h] = lane < C ? (C > 1 ? ld_dsmem_i32(&cta_i[h], lane) : cta_i[h]) : INT_MAX;
+        warp_best(bv[h], bi[h]);
+      }
+      token = usable && bv[0] > 0.f ? bi[0] : bi[1];
+    }
+  }
+  if (rank == 0 && warp == 0) {
+    for (int j = lane; j <= a.k; j += 32)
+      a.tokens[static_cast<int64_t>(b) * (a.k + 1) + j] = j < n ? a.draft[static_cast<int64_t>(b) * a.k + j] : j == n ? token : -1;
+    if (lane == 0) a.accepted[b] = n;
+  }
+  if (C > 1) cluster_sync_all();  // nobody leaves while its shared memory is read
+}
+
+template <bool F32>
+cudaError_t launch_verify(VerifyArgs a, cudaStream_t stream) {
+  if (injected_launch_failure()) return cudaErrorLaunchFailure;
+  // CTAs of a cluster: about two an SM over all sequences, and no more than one
+  // for every 2048 logits of a row.
+  const int sms = device_sm_count();
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && static_cast<int64_t>(a.B) * a.cluster * 2 <= 2 * sms && a.V > a.cluster * 2048) a.cluster *= 2;
+  // All rows in one round while reading them takes less than the exchanges saved (about 16 MB: 2.5 us).
+  a.round = static_cast<int64_t>(a.B) * (a.k + 1) * a.V * (F32 ? 4 : 2) <= (16 << 20) ? a.k + 1 : 1;
+  auto kern = verify_kernel<F32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
@@ -122,7 +364,7 @@ extern "C" qmm_status qmm_verify_draft(const void* logits, int logits_dtype, int
                                        int k, int V, int32_t* tokens, int32_t* accepted, void* stream) {
   using namespace qmm;
   if (logits_dtype != QMM_OUT_BF16 && logits_dtype != QMM_OUT_F32) return QMM_ERR_UNSUPPORTED;
-  if (B < 0 || k < 0 || k > 31 || V < 1 || row_stride < V || batch_stride < 0) return QMM_ERR_SHAPE;
+  if (B < 0 || B > INT_MAX / 16 || k < 0 || k > 31 || V < 1 || row_stride < V || batch_stride < 0) return QMM_ERR_SHAPE;
   if (B == 0) return QMM_OK;
   if (logits == nullptr || noise == nullptr || temperature == nullptr || tokens == nullptr || accepted == nullptr)
     return QMM_ERR_NULL;
@@ -135,9 +377,8 @@ extern "C" qmm_status qmm_verify_draft(const void* logits, int logits_dtype, int
         reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(accepted)) & 3))
     return QMM_ERR_ALIGN;
   const VerifyArgs a{logits, batch_stride, row_stride, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens,
-                     B, k, V, tokens, accepted};
+                     B, k, V, tokens, accepted, 1, 1};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_dtype == QMM_OUT_F32 ? launch_dependent(verify_kernel<true>, dim3(B), kThreads, 0, st, a)
-                                                    : launch_dependent(verify_kernel<false>, dim3(B), kThreads, 0, st, a);
+  const cudaError_t e = logits_dtype == QMM_OUT_F32 ? launch_verify<true>(a, st) : launch_verify<false>(a, st);
   return static_cast<qmm_status>(finish_call(e));
 }
