@@ -100,19 +100,26 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   const float c = greedy ? 1.f : fmaxf(1.4426950408889634f / temp, 1e-30f);
   int drafts = a.draft_lens != nullptr ? a.draft_lens[b] : a.k;
   drafts = drafts < 0 ? 0 : drafts > a.k ? a.k : drafts;
+  // draft tid's logit, draft probability and random number: used after the first round
+  int my_d = -1;
+  float my_u = 0.f, my_x = 0.f, my_q = 1.f;
   if (tid < drafts) {
-    const int d = a.draft[static_cast<int64_t>(b) * a.k + tid];
-    const bool valid = d >= 0 && d < a.V;
-    s_d[tid] = valid ? d : -1;
-    s_u[tid] = a.u[static_cast<int64_t>(b) * a.k + tid];
-    s_xd[tid] = valid ? value(rows[tid * a.row_stride + d]) : 0.f;
-    s_qd[tid] = valid && a.q != nullptr ? a.q[(static_cast<int64_t>(b) * a.k + tid) * a.V + d] : 1.f;
+    const int64_t at = static_cast<int64_t>(b) * a.k + tid;
+    my_d = a.draft[at];
+    my_u = a.u[at];
+    if (my_d < 0 || my_d >= a.V) my_d = -1;
+    if (my_d >= 0) my_x = value(rows[tid * a.row_stride + my_d]);
+    if (my_d >= 0 && a.q != nullptr) my_q = a.q[at * a.V + my_d];
   }
 
   int n = 0;  // accepted drafts
   for (int r0 = 0, parity = 0;; r0 += a.round, parity ^= 1) {
     const int r1 = min(r0 + a.round, drafts + 1);
-    for (int r = r0; r < r1; ++r) {
+    // the warps in groups, a row each, when there are several
+    int per = kWarps;  // warps of a row
+    while (per > 1 && per * (r1 - r0) > kWarps) per /= 2;
+    const int threads = 32 * per, t_row = tid & (threads - 1);
+    for (int r = r0 + warp / per; r < r1; r += kWarps / per) {
       const T* const x = rows + r * a.row_stride;
       // elements before the first 16-byte boundary and after the last go to CTA 0
       const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
@@ -143,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
             if (j >= count) f[j][i] = -INFINITY;
-            if (greedy) best_of(m, at, f[j][i], head + (first + j * kThreads) * VEC + i);
+            if (greedy) best_of(m, at, f[j][i], head + (first + j * threads) * VEC + i);
             else top = fmaxf(top, f[j][i]);
           }
         }
@@ -156,11 +163,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) s += ex2((f[j][i] - base) * c);
       };
-      int v = v0 + tid;
-      for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
+      int v = v0 + t_row;
+      for (; v + 3 * threads < v1; v += 4 * threads) {
         uint4 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __ldg(xv + v + j * kThreads);
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(xv + v + j * threads);
         take(w, 4, v);
       }
       if (v < v1) {
@@ -168,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         int count = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (v + j * kThreads < v1) {
-            w[j] = __ldg(xv + v + j * kThreads);
+          if (v + j * threads < v1) {
+            w[j] = __ldg(xv + v + j * threads);
             count = j + 1;
           }
         take(w, count, v);
@@ -185,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             m = t;
           }
         };
-        if (tid < head) one(tid);
-        if (tail + tid < a.V && tid < VEC) one(tail + tid);
+        if (t_row < head) one(t_row);
+        if (tail + t_row < a.V && t_row < VEC) one(tail + t_row);
       }
       if (greedy) {
         warp_best(m, at);
@@ -202,21 +209,20 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
       }
-      if (lane == 0) warp_part[r - r0][warp] = Partial{m, s, at};
+      if (lane == 0) warp_part[r - r0][warp & (per - 1)] = Partial{m, s, at};
     }
+    if (r0 == 0 && tid < drafts) s_d[tid] = my_d, s_u[tid] = my_u, s_xd[tid] = my_x, s_qd[tid] = my_q;
     __syncthreads();
-    // a warp joins a row's warps, in order
-    for (int r = r0 + warp; r < r1; r += kWarps) {
-      if (lane == 0) {
-        Partial p = warp_part[r - r0][0];
+    // a thread joins a row's warps, in order
+    if (tid < r1 - r0) {
+      Partial p = warp_part[tid][0];
 #pragma unroll 4
-        for (int w = 1; w < kWarps; ++w) {
-          const Partial o = warp_part[r - r0][w];
-          if (greedy) best_of(p.m, p.at, o.m, o.at);
-          else join(p.m, p.s, o.m, o.s, c);
-        }
-        part[parity][r - r0] = p;
+      for (int w = 1; w < per; ++w) {
+        const Partial o = warp_part[tid][w];
+        if (greedy) best_of(p.m, p.at, o.m, o.at);
+        else join(p.m, p.s, o.m, o.s, c);
       }
+      part[parity][tid] = p;
     }
     if (C > 1) cluster_sync_all();
     else __syncthreads();
