@@ -8,6 +8,7 @@ stream.  If the library has not been built, the first call raises
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import numpy as np
@@ -321,45 +322,53 @@ def small_m(x, wq, scales, biases, bits: int, group_size: int, out=None, out_dty
 
 
 # ------------------------------------------------- the operators around the product
-def _launch_on(stream, device):
+# A call of these takes microseconds on the GPU, so the checks below are written
+# for their cost: integers for devices, one comparison per property.
+def _index(t, name: str) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return i
+
+
+def _same_device(index: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on CUDA device {index}")
+
+
+def _launch_on(stream, index: int):
     """(cudaStream_t as int, the stream to record new tensors on or None) of a
     call.  Outputs and workspaces are allocated on the current stream; a call
     that runs on another one has them recorded there, so that their memory is
     not handed out again before the call is done."""
     import torch
 
-    current = torch.cuda.current_stream(device)
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError(f"the current CUDA device must be the tensors' device {index}")
+    current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None:
-        return current.cuda_stream, None
+        return current, None
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == current.cuda_stream:
+    if handle == current:
         return handle, None
-    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=index)
 
 
-def _new(shape, dtype, device, record):
+def _new(like, shape, dtype, record):
     import torch
 
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if record is not None:
         # the caching allocator may have handed out memory that the current
         # stream still works on: the call's stream waits for it
-        record.wait_stream(torch.cuda.current_stream(device))
+        record.wait_stream(torch.cuda.current_stream(t.device))
         t.record_stream(record)
     return t
 
 
-def _cuda(device, **tensors):
-    """All given tensors live on ``device``."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if device.type != "cuda":
-        raise ValueError("CUDA tensors are needed")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _is(t, dtype, shape) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def quantize_mx(x, fmt: str, values=None, out=None, stream=None):
@@ -370,28 +379,33 @@ def quantize_mx(x, fmt: str, values=None, out=None, stream=None):
     import torch
 
     f, bits, g = MX_FORMATS[fmt]
-    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+    f32 = x.dtype is torch.float32
+    if x.dim() != 2 or not (f32 or x.dtype is torch.bfloat16):
         raise TypeError("x must be a bfloat16 or float32 matrix")
     R, K = x.shape
-    dev = x.device
-    _cuda(dev, values=values)
+    index = _index(x, "x")
     if K % 32 != 0:
         raise ValueError("K must be a multiple of 32")
-    if K > 1 and x.stride(1) != 1 or R > 1 and x.stride(0) < K:
+    ld, one = x.stride()
+    if R <= 1:
+        ld = K
+    if K > 1 and one != 1 or ld < K:
         raise ValueError("the elements of a row of x must be contiguous, and its rows apart")
-    if values is not None and (values.dtype != torch.bfloat16 or values.shape != x.shape or not values.is_contiguous()):
-        raise ValueError("values must be a contiguous bfloat16 tensor of x's shape")
-    handle, record = _launch_on(stream, dev)
+    if values is not None and (not _is(values, torch.bfloat16, x.shape) or values.get_device() != index):
+        raise ValueError("values must be a contiguous bfloat16 tensor of x's shape, on its device")
+    handle, record = _launch_on(stream, index)
     if out is None:
-        out = _new((R, K * bits // 32), torch.int32, dev, record), _new((R, K // g), torch.uint8, dev, record)
-    codes, scales = out
-    _cuda(dev, codes=codes, scales=scales)
-    if (tuple(codes.shape) != (R, K * bits // 32) or codes.dtype != torch.int32 or not codes.is_contiguous()
-            or tuple(scales.shape) != (R, K // g) or scales.dtype != torch.uint8 or not scales.is_contiguous()):
-        raise ValueError("out must be contiguous (int32 [R, K*bits/32], uint8 [R, K/g])")
-    _check(lib().qmm_quantize_mx(x.data_ptr(), OUT_F32 if x.dtype == torch.float32 else OUT_BF16, R, K,
-                                 x.stride(0) if R > 1 else K, f, codes.data_ptr(), scales.data_ptr(), _ptr(values),
-                                 handle), "qmm_quantize_mx")
+        codes = _new(x, (R, K * bits // 32), torch.int32, record)
+        scales = _new(x, (R, K // g), torch.uint8, record)
+    else:
+        codes, scales = out
+        _same_device(index, codes, scales)
+        if not _is(codes, torch.int32, (R, K * bits // 32)) or not _is(scales, torch.uint8, (R, K // g)):
+            raise ValueError("out must be contiguous (int32 [R, K*bits/32], uint8 [R, K/g])")
+    rc = lib().qmm_quantize_mx(x.data_ptr(), OUT_F32 if f32 else OUT_BF16, R, K, ld, f, codes.data_ptr(),
+                               scales.data_ptr(), None if values is None else values.data_ptr(), handle)
+    if rc != 0:
+        _check(rc, "qmm_quantize_mx")
     return codes, scales
 
 
@@ -403,74 +417,72 @@ def matmul_mx(xq, x_scales, wq, w_scales, fmt: str, out=None, out_dtype=None, st
     f, bits, g = MX_FORMATS[fmt]
     if bits != 4:
         raise ValueError("matmul_mx takes the 4-bit formats")
-    dev = xq.device
-    _cuda(dev, x_scales=x_scales, wq=wq, w_scales=w_scales, out=out)
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
-    if out_dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError("out dtype must be bfloat16 or float32")
     if xq.dim() != 2 or wq.dim() != 2:
         raise ValueError("codes must be matrices")
-    (M, words), N = xq.shape, wq.shape[0]
-    K = words * 8
-    for name, t, dtype, shape in (("xq", xq, torch.int32, (M, words)), ("wq", wq, torch.int32, (N, words)),
-                                  ("x_scales", x_scales, torch.uint8, (M, K // g)),
-                                  ("w_scales", w_scales, torch.uint8, (N, K // g))):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    handle, record = _launch_on(stream, dev)
+    index = _index(xq, "xq")
+    _same_device(index, x_scales, wq, w_scales, out)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    f32 = out_dtype is torch.float32
+    if not (f32 or out_dtype is torch.bfloat16):
+        raise TypeError("out dtype must be bfloat16 or float32")
+    M, words = xq.shape
+    N, K = wq.shape[0], words * 8
+    if not (_is(xq, torch.int32, (M, words)) and _is(wq, torch.int32, (N, words))):
+        raise ValueError("xq and wq must be contiguous int32 [M, K/8] and [N, K/8]")
+    if not (_is(x_scales, torch.uint8, (M, K // g)) and _is(w_scales, torch.uint8, (N, K // g))):
+        raise ValueError("x_scales and w_scales must be contiguous uint8 [M, K/g] and [N, K/g]")
+    handle, record = _launch_on(stream, index)
     if out is None:
-        out = _new((M, N), out_dtype, dev, record)
-    elif tuple(out.shape) != (M, N) or out.dtype != out_dtype or not out.is_contiguous():
+        out = _new(xq, (M, N), out_dtype, record)
+    elif not _is(out, out_dtype, (M, N)):
         raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
-    _check(lib().qmm_matmul_mx(xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), M, N, K, f,
-                               out.data_ptr(), OUT_F32 if out_dtype == torch.float32 else OUT_BF16, handle),
-           "qmm_matmul_mx")
+    rc = lib().qmm_matmul_mx(xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), M, N, K, f,
+                             out.data_ptr(), OUT_F32 if f32 else OUT_BF16, handle)
+    if rc != 0:
+        _check(rc, "qmm_matmul_mx")
     return out
 
 
-def _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B):
+def _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B):
     import torch
 
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    _same_device(index, k_cache, v_cache, block_table, lengths, q_lens)
+    dtype = k_cache.dtype
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must be [pages, page_size, heads, D] of one shape and dtype")
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+    if not (dtype is torch.bfloat16 or dtype is torch.float8_e4m3fn):
         raise TypeError("the cache must be bfloat16 or float8_e4m3fn")
-    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+    k_page, k_token, k_head, k_one = k_cache.stride()
+    v_page, v_token, v_head, v_one = v_cache.stride()
+    if k_one != 1 or v_one != 1:
         raise ValueError("the D elements of a head must be contiguous")
-    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+    rows, width = block_table.shape
+    ld, one = block_table.stride()
+    if rows != B or block_table.dtype is not torch.int32 or (width > 1 and one != 1):
         raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
-    if tuple(lengths.shape) != (B,) or lengths.dtype != torch.int32 or not lengths.is_contiguous():
-        raise ValueError("lengths must be int32 [B]")
+    if not _is(lengths, torch.int32, (B,)):
+        raise ValueError("lengths must be contiguous int32 [B]")
+    if q_lens is not None and not _is(q_lens, torch.int32, (B,)):
+        raise ValueError("q_lens must be contiguous int32 [B]")
     pages, page_size, heads, D = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    width = block_table.shape[1]
-    return PagedCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                            block_table.data_ptr(), lengths.data_ptr(), block_table.stride(0) if B > 1 else width, pages,
-                            width, page_size, heads, D, 0 if k_cache.dtype == torch.bfloat16 else 1, k_scale, v_scale)
+    return PagedCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), k_page, k_token, k_head, v_page, v_token, v_head,
+                            block_table.data_ptr(), lengths.data_ptr(), ld if B > 1 else width, pages, width, page_size,
+                            heads, D, 0 if dtype is torch.bfloat16 else 1, k_scale, v_scale)
 
 
-def _rows(t, B, M, name):
+def _rows(t, B, M, heads, D, name):
     """Distance of the [B, M] rows of ``t`` [B, M, heads, D] (one distance for
     all; a row's elements are contiguous)."""
     import torch
 
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
-    heads, D = t.shape[2], t.shape[3]
-    s = t.stride()
-    ld = s[1] if M > 1 else s[0] if B > 1 else heads * D
-    if ((D > 1 and s[3] != 1) or (heads > 1 and s[2] != D) or (B > 1 and M > 1 and s[0] != M * ld)):
+    s0, s1, s2, s3 = t.stride()
+    ld = s1 if M > 1 else s0 if B > 1 else heads * D
+    if (D > 1 and s3 != 1) or (heads > 1 and s2 != D) or (B > 1 and M > 1 and s0 != M * ld):
         raise ValueError(f"{name}: the heads of a row must be contiguous and its rows evenly apart")
     return ld
-
-
-def _q_lens(q_lens, B):
-    import torch
-
-    if q_lens is not None and (tuple(q_lens.shape) != (B,) or q_lens.dtype != torch.int32 or not q_lens.is_contiguous()):
-        raise ValueError("q_lens must be int32 [B]")
 
 
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None, k_scale: float = 1.0,
@@ -486,17 +498,24 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None,
     lengths[b] - q_lens[b] + i.  E4M3 elements hold x / scale."""
     if k_new.dim() != 4 or k_new.shape != v_new.shape:
         raise ValueError("k_new and v_new must be [B, M, heads, D] of one shape")
-    B, M = k_new.shape[:2]
-    dev = k_new.device
-    _cuda(dev, v_new=v_new, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths, q_lens=q_lens)
-    cache = _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B)
-    if tuple(k_new.shape[2:]) != tuple(k_cache.shape[2:]):
+    B, M, heads, D = k_new.shape
+    index = _index(k_new, "k_new")
+    _same_device(index, v_new)
+    cache = _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B)
+    if heads != cache.heads or D != cache.head_dim:
         raise ValueError("k_new and the cache must have the same heads and D")
-    _q_lens(q_lens, B)
-    k_ld, v_ld = _rows(k_new, B, M, "k_new"), _rows(v_new, B, M, "v_new")
-    handle, _ = _launch_on(stream, dev)
-    _check(lib().qmm_kv_append(ctypes.byref(cache), k_new.data_ptr(), k_ld, v_new.data_ptr(), v_ld, B, M, _ptr(q_lens),
-                               handle), "qmm_kv_append")
+    k_ld, v_ld = _rows(k_new, B, M, heads, D, "k_new"), _rows(v_new, B, M, heads, D, "v_new")
+    handle, _ = _launch_on(stream, index)
+    rc = lib().qmm_kv_append(ctypes.byref(cache), k_new.data_ptr(), k_ld, v_new.data_ptr(), v_ld, B, M,
+                             None if q_lens is None else q_lens.data_ptr(), handle)
+    if rc != 0:
+        _check(rc, "qmm_kv_append")
+
+
+@functools.lru_cache(maxsize=256)
+def paged_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
+    """Bytes of workspace that :func:`paged_attention` needs for these sizes."""
+    return int(lib().qmm_paged_attention_workspace(B, M, q_heads, heads, head_dim))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens=None, scale: float | None = None, window: int = 0,
@@ -511,34 +530,34 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens=None, scal
     defaults to 1/sqrt(D).  Returns ``out`` bf16 [B, M, q_heads, D], with
     ``return_lse`` also the fp32 [B, M, q_heads] log-sum-exp of the scaled
     scores (-inf, and 0 in ``out``, for rows that see nothing).  ``workspace``:
-    a uint8 tensor of ``lib().qmm_paged_attention_workspace`` bytes to reuse."""
+    a uint8 tensor of :func:`paged_attention_workspace` bytes to reuse."""
     import torch
 
     if q.dim() != 4:
         raise ValueError("q must be [B, M, q_heads, D]")
     B, M, Hq, D = q.shape
-    dev = q.device
-    _cuda(dev, k_cache=k_cache, v_cache=v_cache, block_table=block_table, lengths=lengths, q_lens=q_lens, out=out,
-          workspace=workspace)
-    cache = _paged_cache(k_cache, v_cache, block_table, lengths, k_scale, v_scale, B)
+    index = _index(q, "q")
+    _same_device(index, out, workspace)
+    cache = _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B)
     if D != cache.head_dim:
         raise ValueError("q and the cache must have the same D")
-    _q_lens(q_lens, B)
-    q_ld = _rows(q, B, M, "q")
-    handle, record = _launch_on(stream, dev)
+    q_ld = _rows(q, B, M, Hq, D, "q")
+    handle, record = _launch_on(stream, index)
     if out is None:
-        out = _new((B, M, Hq, D), torch.bfloat16, dev, record)
-    elif tuple(out.shape) != (B, M, Hq, D) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        out = _new(q, (B, M, Hq, D), torch.bfloat16, record)
+    elif not _is(out, torch.bfloat16, (B, M, Hq, D)):
         raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
-    lse = _new((B, M, Hq), torch.float32, dev, record) if return_lse else None
-    need = lib().qmm_paged_attention_workspace(B, M, Hq, cache.heads, D)
+    lse = _new(q, (B, M, Hq), torch.float32, record) if return_lse else None
     if workspace is None:
-        workspace = _new((need,), torch.uint8, dev, record)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        workspace = _new(q, (paged_attention_workspace(B, M, Hq, cache.heads, D),), torch.uint8, record)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check(lib().qmm_paged_attention(ctypes.byref(cache), q.data_ptr(), q_ld, B, M, Hq, _ptr(q_lens),
-                                     D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(lse),
-                                     workspace.data_ptr(), workspace.numel(), handle), "qmm_paged_attention")
+    rc = lib().qmm_paged_attention(ctypes.byref(cache), q.data_ptr(), q_ld, B, M, Hq,
+                                   None if q_lens is None else q_lens.data_ptr(), D ** -0.5 if scale is None else scale,
+                                   window, sinks, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel(), handle)
+    if rc != 0:
+        _check(rc, "qmm_paged_attention")
     return (out, lse) if return_lse else out
 
 
@@ -556,30 +575,33 @@ def verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature,
 
     if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
         raise ValueError("logits must be [B, k+1, V]")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
+    f32 = logits.dtype is torch.float32
+    if not (f32 or logits.dtype is torch.bfloat16):
         raise TypeError("logits must be bfloat16 or float32")
     B, rows, V = logits.shape
     k = rows - 1
-    dev = logits.device
-    if V > 1 and logits.stride(2) != 1:
+    index = _index(logits, "logits")
+    _same_device(index, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens)
+    s_batch, s_row, one = logits.stride()
+    if V > 1 and one != 1:
         raise ValueError("the elements of a row of logits must be contiguous")
-    for name, t, dtype, shape in (("draft_tokens", draft_tokens, torch.int32, (B, k)),
-                                  ("draft_probs", draft_probs, torch.float32, (B, k, V)),
-                                  ("uniform", uniform, torch.float32, (B, k)), ("noise", noise, torch.float32, (B, V)),
-                                  ("temperature", temperature, torch.float32, (B,)),
-                                  ("draft_lens", draft_lens, torch.int32, (B,))):
-        if t is None and name in ("draft_probs", "draft_lens"):
-            continue
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    _cuda(dev, draft_tokens=draft_tokens, draft_probs=draft_probs, uniform=uniform, noise=noise, temperature=temperature,
-          draft_lens=draft_lens)
-    handle, record = _launch_on(stream, dev)
-    tokens = _new((B, rows), torch.int32, dev, record)
-    accepted = _new((B,), torch.int32, dev, record)
-    _check(lib().qmm_verify_draft(logits.data_ptr(), OUT_F32 if logits.dtype == torch.float32 else OUT_BF16,
-                                  logits.stride(0) if B > 1 else rows * V, logits.stride(1) if rows > 1 else V,
-                                  draft_tokens.data_ptr(), _ptr(draft_probs), uniform.data_ptr(), noise.data_ptr(),
-                                  temperature.data_ptr(), _ptr(draft_lens), B, k, V, tokens.data_ptr(),
-                                  accepted.data_ptr(), handle), "qmm_verify_draft")
+    if not (_is(draft_tokens, torch.int32, (B, k)) and _is(uniform, torch.float32, (B, k))):
+        raise ValueError("draft_tokens and uniform must be contiguous int32 and float32 [B, k]")
+    if not (_is(noise, torch.float32, (B, V)) and _is(temperature, torch.float32, (B,))):
+        raise ValueError("noise and temperature must be contiguous float32 [B, V] and [B]")
+    if draft_probs is not None and not _is(draft_probs, torch.float32, (B, k, V)):
+        raise ValueError("draft_probs must be contiguous float32 [B, k, V]")
+    if draft_lens is not None and not _is(draft_lens, torch.int32, (B,)):
+        raise ValueError("draft_lens must be contiguous int32 [B]")
+    handle, record = _launch_on(stream, index)
+    tokens = _new(logits, (B, rows), torch.int32, record)
+    accepted = _new(logits, (B,), torch.int32, record)
+    rc = lib().qmm_verify_draft(logits.data_ptr(), OUT_F32 if f32 else OUT_BF16, s_batch if B > 1 else rows * V,
+                                s_row if rows > 1 else V, draft_tokens.data_ptr(),
+                                None if draft_probs is None else draft_probs.data_ptr(), uniform.data_ptr(),
+                                noise.data_ptr(), temperature.data_ptr(),
+                                None if draft_lens is None else draft_lens.data_ptr(), B, k, V, tokens.data_ptr(),
+                                accepted.data_ptr(), handle)
+    if rc != 0:
+        _check(rc, "qmm_verify_draft")
     return tokens, accepted

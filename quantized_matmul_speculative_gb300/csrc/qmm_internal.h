@@ -1,6 +1,7 @@
 // Internal interface between the C ABI (qmm_api.cu) and the kernel launchers.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -93,6 +94,15 @@ constexpr unsigned int kStatusBadPage = 32u;
 unsigned int read_paged_status(int clear);
 // Device status word of the microscaled product's unit (bounded waits).
 unsigned int read_mx_matmul_status(int clear);
+
+// Whether this is the first call with `done` on the current device: a kernel's
+// attributes are set once per device (again, harmlessly, if two threads meet).
+inline bool first_on_device(std::atomic<uint64_t>& done, uint64_t* bit) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+  *bit = uint64_t(1) << dev;
+  return (done.load(std::memory_order_acquire) & *bit) == 0;
+}
 
 // Launch with programmatic stream serialization: the kernel may start while its
 // predecessor finishes and calls griddepcontrol.wait before it touches memory

@@ -501,8 +501,13 @@ cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cud
   CUtensorMap wmap, xmap;
   if (!codes_map(&wmap, Wq, a.N, a.K, kTileN) || !codes_map(&xmap, Xq, a.M, a.K, a.BN)) return cudaErrorNotSupported;
   auto kern = a.BN > 128 ? mx_matmul_kernel<NV, 2> : mx_matmul_kernel<NV, 1>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready[2] = {};
+  uint64_t bit;
+  if (first_on_device(ready[a.BN > 128], &bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    ready[a.BN > 128].fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kGemmThreads);

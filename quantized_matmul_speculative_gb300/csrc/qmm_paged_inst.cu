@@ -53,13 +53,18 @@ template <int D, bool E8, int RG, int RPW>
 cudaError_t launch_rows(const AttentionArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using Cfg = AttnCfg<D, E8, RG, RPW>;
   auto kern = attention_kernel<D, E8, RG, RPW>;
-  // the register split needs what the kernel was built with: never launched with less
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};
+  uint64_t bit;
+  if (first_on_device(ready, &bit)) {
+    // the register split needs what the kernel was built with: never launched with less
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   return launch_dependent(kern, dim3(a.parts), kAttnThreads, Cfg::SMEM, stream, a, kmap, vmap);
 }
 

@@ -344,8 +344,13 @@ cudaError_t launch_verify(VerifyArgs a, cudaStream_t stream) {
   // All rows in one round while reading them takes less than the exchanges saved (about 16 MB: 2.5 us).
   a.round = static_cast<int64_t>(a.B) * (a.k + 1) * a.V * (F32 ? 4 : 2) <= (16 << 20) ? a.k + 1 : 1;
   auto kern = verify_kernel<F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};
+  uint64_t bit;
+  if (first_on_device(ready, &bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cluster);
   cfg.blockDim = dim3(kThreads);
