@@ -171,10 +171,13 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.lse = lse;
   a.RB = attention_row_block(M * a.G);
   a.RT = (M * a.G + a.RB - 1) / a.RB;
-  a.TN = attention_tile(cache->head_dim);
+  const int tile = attention_tile(cache->head_dim);
+  a.tn_log2 = tile == 64 ? 6 : tile == 32 ? 5 : 4;
+  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
   // one CTA an SM, at most one a tile
   const int64_t tiles = static_cast<int64_t>(B) * cache->heads * a.RT *
-                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + a.TN - 1) / a.TN);
+                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + tile - 1) / tile);
+  if (tiles > 0x7fffffff) return QMM_ERR_SHAPE;
   const int64_t fit = device_sm_count();
   a.parts = static_cast<int>(tiles < 1 ? 1 : tiles < fit ? tiles : fit);
   if (workspace_bytes < attention_workspace(a.parts, a.RB, cache->head_dim)) return QMM_ERR_SHAPE;

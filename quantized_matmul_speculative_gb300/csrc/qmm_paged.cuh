@@ -51,7 +51,8 @@ struct AttentionArgs {
   float* lse;
   int box;        // tokens of a TMA box (8 or 16); 0: copied row by row
   int RB, RT;     // rows of a row block, row blocks of a segment's M * G rows
-  int TN;         // attention_tile()
+  int tn_log2;    // of attention_tile()
+  uint32_t g_magic;          // ceil(2^32 / G); 0 for G = 1
   int parts;      // CTAs of the attention kernel
   float* part_o;  // [parts][2][RB][D]
   float2* part_ml;  // [parts][2][RB]
@@ -80,6 +81,11 @@ __device__ __forceinline__ int new_rows(const int32_t* q_lens, int b, int M) {
 }
 __device__ __forceinline__ void bad_page() { atomicOr(&g_qmm_status, kStatusBadPage); }
 
+// The new row that row gr of a segment belongs to: gr / G (exact for gr * G < 2^32).
+__device__ __forceinline__ int row_of(const AttentionArgs& a, int gr) {
+  return a.G == 1 ? gr : static_cast<int>(__umulhi(static_cast<uint32_t>(gr), a.g_magic));
+}
+
 // What the rows of row block rt of a sequence (L tokens, m new rows) see.
 struct Visible {
   int pos_lo, pos_hi;  // positions of its first and last valid row
@@ -90,10 +96,8 @@ struct Visible {
 };
 __device__ __forceinline__ Visible visible(const AttentionArgs& a, int L, int m, int rt) {
   Visible v;
-  const int rows = a.M * a.G;
-  const int i0 = rt * a.RB / a.G;
-  const int last = min((rt + 1) * a.RB, rows) - 1;
-  const int i1 = min(last / a.G, m - 1);
+  const int i0 = row_of(a, rt * a.RB);
+  const int i1 = min(row_of(a, min((rt + 1) * a.RB, a.M * a.G) - 1), m - 1);
   v.pos_lo = L - m + i0;
   v.pos_hi = L - m + i1;
   v.hi = v.pos_hi + 1;
@@ -102,9 +106,10 @@ __device__ __forceinline__ Visible visible(const AttentionArgs& a, int L, int m,
   v.win_tile = 0;
   v.tiles = 0;
   if (i0 > i1 || v.hi <= 0) return v;
-  const int all = (v.hi + a.TN - 1) / a.TN;
-  const int ns = a.window ? (min(a.sinks, v.hi) + a.TN - 1) / a.TN : 0;
-  const int w0 = v.first / a.TN;
+  const int up = (1 << a.tn_log2) - 1;
+  const int all = (v.hi + up) >> a.tn_log2;
+  const int ns = a.window ? (min(a.sinks, v.hi) + up) >> a.tn_log2 : 0;
+  const int w0 = v.first >> a.tn_log2;
   if (ns >= w0) {
     v.tiles = all;
   } else {
@@ -123,30 +128,32 @@ __device__ __forceinline__ int head_tiles(const AttentionArgs& a, int b) {
   return n;
 }
 
-// Total of `v` over the warp; inclusive prefix in `inc`.
-__device__ __forceinline__ long long warp_scan(long long v, long long& inc) {
-  inc = v;
+// Inclusive prefix of v over the warp.
+__device__ __forceinline__ int warp_scan(int v) {
 #pragma unroll
   for (int s = 1; s < 32; s *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, s);
-    if ((threadIdx.x & 31) >= s) inc += o;
+    const int o = __shfl_up_sync(0xffffffffu, v, s);
+    if ((threadIdx.x & 31) >= s) v += o;
   }
-  return __shfl_sync(0xffffffffu, inc, 31);
+  return v;
 }
 
-// CTAs that work: no more than there are tiles, so that every share holds one.
-__device__ __forceinline__ int working(const AttentionArgs& a, long long T) {
-  return T < a.parts ? static_cast<int>(T) : a.parts;
-}
-// First tile of CTA c's share of T tiles over P working CTAs.
-__device__ __forceinline__ long long share_begin(long long T, int P, int c) { return T * c / P; }
-// The CTA whose share holds tile t.
-__device__ __forceinline__ int share_of(long long T, int P, long long t) {
-  int c = static_cast<int>((t * P) / T);
-  while (c + 1 < P && share_begin(T, P, c + 1) <= t) ++c;
-  while (c > 0 && share_begin(T, P, c) > t) --c;
-  return c;
-}
+// How the list of T tiles is shared: CTAs that work (no more than there are
+// tiles, so that every share holds one), tiles of each, and how many of the
+// first ones hold one more.
+struct Shares {
+  int parts, each, more;
+  __device__ __forceinline__ Shares(const AttentionArgs& a, int T) {
+    parts = min(T, a.parts);
+    each = parts > 0 ? T / parts : 0;
+    more = T - each * parts;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int holder(int t) const {  // the CTA whose share holds tile t
+    const int long_ones = more * (each + 1);
+    return t < long_ones ? t / (each + 1) : more + (t - long_ones) / each;
+  }
+};
 
 // A CTA's share of the list, segment by segment.
 struct Cursor {
@@ -161,41 +168,44 @@ struct Cursor {
     L = seq_length(a.c, b);
     m = new_rows(a.q_lens, b, a.M);
   }
+  // Tiles of sequence s over all heads.
+  static __device__ __forceinline__ int seq_tiles(const AttentionArgs& a, int s) {
+    return s < a.B ? head_tiles(a, s) * a.c.heads : 0;
+  }
   // The share of this CTA (every lane of the warp calls); false: none.
-  // `parts`: CTAs that share the list; T: its tiles; t0: the share's first.
-  __device__ __forceinline__ bool begin(const AttentionArgs& a, int& parts, long long& T, long long& t0) {
+  __device__ __forceinline__ bool begin(const AttentionArgs& a, int& T, int& t0) {
     const int lane = threadIdx.x & 31;
     T = 0;
-    long long n = 0;  // tiles of sequence (last base) + lane
+    int n = 0;  // tiles of sequence (last base) + lane
+#pragma unroll 1
     for (int base = 0; base < a.B; base += 32) {
-      n = base + lane < a.B ? static_cast<long long>(head_tiles(a, base + lane)) * a.c.heads : 0;
-      long long inc;
-      T += warp_scan(n, inc);
+      n = seq_tiles(a, base + lane);
+      T += __reduce_add_sync(0xffffffffu, n);
     }
-    parts = working(a, T);
-    if (static_cast<int>(blockIdx.x) >= parts) return false;
-    t0 = share_begin(T, parts, blockIdx.x);
-    left = static_cast<int>(share_begin(T, parts, blockIdx.x + 1) - t0);
+    const Shares sh(a, T);
+    if (static_cast<int>(blockIdx.x) >= sh.parts) return false;
+    t0 = sh.begin(blockIdx.x);
+    left = sh.begin(blockIdx.x + 1) - t0;
     it = 0;
-    long long before = 0;
+    int before = 0;
     b = 0;
+#pragma unroll 1
     for (int base = 0; base < a.B; base += 32) {
-      if (a.B > 32) n = base + lane < a.B ? static_cast<long long>(head_tiles(a, base + lane)) * a.c.heads : 0;
-      long long inc;
-      const long long sum = warp_scan(n, inc);
-      if (before + sum > t0) {
-        const unsigned who = __ballot_sync(0xffffffffu, before + inc > t0);
+      if (a.B > 32) n = seq_tiles(a, base + lane);
+      const int inc = warp_scan(n);
+      const unsigned who = __ballot_sync(0xffffffffu, before + inc > t0);
+      if (who != 0) {
         const int l = __ffs(who) - 1;
         b = base + l;
         before += __shfl_sync(0xffffffffu, inc - n, l);
         break;
       }
-      before += sum;
+      before += __shfl_sync(0xffffffffu, inc, 31);
     }
     load(a);
     const int per_head = max(head_tiles(a, b), 1);
-    h = static_cast<int>((t0 - before) / per_head);
-    int r = static_cast<int>(t0 - before - static_cast<long long>(h) * per_head);
+    h = (t0 - before) / per_head;
+    int r = t0 - before - h * per_head;
     for (rt = 0; rt < a.RT - 1; ++rt) {
       v = visible(a, L, m, rt);
       if (r < v.tiles) break;
@@ -448,6 +458,8 @@ __device__ __forceinline__ void load_tiles(const AttentionArgs& a, uint32_t sbas
   const int per = a.box == 16 ? 1 : SL;                                      // copies of a box
   int k = pc.kb + part;  // the tile; past ke: in a later segment
   int page[RPL], slot[RPL], head = 0;
+#pragma unroll
+  for (int x = 0; x < RPL; ++x) page[x] = 0, slot[x] = -1;
   bool more = true;
   auto find = [&]() {
     while (k >= pc.ke) {
@@ -472,11 +484,11 @@ __device__ __forceinline__ void load_tiles(const AttentionArgs& a, uint32_t sbas
     }
     k += 2;
   };
-  find();
-  for (int it = part; more; it += 2) {
-    const int stage = it % ST;
-    const uint32_t full = full0 + stage * 8, base = tile0 + stage * 2 * Cfg::TILEB;
-    int pg[RPL], st[RPL];
+  int pg[RPL], st[RPL];
+#pragma unroll
+  for (int x = 0; x < RPL; ++x) pg[x] = 0, st[x] = -1;
+  // the page numbers of a tile are loaded while the one before is copied
+  for (int it = part - 2, last = 0; !last; it += 2) {
     const int hd = head;
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
@@ -487,7 +499,11 @@ __device__ __forceinline__ void load_tiles(const AttentionArgs& a, uint32_t sbas
       pg[x] = page[x];
       st[x] = slot[x];
     }
-    find();  // the page numbers of the tile after this one
+    find();
+    last = !more;
+    if (it < 0) continue;
+    const int stage = it % ST;
+    const uint32_t full = full0 + stage * 8, base = tile0 + stage * 2 * Cfg::TILEB;
     if (it >= ST && __any_sync(0xffffffffu, !mbar_wait(empty0 + stage * 8, ((it / ST) & 1) ^ 1, kStatusTimeoutEmpty))) break;
     if (a.box) {
       const uint32_t loaded = __ballot_sync(0xffffffffu, st[0] >= 0);
@@ -558,7 +574,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       if (visible(a, L, m, rt).tiles != 0) continue;
       const int r0 = rt * a.RB, rows = min(a.RB, a.M * a.G - r0), per_head = rows * (D / 8);
       for (int x = tid; x < per_head * a.c.heads; x += kAttnThreads) {
-        const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = gr / a.G;
+        const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = row_of(a, gr);
         const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
         *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
         if (col == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
@@ -566,9 +582,8 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
     }
   }
   Cursor cc;
-  int P;
-  long long T, t0;
-  if (!cc.begin(a, P, T, t0)) {
+  int T, t0;
+  if (!cc.begin(a, T, t0)) {
     if (tid == 0) a.part_seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
@@ -599,7 +614,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           mx[w][r] = -INFINITY;
           sum[w][r][0] = sum[w][r][1] = 0.f;
           const int gr = cc.rt * a.RB + (rg * RPW + w) * 16 + (lane >> 2) + 8 * r;
-          const int i = gr / a.G;
+          const int i = row_of(a, gr);
           const bool ok = gr < a.M * a.G && i < cc.m;
           pos[w][r] = ok ? cc.L - cc.m + i : INT_MIN / 2;
           row[r] = ok ? a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld +
@@ -748,21 +763,19 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       // what lies past the length), the product is taken with 0 in the place of
       // every value that is not, and those are added element by element to the
       // rows that see them.
-      auto row_bad = [&](int t) {  // some element of token t's value is not finite (this lane's chunks)
-        uint32_t x = 0;
-        for (int ch = lane; ch < CPR; ch += 32) {
-          const uint4 u = *reinterpret_cast<const uint4*>(smem + voff + tile_at<ROWB>(t, ch));
-          x |= not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w);
-        }
-        return x != 0;
+      constexpr int RPI = 32 / CPR;  // rows a warp looks at at once, a chunk a lane
+      auto row_bad = [&](int t) {    // some element of this lane's chunk of row t + lane / CPR is not finite
+        const uint4 u = *reinterpret_cast<const uint4*>(smem + voff + tile_at<ROWB>(t + lane / CPR, lane % CPR));
+        return (not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w)) != 0;
       };
       bool bad = false;
       if (!full) {
-        auto scan = [&](int from, int to) {
-          for (int j = max(from, j0); j < min(to, j0 + NT); ++j) bad |= row_bad(j - j0);
-        };
-        scan(max(cc.v.pos_lo + 1, 0), INT_MAX);
-        if (a.window != 0) scan(a.sinks, min(cc.v.pos_hi - a.window, cc.v.pos_lo) + 1);
+#pragma unroll 1
+        for (int t = 0; t < NT; t += RPI) {
+          const int j = j0 + t + lane / CPR;
+          const bool unseen = j > cc.v.pos_lo || (a.window != 0 && j >= a.sinks && j <= cc.v.pos_hi - a.window);
+          if (unseen) bad |= row_bad(t);
+        }
       }
       bad = __any_sync(0xffffffffu, bad);
       auto values = [&](auto clean) {
@@ -818,33 +831,40 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
         values(std::true_type{});
 #pragma unroll 1
         for (int t = 0; t < NT; ++t) {
-          if (!__any_sync(0xffffffffu, row_bad(t))) continue;
+          if (t % RPI == 0) bad = row_bad(t);
+          if (((__ballot_sync(0xffffffffu, bad) >> (t % RPI * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << (CPR & 31)) - 1u)) == 0)
+            continue;
           const int src = (lane & 28) | ((t & 7) >> 1), j = j0 + t;
+          float p[RPW][2];  // the token's weight for this thread's rows; 0 and not added where it is not seen
+          bool see[RPW][2];
 #pragma unroll
-          for (int w = 0; w < RPW; ++w) {
-            float p[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < NT / 8; ++i)
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                if (i == t >> 3) p[r] = (t & 1) ? s[w][i][2 * r + 1] : s[w][i][2 * r];
-            bool see[2];
+          for (int w = 0; w < RPW; ++w)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              p[r] = __shfl_sync(0xffffffffu, p[r], src);
-              see[r] = j <= pos[w][r] && (a.window == 0 || j > pos[w][r] - a.window || j < a.sinks);
+              float x = 0.f;
+#pragma unroll
+              for (int i = 0; i < NT / 8; ++i)
+                if (i == t >> 3) x = (t & 1) ? s[w][i][2 * r + 1] : s[w][i][2 * r];
+              p[w][r] = __shfl_sync(0xffffffffu, x, src);
+              see[w][r] = j <= pos[w][r] && (a.window == 0 || j > pos[w][r] - a.window || j < a.sinks);
             }
+          // four bytes at a time: two columns of one output tile, or (E4M3) two each of two
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+          for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
+            const int at = out_col<E8>(i, 0) * (E8 ? 1 : 2);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(smem + voff + tile_at<ROWB>(t, at / 16) + at % 16);
+            if (not_finite<E8>(u) == 0) continue;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int col = out_col<E8>(i, e) * (E8 ? 1 : 2);
-                const unsigned char* u = smem + voff + tile_at<ROWB>(t, col / 16) + col % 16;
-                const float v = E8 ? e4m3_to_float(*u) : bf16_lo(*reinterpret_cast<const uint16_t*>(u));
-                const bool odd = !(fabsf(v) <= 3.4028235e38f);
-                if (odd && see[0]) o[w][i][e] += p[0] * v;
-                if (odd && see[1]) o[w][i][2 + e] += p[1] * v;
+            for (int x = 0; x < (E8 ? 4 : 2); ++x) {
+              const float f = E8 ? e4m3_to_float((u >> (8 * x)) & 0xFFu) : x ? bf16_hi(u) : bf16_lo(u);
+              if (fabsf(f) <= 3.4028235e38f) continue;
+              const int ot = E8 ? i + (x & 1) : i, e = E8 ? x >> 1 : x;
+#pragma unroll
+              for (int w = 0; w < RPW; ++w) {
+                if (see[w][0]) o[w][ot][e] += p[w][0] * f;
+                if (see[w][1]) o[w][ot][2 + e] += p[w][1] * f;
               }
+            }
           }
         }
       }
@@ -857,9 +877,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       const bool whole = cc.kb == 0 && cc.ke == cc.v.tiles;
       const int slot = blockIdx.x * 2 + (cc.kb == 0 ? 1 : 0);
       if (cc.left == cc.ke - cc.kb && tid == 0) {  // the last segment of the share: how many CTAs hold it
-        const long long end = t0 + cc.it + cc.v.tiles - 1;  // its last tile, if it begins here
-        a.part_seg[blockIdx.x] = whole || cc.kb != 0 ? make_int4(0, 0, 0, 0)
-                                                     : make_int4(cc.b, cc.h, cc.rt, share_of(T, P, end) - blockIdx.x + 1);
+        const int end = t0 + cc.it + cc.v.tiles - 1;  // its last tile, if it begins here
+        a.part_seg[blockIdx.x] = whole || cc.kb != 0
+                                     ? make_int4(0, 0, 0, 0)
+                                     : make_int4(cc.b, cc.h, cc.rt, Shares(a, T).holder(end) - static_cast<int>(blockIdx.x) + 1);
       }
       float l[RPW][2];
 #pragma unroll
@@ -875,7 +896,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       auto put = [&](int row, int col, float4 v, float m_all, float l_all) {
         if (row >= rows) return;
         if (whole) {
-          const int gr = cc.rt * a.RB + row, i = gr / a.G;
+          const int gr = cc.rt * a.RB + row, i = row_of(a, gr);
           const bool some = i < cc.m && l_all != 0.f;  // NaN sums count
           const float f = some ? a.v_scale / l_all : 0.f;
           const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
@@ -900,17 +921,23 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           for (int r = 0; r < 2; ++r)
             ml[warp * WR + w * 16 + r * 8 + (lane >> 2)] = make_float2(mx[w][r], l[w][r]);
       }
-#pragma unroll
+#pragma unroll 1
       for (int d0 = 0; d0 < D; d0 += DS) {
         compute_sync();
+        // (the slice's registers by compile-time numbers, the rest of the round once)
 #pragma unroll
-        for (int w = 0; w < RPW; ++w)
+        for (int d1 = 0; d1 < D; d1 += DS) {
+          if (d1 != d0) continue;
 #pragma unroll
-          for (int i = d0 / 8; i < (d0 + DS) / 8; ++i)
+          for (int w = 0; w < RPW; ++w)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              join[(warp * WR + w * 16 + (lane >> 2) + 8 * (e >> 1)) * (DS + 4) + out_col<E8>(i, e & 1) - d0] = o[w][i][e];
+            for (int i = d1 / 8; i < (d1 + DS) / 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                join[(warp * WR + w * 16 + (lane >> 2) + 8 * (e >> 1)) * (DS + 4) + out_col<E8>(i, e & 1) - d1] = o[w][i][e];
+        }
         compute_sync();
+#pragma unroll 1
         for (int x = tid; x < RG * WR * (DS / 4); x += 32 * kComputeWarps) {
           const int row = x / (DS / 4), col = (x % (DS / 4)) * 4, w0 = row / WR;  // the row's warp in each team
           float m_all = -INFINITY, l_all = 0.f;
@@ -949,7 +976,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
   const int row = (blockIdx.x % per_seg) * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int gr = seg.z * a.RB + row;
   if (seg.w < 2 || gr >= a.M * a.G) return;
-  const int b = seg.x, h = seg.y, i = gr / a.G;
+  const int b = seg.x, h = seg.y, i = row_of(a, gr);
   const bool valid = i < new_rows(a.q_lens, b, a.M);
   const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
   constexpr int E = D / 32;  // 2, 4 or 8 columns
