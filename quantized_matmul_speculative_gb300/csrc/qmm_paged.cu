@@ -89,9 +89,9 @@ qmm_status check_cache(const qmm_paged_cache* c, int B, int M) {
 
 }  // namespace
 
-extern template cudaError_t launch_attention<64>(AttentionArgs, bool, cudaStream_t);
-extern template cudaError_t launch_attention<128>(AttentionArgs, bool, cudaStream_t);
-extern template cudaError_t launch_attention<256>(AttentionArgs, bool, cudaStream_t);
+extern template cudaError_t launch_attention<64>(AttentionArgs, bool, int, cudaStream_t);
+extern template cudaError_t launch_attention<128>(AttentionArgs, bool, int, cudaStream_t);
+extern template cudaError_t launch_attention<256>(AttentionArgs, bool, int, cudaStream_t);
 extern template unsigned int read_attention_status<64>(int);
 extern template unsigned int read_attention_status<128>(int);
 extern template unsigned int read_attention_status<256>(int);
@@ -132,7 +132,7 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
 size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim) {
   if (B <= 0 || M <= 0 || M > 16 || heads <= 0 || q_heads <= 0 || q_heads % heads != 0 || q_heads > 65535 || head_dim <= 0)
     return 0;
-  return attention_workspace(device_sm_count(), attention_row_block(M * (q_heads / heads)), head_dim);
+  return attention_workspace(kMaxWorkers * device_sm_count(), attention_row_block(M * (q_heads / heads), head_dim), head_dim);
 }
 
 qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
@@ -169,25 +169,22 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.sinks = window != 0 ? sinks : 0;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.RB = attention_row_block(M * a.G);
+  a.RB = attention_row_block(M * a.G, cache->head_dim);
   a.RT = (M * a.G + a.RB - 1) / a.RB;
-  const int tile = attention_tile(cache->head_dim);
-  a.tn_log2 = tile == 64 ? 6 : tile == 32 ? 5 : 4;
   a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
-  // one CTA an SM, at most one a tile
-  const int64_t tiles = static_cast<int64_t>(B) * cache->heads * a.RT *
-                        ((static_cast<int64_t>(cache->max_pages) * cache->page_size + tile - 1) / tile);
-  if (tiles > 0x7fffffff) return QMM_ERR_SHAPE;
-  const int64_t fit = device_sm_count();
-  a.parts = static_cast<int>(tiles < 1 ? 1 : tiles < fit ? tiles : fit);
-  if (workspace_bytes < attention_workspace(a.parts, a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
+  // (tiles are numbered in 32 bits; they hold 16 tokens at least)
+  if (static_cast<int64_t>(B) * cache->heads * a.RT * (static_cast<int64_t>(cache->max_pages) * cache->page_size / 16 + 1) > 0x7fffffff)
+    return QMM_ERR_SHAPE;
+  const int ctas = device_sm_count();
+  const size_t workers = static_cast<size_t>(ctas) * kMaxWorkers;
+  if (workspace_bytes < attention_workspace(static_cast<int>(workers), a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(a.parts) * 2 * a.RB * cache->head_dim);
-  a.part_seg = reinterpret_cast<int4*>(a.part_ml + static_cast<size_t>(a.parts) * 2 * a.RB);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + workers * 2 * a.RB * cache->head_dim);
+  a.part_seg = reinterpret_cast<int4*>(a.part_ml + workers * 2 * a.RB);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->head_dim == 64    ? launch_attention<64>(a, e8, st)
-                        : cache->head_dim == 128 ? launch_attention<128>(a, e8, st)
-                                                 : launch_attention<256>(a, e8, st);
+  const cudaError_t e = cache->head_dim == 64    ? launch_attention<64>(a, e8, ctas, st)
+                        : cache->head_dim == 128 ? launch_attention<128>(a, e8, ctas, st)
+                                                 : launch_attention<256>(a, e8, ctas, st);
   return static_cast<qmm_status>(finish_call(e));
 }
 

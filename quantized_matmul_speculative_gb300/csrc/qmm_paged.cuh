@@ -3,13 +3,18 @@
 //
 // The work.  A segment is one (sequence, key-value head, block of query rows):
 // its rows are the new rows x the G query heads of the key-value head, so one
-// pass over the keys and values serves them all.  A segment's visible tokens
-// are cut into tiles of 32 or 64; the tiles of all segments form one list (sequence,
-// head, row block, tile order), and CTA c of the grid takes the c-th equal
-// share of it, whatever the lengths: a single long sequence is split over all
-// SMs, a batch of ragged ones is balanced.  A segment that one CTA finishes is
-// written directly; the others leave (max, sum, unnormalised output) of their
-// share in the workspace, which join_kernel combines in list order.
+// pass over the keys and values serves 16 or 32 of them.  A segment's visible
+// tokens are cut into tiles; the tiles of all segments form one list (sequence,
+// head, row block, tile order), and every warp of the grid is a worker with an
+// equal, contiguous share of it, whatever the lengths: a single long sequence
+// is split over all SMs, a batch of ragged ones is balanced, and no warp waits
+// for another.  A segment that one worker finishes is written directly; the
+// others leave (maximum, sum, unnormalised output) of their share in the
+// workspace, which join_kernel combines in list order.
+//
+// A worker streams its own tiles: a ring of SLOTS pieces (the keys of a tile,
+// its values, the next tile's keys, ..), each refilled by TMA as soon as the
+// warp has read it.
 //
 // The mathematics.  One pass with running maximum m and sum l per row, in
 // base-2 exponents: s = q.k scale log2(e), p = 2^(s - m'), o = o 2^(m - m') +
@@ -27,15 +32,8 @@
 
 namespace qmm {
 
-// Tokens of a tile: as many as leave the accumulators their registers and every
-// team of warps a stage of its own.
-__host__ __device__ constexpr int attention_tile(int D) { return D >= 256 ? 16 : D >= 128 ? 32 : 64; }
-constexpr int kComputeWarps = 8;
-// Two computing warpgroups and one that loads; the registers a thread is
-// launched with (168 of 384 threads: 64512) move to the computing ones.
-constexpr int kAttnThreads = 32 * (kComputeWarps + 4);
-constexpr int kLaunchRegs = 168;
 constexpr int kJoinThreads = 128;
+constexpr int kMaxWorkers = 8;  // of a CTA, at most
 
 struct AttentionArgs {
   qmm_paged_cache c;
@@ -50,20 +48,21 @@ struct AttentionArgs {
   __nv_bfloat16* out;
   float* lse;
   int box;        // tokens of a TMA box (8 or 16); 0: copied row by row
-  int RB, RT;     // rows of a row block, row blocks of a segment's M * G rows
-  int tn_log2;    // of attention_tile()
+  int RB, RT;     // rows of a row block (16 or 32), row blocks of a segment's M * G rows
+  int tn_log2;    // of a tile's tokens
   uint32_t g_magic;          // ceil(2^32 / G); 0 for G = 1
-  int parts;      // CTAs of the attention kernel
-  float* part_o;  // [parts][2][RB][D]
+  int parts;      // workers
+  float* part_o;  // [parts][2][RB / 16][D / 8][32 lanes][4], as the MMA leaves them
   float2* part_ml;  // [parts][2][RB]
-  int4* part_seg;   // [parts] the segment that begins in a CTA's share and goes on: (b, h, rt, parts), parts 0: none
+  int4* part_seg;   // [parts] the segment that begins in a worker's share and goes on: (b, h, rt, parts), parts 0: none
 };
 
-// Bytes of the parts that `ctas` CTAs can leave.
-inline size_t attention_workspace(int ctas, int RB, int D) {
-  return static_cast<size_t>(ctas) * (2 * RB * (static_cast<size_t>(D) * 4 + 8) + 16);
+// Bytes of the parts that `workers` can leave.
+inline size_t attention_workspace(int workers, int RB, int D) {
+  return static_cast<size_t>(workers) * (2 * RB * (static_cast<size_t>(D) * 4 + 8) + 16);
 }
-inline int attention_row_block(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a block: what one warp holds the outputs of.
+inline int attention_row_block(int rows, int D) { return rows <= 16 || D == 256 ? 16 : 32; }
 
 // Tokens of sequence b, clamped to what its block table can hold.
 __device__ __forceinline__ int seq_length(const qmm_paged_cache& c, int b) {
@@ -138,7 +137,7 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 
-// How the list of T tiles is shared: CTAs that work (no more than there are
+// How the list of T tiles is shared: workers with a share (no more than there are
 // tiles, so that every share holds one), tiles of each, and how many of the
 // first ones hold one more.
 struct Shares {
@@ -149,13 +148,13 @@ struct Shares {
     more = T - each * parts;
   }
   __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int holder(int t) const {  // the CTA whose share holds tile t
+  __device__ __forceinline__ int holder(int t) const {  // the worker whose share holds tile t
     const int long_ones = more * (each + 1);
     return t < long_ones ? t / (each + 1) : more + (t - long_ones) / each;
   }
 };
 
-// A CTA's share of the list, segment by segment.
+// A worker's share of the list, segment by segment.
 struct Cursor {
   int left;    // tiles of the share from this segment on
   int it;      // the share's tiles before this segment
@@ -172,8 +171,8 @@ struct Cursor {
   static __device__ __forceinline__ int seq_tiles(const AttentionArgs& a, int s) {
     return s < a.B ? head_tiles(a, s) * a.c.heads : 0;
   }
-  // The share of this CTA (every lane of the warp calls); false: none.
-  __device__ __forceinline__ bool begin(const AttentionArgs& a, int& T, int& t0) {
+  // The share of this worker (every lane of the warp calls); false: none.
+  __device__ __forceinline__ bool begin(const AttentionArgs& a, int worker, int& T, int& t0) {
     const int lane = threadIdx.x & 31;
     T = 0;
     int n = 0;  // tiles of sequence (last base) + lane
@@ -183,9 +182,9 @@ struct Cursor {
       T += __reduce_add_sync(0xffffffffu, n);
     }
     const Shares sh(a, T);
-    if (static_cast<int>(blockIdx.x) >= sh.parts) return false;
-    t0 = sh.begin(blockIdx.x);
-    left = sh.begin(blockIdx.x + 1) - t0;
+    if (worker >= sh.parts) return false;
+    t0 = sh.begin(worker);
+    left = sh.begin(worker + 1) - t0;
     it = 0;
     int before = 0;
     b = 0;
@@ -254,10 +253,6 @@ __device__ __forceinline__ uint32_t tile_at(int token, int chunk) {
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, unsigned long long src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
-}
-// Arrives on `bar` when this thread's earlier cp.async copies have landed.
-__device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
                                             uint32_t bar) {
@@ -333,34 +328,25 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
             : (((((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 15) * 0xFFFFu);
 }
 
-// RPW 16-row tiles a warp, RG warps a team (RG * RPW * 16 rows a row block).
-template <int D, bool E8, int RG, int RPW>
+// RPW 16-row tiles a worker.
+template <int D, bool E8, int RPW>
 struct AttnCfg {
-  static constexpr int TN = attention_tile(D);
+  // Tokens of a tile: 4 or 8 KB of keys, as many as leave the accumulators their registers.
+  static constexpr int TN = D == 256 ? 16 : D == 128 ? 32 : 64;
+  static constexpr int TN_LOG2 = TN == 64 ? 6 : TN == 32 ? 5 : 4;
   static constexpr int ROWB = D * (E8 ? 1 : 2);
-  static constexpr int TILEB = TN * ROWB;  // bytes of a key (or value) tile
-  static constexpr int TEAMS = kComputeWarps / RG;
-  static constexpr int DS = RPW == 1 ? 64 : 32;   // output columns joined at a time
-  static constexpr bool QREG = D * RPW <= 128;    // query fragments stay in registers
-  static constexpr int JOINB = TEAMS > 1 ? kComputeWarps * 16 * RPW * (DS + 4) * 4 : 0;  // [8][16 RPW][DS + 4] floats
-  static constexpr int MLB = TEAMS > 1 ? kComputeWarps * 16 * RPW * 8 : 0;               // [8][16 RPW] (m, l)
-  static constexpr int QB = QREG ? 0 : RG * RPW * 16 * D * 2;  // [RG][D / 16][RPW][32] query fragments
-  // A multiple of the teams and of the loading warps of a kind: a stage always
-  // belongs to one team and one loader, which see its phases in order (a
-  // barrier's parity tells a phase from its neighbour only).
-  static constexpr int MULT = TEAMS > 2 ? TEAMS : 2;
-  static constexpr int STAGES = (232448 - 1024 - JOINB - MLB - QB) / (2 * TILEB + 32) / MULT * MULT;
-  // registers of a computing and of a loading thread: the outputs of 32 rows of
-  // 128 columns (or 16 of 256) need most of them
-  static constexpr int COMPUTE_REGS = D * RPW > 128 ? 224 : 208, LOAD_REGS = D * RPW > 128 ? 56 : 88;
-  static_assert(256 * COMPUTE_REGS + 128 * LOAD_REGS <= kAttnThreads * kLaunchRegs, "setmaxnreg would wait forever");
-  // Barriers: keys full, values full, keys empty, values empty, [STAGES] each
-  static constexpr int OFF_BAR = STAGES * 2 * TILEB;
-  static constexpr int OFF_JOIN = OFF_BAR + STAGES * 32;
-  static constexpr int OFF_ML = OFF_JOIN + JOINB;
-  static constexpr int OFF_Q = OFF_ML + MLB;
-  static constexpr int SMEM = OFF_Q + QB + 1024;  // and the alignment of its start
-  static_assert(TILEB % 1024 == 0 && SMEM <= 232448 && STAGES >= 2, "shared memory of an SM");
+  static constexpr int TILEB = TN * ROWB;          // bytes of a key (or value) tile
+  static constexpr bool QREG = D * RPW <= 128;     // query fragments stay in registers
+  static constexpr int QB = QREG ? 0 : RPW * 16 * D * 2;  // [D / 16][RPW][32] query fragments, if not
+  // seven workers where eight would have room for two pieces only
+  static constexpr int WORKERS = !QREG && !E8 ? 7 : 8;
+  static constexpr int ROOM = (232448 - 1024) / WORKERS - QB;
+  static constexpr int SLOTS = ROOM / (TILEB + 8) > 6 ? 6 : ROOM / (TILEB + 8);
+  static constexpr int OFF_Q = WORKERS * SLOTS * TILEB;
+  static constexpr int OFF_BAR = OFF_Q + WORKERS * QB;
+  static constexpr int SMEM = OFF_BAR + WORKERS * SLOTS * 8 + 1024;  // and the alignment of its start
+  static constexpr int THREADS = 32 * WORKERS;
+  static_assert(TILEB % 1024 == 0 && SMEM <= 232448 && SLOTS >= 3, "shared memory of an SM");
 };
 
 // Query fragments of one warp: rows r0 = lane / 4 and r0 + 8 of its row group.
@@ -422,18 +408,17 @@ __device__ __forceinline__ int out_col(int ot, int e) {
   return E8 ? (ot >> 1) * 16 + 4 * c + 2 * e + (ot & 1) : ot * 8 + 2 * c + e;
 }
 
-__device__ __forceinline__ void compute_sync() {
-  asm volatile("barrier.sync 1, %0;" ::"n"(32 * kComputeWarps) : "memory");
-}
-
 // Whether some row of queries sees one of the tokens j .. j + count - 1.
 __device__ __forceinline__ bool seen(const AttentionArgs& a, const Cursor& p, int j, int count) {
   return j < p.v.hi && (j + count > p.v.first || j < a.sinks);
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-// A loading warp: of four, two load keys and two values, every second tile
-// each, so that one's chain of page number, free stage and copies overlaps the
-// others', and a stage's keys are refilled while its values are still in use.
+// A worker's stream of pieces.
 //
 // Where pages divide into boxes of 8 or 16 tokens (a.box), TMA copies boxes of
 // [tokens][128 bytes] (16 tokens: all slices at once); coordinates are (byte
@@ -443,137 +428,147 @@ __device__ __forceinline__ bool seen(const AttentionArgs& a, const Cursor& p, in
 // used.  Any other page size: 16-byte asynchronous copies of the tokens' rows;
 // tokens that nobody sees and those of pages outside the cache become zeros.
 template <class Cfg, bool E8>
-__device__ __forceinline__ void load_tiles(const AttentionArgs& a, uint32_t sbase, Cursor pc, int part, bool values,
-                                           const void* map) {
-  constexpr int ST = Cfg::STAGES, SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
-  constexpr int CPR = Cfg::ROWB / 16, RPL = (Cfg::TN + 31) / 32, ES = E8 ? 1 : 2, RPI = 32 / CPR;
-  const int lane = threadIdx.x & 31;
-  const uint32_t full0 = sbase + Cfg::OFF_BAR + (values ? ST * 8 : 0), empty0 = full0 + 2 * ST * 8;
-  const uint32_t tile0 = sbase + (values ? Cfg::TILEB : 0);
-  const unsigned long long cache = reinterpret_cast<unsigned long long>(values ? a.c.v : a.c.k);
-  const int64_t s_page = values ? a.c.v_page : a.c.k_page, s_token = values ? a.c.v_token : a.c.k_token,
-                s_head = values ? a.c.v_head : a.c.k_head;
-  const int step = a.box ? a.box : 1;                                        // tokens a lane finds the page of
-  const int finders = a.box ? Cfg::TN / a.box : Cfg::TN < 32 ? Cfg::TN : 32;  // lanes that do
-  const int per = a.box == 16 ? 1 : SL;                                      // copies of a box
-  int k = pc.kb + part;  // the tile; past ke: in a later segment
-  int page[RPL], slot[RPL], head = 0;
-#pragma unroll
-  for (int x = 0; x < RPL; ++x) page[x] = 0, slot[x] = -1;
-  bool more = true;
-  auto find = [&]() {
-    while (k >= pc.ke) {
-      const int over = k - pc.ke;
-      if (!pc.next(a)) {
+struct Stream {
+  static constexpr int SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
+  static constexpr int CPR = Cfg::ROWB / 16, RPL = (Cfg::TN + 31) / 32, ES = E8 ? 1 : 2, RPI = 32 / CPR;
+  uint32_t ring, bars;  // shared-memory addresses
+  Cursor c;             // where the next tile's page numbers come from
+  int k;
+  bool more;            // there is such a tile
+  int slot;             // of the next piece
+  bool values;          // the next piece is a tile's values
+  int page[RPL], place[RPL], head;  // of the tile that is copied: this lane's tokens (row copies) or boxes
+  int page2[RPL], place2[RPL], head2;  // and of the one after it, on their way
+
+  // Load the page numbers of the next tile; place -1: nobody sees it.
+  __device__ __forceinline__ void find(const AttentionArgs& a) {
+    const int lane = threadIdx.x & 31;
+    if (k >= c.ke) {
+      if (!c.next(a)) {
         more = false;
         return;
       }
-      k = pc.kb + over;
+      k = c.kb;
     }
-    head = pc.h;
+    const int step = a.box ? a.box : 1;                                         // tokens a lane finds the page of
+    const int finders = a.box ? Cfg::TN / a.box : Cfg::TN < 32 ? Cfg::TN : 32;  // lanes that do
+    head2 = c.h;
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
-      const int j = pc.tile(k) * Cfg::TN + lane * step + 32 * x;
-      slot[x] = -1;
-      page[x] = 0;
-      if (lane < finders && (x == 0 || !a.box) && seen(a, pc, j, step)) {
+      const int j = c.tile(k) * Cfg::TN + lane * step + 32 * x;
+      place2[x] = -1;
+      page2[x] = 0;
+      if (lane < finders && (x == 0 || !a.box) && seen(a, c, j, step)) {
         const int block = j / a.c.page_size;
-        slot[x] = j - block * a.c.page_size;
-        page[x] = a.c.block_table[pc.b * a.c.table_stride + block];
+        place2[x] = j - block * a.c.page_size;
+        page2[x] = a.c.block_table[c.b * a.c.table_stride + block];
       }
     }
-    k += 2;
-  };
-  int pg[RPL], st[RPL];
-#pragma unroll
-  for (int x = 0; x < RPL; ++x) pg[x] = 0, st[x] = -1;
-  // the page numbers of a tile are loaded while the one before is copied
-  for (int it = part - 2, last = 0; !last; it += 2) {
-    const int hd = head;
-#pragma unroll
-    for (int x = 0; x < RPL; ++x) {
-      if (slot[x] >= 0 && (page[x] < 0 || page[x] >= a.c.num_pages)) {
-        bad_page();
-        page[x] = -1;
-      }
-      pg[x] = page[x];
-      st[x] = slot[x];
-    }
-    find();
-    last = !more;
-    if (it < 0) continue;
-    const int stage = it % ST;
-    const uint32_t full = full0 + stage * 8, base = tile0 + stage * 2 * Cfg::TILEB;
-    if (it >= ST && __any_sync(0xffffffffu, !mbar_wait(empty0 + stage * 8, ((it / ST) & 1) ^ 1, kStatusTimeoutEmpty))) break;
-    if (a.box) {
-      const uint32_t loaded = __ballot_sync(0xffffffffu, st[0] >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(full, __popc(loaded) * a.box * Cfg::ROWB);
-      __syncwarp();
-      const int copies = finders * per;  // at most 32
-      const int box = lane / per, sl = lane - box * per;
-      const int p = __shfl_sync(0xffffffffu, pg[0], box & 31), s = __shfl_sync(0xffffffffu, st[0], box & 31);
-      if (lane < copies && s >= 0) {
-        const int token = box * a.box;
-        tma_load_5d(base + (token >> 4) * 16 * Cfg::ROWB + sl * 2048 + (token & 15) * ROW, map, 0, s, sl, hd, p, full);
-      }
-    } else {
-      // byte offsets of this lane's tokens from the cache's start, -1: zeros;
-      // they reach the lanes that copy the rows by shuffles
-      long long at[RPL];
-#pragma unroll
-      for (int x = 0; x < RPL; ++x)
-        at[x] = st[x] >= 0 && pg[x] >= 0 ? (pg[x] * s_page + st[x] * s_token + hd * s_head) * ES : -1;
-      const int ch = lane % CPR;
-#pragma unroll 8
-      for (int g = 0; g < Cfg::TN / RPI; ++g) {
-        const int row = g * RPI + lane / CPR;
-        long long r = __shfl_sync(0xffffffffu, at[0], row & 31);
-        if constexpr (RPL == 2) {
-          const long long r2 = __shfl_sync(0xffffffffu, at[1], row & 31);
-          r = row < 32 ? r : r2;
-        }
-        // nothing is read where zeros are filled in
-        cp_async_16(base + tile_at<Cfg::ROWB>(row, ch), cache + (r < 0 ? 0 : r) + ch * 16, r >= 0);
-      }
-      cp_async_mbar_arrive_noinc(full);
-    }
+    ++k;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
+  __device__ __forceinline__ void begin(const AttentionArgs& a, const Cursor& at, uint32_t ring_addr, uint32_t bar_addr) {
+    ring = ring_addr;
+    bars = bar_addr;
+    c = at;
+    k = c.kb;
+    more = true;
+    slot = 0;
+    values = false;
+    find(a);
+  }
+  // Copy the next piece into its slot (which the warp is done with).
+  __device__ __forceinline__ void issue(const AttentionArgs& a, const void* kmap, const void* vmap) {
+    const int lane = threadIdx.x & 31;
+    bool any = true;
+    if (!values) {
+      any = more;
+      if (any) {
+#pragma unroll
+        for (int x = 0; x < RPL; ++x) {
+          if (place2[x] >= 0 && (page2[x] < 0 || page2[x] >= a.c.num_pages)) {
+            bad_page();
+            page2[x] = -1;
+          }
+          page[x] = page2[x];
+          place[x] = place2[x];
+        }
+        head = head2;
+        find(a);
+      }
+    }
+    if (any) {
+      const uint32_t base = ring + slot * Cfg::TILEB;
+      if (a.box) {
+        const uint32_t full = bars + slot * 8;
+        const int per = a.box == 16 ? 1 : SL;  // copies of a box
+        const uint32_t loaded = __ballot_sync(0xffffffffu, place[0] >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(full, __popc(loaded) * a.box * Cfg::ROWB);
+        __syncwarp();
+        const int box = lane / per, sl = lane - box * per;  // at most 16 boxes x slices
+        const int p = __shfl_sync(0xffffffffu, page[0], box & 31), s = __shfl_sync(0xffffffffu, place[0], box & 31);
+        if (box * a.box < Cfg::TN && s >= 0) {
+          const int token = box * a.box;
+          tma_load_5d(base + (token >> 4) * 16 * Cfg::ROWB + sl * 2048 + (token & 15) * ROW, values ? vmap : kmap, 0, s, sl, head,
+                      p, full);
+        }
+      } else {
+        // byte offsets of this lane's tokens from the cache's start, -1: zeros;
+        // they reach the lanes that copy the rows by shuffles
+        const unsigned long long cache = reinterpret_cast<unsigned long long>(values ? a.c.v : a.c.k);
+        const int64_t s_page = values ? a.c.v_page : a.c.k_page, s_token = values ? a.c.v_token : a.c.k_token,
+                      s_head = values ? a.c.v_head : a.c.k_head;
+        long long at[RPL];
+#pragma unroll
+        for (int x = 0; x < RPL; ++x)
+          at[x] = place[x] >= 0 && page[x] >= 0 ? (page[x] * s_page + place[x] * s_token + head * s_head) * ES : -1;
+        const int ch = lane % CPR;
+#pragma unroll 4
+        for (int g = 0; g < Cfg::TN / RPI; ++g) {
+          const int row = g * RPI + lane / CPR;
+          long long r = __shfl_sync(0xffffffffu, at[0], row & 31);
+          if constexpr (RPL == 2) {
+            const long long r2 = __shfl_sync(0xffffffffu, at[1], row & 31);
+            r = row < 32 ? r : r2;
+          }
+          // nothing is read where zeros are filled in
+          cp_async_16(base + tile_at<Cfg::ROWB>(row, ch), cache + (r < 0 ? 0 : r) + ch * 16, r >= 0);
+        }
+      }
+      slot = slot + 1 == Cfg::SLOTS ? 0 : slot + 1;
+      values = !values;
+    }
+    if (!a.box) cp_async_commit();  // a group for every call, so that counting them back finds a piece's
+  }
+};
 
-// Computing warps in teams of RG (RPW 16-row tiles a warp); team t takes the
-// CTA's tiles t, t + TEAMS, ..., each warp with a running softmax of its own,
-// so that no warp waits for another before the end of a segment.
-template <int D, bool E8, int RG, int RPW>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <int D, bool E8, int RPW>
+__global__ void __launch_bounds__(AttnCfg<D, E8, RPW>::THREADS, 1)
 attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using Cfg = AttnCfg<D, E8, RG, RPW>;
-  constexpr int ST = Cfg::STAGES, NT = Cfg::TN, ROWB = Cfg::ROWB, CPR = ROWB / 16, TEAMS = Cfg::TEAMS;
+  using Cfg = AttnCfg<D, E8, RPW>;
+  constexpr int SLOTS = Cfg::SLOTS, NT = Cfg::TN, ROWB = Cfg::ROWB, CPR = ROWB / 16;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   unsigned char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
-  const uint32_t bars = sbase + Cfg::OFF_BAR;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int worker = warp * gridDim.x + blockIdx.x;  // the first shares go to different SMs
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
-      mbar_init(bars + s * 8, a.box ? 1 : 32);
-      mbar_init(bars + (ST + s) * 8, a.box ? 1 : 32);
-      mbar_init(bars + (2 * ST + s) * 8, RG);
-      mbar_init(bars + (3 * ST + s) * 8, RG);
-    }
+    for (int s = 0; s < Cfg::WORKERS * SLOTS; ++s) mbar_init(sbase + Cfg::OFF_BAR + s * 8, 1);
     fence_mbar_init();
   }
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   // rows of segments without tiles: the CTA of the sequence's number writes them
+#pragma unroll 1
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
+#pragma unroll 1
     for (int rt = 0; rt < a.RT; ++rt) {
       if (visible(a, L, m, rt).tiles != 0) continue;
       const int r0 = rt * a.RB, rows = min(a.RB, a.M * a.G - r0), per_head = rows * (D / 8);
-      for (int x = tid; x < per_head * a.c.heads; x += kAttnThreads) {
+#pragma unroll 1
+      for (int x = tid; x < per_head * a.c.heads; x += Cfg::THREADS) {
         const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = row_of(a, gr);
         const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
         *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
@@ -583,69 +578,80 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   }
   Cursor cc;
   int T, t0;
-  if (!cc.begin(a, T, t0)) {
-    if (tid == 0) a.part_seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (!cc.begin(a, worker, T, t0)) {
+    if (lane == 0) a.part_seg[worker] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (warp >= kComputeWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::LOAD_REGS));
-    load_tiles<Cfg, E8>(a, sbase, cc, warp & 1, (warp & 2) != 0, (warp & 2) != 0 ? &vmap : &kmap);
-    return;
-  }
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::COMPUTE_REGS));
-  const int rg = warp % RG, team = warp / RG;
+  const int ring_off = warp * SLOTS * Cfg::TILEB;
+  const uint32_t bars = sbase + Cfg::OFF_BAR + warp * SLOTS * 8;
+  Stream<Cfg, E8> in;
+  in.begin(a, cc, sbase + ring_off, bars);
+#pragma unroll 1
+  for (int s = 0; s < SLOTS; ++s) in.issue(a, &kmap, &vmap);
 
   float o[RPW][D / 8][4];
   float mx[RPW][2], sum[RPW][2][2];  // running maximum; sum of the even and of the odd columns
   Query<Cfg::QREG ? D : 16, E8> qf[RPW];  // the query fragments, or where they are
-  uint4* const q_frag = reinterpret_cast<uint4*>(smem + Cfg::OFF_Q) + rg * (D / 16) * RPW * 32 + lane;
+  uint4* const q_frag = reinterpret_cast<uint4*>(smem + Cfg::OFF_Q + warp * Cfg::QB) + lane;
   int pos[RPW][2];  // positions of this thread's rows; INT_MIN / 2 for rows that do not exist
   bool lost = false;
+  int slot = 0;        // of the next piece to use
+  uint32_t phase = 0;  // of its barrier
+  // A wait that gave up (status bit 0) leaves wrong results, never a hang: later waits are skipped.
+  auto wait = [&]() {
+    if (a.box) {
+      if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bars + slot * 8, phase, kStatusTimeoutFull));
+    } else {
+      cp_async_wait<SLOTS - 1>();
+      __syncwarp();
+    }
+  };
+  auto used = [&]() {
+    __syncwarp();
+    in.issue(a, &kmap, &vmap);
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1;
+    }
+  };
 
   do {  // segment by segment
-    {
 #pragma unroll
-      for (int w = 0; w < RPW; ++w) {
+    for (int w = 0; w < RPW; ++w) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[w][i][0] = o[w][i][1] = o[w][i][2] = o[w][i][3] = 0.f;
-        const uint16_t* row[2];
+      for (int i = 0; i < D / 8; ++i) o[w][i][0] = o[w][i][1] = o[w][i][2] = o[w][i][3] = 0.f;
+      const uint16_t* row[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mx[w][r] = -INFINITY;
-          sum[w][r][0] = sum[w][r][1] = 0.f;
-          const int gr = cc.rt * a.RB + (rg * RPW + w) * 16 + (lane >> 2) + 8 * r;
-          const int i = row_of(a, gr);
-          const bool ok = gr < a.M * a.G && i < cc.m;
-          pos[w][r] = ok ? cc.L - cc.m + i : INT_MIN / 2;
-          row[r] = ok ? a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld +
-                            static_cast<int64_t>(cc.h * a.G + gr - i * a.G) * D
-                      : nullptr;
-        }
-        if constexpr (Cfg::QREG) {
-          load_query<Cfg::QREG ? D : 16>(a, qf[w], row);
-        } else {
-          Query<D, E8> f;
-          load_query<D>(a, f, row);
-          qf[w].scale[0] = f.scale[0];
-          qf[w].scale[1] = f.scale[1];
-          if (team == 0)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              q_frag[(kk * RPW + w) * 32] = make_uint4(f.a[kk][0], f.a[kk][1], f.a[kk][2], f.a[kk][3]);
-        }
+      for (int r = 0; r < 2; ++r) {
+        mx[w][r] = -INFINITY;
+        sum[w][r][0] = sum[w][r][1] = 0.f;
+        const int gr = cc.rt * a.RB + w * 16 + (lane >> 2) + 8 * r;
+        const int i = row_of(a, gr);
+        const bool ok = gr < a.M * a.G && i < cc.m;
+        pos[w][r] = ok ? cc.L - cc.m + i : INT_MIN / 2;
+        row[r] = ok ? a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld +
+                          static_cast<int64_t>(cc.h * a.G + gr - i * a.G) * D
+                    : nullptr;
       }
-      if (!Cfg::QREG) compute_sync();
+      if constexpr (Cfg::QREG) {
+        load_query<Cfg::QREG ? D : 16>(a, qf[w], row);
+      } else {
+        Query<D, E8> f;
+        load_query<D>(a, f, row);
+        qf[w].scale[0] = f.scale[0];
+        qf[w].scale[1] = f.scale[1];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          q_frag[(kk * RPW + w) * 32] = make_uint4(f.a[kk][0], f.a[kk][1], f.a[kk][2], f.a[kk][3]);
+      }
     }
-    // this team's tiles
-    for (int k = cc.kb + (team + TEAMS - cc.it % TEAMS) % TEAMS; k < cc.ke; k += TEAMS) {
-      const int it = cc.it + k - cc.kb, stage = it % ST;
-      // a wait that gave up (status bit 0) leaves wrong results, never a hang: later waits are skipped
-      if (!lost) lost = !mbar_wait(bars + stage * 8, (it / ST) & 1, kStatusTimeoutFull);
+#pragma unroll 1
+    for (int k = cc.kb; k < cc.ke; ++k) {
+      wait();
       const int j0 = cc.tile(k) * NT;
       const bool full = j0 + NT - 1 <= cc.v.pos_lo &&
                         (a.window == 0 || j0 > cc.v.pos_hi - a.window || j0 + NT <= a.sinks);
-      const int koff = stage * 2 * Cfg::TILEB, voff = koff + Cfg::TILEB;
-      const uint32_t kt = sbase + koff, vt = sbase + voff;
+      const uint32_t kt = sbase + ring_off + slot * Cfg::TILEB;
 
       // scores
       float s[RPW][NT / 8][4];
@@ -708,8 +714,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
         }
       }
 
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + (2 * ST + stage) * 8);
+      used();
 
 #pragma unroll
       for (int w = 0; w < RPW; ++w) {
@@ -757,7 +762,9 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           }
       }
 
-      if (!lost) lost = !mbar_wait(bars + (ST + stage) * 8, (it / ST) & 1, kStatusTimeoutFull);
+      wait();
+      const int voff = ring_off + slot * Cfg::TILEB;
+      const uint32_t vt = sbase + voff;
       // A token that a row does not see meets it with weight 0, and 0 times its
       // value must be 0.  Where such a value is not finite (a later draft row's, or
       // what lies past the length), the product is taken with 0 in the place of
@@ -868,162 +875,162 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + (3 * ST + stage) * 8);
+      used();
     }
 
-    {
-      // the end of the segment, or of this CTA's share of it
-      const bool whole = cc.kb == 0 && cc.ke == cc.v.tiles;
-      const int slot = blockIdx.x * 2 + (cc.kb == 0 ? 1 : 0);
-      if (cc.left == cc.ke - cc.kb && tid == 0) {  // the last segment of the share: how many CTAs hold it
-        const int end = t0 + cc.it + cc.v.tiles - 1;  // its last tile, if it begins here
-        a.part_seg[blockIdx.x] = whole || cc.kb != 0
-                                     ? make_int4(0, 0, 0, 0)
-                                     : make_int4(cc.b, cc.h, cc.rt, Shares(a, T).holder(end) - static_cast<int>(blockIdx.x) + 1);
-      }
-      float l[RPW][2];
+    // the end of the segment, or of this worker's share of it
+    const bool whole = cc.kb == 0 && cc.ke == cc.v.tiles;
+    const int64_t part = static_cast<int64_t>(worker) * 2 + (cc.kb == 0 ? 1 : 0);
+    if (cc.left == cc.ke - cc.kb && lane == 0) {  // the share's last segment: how many workers hold it, if it begins here
+      const int end = t0 + cc.it + cc.v.tiles - 1;  // its last tile then
+      a.part_seg[worker] =
+          whole || cc.kb != 0 ? make_int4(0, 0, 0, 0) : make_int4(cc.b, cc.h, cc.rt, Shares(a, T).holder(end) - worker + 1);
+    }
 #pragma unroll
-      for (int w = 0; w < RPW; ++w)
+    for (int w = 0; w < RPW; ++w) {
+      float f[2];
+      __nv_bfloat16* to[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float l = sum[w][r][0] + sum[w][r][1];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int row = w * 16 + (lane >> 2) + 8 * r, gr = cc.rt * a.RB + row;
+        to[r] = nullptr;
+        if (!whole) {
+          if ((lane & 3) == 0) a.part_ml[part * a.RB + row] = make_float2(mx[w][r], l);
+        } else if (gr < a.M * a.G) {
+          const int i = row_of(a, gr);
+          const bool some = i < cc.m && l != 0.f;  // NaN sums count
+          f[r] = some ? a.v_scale / l : 0.f;
+          const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
+          to[r] = a.out + at * D;
+          if (a.lse != nullptr && (lane & 3) == 0) a.lse[at] = some ? (mx[w][r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      if (!whole) {
+        float4* const dst = reinterpret_cast<float4*>(a.part_o) + (part * RPW + w) * (D / 8) * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) dst[i * 32] = make_float4(o[w][i][0], o[w][i][1], o[w][i][2], o[w][i][3]);
+      } else {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          l[w][r] = sum[w][r][0] + sum[w][r][1];
-          l[w][r] += __shfl_xor_sync(0xffffffffu, l[w][r], 1);
-          l[w][r] += __shfl_xor_sync(0xffffffffu, l[w][r], 2);
-        }
-      // Four columns of a row: to the outputs, or to this CTA's part.
-      const int rows = a.M * a.G - cc.rt * a.RB;  // rows of this block that exist
-      auto put = [&](int row, int col, float4 v, float m_all, float l_all) {
-        if (row >= rows) return;
-        if (whole) {
-          const int gr = cc.rt * a.RB + row, i = row_of(a, gr);
-          const bool some = i < cc.m && l_all != 0.f;  // NaN sums count
-          const float f = some ? a.v_scale / l_all : 0.f;
-          const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
-          uint2 u = make_uint2(0u, 0u);
-          if (some) u = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
-          *reinterpret_cast<uint2*>(a.out + at * D + col) = u;
-          if (col == 0 && a.lse != nullptr) a.lse[at] = some ? (m_all + log2f(l_all)) * 0.6931471805599453f : -INFINITY;
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + (static_cast<int64_t>(slot) * a.RB + row) * D + col) = v;
-          if (col == 0) a.part_ml[static_cast<int64_t>(slot) * a.RB + row] = make_float2(m_all, l_all);
-        }
-      };
-      // Rows in slices of DS columns through shared memory: the teams are added
-      // there, and a thread then holds four columns of a row.
-      constexpr int DS = Cfg::DS, WR = 16 * RPW;  // rows of a warp
-      float2* const ml = reinterpret_cast<float2*>(smem + Cfg::OFF_ML);
-      float* const join = reinterpret_cast<float*>(smem + Cfg::OFF_JOIN);
-      if ((lane & 3) == 0) {
+          if (to[r] == nullptr) continue;
 #pragma unroll
-        for (int w = 0; w < RPW; ++w)
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            ml[warp * WR + w * 16 + r * 8 + (lane >> 2)] = make_float2(mx[w][r], l[w][r]);
-      }
-#pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += DS) {
-        compute_sync();
-        // (the slice's registers by compile-time numbers, the rest of the round once)
-#pragma unroll
-        for (int d1 = 0; d1 < D; d1 += DS) {
-          if (d1 != d0) continue;
-#pragma unroll
-          for (int w = 0; w < RPW; ++w)
-#pragma unroll
-            for (int i = d1 / 8; i < (d1 + DS) / 8; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                join[(warp * WR + w * 16 + (lane >> 2) + 8 * (e >> 1)) * (DS + 4) + out_col<E8>(i, e & 1) - d1] = o[w][i][e];
-        }
-        compute_sync();
-#pragma unroll 1
-        for (int x = tid; x < RG * WR * (DS / 4); x += 32 * kComputeWarps) {
-          const int row = x / (DS / 4), col = (x % (DS / 4)) * 4, w0 = row / WR;  // the row's warp in each team
-          float m_all = -INFINITY, l_all = 0.f;
-#pragma unroll
-          for (int t = 0; t < TEAMS; ++t) m_all = fmaxf(m_all, ml[(w0 + t * RG) * WR + row % WR].x);
-          const float base = m_all == -INFINITY ? 0.f : m_all;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int t = 0; t < TEAMS; ++t) {
-            const float2 p = ml[(w0 + t * RG) * WR + row % WR];
-            const float f = ex2(p.x - base);
-            const float4 u = *reinterpret_cast<const float4*>(join + ((w0 + t * RG) * WR + row % WR) * (DS + 4) + col);
-            l_all += f * p.y;
-            v.x += f * u.x;
-            v.y += f * u.y;
-            v.z += f * u.z;
-            v.w += f * u.w;
+          for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
+            // (a row without weight: 0 whatever the accumulators hold)
+            const bool some = f[r] != 0.f;
+            if constexpr (E8) {
+              uint2 u = make_uint2(0u, 0u);
+              if (some) u = make_uint2(pack_bf16(o[w][i][2 * r] * f[r], o[w][i + 1][2 * r] * f[r]),
+                                       pack_bf16(o[w][i][2 * r + 1] * f[r], o[w][i + 1][2 * r + 1] * f[r]));
+              *reinterpret_cast<uint2*>(to[r] + out_col<true>(i, 0)) = u;
+            } else {
+              *reinterpret_cast<uint32_t*>(to[r] + out_col<false>(i, 0)) =
+                  some ? pack_bf16(o[w][i][2 * r] * f[r], o[w][i][2 * r + 1] * f[r]) : 0u;
+            }
           }
-          put(row, d0 + col, v, m_all, l_all);
         }
       }
-      compute_sync();
     }
   } while (cc.next(a));
+  if (!a.box) cp_async_wait<0>();
 }
 
-// Combines the parts of segments that several CTAs share: the CTA a segment
-// begins in left its place and the number of parts.  One warp per row, D / 32
-// columns a lane; the parts' statistics are loaded by one lane each.
-template <int D>
+// Combines the parts of segments that several workers share: the one a segment
+// begins in left its place and the number of parts.  A warp takes 16 rows and
+// IW of the D / 8 output tiles of them, in the layout the parts are in.
+template <int D, bool E8>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int per_seg = a.RB / 4, c0 = blockIdx.x / per_seg;
-  const int4 seg = a.part_seg[c0];
-  const int row = (blockIdx.x % per_seg) * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int gr = seg.z * a.RB + row;
-  if (seg.w < 2 || gr >= a.M * a.G) return;
-  const int b = seg.x, h = seg.y, i = row_of(a, gr);
-  const bool valid = i < new_rows(a.q_lens, b, a.M);
-  const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
-  constexpr int E = D / 32;  // 2, 4 or 8 columns
-  float v[E] = {};
-  float top = -INFINITY, sum = 0.f;
-  for (int base = 0; base < seg.w; base += 32) {
-    // the first part is its CTA's second slot, the others the first
-    const int n = min(32, seg.w - base);
-    const int64_t mine = static_cast<int64_t>((c0 + base + lane) * 2 + (base + lane == 0)) * a.RB + row;
-    const float2 ml = lane < n ? a.part_ml[mine] : make_float2(-INFINITY, 0.f);
-    float t = ml.x;
+  constexpr int IW = 2, PER = D / 8 / IW;  // warps of 16 rows
+  const int per_part = PER * (a.RB / 16);
+  const int x = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int w0 = x / per_part, sub = x - w0 * per_part, w = sub / PER, i0 = (sub - w * PER) * IW;
+  if (w0 >= a.parts) return;
+  const int4 seg = a.part_seg[w0];
+  const int base_row = seg.z * a.RB + w * 16;
+  if (seg.w < 2 || base_row >= a.M * a.G) return;
+  const int RPW = a.RB / 16;
+  float v[IW][4] = {};
+  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  const int r0 = w * 16 + (lane >> 2);
+  // the first part is its worker's second slot, the others the first
+  auto part = [&](int c) { return static_cast<int64_t>(w0 + c) * 2 + (c == 0); };
+#pragma unroll 1
+  for (int base = 0; base < seg.w; base += 8) {
+    float2 ml[8][2];
+    float4 u[8][IW];
+    const int n = min(8, seg.w - base);
 #pragma unroll
-    for (int x = 16; x > 0; x /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, x));
-    t = fmaxf(t, top);
-    const float ref = t == -INFINITY ? 0.f : t, old = ex2(top - ref);
-    const float f = ex2(ml.x - ref);
-    float l = f * ml.y;
+    for (int c = 0; c < 8; ++c) {
+      if (c >= n) break;
+      const int64_t p = part(base + c);
+      ml[c][0] = a.part_ml[p * a.RB + r0];
+      ml[c][1] = a.part_ml[p * a.RB + r0 + 8];
 #pragma unroll
-    for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
-    sum = sum * old + l;
-    top = t;
+      for (int i = 0; i < IW; ++i)
+        u[c][i] = reinterpret_cast<const float4*>(a.part_o)[((p * RPW + w) * (D / 8) + i0 + i) * 32 + lane];
+    }
+    float t[2] = {top[0], top[1]}, old[2], ref[2];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= old;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-      const float g = __shfl_sync(0xffffffffu, f, c);
-      const int64_t p = static_cast<int64_t>((c0 + base + c) * 2 + (base + c == 0)) * a.RB + row;
-      const float2* src = reinterpret_cast<const float2*>(a.part_o + p * D + lane * E);
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const float2 u = src[e];
-        v[2 * e] += g * u.x;
-        v[2 * e + 1] += g * u.y;
+      for (int c = 0; c < 8; ++c)
+        if (c < n) t[r] = fmaxf(t[r], ml[c][r].x);
+      ref[r] = t[r] == -INFINITY ? 0.f : t[r];
+      old[r] = ex2(top[r] - ref[r]);
+      top[r] = t[r];
+      sum[r] *= old[r];
+    }
+#pragma unroll
+    for (int i = 0; i < IW; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] *= old[e >> 1];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c >= n) break;
+      const float f0 = ex2(ml[c][0].x - ref[0]), f1 = ex2(ml[c][1].x - ref[1]);
+      sum[0] += f0 * ml[c][0].y;
+      sum[1] += f1 * ml[c][1].y;
+#pragma unroll
+      for (int i = 0; i < IW; ++i) {
+        v[i][0] += f0 * u[c][i].x;
+        v[i][1] += f0 * u[c][i].y;
+        v[i][2] += f1 * u[c][i].z;
+        v[i][3] += f1 * u[c][i].w;
       }
     }
   }
-  const bool some = valid && sum != 0.f;
-  const float f = some ? a.v_scale / sum : 0.f;
+  const int m = new_rows(a.q_lens, seg.x, a.M);
 #pragma unroll
-  for (int e = 0; e < E / 2; ++e)
-    reinterpret_cast<uint32_t*>(a.out + at * D + lane * E)[e] = some ? pack_bf16(v[2 * e] * f, v[2 * e + 1] * f) : 0u;
-  if (a.lse != nullptr && lane == 0) a.lse[at] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  for (int r = 0; r < 2; ++r) {
+    const int gr = base_row + (lane >> 2) + 8 * r;
+    if (gr >= a.M * a.G) continue;
+    const int i = row_of(a, gr);
+    const bool some = i < m && sum[r] != 0.f;
+    const float f = some ? a.v_scale / sum[r] : 0.f;
+    const int64_t at = (static_cast<int64_t>(seg.x) * a.M + i) * a.Hq + seg.y * a.G + gr - i * a.G;
+    __nv_bfloat16* const to = a.out + at * D;
+    if constexpr (E8) {
+      static_assert(IW == 2, "an E4M3 cache's output tiles come in pairs");
+      uint2 p = make_uint2(0u, 0u);
+      if (some) p = make_uint2(pack_bf16(v[0][2 * r] * f, v[1][2 * r] * f), pack_bf16(v[0][2 * r + 1] * f, v[1][2 * r + 1] * f));
+      *reinterpret_cast<uint2*>(to + out_col<true>(i0, 0)) = p;
+    } else {
+#pragma unroll
+      for (int j = 0; j < IW; ++j)
+        *reinterpret_cast<uint32_t*>(to + out_col<false>(i0 + j, 0)) = some ? pack_bf16(v[j][2 * r] * f, v[j][2 * r + 1] * f) : 0u;
+    }
+    if (a.lse != nullptr && i0 == 0 && (lane & 3) == 0) a.lse[at] = some ? (top[r] + log2f(sum[r])) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
-// Launcher of one head size (qmm_paged_inst.cu): a.parts CTAs, then the join.
+// Launcher of one head size (qmm_paged_inst.cu): the attention kernel, of at most
+// `ctas` CTAs, then the join.
 template <int D>
-cudaError_t launch_attention(AttentionArgs a, bool e8, cudaStream_t stream);
+cudaError_t launch_attention(AttentionArgs a, bool e8, int ctas, cudaStream_t stream);
 template <int D>
 unsigned int read_attention_status(int clear);
 

@@ -49,27 +49,32 @@ static bool cache_map(CUtensorMap* map, const AttentionArgs& a, int D, bool e8, 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool E8, int RG, int RPW>
-cudaError_t launch_rows(const AttentionArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
-  using Cfg = AttnCfg<D, E8, RG, RPW>;
-  auto kern = attention_kernel<D, E8, RG, RPW>;
+template <int D, bool E8, int RPW>
+cudaError_t launch_rows(AttentionArgs a, int ctas, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  using Cfg = AttnCfg<D, E8, RPW>;
+  auto kern = attention_kernel<D, E8, RPW>;
   static std::atomic<uint64_t> ready{0};
   uint64_t bit;
   if (first_on_device(ready, &bit)) {
-    // the register split needs what the kernel was built with: never launched with less
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  return launch_dependent(kern, dim3(a.parts), kAttnThreads, Cfg::SMEM, stream, a, kmap, vmap);
+  a.tn_log2 = Cfg::TN_LOG2;
+  // one CTA an SM, at most one a tile
+  const int64_t cap = static_cast<int64_t>(a.c.max_pages) * a.c.page_size;
+  const int64_t tiles = static_cast<int64_t>(a.B) * a.c.heads * a.RT * ((cap + Cfg::TN - 1) >> Cfg::TN_LOG2);
+  if (tiles < ctas) ctas = tiles < 1 ? 1 : static_cast<int>(tiles);
+  a.parts = ctas * Cfg::WORKERS;
+  const cudaError_t e = launch_dependent(kern, dim3(ctas), Cfg::THREADS, Cfg::SMEM, stream, a, kmap, vmap);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = static_cast<int64_t>(a.parts) * (a.RB / 16) * (D / 16);
+  return launch_dependent(join_kernel<D, E8>, dim3(static_cast<unsigned>((warps * 32 + kJoinThreads - 1) / kJoinThreads)),
+                          kJoinThreads, 0, stream, a);
 }
 
 template <int D>
-cudaError_t launch_attention(AttentionArgs a, bool e8, cudaStream_t stream) {
+cudaError_t launch_attention(AttentionArgs a, bool e8, int ctas, cudaStream_t stream) {
   // TMA boxes where they divide a page; else, and for strides the TMA cannot
   // take, row by row.
   CUtensorMap kmap = {}, vmap = {};
@@ -78,15 +83,13 @@ cudaError_t launch_attention(AttentionArgs a, bool e8, cudaStream_t stream) {
   if (a.box != 0 && (!cache_map(&kmap, a, D, e8, a.c.k, a.c.k_page, a.c.k_token, a.c.k_head) ||
                      !cache_map(&vmap, a, D, e8, a.c.v, a.c.v_page, a.c.v_token, a.c.v_head)))
     a.box = 0;
-  // Two row tiles a warp share its key and value fragments (and an E4M3
+  // Two row tiles a worker share its key and value fragments (and an E4M3
   // cache's conversions); D = 256 has registers for the outputs of one only.
-  constexpr int W = D == 256 ? 1 : 2;
-  const cudaError_t e =
-      a.RB == 16   ? (e8 ? launch_rows<D, true, 1, 1>(a, kmap, vmap, stream) : launch_rows<D, false, 1, 1>(a, kmap, vmap, stream))
-      : a.RB == 32 ? (e8 ? launch_rows<D, true, 2 / W, W>(a, kmap, vmap, stream) : launch_rows<D, false, 2 / W, W>(a, kmap, vmap, stream))
-                   : (e8 ? launch_rows<D, true, 4 / W, W>(a, kmap, vmap, stream) : launch_rows<D, false, 4 / W, W>(a, kmap, vmap, stream));
-  if (e != cudaSuccess) return e;
-  return launch_dependent(join_kernel<D>, dim3(a.parts * (a.RB / 4)), kJoinThreads, 0, stream, a);
+  if (a.RB == 16)
+    return e8 ? launch_rows<D, true, 1>(a, ctas, kmap, vmap, stream) : launch_rows<D, false, 1>(a, ctas, kmap, vmap, stream);
+  if constexpr (D != 256)
+    return e8 ? launch_rows<D, true, 2>(a, ctas, kmap, vmap, stream) : launch_rows<D, false, 2>(a, ctas, kmap, vmap, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <int D>
@@ -100,7 +103,7 @@ unsigned int read_attention_status(int clear) {
   return v;
 }
 
-template cudaError_t launch_attention<QMM_HEAD_DIM>(AttentionArgs, bool, cudaStream_t);
+template cudaError_t launch_attention<QMM_HEAD_DIM>(AttentionArgs, bool, int, cudaStream_t);
 template unsigned int read_attention_status<QMM_HEAD_DIM>(int);
 
 }  // namespace qmm
