@@ -48,18 +48,19 @@ struct AttentionArgs {
   __nv_bfloat16* out;
   float* lse;
   int box;        // tokens of a TMA box (8 or 16); 0: copied row by row
+  int page_log2;  // of the page size, or -1
   int RB, RT;     // rows of a row block (16 or 32), row blocks of a segment's M * G rows
   int tn_log2;    // of a tile's tokens
   uint32_t g_magic;          // ceil(2^32 / G); 0 for G = 1
   int parts;      // workers
   float* part_o;  // [parts][2][RB / 16][D / 8][32 lanes][4], as the MMA leaves them
   float2* part_ml;  // [parts][2][RB]
-  int4* part_seg;   // [parts] the segment that begins in a worker's share and goes on: (b, h, rt, parts), parts 0: none
+  int4* part_seg;   // [parts][2][2] of a part: (b, h, rt, workers that hold the segment; 0: no such part), (the first of them, -, -, -)
 };
 
 // Bytes of the parts that `workers` can leave.
 inline size_t attention_workspace(int workers, int RB, int D) {
-  return static_cast<size_t>(workers) * (2 * RB * (static_cast<size_t>(D) * 4 + 8) + 16);
+  return static_cast<size_t>(workers) * (2 * RB * (static_cast<size_t>(D) * 4 + 8) + 64);
 }
 // Rows of a block: what one warp holds the outputs of.
 inline int attention_row_block(int rows, int D) { return rows <= 16 || D == 256 ? 16 : 32; }
@@ -332,14 +333,15 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 template <int D, bool E8, int RPW>
 struct AttnCfg {
   // Tokens of a tile: 4 or 8 KB of keys, as many as leave the accumulators their registers.
-  static constexpr int TN = D == 256 ? 16 : D == 128 ? 32 : 64;
+  // (Spilled registers would go to L2: shared memory takes the L1's room.)
+  static constexpr int TN = D == 256 ? 16 : (D == 128 ? 32 : 64) / RPW;
   static constexpr int TN_LOG2 = TN == 64 ? 6 : TN == 32 ? 5 : 4;
   static constexpr int ROWB = D * (E8 ? 1 : 2);
   static constexpr int TILEB = TN * ROWB;          // bytes of a key (or value) tile
   static constexpr bool QREG = D * RPW <= 128;     // query fragments stay in registers
   static constexpr int QB = QREG ? 0 : RPW * 16 * D * 2;  // [D / 16][RPW][32] query fragments, if not
   // seven workers where eight would have room for two pieces only
-  static constexpr int WORKERS = !QREG && !E8 ? 7 : 8;
+  static constexpr int WORKERS = D == 256 && !E8 ? 7 : 8;
   static constexpr int ROOM = (232448 - 1024) / WORKERS - QB;
   static constexpr int SLOTS = ROOM / (TILEB + 8) > 6 ? 6 : ROOM / (TILEB + 8);
   static constexpr int OFF_Q = WORKERS * SLOTS * TILEB;
@@ -432,39 +434,69 @@ struct Stream {
   static constexpr int SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
   static constexpr int CPR = Cfg::ROWB / 16, RPL = (Cfg::TN + 31) / 32, ES = E8 ? 1 : 2, RPI = 32 / CPR;
   uint32_t ring, bars;  // shared-memory addresses
-  Cursor c;             // where the next tile's page numbers come from
+  Cursor c;             // the segment of the next tile
   int k;
   bool more;            // there is such a tile
   int slot;             // of the next piece
   bool values;          // the next piece is a tile's values
   int page[RPL], place[RPL], head;  // of the tile that is copied: this lane's tokens (row copies) or boxes
-  int page2[RPL], place2[RPL], head2;  // and of the one after it, on their way
+  // Page numbers of the blocks first .. first + 31 of the sequence, a lane each,
+  // and of the 32 after them, loaded when the ones before come into use.
+  int pages, pages2, first, seq;
 
-  // Load the page numbers of the next tile; place -1: nobody sees it.
+  static __device__ __forceinline__ int block_of(const AttentionArgs& a, int j) {
+    return a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
+  }
+  __device__ __forceinline__ int load_pages(const AttentionArgs& a, int block) const {
+    const int i = block + (threadIdx.x & 31);
+    return i < a.c.max_pages ? a.c.block_table[seq * a.c.table_stride + i] : -1;
+  }
+  // Page numbers and places in their pages of the next tile's tokens or boxes;
+  // place -1: nobody sees it, page -1: outside the cache.
   __device__ __forceinline__ void find(const AttentionArgs& a) {
     const int lane = threadIdx.x & 31;
-    if (k >= c.ke) {
-      if (!c.next(a)) {
-        more = false;
-        return;
-      }
-      k = c.kb;
-    }
     const int step = a.box ? a.box : 1;                                         // tokens a lane finds the page of
     const int finders = a.box ? Cfg::TN / a.box : Cfg::TN < 32 ? Cfg::TN : 32;  // lanes that do
-    head2 = c.h;
+    head = c.h;
+    const int t0 = c.tile(k) * Cfg::TN;
 #pragma unroll
     for (int x = 0; x < RPL; ++x) {
-      const int j = c.tile(k) * Cfg::TN + lane * step + 32 * x;
-      place2[x] = -1;
-      page2[x] = 0;
-      if (lane < finders && (x == 0 || !a.box) && seen(a, c, j, step)) {
-        const int block = j / a.c.page_size;
-        place2[x] = j - block * a.c.page_size;
-        page2[x] = a.c.block_table[c.b * a.c.table_stride + block];
+      const int j = t0 + lane * step + 32 * x;
+      int block = block_of(a, j);
+      place[x] = lane < finders && (x == 0 || !a.box) && seen(a, c, j, step) ? j - block * a.c.page_size : -1;
+      if (place[x] < 0) block = INT_MAX;
+      page[x] = -1;
+      if (c.b == seq && block_of(a, t0) >= first && block_of(a, t0 + Cfg::TN - 1) < first + 32) {
+        const int got = __shfl_sync(0xffffffffu, pages, (block - first) & 31);
+        if (block != INT_MAX) page[x] = got;
+        block = INT_MAX;
+      } else
+      // the lanes' blocks ascend: a window after another until all have been met
+      for (;;) {
+        const int low = __reduce_min_sync(0xffffffffu, block);
+        if (low == INT_MAX) break;
+        if (c.b != seq || low < first || low >= first + 32) {
+          const bool follows = c.b == seq && low >= first + 32 && low < first + 64;
+          seq = c.b;
+          first = follows ? first + 32 : low;
+          pages = follows ? pages2 : load_pages(a, first);
+          pages2 = load_pages(a, first + 32);
+        }
+        const int got = __shfl_sync(0xffffffffu, pages, (block - first) & 31);
+        if (block < first + 32) {
+          page[x] = got;
+          block = INT_MAX;
+        }
+      }
+      if (place[x] >= 0 && (page[x] < 0 || page[x] >= a.c.num_pages)) {
+        bad_page();
+        page[x] = -1;
       }
     }
-    ++k;
+    if (++k >= c.ke) {
+      more = c.next(a);
+      k = c.kb;
+    }
   }
   __device__ __forceinline__ void begin(const AttentionArgs& a, const Cursor& at, uint32_t ring_addr, uint32_t bar_addr) {
     ring = ring_addr;
@@ -474,7 +506,9 @@ struct Stream {
     more = true;
     slot = 0;
     values = false;
-    find(a);
+    seq = -1;
+    first = 0;
+    pages = pages2 = -1;
   }
   // Copy the next piece into its slot (which the warp is done with).
   __device__ __forceinline__ void issue(const AttentionArgs& a, const void* kmap, const void* vmap) {
@@ -482,19 +516,7 @@ struct Stream {
     bool any = true;
     if (!values) {
       any = more;
-      if (any) {
-#pragma unroll
-        for (int x = 0; x < RPL; ++x) {
-          if (place2[x] >= 0 && (page2[x] < 0 || page2[x] >= a.c.num_pages)) {
-            bad_page();
-            page2[x] = -1;
-          }
-          page[x] = page2[x];
-          place[x] = place2[x];
-        }
-        head = head2;
-        find(a);
-      }
+      if (any) find(a);
     }
     if (any) {
       const uint32_t base = ring + slot * Cfg::TILEB;
@@ -541,6 +563,28 @@ struct Stream {
   }
 };
 
+// Rows of segments without tiles: the worker of the sequence's number writes them.
+template <int D>
+__device__ __forceinline__ void empty_rows(const AttentionArgs& a, int worker) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b = worker; b < a.B; b += a.parts) {
+    const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
+#pragma unroll 1
+    for (int rt = 0; rt < a.RT; ++rt) {
+      if (visible(a, L, m, rt).tiles != 0) continue;
+      const int r0 = rt * a.RB, rows = min(a.RB, a.M * a.G - r0), per_head = rows * (D / 8);
+#pragma unroll 1
+      for (int x = lane; x < per_head * a.c.heads; x += 32) {
+        const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = row_of(a, gr);
+        const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
+        *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
+        if (col == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
+      }
+    }
+  }
+}
+
 template <int D, bool E8, int RPW>
 __global__ void __launch_bounds__(AttnCfg<D, E8, RPW>::THREADS, 1)
 attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -559,28 +603,20 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  // rows of segments without tiles: the CTA of the sequence's number writes them
-#pragma unroll 1
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
-#pragma unroll 1
-    for (int rt = 0; rt < a.RT; ++rt) {
-      if (visible(a, L, m, rt).tiles != 0) continue;
-      const int r0 = rt * a.RB, rows = min(a.RB, a.M * a.G - r0), per_head = rows * (D / 8);
-#pragma unroll 1
-      for (int x = tid; x < per_head * a.c.heads; x += Cfg::THREADS) {
-        const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = row_of(a, gr);
-        const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
-        *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
-        if (col == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
-      }
-    }
-  }
   Cursor cc;
   int T, t0;
+  if (lane < 2) a.part_seg[(worker * 2 + lane) * 2] = make_int4(0, 0, 0, 0);
+  __syncwarp();
   if (!cc.begin(a, worker, T, t0)) {
-    if (lane == 0) a.part_seg[worker] = make_int4(0, 0, 0, 0);
+    empty_rows<D>(a, worker);
     return;
+  }
+  {
+    // the first segment's queries, on their way while the first pieces are asked for
+    const int gr = cc.rt * a.RB + lane, i = row_of(a, gr);
+    if (lane < a.RB && gr < a.M * a.G)
+      for (int x = 0; x < D; x += 64)
+        prefetch_l2(a.q + (static_cast<int64_t>(cc.b) * a.M + i) * a.q_ld + static_cast<int64_t>(cc.h * a.G + gr - i * a.G) * D + x);
   }
   const int ring_off = warp * SLOTS * Cfg::TILEB;
   const uint32_t bars = sbase + Cfg::OFF_BAR + warp * SLOTS * 8;
@@ -647,14 +683,19 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
     }
 #pragma unroll 1
     for (int k = cc.kb; k < cc.ke; ++k) {
-      wait();
       const int j0 = cc.tile(k) * NT;
       const bool full = j0 + NT - 1 <= cc.v.pos_lo &&
                         (a.window == 0 || j0 > cc.v.pos_hi - a.window || j0 + NT <= a.sinks);
-      const uint32_t kt = sbase + ring_off + slot * Cfg::TILEB;
+      float s[RPW][NT / 8][4];
+      // the tile's keys, then its values (a loop, so that the refill's code is there once)
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+      wait();
+      const int off = ring_off + slot * Cfg::TILEB;
+      const uint32_t kt = sbase + off, vt = kt;
+      if (half == 0) {
 
       // scores
-      float s[RPW][NT / 8][4];
       auto query = [&](int kk, int w, uint32_t (&f)[4]) {
         if constexpr (Cfg::QREG) {
 #pragma unroll
@@ -714,8 +755,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
         }
       }
 
-      used();
-
+      } else {
+      // Whether some row has a token of more than about 1/16 of its sum so far.
+      bool heavy = false;
+      float tile_top[RPW][2];
 #pragma unroll
       for (int w = 0; w < RPW; ++w) {
         // mask, running maximum, weights 2^(s scale - m)
@@ -737,7 +780,8 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          top = fmaxf(top * qf[w].scale[r], mx[w][r]);
+          tile_top[w][r] = top * qf[w].scale[r];
+          top = fmaxf(tile_top[w][r], mx[w][r]);
           base[r] = top == -INFINITY ? 0.f : top;
           corr[r] = ex2(mx[w][r] - base[r]);
           mx[w][r] = top;
@@ -760,11 +804,11 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             s[w][i][2 * r + 1] = ex2(s[w][i][2 * r + 1]);
             fadd2(sum[w][r][0], sum[w][r][1], s[w][i][2 * r], s[w][i][2 * r + 1]);
           }
+        // (a thread's sum is over a quarter of the columns)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) heavy |= ex2(tile_top[w][r] - base[r]) > 0.25f * (sum[w][r][0] + sum[w][r][1]);
       }
 
-      wait();
-      const int voff = ring_off + slot * Cfg::TILEB;
-      const uint32_t vt = sbase + voff;
       // A token that a row does not see meets it with weight 0, and 0 times its
       // value must be 0.  Where such a value is not finite (a later draft row's, or
       // what lies past the length), the product is taken with 0 in the place of
@@ -772,7 +816,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       // rows that see them.
       constexpr int RPI = 32 / CPR;  // rows a warp looks at at once, a chunk a lane
       auto row_bad = [&](int t) {    // some element of this lane's chunk of row t + lane / CPR is not finite
-        const uint4 u = *reinterpret_cast<const uint4*>(smem + voff + tile_at<ROWB>(t + lane / CPR, lane % CPR));
+        const uint4 u = *reinterpret_cast<const uint4*>(smem + off + tile_at<ROWB>(t + lane / CPR, lane % CPR));
         return (not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w)) != 0;
       };
       bool bad = false;
@@ -785,11 +829,12 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
         }
       }
       bad = __any_sync(0xffffffffu, bad);
-      auto values = [&](auto clean) {
-        constexpr bool kClean = decltype(clean)::value;
+      auto values = [&](auto clean, auto with_rest) {
+        constexpr bool kClean = decltype(clean)::value, kRest = decltype(with_rest)::value && !E8;
 #pragma unroll
         for (int t = 0; t < NT / 16; ++t) {
-          // fp16 holds a probability to 11 bits; bf16 to 8 only, so its rest goes in as a second operand
+          // fp16 holds a probability to 11 bits, bf16 to 8 only: where one token weighs much, its rest goes in
+          // as a second operand; else 16 and more roundings of either sign are added
           uint32_t p[RPW][4], rest[RPW][4];
 #pragma unroll
           for (int w = 0; w < RPW; ++w)
@@ -797,7 +842,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             for (int x = 0; x < 4; ++x) {
               const float lo = s[w][2 * t + (x >> 1)][2 * (x & 1)], hi = s[w][2 * t + (x >> 1)][2 * (x & 1) + 1];
               p[w][x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-              rest[w][x] = E8 ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
+              rest[w][x] = !kRest ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
             }
 #pragma unroll
           for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
@@ -811,8 +856,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
               for (int w = 0; w < RPW; ++w) {
                 mma_bf16_16816(o[w][2 * d], p[w], b[0], b[1]);
                 mma_bf16_16816(o[w][2 * d + 1], p[w], b[2], b[3]);
-                mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
-                mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
+                if (kRest) {
+                  mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
+                  mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
+                }
               }
             } else {
               // a chunk's 16 dims come in pairs: even and odd dims become one tile each
@@ -833,9 +880,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
         }
       };
       if (!bad) {
-        values(std::false_type{});
+        if (E8 || !__any_sync(0xffffffffu, heavy)) values(std::false_type{}, std::false_type{});
+        else values(std::false_type{}, std::true_type{});
       } else {
-        values(std::true_type{});
+        values(std::true_type{}, std::true_type{});
 #pragma unroll 1
         for (int t = 0; t < NT; ++t) {
           if (t % RPI == 0) bad = row_bad(t);
@@ -859,7 +907,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
           for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
             const int at = out_col<E8>(i, 0) * (E8 ? 1 : 2);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(smem + voff + tile_at<ROWB>(t, at / 16) + at % 16);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(smem + off + tile_at<ROWB>(t, at / 16) + at % 16);
             if (not_finite<E8>(u) == 0) continue;
 #pragma unroll
             for (int x = 0; x < (E8 ? 4 : 2); ++x) {
@@ -875,16 +923,19 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           }
         }
       }
+      }
       used();
+      }
     }
 
     // the end of the segment, or of this worker's share of it
     const bool whole = cc.kb == 0 && cc.ke == cc.v.tiles;
     const int64_t part = static_cast<int64_t>(worker) * 2 + (cc.kb == 0 ? 1 : 0);
-    if (cc.left == cc.ke - cc.kb && lane == 0) {  // the share's last segment: how many workers hold it, if it begins here
-      const int end = t0 + cc.it + cc.v.tiles - 1;  // its last tile then
-      a.part_seg[worker] =
-          whole || cc.kb != 0 ? make_int4(0, 0, 0, 0) : make_int4(cc.b, cc.h, cc.rt, Shares(a, T).holder(end) - worker + 1);
+    if (!whole && lane == 0) {
+      const Shares sh(a, T);
+      const int begin = t0 + cc.it - cc.kb, first = sh.holder(begin);  // the segment's first tile, and its holder
+      a.part_seg[part * 2] = make_int4(cc.b, cc.h, cc.rt, sh.holder(begin + cc.v.tiles - 1) - first + 1);
+      a.part_seg[part * 2 + 1] = make_int4(first, 0, 0, 0);
     }
 #pragma unroll
     for (int w = 0; w < RPW; ++w) {
@@ -935,95 +986,146 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
     }
   } while (cc.next(a));
   if (!a.box) cp_async_wait<0>();
+  empty_rows<D>(a, worker);
 }
 
-// Combines the parts of segments that several workers share: the one a segment
-// begins in left its place and the number of parts.  A warp takes 16 rows and
-// IW of the D / 8 output tiles of them, in the layout the parts are in.
+// Combines the parts of segments that several workers share.  A segment's
+// output is cut into items of 16 rows and two output tiles (of 8 columns, in
+// the layout the parts are in); the CTA of a part, the j-th of its segment's n,
+// takes the items j, j + n, ..  Up to eight parts are added by one warp, which
+// has an item of its own; of more, the warps share the parts of an item and are
+// added in order through shared memory.  (One warp an item for any number: 25 us
+// of the 72 us that one 65001-token row took, in 152 parts a head.)
 template <int D, bool E8>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a) {
+  constexpr int IW = 2, PER = D / 8 / IW, WARPS = kJoinThreads / 32;
+  __shared__ float4 s_v[WARPS][IW][32];
+  __shared__ float4 s_ml[WARPS][32];  // (max, sum) of the lane's two rows
   griddep_wait();
   griddep_launch_dependents();
-  constexpr int IW = 2, PER = D / 8 / IW;  // warps of 16 rows
-  const int per_part = PER * (a.RB / 16);
-  const int x = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int w0 = x / per_part, sub = x - w0 * per_part, w = sub / PER, i0 = (sub - w * PER) * IW;
-  if (w0 >= a.parts) return;
-  const int4 seg = a.part_seg[w0];
-  const int base_row = seg.z * a.RB + w * 16;
-  if (seg.w < 2 || base_row >= a.M * a.G) return;
-  const int RPW = a.RB / 16;
-  float v[IW][4] = {};
-  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
-  const int r0 = w * 16 + (lane >> 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t mine = blockIdx.x;  // a part: worker * 2 + slot
+  const int4 seg = a.part_seg[mine * 2];
+  if (seg.w < 2) return;
+  const int first = a.part_seg[mine * 2 + 1].x, nth = static_cast<int>(mine >> 1) - first;
+  const int RPW = a.RB / 16, m = new_rows(a.q_lens, seg.x, a.M);
   // the first part is its worker's second slot, the others the first
-  auto part = [&](int c) { return static_cast<int64_t>(w0 + c) * 2 + (c == 0); };
+  auto part = [&](int c) { return static_cast<int64_t>(first + c) * 2 + (c == 0); };
+  const bool solo = seg.w <= 8;
+  for (int item = solo ? nth * WARPS + warp : nth; item < RPW * PER; item += solo ? seg.w * WARPS : seg.w) {
+    const int w = item / PER, i0 = (item - w * PER) * IW;
+    const int base_row = seg.z * a.RB + w * 16;
+    if (base_row >= a.M * a.G) continue;
+    float v[IW][4] = {};
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+    const int r0 = w * 16 + (lane >> 2);
+    const int c0 = solo ? 0 : seg.w * warp / WARPS, c1 = solo ? seg.w : seg.w * (warp + 1) / WARPS;
 #pragma unroll 1
-  for (int base = 0; base < seg.w; base += 8) {
-    float2 ml[8][2];
-    float4 u[8][IW];
-    const int n = min(8, seg.w - base);
+    for (int base = c0; base < c1; base += 4) {
+      float2 ml[4][2];
+      float4 u[4][IW];
+      const int n = min(4, c1 - base);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c >= n) break;
-      const int64_t p = part(base + c);
-      ml[c][0] = a.part_ml[p * a.RB + r0];
-      ml[c][1] = a.part_ml[p * a.RB + r0 + 8];
+      for (int c = 0; c < 4; ++c) {
+        if (c >= n) break;
+        const int64_t p = part(base + c);
+        ml[c][0] = a.part_ml[p * a.RB + r0];
+        ml[c][1] = a.part_ml[p * a.RB + r0 + 8];
+#pragma unroll
+        for (int i = 0; i < IW; ++i)
+          u[c][i] = reinterpret_cast<const float4*>(a.part_o)[((p * RPW + w) * (D / 8) + i0 + i) * 32 + lane];
+      }
+      float ref[2], old[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float t = top[r];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < n) t = fmaxf(t, ml[c][r].x);
+        ref[r] = t == -INFINITY ? 0.f : t;
+        old[r] = ex2(top[r] - ref[r]);
+        top[r] = t;
+        sum[r] *= old[r];
+      }
 #pragma unroll
       for (int i = 0; i < IW; ++i)
-        u[c][i] = reinterpret_cast<const float4*>(a.part_o)[((p * RPW + w) * (D / 8) + i0 + i) * 32 + lane];
-    }
-    float t[2] = {top[0], top[1]}, old[2], ref[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int e = 0; e < 4; ++e) v[i][e] *= old[e >> 1];
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (c < n) t[r] = fmaxf(t[r], ml[c][r].x);
-      ref[r] = t[r] == -INFINITY ? 0.f : t[r];
-      old[r] = ex2(top[r] - ref[r]);
-      top[r] = t[r];
-      sum[r] *= old[r];
+      for (int c = 0; c < 4; ++c) {
+        if (c >= n) break;
+        const float f0 = ex2(ml[c][0].x - ref[0]), f1 = ex2(ml[c][1].x - ref[1]);
+        sum[0] += f0 * ml[c][0].y;
+        sum[1] += f1 * ml[c][1].y;
+#pragma unroll
+        for (int i = 0; i < IW; ++i) {
+          v[i][0] += f0 * u[c][i].x;
+          v[i][1] += f0 * u[c][i].y;
+          v[i][2] += f1 * u[c][i].z;
+          v[i][3] += f1 * u[c][i].w;
+        }
+      }
     }
+    float t[2] = {top[0], top[1]}, l[2] = {sum[0], sum[1]}, o[IW][4];
 #pragma unroll
     for (int i = 0; i < IW; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[i][e] *= old[e >> 1];
+      for (int e = 0; e < 4; ++e) o[i][e] = v[i][e];
+    if (!solo) {
+    __syncthreads();  // (of the item before: read)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c >= n) break;
-      const float f0 = ex2(ml[c][0].x - ref[0]), f1 = ex2(ml[c][1].x - ref[1]);
-      sum[0] += f0 * ml[c][0].y;
-      sum[1] += f1 * ml[c][1].y;
+    for (int i = 0; i < IW; ++i) s_v[warp][i][lane] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    s_ml[warp][lane] = make_float4(top[0], sum[0], top[1], sum[1]);
+    __syncthreads();
+    if (warp != 0) continue;
+    t[0] = t[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < IW; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float4 q[WARPS];
+#pragma unroll
+    for (int x = 0; x < WARPS; ++x) {
+      q[x] = s_ml[x][lane];
+      t[0] = fmaxf(t[0], q[x].x);
+      t[1] = fmaxf(t[1], q[x].z);
+    }
+    const float b0 = t[0] == -INFINITY ? 0.f : t[0], b1 = t[1] == -INFINITY ? 0.f : t[1];
+#pragma unroll
+    for (int x = 0; x < WARPS; ++x) {
+      const float f0 = ex2(q[x].x - b0), f1 = ex2(q[x].z - b1);
+      l[0] += f0 * q[x].y;
+      l[1] += f1 * q[x].w;
 #pragma unroll
       for (int i = 0; i < IW; ++i) {
-        v[i][0] += f0 * u[c][i].x;
-        v[i][1] += f0 * u[c][i].y;
-        v[i][2] += f1 * u[c][i].z;
-        v[i][3] += f1 * u[c][i].w;
+        const float4 u = s_v[x][i][lane];
+        o[i][0] += f0 * u.x;
+        o[i][1] += f0 * u.y;
+        o[i][2] += f1 * u.z;
+        o[i][3] += f1 * u.w;
       }
     }
-  }
-  const int m = new_rows(a.q_lens, seg.x, a.M);
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int gr = base_row + (lane >> 2) + 8 * r;
-    if (gr >= a.M * a.G) continue;
-    const int i = row_of(a, gr);
-    const bool some = i < m && sum[r] != 0.f;
-    const float f = some ? a.v_scale / sum[r] : 0.f;
-    const int64_t at = (static_cast<int64_t>(seg.x) * a.M + i) * a.Hq + seg.y * a.G + gr - i * a.G;
-    __nv_bfloat16* const to = a.out + at * D;
-    if constexpr (E8) {
-      static_assert(IW == 2, "an E4M3 cache's output tiles come in pairs");
-      uint2 p = make_uint2(0u, 0u);
-      if (some) p = make_uint2(pack_bf16(v[0][2 * r] * f, v[1][2 * r] * f), pack_bf16(v[0][2 * r + 1] * f, v[1][2 * r + 1] * f));
-      *reinterpret_cast<uint2*>(to + out_col<true>(i0, 0)) = p;
-    } else {
-#pragma unroll
-      for (int j = 0; j < IW; ++j)
-        *reinterpret_cast<uint32_t*>(to + out_col<false>(i0 + j, 0)) = some ? pack_bf16(v[j][2 * r] * f, v[j][2 * r + 1] * f) : 0u;
     }
-    if (a.lse != nullptr && i0 == 0 && (lane & 3) == 0) a.lse[at] = some ? (top[r] + log2f(sum[r])) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int gr = base_row + (lane >> 2) + 8 * r;
+      if (gr >= a.M * a.G) continue;
+      const int i = row_of(a, gr);
+      const bool some = i < m && l[r] != 0.f;
+      const float f = some ? a.v_scale / l[r] : 0.f;
+      const int64_t at = (static_cast<int64_t>(seg.x) * a.M + i) * a.Hq + seg.y * a.G + gr - i * a.G;
+      __nv_bfloat16* const to = a.out + at * D;
+      if constexpr (E8) {
+        static_assert(IW == 2, "an E4M3 cache's output tiles come in pairs");
+        uint2 p = make_uint2(0u, 0u);
+        if (some) p = make_uint2(pack_bf16(o[0][2 * r] * f, o[1][2 * r] * f), pack_bf16(o[0][2 * r + 1] * f, o[1][2 * r + 1] * f));
+        *reinterpret_cast<uint2*>(to + out_col<true>(i0, 0)) = p;
+      } else {
+#pragma unroll
+        for (int j = 0; j < IW; ++j)
+          *reinterpret_cast<uint32_t*>(to + out_col<false>(i0 + j, 0)) = some ? pack_bf16(o[j][2 * r] * f, o[j][2 * r + 1] * f) : 0u;
+      }
+      if (a.lse != nullptr && i0 == 0 && (lane & 3) == 0) a.lse[at] = some ? (t[r] + log2f(l[r])) * 0.6931471805599453f : -INFINITY;
+    }
   }
 }
 

@@ -68,9 +68,7 @@ cudaError_t launch_rows(AttentionArgs a, int ctas, const CUtensorMap& kmap, cons
   a.parts = ctas * Cfg::WORKERS;
   const cudaError_t e = launch_dependent(kern, dim3(ctas), Cfg::THREADS, Cfg::SMEM, stream, a, kmap, vmap);
   if (e != cudaSuccess) return e;
-  const int64_t warps = static_cast<int64_t>(a.parts) * (a.RB / 16) * (D / 16);
-  return launch_dependent(join_kernel<D, E8>, dim3(static_cast<unsigned>((warps * 32 + kJoinThreads - 1) / kJoinThreads)),
-                          kJoinThreads, 0, stream, a);
+  return launch_dependent(join_kernel<D, E8>, dim3(2 * a.parts), kJoinThreads, 0, stream, a);
 }
 
 template <int D>
@@ -78,6 +76,7 @@ cudaError_t launch_attention(AttentionArgs a, bool e8, int ctas, cudaStream_t st
   // TMA boxes where they divide a page; else, and for strides the TMA cannot
   // take, row by row.
   CUtensorMap kmap = {}, vmap = {};
+  a.page_log2 = (a.c.page_size & (a.c.page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(a.c.page_size)) : -1;
   a.box = a.c.page_size % 16 == 0 ? 16 : a.c.page_size % 8 == 0 ? 8 : 0;
   if (a.c.num_pages < 1) a.box = 0;
   if (a.box != 0 && (!cache_map(&kmap, a, D, e8, a.c.k, a.c.k_page, a.c.k_token, a.c.k_head) ||
