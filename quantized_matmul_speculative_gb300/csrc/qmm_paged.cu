@@ -172,8 +172,9 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.RB = attention_row_block(M * a.G, cache->head_dim);
   a.RT = (M * a.G + a.RB - 1) / a.RB;
   a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
-  // (tiles are numbered in 32 bits; they hold 16 tokens at least)
-  if (static_cast<int64_t>(B) * cache->heads * a.RT * (static_cast<int64_t>(cache->max_pages) * cache->page_size / 16 + 1) > 0x7fffffff)
+  // (places of the list of tiles are numbered in 32 bits; a tile holds 16 tokens at least)
+  if (static_cast<int64_t>(B) * cache->heads * a.RT * (static_cast<int64_t>(cache->max_pages) * cache->page_size / 16 + 1 + kLead) >
+      0x7fffffff)
     return QMM_ERR_SHAPE;
   const int ctas = device_sm_count();
   const size_t workers = static_cast<size_t>(ctas) * kMaxWorkers;

@@ -120,11 +120,18 @@ __device__ __forceinline__ Visible visible(const AttentionArgs& a, int L, int m,
   return v;
 }
 
-// Tiles of one head of sequence b, over its row blocks.
-__device__ __forceinline__ int head_tiles(const AttentionArgs& a, int b) {
+// The list counts kLead places before a segment's tiles: what its start and end
+// cost (queries, outputs), in tiles, so that shares of many short segments are
+// not longer than the others.  32 ragged sequences x 8 rows took 186, 149 and
+// 143 us with 0, 2 and 4; a single long sequence is indifferent.
+constexpr int kLead = 4;
+__device__ __forceinline__ int places(const Visible& v) { return v.tiles > 0 ? v.tiles + kLead : 0; }
+
+// Places of one head of sequence b, over its row blocks.
+__device__ __forceinline__ int head_places(const AttentionArgs& a, int b) {
   const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
   int n = 0;
-  for (int rt = 0; rt < a.RT; ++rt) n += visible(a, L, m, rt).tiles;
+  for (int rt = 0; rt < a.RT; ++rt) n += places(visible(a, L, m, rt));
   return n;
 }
 
@@ -138,8 +145,8 @@ __device__ __forceinline__ int warp_scan(int v) {
   return v;
 }
 
-// How the list of T tiles is shared: workers with a share (no more than there are
-// tiles, so that every share holds one), tiles of each, and how many of the
+// How the list of T places is shared: workers with a share (no more than there are
+// places, so that every share holds one), places of each, and how many of the
 // first ones hold one more.
 struct Shares {
   int parts, each, more;
@@ -149,7 +156,7 @@ struct Shares {
     more = T - each * parts;
   }
   __device__ __forceinline__ int begin(int c) const { return c * each + min(c, more); }
-  __device__ __forceinline__ int holder(int t) const {  // the worker whose share holds tile t
+  __device__ __forceinline__ int holder(int t) const {  // the worker whose share holds place t
     const int long_ones = more * (each + 1);
     return t < long_ones ? t / (each + 1) : more + (t - long_ones) / each;
   }
@@ -157,8 +164,7 @@ struct Shares {
 
 // A worker's share of the list, segment by segment.
 struct Cursor {
-  int left;    // tiles of the share from this segment on
-  int it;      // the share's tiles before this segment
+  int u, end;  // place of the list that this segment begins at; end of the share
   int b, h, rt;
   int kb, ke;  // tiles of the segment in this share
   int L, m;
@@ -168,32 +174,32 @@ struct Cursor {
     L = seq_length(a.c, b);
     m = new_rows(a.q_lens, b, a.M);
   }
-  // Tiles of sequence s over all heads.
-  static __device__ __forceinline__ int seq_tiles(const AttentionArgs& a, int s) {
-    return s < a.B ? head_tiles(a, s) * a.c.heads : 0;
+  // Places of sequence s over all heads.
+  static __device__ __forceinline__ int seq_places(const AttentionArgs& a, int s) {
+    return s < a.B ? head_places(a, s) * a.c.heads : 0;
   }
-  // The share of this worker (every lane of the warp calls); false: none.
-  __device__ __forceinline__ bool begin(const AttentionArgs& a, int worker, int& T, int& t0) {
+  // The first segment with tiles in this worker's share (every lane of the warp
+  // calls); false: none.  T: the list's places.
+  __device__ __forceinline__ bool begin(const AttentionArgs& a, int worker, int& T) {
     const int lane = threadIdx.x & 31;
     T = 0;
-    int n = 0;  // tiles of sequence (last base) + lane
+    int n = 0;  // places of sequence (last base) + lane
 #pragma unroll 1
     for (int base = 0; base < a.B; base += 32) {
-      n = seq_tiles(a, base + lane);
+      n = seq_places(a, base + lane);
       T += __reduce_add_sync(0xffffffffu, n);
     }
     const Shares sh(a, T);
     if (worker >= sh.parts) return false;
-    t0 = sh.begin(worker);
-    left = sh.begin(worker + 1) - t0;
-    it = 0;
+    const int start = sh.begin(worker);
+    end = sh.begin(worker + 1);
     int before = 0;
     b = 0;
 #pragma unroll 1
     for (int base = 0; base < a.B; base += 32) {
-      if (a.B > 32) n = seq_tiles(a, base + lane);
+      if (a.B > 32) n = seq_places(a, base + lane);
       const int inc = warp_scan(n);
-      const unsigned who = __ballot_sync(0xffffffffu, before + inc > t0);
+      const unsigned who = __ballot_sync(0xffffffffu, before + inc > start);
       if (who != 0) {
         const int l = __ffs(who) - 1;
         b = base + l;
@@ -203,24 +209,23 @@ struct Cursor {
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
     load(a);
-    const int per_head = max(head_tiles(a, b), 1);
-    h = (t0 - before) / per_head;
-    int r = t0 - before - h * per_head;
+    const int per_head = max(head_places(a, b), 1);
+    h = (start - before) / per_head;
+    u = before + h * per_head;
     for (rt = 0; rt < a.RT - 1; ++rt) {
       v = visible(a, L, m, rt);
-      if (r < v.tiles) break;
-      r -= v.tiles;
+      if (start < u + places(v)) break;
+      u += places(v);
     }
     v = visible(a, L, m, rt);
-    kb = r;
-    ke = min(v.tiles, kb + left);
-    return true;
+    kb = max(0, start - u - kLead);
+    ke = min(v.tiles, end - u - kLead);
+    return kb < ke || next(a);
   }
-  // The next segment; false past the last one.
+  // The next segment with tiles in the share; false: none.
   __device__ __forceinline__ bool next(const AttentionArgs& a) {
-    it += ke - kb;
-    left -= ke - kb;
-    if (left <= 0) return false;
+    u += places(v);
+    if (u + kLead >= end) return false;
     do {
       if (++rt == a.RT) {
         rt = 0;
@@ -233,7 +238,7 @@ struct Cursor {
       v = visible(a, L, m, rt);
     } while (v.tiles == 0);
     kb = 0;
-    ke = min(v.tiles, left);
+    ke = min(v.tiles, end - u - kLead);
     return true;
   }
   __device__ __forceinline__ int tile(int k) const { return k < v.sink_tiles ? k : k - v.sink_tiles + v.win_tile; }
@@ -604,10 +609,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   griddep_wait();
   griddep_launch_dependents();
   Cursor cc;
-  int T, t0;
+  int T;
   if (lane < 2) a.part_seg[(worker * 2 + lane) * 2] = make_int4(0, 0, 0, 0);
   __syncwarp();
-  if (!cc.begin(a, worker, T, t0)) {
+  if (!cc.begin(a, worker, T)) {
     empty_rows<D>(a, worker);
     return;
   }
@@ -933,7 +938,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
     const int64_t part = static_cast<int64_t>(worker) * 2 + (cc.kb == 0 ? 1 : 0);
     if (!whole && lane == 0) {
       const Shares sh(a, T);
-      const int begin = t0 + cc.it - cc.kb, first = sh.holder(begin);  // the segment's first tile, and its holder
+      const int begin = cc.u + kLead, first = sh.holder(begin);  // the segment's first tile, and its holder
       a.part_seg[part * 2] = make_int4(cc.b, cc.h, cc.rt, sh.holder(begin + cc.v.tiles - 1) - first + 1);
       a.part_seg[part * 2 + 1] = make_int4(first, 0, 0, 0);
     }
