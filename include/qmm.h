@@ -211,8 +211,9 @@ qmm_status qmm_quantize_mx(const void* X, int x_dtype, int64_t R, int64_t K, int
  * [M, K/g] and [N, K/g]; format QMM_MXFP4 or QMM_NVFP4 (QMM_MXFP8:
  * QMM_ERR_UNSUPPORTED); as qmm_quantize_mx writes them.  Products of codes and
  * scales are exact, sums fp32; Y is bf16 (round to nearest even) or fp32.  NaN
- * scales give NaN outputs.  K must be a multiple of 32; Xq and Wq are 16-byte
- * aligned.  M == 0 or N == 0 launches nothing, K == 0 fills Y with zeros.     */
+ * scales give NaN outputs.  K must be a multiple of 32, M and N at most 2^30;
+ * Xq and Wq are 16-byte aligned.  M == 0 or N == 0 launches nothing, K == 0
+ * fills Y with zeros.                                                         */
 qmm_status qmm_matmul_mx(const uint32_t* Xq, const uint8_t* x_scales, const uint32_t* Wq, const uint8_t* w_scales,
                          int M, int N, int K, int format, void* Y, int out_dtype, void* stream);
 
@@ -261,13 +262,14 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
  * i < m_b of sequence b stands at position p = lengths[b] - m_b + i and sees
  * the tokens j <= p with window == 0, or j > p - window, or j < sinks:
  *     out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k[j,h / G]) v[j,h / G],
- * G = q_heads / cache heads (a whole number).  q: bf16, row b*M + i q_ld
+ * G = q_heads / cache heads (a whole number up to 1024).  q: bf16, row b*M + i q_ld
  * elements apart, q_heads * D contiguous; out: bf16 [B, M, q_heads, D]; lse:
  * null or fp32 [B, M, q_heads], log sum_j exp(scale * q . k_j).  A row that
  * sees no token, and rows i >= m_b: out 0, lse -inf.  What a row does not see
  * never reaches it, whatever is stored there.  Scores, softmax statistics and
- * sums are fp32; probabilities enter the second product with 16 bits (two bf16
- * parts; one fp16 for an E4M3 cache).
+ * sums are fp32; probabilities enter the second product as bf16, with their
+ * rest as a second operand wherever one token weighs more than about 1/16 of
+ * its row (as fp16 for an E4M3 cache).
  * workspace: qmm_paged_attention_workspace() bytes, 16-byte aligned, not shared
  * by calls that may run at the same time; contents need no initialisation.
  * Alignment as qmm_kv_append (q and out too).                                 */
@@ -295,7 +297,7 @@ size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int h
  * row whose largest logit is not finite (-inf everywhere, or a +inf) has no
  * softmax: no draft is accepted on it and its token is its lowest argmax.
  * tokens int32 [B, k+1]: the accepted drafts, the next token, then -1;
- * accepted int32 [B]: n.  0 <= k <= 31, V >= 1.                                */
+ * accepted int32 [B]: n.  0 <= k <= 31, 1 <= V <= 2^30.                        */
 qmm_status qmm_verify_draft(const void* logits, int logits_dtype, int64_t batch_stride, int64_t row_stride,
                             const int32_t* draft_tokens, const float* draft_probs, const float* uniform,
                             const float* noise, const float* temperature, const int32_t* draft_lens, int B, int k,

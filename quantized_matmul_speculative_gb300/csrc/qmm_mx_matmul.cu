@@ -542,7 +542,7 @@ extern "C" qmm_status qmm_matmul_mx(const uint32_t* Xq, const uint8_t* x_scales,
                                     const uint8_t* w_scales, int M, int N, int K, int format, void* Y, int out_dtype,
                                     void* stream) {
   using namespace qmm;
-  if (M < 0 || N < 0 || K < 0 || K % 32 != 0) return QMM_ERR_SHAPE;
+  if (M < 0 || N < 0 || K < 0 || K % 32 != 0 || M > (1 << 30) || N > (1 << 30)) return QMM_ERR_SHAPE;
   if (format != QMM_MXFP4 && format != QMM_NVFP4) return QMM_ERR_UNSUPPORTED;
   if (out_dtype != QMM_OUT_BF16 && out_dtype != QMM_OUT_F32) return QMM_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return QMM_OK;

@@ -140,7 +140,7 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
                                void* workspace, size_t workspace_bytes, void* stream) {
   const qmm_status rc = check_cache(cache, B, M);
   if (rc != QMM_OK) return rc;
-  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || window < 0 || sinks < 0 ||
+  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || q_heads / cache->heads > 1024 || window < 0 || sinks < 0 ||
       q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)
     return QMM_ERR_SHAPE;
   if (B == 0 || M == 0) return QMM_OK;

@@ -375,7 +375,7 @@ extern "C" qmm_status qmm_verify_draft(const void* logits, int logits_dtype, int
                                        int k, int V, int32_t* tokens, int32_t* accepted, void* stream) {
   using namespace qmm;
   if (logits_dtype != QMM_OUT_BF16 && logits_dtype != QMM_OUT_F32) return QMM_ERR_UNSUPPORTED;
-  if (B < 0 || B > INT_MAX / 16 || k < 0 || k > 31 || V < 1 || row_stride < V || batch_stride < 0) return QMM_ERR_SHAPE;
+  if (B < 0 || B > INT_MAX / 16 || k < 0 || k > 31 || V < 1 || V > (1 << 30) || row_stride < V || batch_stride < 0) return QMM_ERR_SHAPE;
   if (B == 0) return QMM_OK;
   if (logits == nullptr || noise == nullptr || temperature == nullptr || tokens == nullptr || accepted == nullptr)
     return QMM_ERR_NULL;

@@ -34,7 +34,8 @@ def test_quantize(lib):
 def test_matmul(lib):
     good = dict(Xq=P, xs=P, Wq=P, ws=P, M=4, N=8, K=64, format=0, Y=P, out=0, stream=None)
     for changes, rc in (({"M": -1}, SHAPE), ({"N": -1}, SHAPE), ({"K": 40}, SHAPE), ({"format": 1}, UNSUPPORTED),
-                        ({"format": 5}, UNSUPPORTED), ({"out": 2}, UNSUPPORTED), ({"M": 0}, OK), ({"N": 0}, OK),
+                        ({"format": 5}, UNSUPPORTED), ({"out": 2}, UNSUPPORTED), ({"M": 2**30 + 1}, SHAPE),
+                        ({"N": 2**30 + 1}, SHAPE), ({"M": 0}, OK), ({"N": 0}, OK),
                         ({"Y": None}, NULL), ({"Xq": None}, NULL), ({"Wq": None}, NULL), ({"xs": None}, NULL),
                         ({"ws": None}, NULL), ({"Xq": P + 8}, ALIGN), ({"Wq": P + 4}, ALIGN), ({"Y": P + 1}, ALIGN),
                         ({"Y": P + 2, "out": 1}, ALIGN)):
@@ -77,7 +78,9 @@ def test_attention(lib):
     for changes, rc in CACHES:
         assert run(cache(**changes)) == rc, changes
     for kw, rc in ((dict(B=-1), SHAPE), (dict(M=17), SHAPE), (dict(Hq=3), SHAPE), (dict(Hq=0), SHAPE),
-                   (dict(q_ld=255), SHAPE), (dict(window=-1), SHAPE), (dict(sinks=-1), SHAPE), (dict(q=None), NULL),
+                   (dict(q_ld=255), SHAPE), (dict(window=-1), SHAPE), (dict(sinks=-1), SHAPE),
+                   (dict(Hq=4096, q_ld=2**20), SHAPE), (dict(ws=None), NULL), (dict(ws=P + 8), ALIGN),
+                   (dict(ws_bytes=1000), SHAPE), (dict(q=None), NULL),
                    (dict(out=None), NULL), (dict(q=P + 2), ALIGN), (dict(out=P + 8), ALIGN), (dict(q_ld=260), ALIGN),
                    (dict(lse=P + 2), ALIGN), (dict(q_lens=P + 2), ALIGN), (dict(B=0), OK), (dict(M=0), OK)):
         assert run(cache(), **kw) == rc, kw
@@ -87,7 +90,7 @@ def test_verify(lib):
     good = dict(logits=P, dtype=0, batch=400, row=100, d=P, q=P, u=P, e=P, T=P, lens=P, B=2, k=3, V=100, tokens=P,
                 accepted=P, stream=None)
     for changes, rc in (({"dtype": 2}, UNSUPPORTED), ({"B": -1}, SHAPE), ({"k": -1}, SHAPE), ({"k": 32}, SHAPE),
-                        ({"V": 0}, SHAPE), ({"row": 99}, SHAPE), ({"batch": -1}, SHAPE), ({"logits": None}, NULL),
+                        ({"V": 0}, SHAPE), ({"V": 2**30 + 1, "row": 2**31, "batch": 2**34}, SHAPE), ({"row": 99}, SHAPE), ({"batch": -1}, SHAPE), ({"logits": None}, NULL),
                         ({"e": None}, NULL), ({"T": None}, NULL), ({"tokens": None}, NULL), ({"accepted": None}, NULL),
                         ({"d": None}, NULL), ({"u": None}, NULL), ({"logits": P + 1}, ALIGN),
                         ({"logits": P + 2, "dtype": 1}, ALIGN), ({"q": P + 2}, ALIGN), ({"tokens": P + 2}, ALIGN),
