@@ -47,7 +47,8 @@ struct MxMatmulArgs {
   void* Y;
   int M, N, K, out_f32;
   int BN;       // rows of Y of a tile: the MMA's N, a multiple of 16, at most 256
-  int tiles_m;  // tiles along M
+  int tiles;    // of Y
+  int tiles_m;  // along M
   int ktiles;   // stages of K
   int split;    // CTAs of a cluster
   int stages;
@@ -66,7 +67,7 @@ struct GemmSmem {
     stage = x + ((BN * (kTileK / 2) + 1023) & ~1023);
     scales = stages * stage;
     bars = scales + kScaleGroups * 2 * (1 + (BN + 127) / 128) * 128 * 4 * sf_words;
-    total = bars + (2 * stages + 1) * 8 + 16;
+    total = bars + (2 * stages + 2) * 8 + 16;
   }
 };
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::l
 // 0 and their outputs not stored.
 template <int SFW, bool ALIGNED>
 struct ScaleRow {
-  static constexpr int kAhead = ALIGNED ? 4 : 2, kChunks = ALIGNED ? 1 : 2;
+  static constexpr int kAhead = 2, kChunks = ALIGNED ? 1 : 2;
   const uint8_t* next;  // the chunk to load next
   const uint8_t* begin;
   const uint8_t* end;   // of the matrix
@@ -212,42 +213,47 @@ struct ScaleRow {
 // this alone was the bound, 250 us; with one group, whose chain of load, pass,
 // store and wait takes longer than a stage's MMAs, 149 us.
 template <int SFW, bool ALIGNED, int XB>
-__device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSmem& L, unsigned char* smem, uint32_t full,
-                                             uint32_t empty, uint32_t tmem, int m0, int n0, int k_begin, int k_end) {
+struct ScaleFeed {
   using Words = typename std::conditional<SFW == 4, uint4, uint2>::type;
   using Row = ScaleRow<SFW, ALIGNED>;
-  const int r = threadIdx.x & 127, lane = r & 31, group = (threadIdx.x - 64) >> 7;
-  Words* const pass = reinterpret_cast<Words*>(smem + L.scales) + group * 2 * (1 + XB) * 128;  // [2][1 + XB][128]
-  const uint32_t columns = tmem + a.BN + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21);
-  Row sw, sx[XB];
-  sw.start(a.ws, n0 + r, a.N, a.pitch, k_begin + group, k_end);
-#pragma unroll
-  for (int b = 0; b < XB; ++b) sx[b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, k_begin + group, k_end);
+  Row rows[1 + XB];  // a weight row, activation rows
+  int flip = 0;      // place of the next stage's words
   bool ok = true;
-  auto stage = [&](auto u, int k) {
-    constexpr int U = decltype(u)::value;
+
+  // Load ahead for the tile at (m0, n0), whose first stage is the CTA's it0-th.
+  __device__ __forceinline__ void start(const MxMatmulArgs& a, int m0, int n0, int k_begin, int k_end, int it0) {
+    const int r = threadIdx.x & 127, first = k_begin + (half() ^ (it0 & 1));
+    rows[0].start(a.ws, n0 + r, a.N, a.pitch, first, k_end);
+#pragma unroll
+    for (int b = 0; b < XB; ++b) rows[1 + b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, first, k_end);
+  }
+  static __device__ __forceinline__ int half() { return (threadIdx.x - 64) >> 7; }
+
+  template <int U>
+  __device__ __forceinline__ void stage(const MxMatmulArgs& a, unsigned char* pass_all, uint32_t full, uint32_t empty,
+                                        uint32_t columns, int k, int k_end, int it) {
     if (k >= k_end) return;
-    const int it = k - k_begin, s = it % a.stages;
+    const int r = threadIdx.x & 127, lane = r & 31, s = it % a.stages;
     const int valid = a.pitch - k * (4 * SFW);
     const bool wanted = k + kScaleGroups * Row::kAhead < k_end;
     // (two places in turn: a thread that passed the barrier of its next stage has read this one's)
-    Words* const rows = pass + (U & 1) * (1 + XB) * 128;
+    Words* const pass = reinterpret_cast<Words*>(pass_all) + (half() * 2 + flip) * (1 + XB) * 128;
+    flip ^= 1;
 #pragma unroll
     for (int b = 0; b <= XB; ++b) {
       uint32_t w[SFW];
-      if (b == 0) sw.template take<U>(w, valid, wanted);
-      else sx[b > 0 ? b - 1 : 0].template take<U>(w, valid, wanted);
-      if constexpr (SFW == 4) rows[b * 128 + r] = make_uint4(w[0], w[1], w[2], w[3]);
-      else rows[b * 128 + r] = make_uint2(w[0], w[1]);
+      rows[b].template take<U>(w, valid, wanted);
+      if constexpr (SFW == 4) pass[b * 128 + r] = make_uint4(w[0], w[1], w[2], w[3]);
+      else pass[b * 128 + r] = make_uint2(w[0], w[1]);
     }
-    asm volatile("barrier.sync %0, 128;" ::"r"(1 + group) : "memory");
+    asm volatile("barrier.sync %0, 128;" ::"r"(1 + half()) : "memory");
     // columns: word w of the weights' rows (4), then word w of the activations' (4 XB)
     uint32_t v[(1 + XB) * 4 * SFW];
 #pragma unroll
     for (int b = 0; b <= XB; ++b)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const Words x = rows[b * 128 + c * 32 + lane];
+        const Words x = pass[b * 128 + c * 32 + lane];
         uint32_t w[4] = {x.x, x.y, 0, 0};
         if constexpr (SFW == 4) w[2] = x.z, w[3] = x.w;
 #pragma unroll
@@ -267,16 +273,18 @@ __device__ __forceinline__ void stage_scales(const MxMatmulArgs& a, const GemmSm
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     mbar_arrive(full + s * 8);
-  };
-  for (int k = k_begin + group; k < k_end; k += kScaleGroups * Row::kAhead) {
-    stage(std::integral_constant<int, 0>{}, k);
-    stage(std::integral_constant<int, 1>{}, k + kScaleGroups);
-    if constexpr (Row::kAhead == 4) {
-      stage(std::integral_constant<int, 2>{}, k + 2 * kScaleGroups);
-      stage(std::integral_constant<int, 3>{}, k + 3 * kScaleGroups);
+  }
+  // The tile's stages k_begin .. k_end - 1; the first is the CTA's it0-th.
+  __device__ __forceinline__ void run(const MxMatmulArgs& a, unsigned char* pass, uint32_t full, uint32_t empty, uint32_t columns,
+                                      int k_begin, int k_end, int it0) {
+    const int group = half() ^ (it0 & 1);
+    int it = it0 + group;
+    for (int k = k_begin + group; k < k_end; k += kScaleGroups * Row::kAhead, it += kScaleGroups * Row::kAhead) {
+      stage<0>(a, pass, full, empty, columns, k, k_end, it);
+      stage<1>(a, pass, full, empty, columns, k + kScaleGroups, k_end, it + kScaleGroups);
     }
   }
-}
+};
 
 // A warp's 32 accumulator lanes (columns of Y) to the rows `first` .. rows - 1
 // of Y, every second 16 of them; `y` is its lane's element of row 0.  Whole
@@ -308,13 +316,13 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
   unsigned char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
   const GemmSmem L(a.BN, a.stages, SFW);
-  const uint32_t full = sbase + L.bars, empty = full + a.stages * 8, done = empty + a.stages * 8;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L.bars + (2 * a.stages + 1) * 8);
+  // barriers: a stage is full, is empty; a tile's accumulators are done, are free
+  const uint32_t full = sbase + L.bars, empty = full + a.stages * 8, done = empty + a.stages * 8, free = done + 8;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L.bars + (2 * a.stages + 2) * 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int tile = blockIdx.x / a.split;
-  const int m0 = (tile % a.tiles_m) * a.BN, n0 = (tile / a.tiles_m) * kTileN;
-  const int k_begin = a.ktiles * rank / a.split, k_end = a.ktiles * (rank + 1) / a.split;
+  const int tile0 = blockIdx.x / a.split, tile_step = gridDim.x / a.split;
+  const int k_begin = a.ktiles * rank / a.split, k_end = a.ktiles * (rank + 1) / a.split, per_tile = k_end - k_begin;
 
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&wmap);
@@ -324,6 +332,7 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
       mbar_init(empty + s * 8, 1);
     }
     mbar_init(done, 1);
+    mbar_init(free, 128 * kScaleGroups);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -338,18 +347,24 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
   griddep_wait();
   griddep_launch_dependents();
 
-  // A wait that gave up (a status bit) skips the later ones: wrong results, no hang.
+  // Every role walks the CTA's tiles with a running count of stages, so that the
+  // copies for the next tile go on while the last one's outputs are written.  A
+  // wait that gave up (a status bit) skips the later ones: wrong results, no hang.
   if (warp == 0) {
     if (lane == 0) {
       bool lost = false;
       const uint32_t bytes = kCodesW + a.BN * (kTileK / 2);
-      for (int k = k_begin; k < k_end; ++k) {
-        const int it = k - k_begin, s = it % a.stages;
-        if (it >= a.stages && !lost) lost = !mbar_wait(empty + s * 8, ((it / a.stages) & 1) ^ 1, kStatusTimeoutEmpty);
-        if (lost) break;
-        mbar_arrive_expect_tx(full + s * 8, bytes);
-        tma_load_2d(sbase + s * L.stage, &wmap, k * (kTileK / 2), n0, full + s * 8);
-        tma_load_2d(sbase + s * L.stage + L.x, &xmap, k * (kTileK / 2), m0, full + s * 8);
+      int it = 0;
+      for (int tile = tile0; tile < a.tiles && !lost; tile += tile_step) {
+        const int m0 = (tile % a.tiles_m) * a.BN, n0 = (tile / a.tiles_m) * kTileN;
+        for (int k = k_begin; k < k_end; ++k, ++it) {
+          const int s = it % a.stages;
+          if (it >= a.stages) lost = !mbar_wait(empty + s * 8, ((it / a.stages) & 1) ^ 1, kStatusTimeoutEmpty);
+          if (lost) break;
+          mbar_arrive_expect_tx(full + s * 8, bytes);
+          tma_load_2d(sbase + s * L.stage, &wmap, k * (kTileK / 2), n0, full + s * 8);
+          tma_load_2d(sbase + s * L.stage + L.x, &xmap, k * (kTileK / 2), m0, full + s * 8);
+        }
       }
     }
   } else if (warp == 1) {
@@ -357,51 +372,70 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
       bool lost = false;
       const uint32_t idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a.BN >> 3) << 17) | (NV ? 0u : 1u << 23) |
                              (static_cast<uint32_t>(kTileN >> 4) << 24);
-      for (int k = k_begin; k < k_end; ++k) {
-        const int it = k - k_begin, s = it % a.stages;
-        if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull);
+      int it = 0, turn = 0;
+      for (int tile = tile0; tile < a.tiles; tile += tile_step, ++turn) {
+        if (turn > 0 && !lost) lost = !mbar_wait(free, (turn - 1) & 1, kStatusTimeoutEmpty);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t base = sbase + s * L.stage;
-        const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + XB)), sfx = sfw + SFW * 4;
-        const uint64_t da = smem_desc(base, 1024, kSwizzle128), db = smem_desc(base + L.x, 1024, kSwizzle128);
+        for (int k = k_begin; k < k_end; ++k, ++it) {
+          const int s = it % a.stages;
+          if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t base = sbase + s * L.stage;
+          const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + XB)), sfx = sfw + SFW * 4;
+          const uint64_t da = smem_desc(base, 1024, kSwizzle128), db = smem_desc(base + L.x, 1024, kSwizzle128);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // nvfp4: a word of scales for 64 codes; mxfp4: its lower, then its upper half
-          const int w = NV ? j : j >> 1;
-          const uint32_t id = NV ? 0u : (j & 1) * 2u;
-          mma_block_scaled<NV>(tmem, da + j * 2, db + j * 2, idesc | (id << 4) | (id << 29), sfw + w * 4, sfx + w * XB * 4,
-                               it > 0 || j > 0);
+          for (int j = 0; j < 4; ++j) {
+            // nvfp4: a word of scales for 64 codes; mxfp4: its lower, then its upper half
+            const int w = NV ? j : j >> 1;
+            const uint32_t id = NV ? 0u : (j & 1) * 2u;
+            mma_block_scaled<NV>(tmem, da + j * 2, db + j * 2, idesc | (id << 4) | (id << 29), sfw + w * 4, sfx + w * XB * 4,
+                                 k > k_begin || j > 0);
+          }
+          mma_commit(empty + s * 8);
         }
-        mma_commit(empty + s * 8);
+        mma_commit(done);
       }
-      mma_commit(done);
     }
   } else {
-    if (a.aligned) stage_scales<SFW, true, XB>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-    else stage_scales<SFW, false, XB>(a, L, smem, full, empty, tmem, m0, n0, k_begin, k_end);
-    mbar_wait(done, 0, kStatusTimeoutDrain);
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const int q = warp & 3;
-    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    const int n = n0 + q * 32 + lane;
-    const int first = 16 * ((threadIdx.x - 64) >> 7);  // the groups take 16 rows in turn
-    if (a.split > 1) {
-      float* part = reinterpret_cast<float*>(smem) + first * kTileN + q * 32 + lane;  // [BN][128], over the stages
-      for (int c = first; c < a.BN; c += 16 * kScaleGroups, part += 16 * kScaleGroups * kTileN) {
-        uint32_t v[16];
-        tmem_load16(v, acc + c);
-        tmem_wait_load();
+    // scales of a tile, the first ones of the next already asked for, then the tile's outputs
+    auto feed = [&](auto aligned) {
+      ScaleFeed<SFW, decltype(aligned)::value, XB> scales;
+      const uint32_t quarter = static_cast<uint32_t>(warp & 3) << 21;
+      unsigned char* const pass = smem + L.scales;
+      int it = 0, turn = 0;
+      bool lost = false;
+      scales.start(a, (tile0 % a.tiles_m) * a.BN, (tile0 / a.tiles_m) * kTileN, k_begin, k_end, it);
+      for (int tile = tile0; tile < a.tiles; tile += tile_step, ++turn) {
+        const int m0 = (tile % a.tiles_m) * a.BN, n = (tile / a.tiles_m) * kTileN + (warp & 3) * 32 + lane;
+        scales.run(a, pass, full, empty, tmem + a.BN + quarter, k_begin, k_end, it);
+        it += per_tile;
+        const int after = tile + tile_step;
+        if (after < a.tiles) scales.start(a, (after % a.tiles_m) * a.BN, (after / a.tiles_m) * kTileN, k_begin, k_end, it);
+        if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(done, turn & 1, kStatusTimeoutDrain));
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t acc = tmem + quarter;
+        const int first = 16 * scales.half(), rows = min(a.BN, a.M - m0);  // the groups take 16 rows in turn
+        const int64_t at = static_cast<int64_t>(m0) * a.N + n;
+        if (a.split > 1) {  // (one tile a CTA)
+          float* part = reinterpret_cast<float*>(smem) + first * kTileN + (warp & 3) * 32 + lane;  // [BN][128], over the stages
+          for (int c = first; c < a.BN; c += 16 * kScaleGroups, part += 16 * kScaleGroups * kTileN) {
+            uint32_t v[16];
+            tmem_load16(v, acc + c);
+            tmem_wait_load();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[i * kTileN] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) part[i * kTileN] = __uint_as_float(v[i]);
+          }
+        } else if (a.out_f32) {
+          store_tile<float>(acc, static_cast<float*>(a.Y) + at, a.N, first, rows, n < a.N);
+        } else {
+          store_tile<__nv_bfloat16>(acc, static_cast<__nv_bfloat16*>(a.Y) + at, a.N, first, rows, n < a.N);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        mbar_arrive(free);
       }
-    } else if (a.out_f32) {
-      store_tile<float>(acc, static_cast<float*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N, first,
-                        min(a.BN, a.M - m0), n < a.N);
-    } else {
-      store_tile<__nv_bfloat16>(acc, static_cast<__nv_bfloat16*>(a.Y) + static_cast<int64_t>(m0) * a.N + n, a.N,
-                                first, min(a.BN, a.M - m0), n < a.N);
-    }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    };
+    if (a.aligned) feed(std::true_type{});
+    else feed(std::false_type{});
   }
   __syncwarp();
   __syncthreads();
@@ -411,6 +445,7 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
   if (a.split > 1) {
     // the cluster's partial tiles, added in rank order; each CTA writes its share of the rows
     cluster_sync_all();
+    const int m0 = (tile0 % a.tiles_m) * a.BN, n0 = (tile0 / a.tiles_m) * kTileN;
     const int rows = min(a.BN, a.M - m0);
     const int r0 = rows * rank / a.split, r1 = rows * (rank + 1) / a.split;
     for (int x = threadIdx.x; x < (r1 - r0) * kTileN; x += kGemmThreads) {
@@ -486,8 +521,12 @@ cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cud
               ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & (4 * SFW - 1)) == 0;
   plan(a, device_sm_count());
   a.tiles_m = (a.M + a.BN - 1) / a.BN;
-  const int64_t ctas = static_cast<int64_t>((a.N + kTileN - 1) / kTileN) * a.tiles_m * a.split;
-  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>((a.N + kTileN - 1) / kTileN) * a.tiles_m;
+  if (tiles > INT_MAX / 8) return cudaErrorInvalidValue;
+  a.tiles = static_cast<int>(tiles);
+  // as many CTAs as the SMs hold, each with every so manieth tile; a cluster that shares K has one
+  const int per_sm = a.BN <= 32 ? 2 : 1;
+  const int64_t ctas = a.split > 1 ? tiles * a.split : std::min<int64_t>(tiles, static_cast<int64_t>(per_sm) * device_sm_count());
   // Two CTAs an SM up to 32 rows, else one; stages as shared memory and the
   // tensor memory's columns (accumulators, then each stage's scales) allow.
   const int budget = a.BN <= 32 ? 113 * 1024 : 227 * 1024, cols = a.BN <= 32 ? 256 : 512;
