@@ -322,53 +322,30 @@ def small_m(x, wq, scales, biases, bits: int, group_size: int, out=None, out_dty
 
 
 # ------------------------------------------------- the operators around the product
-# A call of these takes microseconds on the GPU, so the checks below are written
-# for their cost: integers for devices, one comparison per property.
-def _index(t, name: str) -> int:
-    i = t.get_device()
-    if i < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return i
+# A call of these takes microseconds on the GPU, so their tensors are checked and
+# allocated by the native module (csrc/qmm_torch.cpp).
+@functools.lru_cache(maxsize=1)
+def _native():
+    import torch  # noqa: F401  (loads the libraries that the module links)
+
+    lib()
+    try:
+        from . import _qmm_torch
+    except ImportError as e:
+        raise RuntimeError("_qmm_torch.so is not built; run __graft_entry__.build() "
+                           "or quantized_matmul_speculative_gb300/build.py") from e
+    return _qmm_torch
 
 
-def _same_device(index: int, *tensors):
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"all tensors must be on CUDA device {index}")
+def _handle(stream):
+    """cudaStream_t of a stream (a torch stream or an integer) or None."""
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
-def _launch_on(stream, index: int):
-    """(cudaStream_t as int, the stream to record new tensors on or None) of a
-    call.  Outputs and workspaces are allocated on the current stream; a call
-    that runs on another one has them recorded there, so that their memory is
-    not handed out again before the call is done."""
-    import torch
-
-    if torch._C._cuda_getDevice() != index:
-        raise ValueError(f"the current CUDA device must be the tensors' device {index}")
-    current = torch._C._cuda_getCurrentRawStream(index)
-    if stream is None:
-        return current, None
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == current:
-        return handle, None
-    return handle, stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=index)
-
-
-def _new(like, shape, dtype, record):
-    import torch
-
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if record is not None:
-        # the caching allocator may have handed out memory that the current
-        # stream still works on: the call's stream waits for it
-        record.wait_stream(torch.cuda.current_stream(t.device))
-        t.record_stream(record)
-    return t
-
-
-def _is(t, dtype, shape) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+def _result(r, where: str):
+    if type(r) is int:
+        _check(r, where)
+    return r
 
 
 def quantize_mx(x, fmt: str, values=None, out=None, stream=None):
@@ -376,37 +353,9 @@ def quantize_mx(x, fmt: str, values=None, out=None, stream=None):
     be strided), formats as :func:`small_m_mx`: returns (codes int32
     [R, K*bits/32], scales uint8 [R, K/g]), into ``out`` if given.  ``values``:
     an optional bf16 [R, K] tensor that receives what the codes stand for."""
-    import torch
-
     f, bits, g = MX_FORMATS[fmt]
-    f32 = x.dtype is torch.float32
-    if x.dim() != 2 or not (f32 or x.dtype is torch.bfloat16):
-        raise TypeError("x must be a bfloat16 or float32 matrix")
-    R, K = x.shape
-    index = _index(x, "x")
-    if K % 32 != 0:
-        raise ValueError("K must be a multiple of 32")
-    ld, one = x.stride()
-    if R <= 1:
-        ld = K
-    if K > 1 and one != 1 or ld < K:
-        raise ValueError("the elements of a row of x must be contiguous, and its rows apart")
-    if values is not None and (not _is(values, torch.bfloat16, x.shape) or values.get_device() != index):
-        raise ValueError("values must be a contiguous bfloat16 tensor of x's shape, on its device")
-    handle, record = _launch_on(stream, index)
-    if out is None:
-        codes = _new(x, (R, K * bits // 32), torch.int32, record)
-        scales = _new(x, (R, K // g), torch.uint8, record)
-    else:
-        codes, scales = out
-        _same_device(index, codes, scales)
-        if not _is(codes, torch.int32, (R, K * bits // 32)) or not _is(scales, torch.uint8, (R, K // g)):
-            raise ValueError("out must be contiguous (int32 [R, K*bits/32], uint8 [R, K/g])")
-    rc = lib().qmm_quantize_mx(x.data_ptr(), OUT_F32 if f32 else OUT_BF16, R, K, ld, f, codes.data_ptr(),
-                               scales.data_ptr(), None if values is None else values.data_ptr(), handle)
-    if rc != 0:
-        _check(rc, "qmm_quantize_mx")
-    return codes, scales
+    codes, scales = (None, None) if out is None else out
+    return _result(_native().quantize_mx(x, f, bits, g, values, codes, scales, _handle(stream)), "qmm_quantize_mx")
 
 
 def matmul_mx(xq, x_scales, wq, w_scales, fmt: str, out=None, out_dtype=None, stream=None):
@@ -417,72 +366,12 @@ def matmul_mx(xq, x_scales, wq, w_scales, fmt: str, out=None, out_dtype=None, st
     f, bits, g = MX_FORMATS[fmt]
     if bits != 4:
         raise ValueError("matmul_mx takes the 4-bit formats")
-    if xq.dim() != 2 or wq.dim() != 2:
-        raise ValueError("codes must be matrices")
-    index = _index(xq, "xq")
-    _same_device(index, x_scales, wq, w_scales, out)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     f32 = out_dtype is torch.float32
     if not (f32 or out_dtype is torch.bfloat16):
         raise TypeError("out dtype must be bfloat16 or float32")
-    M, words = xq.shape
-    N, K = wq.shape[0], words * 8
-    if not (_is(xq, torch.int32, (M, words)) and _is(wq, torch.int32, (N, words))):
-        raise ValueError("xq and wq must be contiguous int32 [M, K/8] and [N, K/8]")
-    if not (_is(x_scales, torch.uint8, (M, K // g)) and _is(w_scales, torch.uint8, (N, K // g))):
-        raise ValueError("x_scales and w_scales must be contiguous uint8 [M, K/g] and [N, K/g]")
-    handle, record = _launch_on(stream, index)
-    if out is None:
-        out = _new(xq, (M, N), out_dtype, record)
-    elif not _is(out, out_dtype, (M, N)):
-        raise ValueError("out must be a contiguous [M, N] tensor of out_dtype")
-    rc = lib().qmm_matmul_mx(xq.data_ptr(), x_scales.data_ptr(), wq.data_ptr(), w_scales.data_ptr(), M, N, K, f,
-                             out.data_ptr(), OUT_F32 if f32 else OUT_BF16, handle)
-    if rc != 0:
-        _check(rc, "qmm_matmul_mx")
-    return out
-
-
-def _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B):
-    import torch
-
-    _same_device(index, k_cache, v_cache, block_table, lengths, q_lens)
-    dtype = k_cache.dtype
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or v_cache.dtype is not dtype:
-        raise ValueError("k_cache and v_cache must be [pages, page_size, heads, D] of one shape and dtype")
-    if not (dtype is torch.bfloat16 or dtype is torch.float8_e4m3fn):
-        raise TypeError("the cache must be bfloat16 or float8_e4m3fn")
-    k_page, k_token, k_head, k_one = k_cache.stride()
-    v_page, v_token, v_head, v_one = v_cache.stride()
-    if k_one != 1 or v_one != 1:
-        raise ValueError("the D elements of a head must be contiguous")
-    rows, width = block_table.shape
-    ld, one = block_table.stride()
-    if rows != B or block_table.dtype is not torch.int32 or (width > 1 and one != 1):
-        raise ValueError("block_table must be int32 [B, max_pages] with contiguous rows")
-    if not _is(lengths, torch.int32, (B,)):
-        raise ValueError("lengths must be contiguous int32 [B]")
-    if q_lens is not None and not _is(q_lens, torch.int32, (B,)):
-        raise ValueError("q_lens must be contiguous int32 [B]")
-    pages, page_size, heads, D = k_cache.shape
-    return PagedCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), k_page, k_token, k_head, v_page, v_token, v_head,
-                            block_table.data_ptr(), lengths.data_ptr(), ld if B > 1 else width, pages, width, page_size,
-                            heads, D, 0 if dtype is torch.bfloat16 else 1, k_scale, v_scale)
-
-
-def _rows(t, B, M, heads, D, name):
-    """Distance of the [B, M] rows of ``t`` [B, M, heads, D] (one distance for
-    all; a row's elements are contiguous)."""
-    import torch
-
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
-    s0, s1, s2, s3 = t.stride()
-    ld = s1 if M > 1 else s0 if B > 1 else heads * D
-    if (D > 1 and s3 != 1) or (heads > 1 and s2 != D) or (B > 1 and M > 1 and s0 != M * ld):
-        raise ValueError(f"{name}: the heads of a row must be contiguous and its rows evenly apart")
-    return ld
+    return _result(_native().matmul_mx(xq, x_scales, wq, w_scales, f, g, out, f32, _handle(stream)), "qmm_matmul_mx")
 
 
 def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None, k_scale: float = 1.0,
@@ -496,20 +385,8 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None,
     each sequence with its new rows; ``q_lens``: int32 [B], new rows of each
     sequence (None: M).  Row i of sequence b goes to position
     lengths[b] - q_lens[b] + i.  E4M3 elements hold x / scale."""
-    if k_new.dim() != 4 or k_new.shape != v_new.shape:
-        raise ValueError("k_new and v_new must be [B, M, heads, D] of one shape")
-    B, M, heads, D = k_new.shape
-    index = _index(k_new, "k_new")
-    _same_device(index, v_new)
-    cache = _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B)
-    if heads != cache.heads or D != cache.head_dim:
-        raise ValueError("k_new and the cache must have the same heads and D")
-    k_ld, v_ld = _rows(k_new, B, M, heads, D, "k_new"), _rows(v_new, B, M, heads, D, "v_new")
-    handle, _ = _launch_on(stream, index)
-    rc = lib().qmm_kv_append(ctypes.byref(cache), k_new.data_ptr(), k_ld, v_new.data_ptr(), v_ld, B, M,
-                             None if q_lens is None else q_lens.data_ptr(), handle)
-    if rc != 0:
-        _check(rc, "qmm_kv_append")
+    _result(_native().kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale,
+                                _handle(stream)), "qmm_kv_append")
 
 
 @functools.lru_cache(maxsize=256)
@@ -531,34 +408,9 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens=None, scal
     ``return_lse`` also the fp32 [B, M, q_heads] log-sum-exp of the scaled
     scores (-inf, and 0 in ``out``, for rows that see nothing).  ``workspace``:
     a uint8 tensor of :func:`paged_attention_workspace` bytes to reuse."""
-    import torch
-
-    if q.dim() != 4:
-        raise ValueError("q must be [B, M, q_heads, D]")
-    B, M, Hq, D = q.shape
-    index = _index(q, "q")
-    _same_device(index, out, workspace)
-    cache = _paged_cache(index, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, B)
-    if D != cache.head_dim:
-        raise ValueError("q and the cache must have the same D")
-    q_ld = _rows(q, B, M, Hq, D, "q")
-    handle, record = _launch_on(stream, index)
-    if out is None:
-        out = _new(q, (B, M, Hq, D), torch.bfloat16, record)
-    elif not _is(out, torch.bfloat16, (B, M, Hq, D)):
-        raise ValueError("out must be a contiguous bfloat16 tensor of q's shape")
-    lse = _new(q, (B, M, Hq), torch.float32, record) if return_lse else None
-    if workspace is None:
-        workspace = _new(q, (paged_attention_workspace(B, M, Hq, cache.heads, D),), torch.uint8, record)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    rc = lib().qmm_paged_attention(ctypes.byref(cache), q.data_ptr(), q_ld, B, M, Hq,
-                                   None if q_lens is None else q_lens.data_ptr(), D ** -0.5 if scale is None else scale,
-                                   window, sinks, out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel(), handle)
-    if rc != 0:
-        _check(rc, "qmm_paged_attention")
-    return (out, lse) if return_lse else out
+    return _result(_native().paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, scale,
+                                             window, sinks, out, return_lse, workspace, _handle(stream)),
+                   "qmm_paged_attention")
 
 
 def verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens=None, stream=None):
@@ -571,37 +423,5 @@ def verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature,
     ``temperature``: fp32 [B], 0 for greedy; ``draft_lens``: int32 [B] or None.
     Returns (tokens int32 [B, k+1]: the accepted drafts, the next token, then
     -1; accepted int32 [B])."""
-    import torch
-
-    if logits.dim() != 3 or logits.shape[1] < 1 or logits.shape[2] < 1:
-        raise ValueError("logits must be [B, k+1, V]")
-    f32 = logits.dtype is torch.float32
-    if not (f32 or logits.dtype is torch.bfloat16):
-        raise TypeError("logits must be bfloat16 or float32")
-    B, rows, V = logits.shape
-    k = rows - 1
-    index = _index(logits, "logits")
-    _same_device(index, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens)
-    s_batch, s_row, one = logits.stride()
-    if V > 1 and one != 1:
-        raise ValueError("the elements of a row of logits must be contiguous")
-    if not (_is(draft_tokens, torch.int32, (B, k)) and _is(uniform, torch.float32, (B, k))):
-        raise ValueError("draft_tokens and uniform must be contiguous int32 and float32 [B, k]")
-    if not (_is(noise, torch.float32, (B, V)) and _is(temperature, torch.float32, (B,))):
-        raise ValueError("noise and temperature must be contiguous float32 [B, V] and [B]")
-    if draft_probs is not None and not _is(draft_probs, torch.float32, (B, k, V)):
-        raise ValueError("draft_probs must be contiguous float32 [B, k, V]")
-    if draft_lens is not None and not _is(draft_lens, torch.int32, (B,)):
-        raise ValueError("draft_lens must be contiguous int32 [B]")
-    handle, record = _launch_on(stream, index)
-    tokens = _new(logits, (B, rows), torch.int32, record)
-    accepted = _new(logits, (B,), torch.int32, record)
-    rc = lib().qmm_verify_draft(logits.data_ptr(), OUT_F32 if f32 else OUT_BF16, s_batch if B > 1 else rows * V,
-                                s_row if rows > 1 else V, draft_tokens.data_ptr(),
-                                None if draft_probs is None else draft_probs.data_ptr(), uniform.data_ptr(),
-                                noise.data_ptr(), temperature.data_ptr(),
-                                None if draft_lens is None else draft_lens.data_ptr(), B, k, V, tokens.data_ptr(),
-                                accepted.data_ptr(), handle)
-    if rc != 0:
-        _check(rc, "qmm_verify_draft")
-    return tokens, accepted
+    return _result(_native().verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens,
+                                          _handle(stream)), "qmm_verify_draft")

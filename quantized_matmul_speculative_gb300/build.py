@@ -1,4 +1,5 @@
-"""Build libqmm.so (all CUDA kernels and the C ABI) for sm_103a with nvcc.
+"""Build libqmm.so (all CUDA kernels and the C ABI) for sm_103a with nvcc, and
+_qmm_torch.so (the native half of the binding for the operators around the product) with g++.
 
 Each (bits, group size) instantiation of the tensor-core kernels is its own
 translation unit; they compile in parallel.  Objects go to ``_build/`` and the
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -20,6 +22,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = ROOT / "_build"
 LIBRARY = PKG / "libqmm.so"
+MODULE = PKG / "_qmm_torch.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -51,15 +54,32 @@ def units():
 
 def _inputs():
     files = list(CSRC.glob("*.cu")) + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + list(CSRC.glob("*.inc"))
+    files += list(CSRC.glob("*.cpp"))
     files += list(INCLUDE.glob("*.h")) + [Path(__file__)]
     return files
 
 
 def up_to_date() -> bool:
-    if not LIBRARY.exists():
+    if not LIBRARY.exists() or not MODULE.exists():
         return False
-    lib_t = LIBRARY.stat().st_mtime
+    lib_t = min(LIBRARY.stat().st_mtime, MODULE.stat().st_mtime)
     return all(f.stat().st_mtime <= lib_t for f in _inputs())
+
+
+def _torch_paths():
+    import torch
+
+    root = Path(torch.__file__).resolve().parent
+    include = [root / "include", root / "include/torch/csrc/api/include", sysconfig.get_paths()["include"],
+               Path(nvcc()).resolve().parent.parent / "include", INCLUDE]
+    return [f"-I{p}" for p in include], root / "lib"
+
+
+def _run(cmd, what: str):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stderr}")
+    return res.stderr
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> Path:
@@ -73,23 +93,32 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra, "-c", str(src), "-o", str(obj)]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {obj.name}:\n{res.stderr}")
-        return obj, res.stderr
+        return obj, _run(cmd, f"nvcc for {obj.name}")
+
+    def compile_module():
+        flags, _ = _torch_paths()
+        obj = BUILD / "qmm_torch.o"
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", str(CSRC / "qmm_torch.cpp"), "-o", str(obj)],
+             f"g++ for {obj.name}")
+        return obj
 
     jobs = jobs or min(len(units()), os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        module = ex.submit(compile_module)
         results = list(ex.map(compile_one, units()))
+        module_object = module.result()
     if verbose:
         for obj, log in results:
             print(f"== {obj.name}\n{log}", file=sys.stderr)
     tmp = LIBRARY.with_name(f"libqmm.{os.getpid()}.tmp.so")
     cmd = [cc, *ARCH, "-shared", "-o", str(tmp), *[str(o) for o, _ in results]]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
+    _run(cmd, "link")
     os.replace(tmp, LIBRARY)
+    _, torch_lib = _torch_paths()
+    tmp = MODULE.with_name(f"_qmm_torch.{os.getpid()}.tmp.so")
+    _run(["g++", "-shared", "-o", str(tmp), str(module_object), f"-L{PKG}", "-lqmm", f"-L{torch_lib}", "-ltorch_python",
+          "-ltorch_cuda", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "module link")
+    os.replace(tmp, MODULE)
     return LIBRARY
 
 
