@@ -43,13 +43,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
-// (m, s) and (m2, s2): maxima and sums of 2^((x - max) c); joined.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
-  const float t = fmaxf(m, m2), b = base_of(t);
-  s = s * ex2((m - b) * c) + s2 * ex2((m2 - b) * c);
-  m = t;
+// The whole 16-byte blocks of [p, p + bytes), or of its first MB, on their way to L2.
+__device__ __forceinline__ void prefetch_l2_range(const void* p, int64_t bytes) {
+  const uintptr_t from = (reinterpret_cast<uintptr_t>(p) + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t to = (reinterpret_cast<uintptr_t>(p) + bytes) & ~static_cast<uintptr_t>(15);
+  if (from < to)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(to - from < (1 << 20) ? to - from : 1 << 20)) : "memory");
 }
-
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxRows = 32, kMaxCluster = 16;
 
@@ -58,6 +58,22 @@ struct Partial {
   float s;  // sum of exponentials relative to it (greedy: unused)
   int at;   // its lowest index (greedy)
 };
+
+// The lanes' partials joined, in every lane: the best of greedy ones, else the
+// largest maximum and the sum relative to it.
+__device__ __forceinline__ void warp_join(Partial& p, bool greedy, float c) {
+  if (greedy) {
+    warp_best(p.m, p.at);
+    return;
+  }
+  float t = p.m;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+  p.s *= ex2((p.m - base_of(t)) * c);
+  p.m = t;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) p.s += __shfl_xor_sync(0xffffffffu, p.s, d);
+}
 
 __device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
   return __float_as_int(ld_dsmem_f32(reinterpret_cast<const float*>(p), rank));
@@ -75,7 +91,12 @@ __device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
 // What bounds it: the bytes of the rows read, where there are many sequences
 // (rounds of one row, several clusters an SM so that one's exchange overlaps
 // another's reads); the latency of its two exchanges, where there are few (all
-// rows in one round).
+// rows in one round).  The noise is fetched into L2 meanwhile (fetching the next
+// row too gains nothing).  Nothing may spill: a thread, not a warp, that joined
+// a row's partials cost 6 us more, 8 elements at a time, not 4, of the last pass
+// 10 us.  64 sequences x 5
+// drafts x 128000 fp32 logits: 66 us, 4.0 TB/s of what it would read were no
+// draft refused; 1 x 7 x 32000 bf16: 10.1 us.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   using T = typename std::conditional<F32, float, uint16_t>::type;
@@ -112,6 +133,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     if (my_d >= 0 && a.q != nullptr) my_q = a.q[at * a.V + my_d];
   }
 
+  // this CTA's elements of the pass for the next token
+  const int i0 = static_cast<int>(static_cast<int64_t>(a.V) * rank / C), i1 = static_cast<int>(static_cast<int64_t>(a.V) * (rank + 1) / C);
+  const float* const e = a.noise + static_cast<int64_t>(b) * a.V;
+  if (!greedy && tid == 0) prefetch_l2_range(e + i0, static_cast<int64_t>(i1 - i0) * 4);
+
   int n = 0;  // accepted drafts
   for (int r0 = 0, parity = 0;; r0 += a.round, parity ^= 1) {
     const int r1 = min(r0 + a.round, drafts + 1);
@@ -141,11 +167,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         }
       };
       // U vectors at a time: their maximum first, so that a thread's sum is rescaled at most once for all
+      constexpr int U = 16 / VEC;
       auto take = [&](const uint4* w, int count, int first) {
-        float f[4][VEC];
+        float f[U][VEC];
         float top = m;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < U; ++j) {
           if (j < count) unpack(w[j], f[j]);
 #pragma unroll
           for (int i = 0; i < VEC; ++i) {
@@ -159,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         s *= ex2((m - base) * c);
         m = top;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < U; ++j)
 #pragma unroll
           for (int i = 0; i < VEC; ++i) s += ex2((f[j][i] - base) * c);
       };
@@ -168,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         uint4 w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = __ldg(xv + v + j * threads);
-        take(w, 4, v);
+#pragma unroll
+        for (int j = 0; j < 4; j += U) take(w + j, U, v + j * threads);
       }
       if (v < v1) {
         uint4 w[4];
@@ -179,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
             w[j] = __ldg(xv + v + j * threads);
             count = j + 1;
           }
-        take(w, count, v);
+#pragma unroll
+        for (int j = 0; j < 4; j += U) take(w + j, count - j, v + j * threads);
       }
       if (rank == 0) {
         auto one = [&](int i) {
@@ -195,55 +224,31 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
         if (t_row < head) one(t_row);
         if (tail + t_row < a.V && t_row < VEC) one(tail + t_row);
       }
-      if (greedy) {
-        warp_best(m, at);
-      } else {
-        const float t = [&] {
-          float u = m;
-#pragma unroll
-          for (int d = 16; d > 0; d /= 2) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, d));
-          return u;
-        }();
-        s *= ex2((m - base_of(t)) * c);
-        m = t;
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-      }
-      if (lane == 0) warp_part[r - r0][warp & (per - 1)] = Partial{m, s, at};
+      Partial p{m, s, at};
+      warp_join(p, greedy, c);
+      if (lane == 0) warp_part[r - r0][warp & (per - 1)] = p;
     }
     if (r0 == 0 && tid < drafts) s_d[tid] = my_d, s_u[tid] = my_u, s_xd[tid] = my_x, s_qd[tid] = my_q;
     __syncthreads();
-    // a thread joins a row's warps, in order
-    if (tid < r1 - r0) {
-      Partial p = warp_part[tid][0];
-#pragma unroll 4
-      for (int w = 1; w < per; ++w) {
-        const Partial o = warp_part[tid][w];
-        if (greedy) best_of(p.m, p.at, o.m, o.at);
-        else join(p.m, p.s, o.m, o.s, c);
-      }
-      part[parity][tid] = p;
+    // a warp joins a row's warps
+    for (int i = warp; i < r1 - r0; i += kWarps) {
+      Partial p = lane < per ? warp_part[i][lane] : Partial{-INFINITY, 0.f, INT_MAX};
+      warp_join(p, greedy, c);
+      if (lane == 0) part[parity][i] = p;
     }
     if (C > 1) cluster_sync_all();
     else __syncthreads();
-    // and a thread a row's CTAs: every CTA finds the same
-    if (tid < r1 - r0) {
-      const int r = r0 + tid;
-      Partial p = part[parity][tid];
+    // and its CTAs: every CTA finds the same
+    for (int i = warp; i < r1 - r0; i += kWarps) {
+      const int r = r0 + i;
+      Partial p = part[parity][i];
       if (C > 1) {
-        const Partial* const at = &part[parity][tid];
-        Partial o[kMaxCluster];
-#pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
-          if (q < C) o[q] = Partial{ld_dsmem_f32(&at->m, q), ld_dsmem_f32(&at->s, q), ld_dsmem_i32(&at->at, q)};
-        p = o[0];
-#pragma unroll
-        for (int q = 1; q < kMaxCluster; ++q)
-          if (q < C) {
-            if (greedy) best_of(p.m, p.at, o[q].m, o[q].at);
-            else join(p.m, p.s, o[q].m, o[q].s, c);
-          }
+        const Partial* const at = &part[parity][i];
+        p = Partial{-INFINITY, 0.f, INT_MAX};
+        if (lane < C) p = Partial{ld_dsmem_f32(&at->m, lane), ld_dsmem_f32(&at->s, lane), ld_dsmem_i32(&at->at, lane)};
+        warp_join(p, greedy, c);
       }
+      if (lane != 0) continue;
       const bool usable = fabsf(p.m) <= 3.4028235e38f;
       s_top[r] = p.m;
       s_sum[r] = p.s;
@@ -269,12 +274,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
     const float top = base_of(s_top[n]), inv = 1.f / s_sum[n];
     const float* const q = refused && a.q != nullptr && usable ? a.q + (static_cast<int64_t>(b) * a.k + n) * a.V : nullptr;
     const int d = refused && a.q == nullptr ? s_d[n] : -1;
-    const float* const e = a.noise + static_cast<int64_t>(b) * a.V;
     // largest w / noise, and largest p / noise, which stands in where w is 0 everywhere; of a row without a
     // softmax the largest logit
     float v[2] = {-INFINITY, -INFINITY};
     int at[2] = {INT_MAX, INT_MAX};
-    const int i0 = static_cast<int>(static_cast<int64_t>(a.V) * rank / C), i1 = static_cast<int>(static_cast<int64_t>(a.V) * (rank + 1) / C);
     auto look = [&](int i, float f, float qi, float ei) {
       if (!usable) {
         best_of(v[1], at[1], f, i);
@@ -285,19 +288,18 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       if (w > 0.f) best_of(v[0], at[0], __fdiv_rn(w, ei), i);
       if (q != nullptr || d >= 0) best_of(v[1], at[1], p > 0.f ? __fdiv_rn(p, ei) : 0.f, i);
     };
-    int i = i0 + tid;
-    for (; i + 7 * kThreads < i1; i += 8 * kThreads) {
-      float f[8], qi[8], ei[8];
+    for (int i = i0 + tid; i < i1; i += 4 * kThreads) {
+      float f[4], qi[4], ei[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = value(x[i + j * kThreads]);
-        qi[j] = q != nullptr ? __ldg(q + i + j * kThreads) : 0.f;
-        ei[j] = __ldg(e + i + j * kThreads);
+      for (int j = 0; j < 4; ++j) {
+        const int at_j = min(i + j * kThreads, i1 - 1);  // (again what the last one reads)
+        f[j] = value(x[at_j]);
+        qi[j] = q != nullptr ? __ldg(q + at_j) : 0.f;
+        ei[j] = __ldg(e + at_j);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) look(i + j * kThreads, f[j], qi[j], ei[j]);
+      for (int j = 0; j < 4; ++j) look(min(i + j * kThreads, i1 - 1), f[j], qi[j], ei[j]);
     }
-    for (; i < i1; i += kThreads) look(i, value(x[i]), q != nullptr ? __ldg(q + i) : 0.f, __ldg(e + i));
     if (usable && q == nullptr && d < 0) v[1] = v[0], at[1] = at[0];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -336,11 +338,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 template <bool F32>
 cudaError_t launch_verify(VerifyArgs a, cudaStream_t stream) {
   if (injected_launch_failure()) return cudaErrorLaunchFailure;
-  // CTAs of a cluster: about two an SM over all sequences, and no more than one
-  // for every 2048 logits of a row.
+  // CTAs of a cluster: two to four an SM over all sequences (64 x 5 x 128000:
+  // 66.4 us; one to two 68.1, four to eight 89.9), and no more than one for
+  // every 2048 logits of a row.
   const int sms = device_sm_count();
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && static_cast<int64_t>(a.B) * a.cluster * 2 <= 2 * sms && a.V > a.cluster * 2048) a.cluster *= 2;
+  while (a.cluster < kMaxCluster && static_cast<int64_t>(a.B) * a.cluster <= 2 * sms && a.V > a.cluster * 2048) a.cluster *= 2;
   // All rows in one round while reading them takes less than the exchanges saved (about 16 MB: 2.5 us).
   a.round = static_cast<int64_t>(a.B) * (a.k + 1) * a.V * (F32 ? 4 : 2) <= (16 << 20) ? a.k + 1 : 1;
   auto kern = verify_kernel<F32>;
