@@ -695,241 +695,239 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
       // the tile's keys, then its values (a loop, so that the refill's code is there once)
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-      wait();
-      const int off = ring_off + slot * Cfg::TILEB;
-      const uint32_t kt = sbase + off, vt = kt;
-      if (half == 0) {
-
-      // scores
-      auto query = [&](int kk, int w, uint32_t (&f)[4]) {
-        if constexpr (Cfg::QREG) {
+        wait();
+        const int off = ring_off + slot * Cfg::TILEB;
+        const uint32_t kt = sbase + off, vt = kt;
+        if (half == 0) {
+          // scores
+          auto query = [&](int kk, int w, uint32_t (&f)[4]) {
+            if constexpr (Cfg::QREG) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) f[x] = qf[w].a[kk][x];
-        } else {
-          const uint4 u = q_frag[(kk * RPW + w) * 32];
-          f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-        }
-      };
-      if constexpr (!E8) {
-        const int kr = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          uint32_t f[RPW][4];
-#pragma unroll
-          for (int w = 0; w < RPW; ++w) query(kk, w, f[w]);
-#pragma unroll
-          for (int t = 0; t < NT / 16; ++t) {
-            uint32_t b[4];
-            ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int w = 0; w < RPW; ++w) {
-              if (kk == 0) {
-                mma_bf16_16816_z(s[w][2 * t], f[w], b[0], b[1]);
-                mma_bf16_16816_z(s[w][2 * t + 1], f[w], b[2], b[3]);
-              } else {
-                mma_bf16_16816(s[w][2 * t], f[w], b[0], b[1]);
-                mma_bf16_16816(s[w][2 * t + 1], f[w], b[2], b[3]);
-              }
-            }
-          }
-        }
-      } else {
-        const int kr = lane & 15;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; kk += 2) {
-          uint32_t f[RPW][2][4];
-#pragma unroll
-          for (int w = 0; w < RPW; ++w) {
-            query(kk, w, f[w][0]);
-            query(kk + 1, w, f[w][1]);
-          }
-#pragma unroll
-          for (int t = 0; t < NT / 16; ++t) {
-            uint32_t b[4];
-            ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk + (lane >> 4)));
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {  // (token octet, k16 step) = (x & 1, x >> 1)
-              const uint32_t b0 = e4m3x2_to_f16x2(b[x]), b1 = e4m3x2_to_f16x2(b[x] >> 16);
-#pragma unroll
-              for (int w = 0; w < RPW; ++w) {
-                if (kk + (x >> 1) == 0) mma_f16_16816_z(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
-                else mma_f16_16816(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
-              }
-            }
-          }
-        }
-      }
-
-      } else {
-      // Whether some row has a token of more than about 1/16 of its sum so far.
-      bool heavy = false;
-      float tile_top[RPW][2];
-#pragma unroll
-      for (int w = 0; w < RPW; ++w) {
-        // mask, running maximum, weights 2^(s scale - m)
-        if (!full) {
-#pragma unroll
-          for (int i = 0; i < NT / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = j0 + i * 8 + 2 * (lane & 3) + (e & 1), p = pos[w][e >> 1];
-              const bool see = j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
-              s[w][i][e] = see ? s[w][i][e] : -INFINITY;
-            }
-        }
-        float corr[2], base[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float top = fmaxf(s[w][0][2 * r], s[w][0][2 * r + 1]);
-#pragma unroll
-          for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          tile_top[w][r] = top * qf[w].scale[r];
-          top = fmaxf(tile_top[w][r], mx[w][r]);
-          base[r] = top == -INFINITY ? 0.f : top;
-          corr[r] = ex2(mx[w][r] - base[r]);
-          mx[w][r] = top;
-          sum[w][r][0] *= corr[r];
-          sum[w][r][1] *= corr[r];
-        }
-        if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            fmul2(o[w][i][0], o[w][i][1], corr[0]);
-            fmul2(o[w][i][2], o[w][i][3], corr[1]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < NT / 8; ++i)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            fms2(s[w][i][2 * r], s[w][i][2 * r + 1], qf[w].scale[r], base[r]);
-            s[w][i][2 * r] = ex2(s[w][i][2 * r]);
-            s[w][i][2 * r + 1] = ex2(s[w][i][2 * r + 1]);
-            fadd2(sum[w][r][0], sum[w][r][1], s[w][i][2 * r], s[w][i][2 * r + 1]);
-          }
-        // (a thread's sum is over a quarter of the columns)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) heavy |= ex2(tile_top[w][r] - base[r]) > 0.25f * (sum[w][r][0] + sum[w][r][1]);
-      }
-
-      // A token that a row does not see meets it with weight 0, and 0 times its
-      // value must be 0.  Where such a value is not finite (a later draft row's, or
-      // what lies past the length), the product is taken with 0 in the place of
-      // every value that is not, and those are added element by element to the
-      // rows that see them.
-      constexpr int RPI = 32 / CPR;  // rows a warp looks at at once, a chunk a lane
-      auto row_bad = [&](int t) {    // some element of this lane's chunk of row t + lane / CPR is not finite
-        const uint4 u = *reinterpret_cast<const uint4*>(smem + off + tile_at<ROWB>(t + lane / CPR, lane % CPR));
-        return (not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w)) != 0;
-      };
-      bool bad = false;
-      if (!full) {
-#pragma unroll 1
-        for (int t = 0; t < NT; t += RPI) {
-          const int j = j0 + t + lane / CPR;
-          const bool unseen = j > cc.v.pos_lo || (a.window != 0 && j >= a.sinks && j <= cc.v.pos_hi - a.window);
-          if (unseen) bad |= row_bad(t);
-        }
-      }
-      bad = __any_sync(0xffffffffu, bad);
-      auto values = [&](auto clean, auto with_rest) {
-        constexpr bool kClean = decltype(clean)::value, kRest = decltype(with_rest)::value && !E8;
-#pragma unroll
-        for (int t = 0; t < NT / 16; ++t) {
-          // fp16 holds a probability to 11 bits, bf16 to 8 only: where one token weighs much, its rest goes in
-          // as a second operand; else 16 and more roundings of either sign are added
-          uint32_t p[RPW][4], rest[RPW][4];
-#pragma unroll
-          for (int w = 0; w < RPW; ++w)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float lo = s[w][2 * t + (x >> 1)][2 * (x & 1)], hi = s[w][2 * t + (x >> 1)][2 * (x & 1) + 1];
-              p[w][x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-              rest[w][x] = !kRest ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
-            }
-#pragma unroll
-          for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
-            uint32_t b[4];
-            ldsm_x4_t(b, vt + tile_at<ROWB>(t * 16 + (lane & 15), (E8 ? d : 2 * d) + (lane >> 4)));
-            if constexpr (kClean)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) b[x] &= ~not_finite<E8>(b[x]);
-            if constexpr (!E8) {
-#pragma unroll
-              for (int w = 0; w < RPW; ++w) {
-                mma_bf16_16816(o[w][2 * d], p[w], b[0], b[1]);
-                mma_bf16_16816(o[w][2 * d + 1], p[w], b[2], b[3]);
-                if (kRest) {
-                  mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
-                  mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
-                }
-              }
+              for (int x = 0; x < 4; ++x) f[x] = qf[w].a[kk][x];
             } else {
-              // a chunk's 16 dims come in pairs: even and odd dims become one tile each
+              const uint4 u = q_frag[(kk * RPW + w) * 32];
+              f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+            }
+          };
+          if constexpr (!E8) {
+            const int kr = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {  // chunk d + x
-                const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4420));
-                const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4420));
-                const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4431));
-                const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4431));
+            for (int kk = 0; kk < D / 16; ++kk) {
+              uint32_t f[RPW][4];
+#pragma unroll
+              for (int w = 0; w < RPW; ++w) query(kk, w, f[w]);
+#pragma unroll
+              for (int t = 0; t < NT / 16; ++t) {
+                uint32_t b[4];
+                ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk * 2 + ((lane >> 3) & 1)));
 #pragma unroll
                 for (int w = 0; w < RPW; ++w) {
-                  mma_f16_16816(o[w][2 * (d + x)], p[w], e0, e1);
-                  mma_f16_16816(o[w][2 * (d + x) + 1], p[w], f0, f1);
+                  if (kk == 0) {
+                    mma_bf16_16816_z(s[w][2 * t], f[w], b[0], b[1]);
+                    mma_bf16_16816_z(s[w][2 * t + 1], f[w], b[2], b[3]);
+                  } else {
+                    mma_bf16_16816(s[w][2 * t], f[w], b[0], b[1]);
+                    mma_bf16_16816(s[w][2 * t + 1], f[w], b[2], b[3]);
+                  }
+                }
+              }
+            }
+          } else {
+            const int kr = lane & 15;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+              uint32_t f[RPW][2][4];
+#pragma unroll
+              for (int w = 0; w < RPW; ++w) {
+                query(kk, w, f[w][0]);
+                query(kk + 1, w, f[w][1]);
+              }
+#pragma unroll
+              for (int t = 0; t < NT / 16; ++t) {
+                uint32_t b[4];
+                ldsm_x4(b, kt + tile_at<ROWB>(t * 16 + kr, kk + (lane >> 4)));
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {  // (token octet, k16 step) = (x & 1, x >> 1)
+                  const uint32_t b0 = e4m3x2_to_f16x2(b[x]), b1 = e4m3x2_to_f16x2(b[x] >> 16);
+#pragma unroll
+                  for (int w = 0; w < RPW; ++w) {
+                    if (kk + (x >> 1) == 0) mma_f16_16816_z(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
+                    else mma_f16_16816(s[w][2 * t + (x & 1)], f[w][x >> 1], b0, b1);
+                  }
+                }
+              }
+            }
+          }
+        } else {
+          // Whether some row has a token of more than about 1/16 of its sum so far.
+          bool heavy = false;
+          float tile_top[RPW][2];
+#pragma unroll
+          for (int w = 0; w < RPW; ++w) {
+            // mask, running maximum, weights 2^(s scale - m)
+            if (!full) {
+#pragma unroll
+              for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int j = j0 + i * 8 + 2 * (lane & 3) + (e & 1), p = pos[w][e >> 1];
+                  const bool see = j <= p && (a.window == 0 || j > p - a.window || j < a.sinks);
+                  s[w][i][e] = see ? s[w][i][e] : -INFINITY;
+                }
+            }
+            float corr[2], base[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float top = fmaxf(s[w][0][2 * r], s[w][0][2 * r + 1]);
+#pragma unroll
+              for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              tile_top[w][r] = top * qf[w].scale[r];
+              top = fmaxf(tile_top[w][r], mx[w][r]);
+              base[r] = top == -INFINITY ? 0.f : top;
+              corr[r] = ex2(mx[w][r] - base[r]);
+              mx[w][r] = top;
+              sum[w][r][0] *= corr[r];
+              sum[w][r][1] *= corr[r];
+            }
+            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i) {
+                fmul2(o[w][i][0], o[w][i][1], corr[0]);
+                fmul2(o[w][i][2], o[w][i][3], corr[1]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                fms2(s[w][i][2 * r], s[w][i][2 * r + 1], qf[w].scale[r], base[r]);
+                s[w][i][2 * r] = ex2(s[w][i][2 * r]);
+                s[w][i][2 * r + 1] = ex2(s[w][i][2 * r + 1]);
+                fadd2(sum[w][r][0], sum[w][r][1], s[w][i][2 * r], s[w][i][2 * r + 1]);
+              }
+            // (a thread's sum is over a quarter of the columns)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) heavy |= ex2(tile_top[w][r] - base[r]) > 0.25f * (sum[w][r][0] + sum[w][r][1]);
+          }
+
+          // A token that a row does not see meets it with weight 0, and 0 times its
+          // value must be 0.  Where such a value is not finite (a later draft row's, or
+          // what lies past the length), the product is taken with 0 in the place of
+          // every value that is not, and those are added element by element to the
+          // rows that see them.
+          constexpr int RPI = 32 / CPR;  // rows a warp looks at at once, a chunk a lane
+          auto row_bad = [&](int t) {    // some element of this lane's chunk of row t + lane / CPR is not finite
+            const uint4 u = *reinterpret_cast<const uint4*>(smem + off + tile_at<ROWB>(t + lane / CPR, lane % CPR));
+            return (not_finite<E8>(u.x) | not_finite<E8>(u.y) | not_finite<E8>(u.z) | not_finite<E8>(u.w)) != 0;
+          };
+          bool bad = false;
+          if (!full) {
+#pragma unroll 1
+            for (int t = 0; t < NT; t += RPI) {
+              const int j = j0 + t + lane / CPR;
+              const bool unseen = j > cc.v.pos_lo || (a.window != 0 && j >= a.sinks && j <= cc.v.pos_hi - a.window);
+              if (unseen) bad |= row_bad(t);
+            }
+          }
+          bad = __any_sync(0xffffffffu, bad);
+          auto values = [&](auto clean, auto with_rest) {
+            constexpr bool kClean = decltype(clean)::value, kRest = decltype(with_rest)::value && !E8;
+#pragma unroll
+            for (int t = 0; t < NT / 16; ++t) {
+              // fp16 holds a probability to 11 bits, bf16 to 8 only: where one token weighs much, its rest goes in
+              // as a second operand; else 16 and more roundings of either sign are added
+              uint32_t p[RPW][4], rest[RPW][4];
+#pragma unroll
+              for (int w = 0; w < RPW; ++w)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const float lo = s[w][2 * t + (x >> 1)][2 * (x & 1)], hi = s[w][2 * t + (x >> 1)][2 * (x & 1) + 1];
+                  p[w][x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
+                  rest[w][x] = !kRest ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
+                }
+#pragma unroll
+              for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
+                uint32_t b[4];
+                ldsm_x4_t(b, vt + tile_at<ROWB>(t * 16 + (lane & 15), (E8 ? d : 2 * d) + (lane >> 4)));
+                if constexpr (kClean)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) b[x] &= ~not_finite<E8>(b[x]);
+                if constexpr (!E8) {
+#pragma unroll
+                  for (int w = 0; w < RPW; ++w) {
+                    mma_bf16_16816(o[w][2 * d], p[w], b[0], b[1]);
+                    mma_bf16_16816(o[w][2 * d + 1], p[w], b[2], b[3]);
+                    if (kRest) {
+                      mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
+                      mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
+                    }
+                  }
+                } else {
+                  // a chunk's 16 dims come in pairs: even and odd dims become one tile each
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {  // chunk d + x
+                    const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4420));
+                    const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4420));
+                    const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4431));
+                    const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4431));
+#pragma unroll
+                    for (int w = 0; w < RPW; ++w) {
+                      mma_f16_16816(o[w][2 * (d + x)], p[w], e0, e1);
+                      mma_f16_16816(o[w][2 * (d + x) + 1], p[w], f0, f1);
+                    }
+                  }
+                }
+              }
+            }
+          };
+          if (!bad) {
+            if (E8 || !__any_sync(0xffffffffu, heavy)) values(std::false_type{}, std::false_type{});
+            else values(std::false_type{}, std::true_type{});
+          } else {
+            values(std::true_type{}, std::true_type{});
+#pragma unroll 1
+            for (int t = 0; t < NT; ++t) {
+              if (t % RPI == 0) bad = row_bad(t);
+              if (((__ballot_sync(0xffffffffu, bad) >> (t % RPI * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << (CPR & 31)) - 1u)) == 0)
+                continue;
+              const int src = (lane & 28) | ((t & 7) >> 1), j = j0 + t;
+              float p[RPW][2];  // the token's weight for this thread's rows; 0 and not added where it is not seen
+              bool see[RPW][2];
+#pragma unroll
+              for (int w = 0; w < RPW; ++w)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  float x = 0.f;
+#pragma unroll
+                  for (int i = 0; i < NT / 8; ++i)
+                    if (i == t >> 3) x = (t & 1) ? s[w][i][2 * r + 1] : s[w][i][2 * r];
+                  p[w][r] = __shfl_sync(0xffffffffu, x, src);
+                  see[w][r] = j <= pos[w][r] && (a.window == 0 || j > pos[w][r] - a.window || j < a.sinks);
+                }
+              // four bytes at a time: two columns of one output tile, or (E4M3) two each of two
+#pragma unroll
+              for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
+                const int at = out_col<E8>(i, 0) * (E8 ? 1 : 2);
+                const uint32_t u = *reinterpret_cast<const uint32_t*>(smem + off + tile_at<ROWB>(t, at / 16) + at % 16);
+                if (not_finite<E8>(u) == 0) continue;
+#pragma unroll
+                for (int x = 0; x < (E8 ? 4 : 2); ++x) {
+                  const float f = E8 ? e4m3_to_float((u >> (8 * x)) & 0xFFu) : x ? bf16_hi(u) : bf16_lo(u);
+                  if (fabsf(f) <= 3.4028235e38f) continue;
+                  const int ot = E8 ? i + (x & 1) : i, e = E8 ? x >> 1 : x;
+#pragma unroll
+                  for (int w = 0; w < RPW; ++w) {
+                    if (see[w][0]) o[w][ot][e] += p[w][0] * f;
+                    if (see[w][1]) o[w][ot][2 + e] += p[w][1] * f;
+                  }
                 }
               }
             }
           }
         }
-      };
-      if (!bad) {
-        if (E8 || !__any_sync(0xffffffffu, heavy)) values(std::false_type{}, std::false_type{});
-        else values(std::false_type{}, std::true_type{});
-      } else {
-        values(std::true_type{}, std::true_type{});
-#pragma unroll 1
-        for (int t = 0; t < NT; ++t) {
-          if (t % RPI == 0) bad = row_bad(t);
-          if (((__ballot_sync(0xffffffffu, bad) >> (t % RPI * CPR)) & (CPR == 32 ? 0xffffffffu : (1u << (CPR & 31)) - 1u)) == 0)
-            continue;
-          const int src = (lane & 28) | ((t & 7) >> 1), j = j0 + t;
-          float p[RPW][2];  // the token's weight for this thread's rows; 0 and not added where it is not seen
-          bool see[RPW][2];
-#pragma unroll
-          for (int w = 0; w < RPW; ++w)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float x = 0.f;
-#pragma unroll
-              for (int i = 0; i < NT / 8; ++i)
-                if (i == t >> 3) x = (t & 1) ? s[w][i][2 * r + 1] : s[w][i][2 * r];
-              p[w][r] = __shfl_sync(0xffffffffu, x, src);
-              see[w][r] = j <= pos[w][r] && (a.window == 0 || j > pos[w][r] - a.window || j < a.sinks);
-            }
-          // four bytes at a time: two columns of one output tile, or (E4M3) two each of two
-#pragma unroll
-          for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
-            const int at = out_col<E8>(i, 0) * (E8 ? 1 : 2);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(smem + off + tile_at<ROWB>(t, at / 16) + at % 16);
-            if (not_finite<E8>(u) == 0) continue;
-#pragma unroll
-            for (int x = 0; x < (E8 ? 4 : 2); ++x) {
-              const float f = E8 ? e4m3_to_float((u >> (8 * x)) & 0xFFu) : x ? bf16_hi(u) : bf16_lo(u);
-              if (fabsf(f) <= 3.4028235e38f) continue;
-              const int ot = E8 ? i + (x & 1) : i, e = E8 ? x >> 1 : x;
-#pragma unroll
-              for (int w = 0; w < RPW; ++w) {
-                if (see[w][0]) o[w][ot][e] += p[w][0] * f;
-                if (see[w][1]) o[w][ot][2 + e] += p[w][1] * f;
-              }
-            }
-          }
-        }
-      }
-      }
-      used();
+        used();
       }
     }
 
@@ -1077,38 +1075,38 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = v[i][e];
     if (!solo) {
-    __syncthreads();  // (of the item before: read)
+      __syncthreads();  // (of the item before: read)
 #pragma unroll
-    for (int i = 0; i < IW; ++i) s_v[warp][i][lane] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-    s_ml[warp][lane] = make_float4(top[0], sum[0], top[1], sum[1]);
-    __syncthreads();
-    if (warp != 0) continue;
-    t[0] = t[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+      for (int i = 0; i < IW; ++i) s_v[warp][i][lane] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      s_ml[warp][lane] = make_float4(top[0], sum[0], top[1], sum[1]);
+      __syncthreads();
+      if (warp != 0) continue;
+      t[0] = t[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < IW; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float4 q[WARPS];
+      for (int i = 0; i < IW; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      float4 q[WARPS];
 #pragma unroll
-    for (int x = 0; x < WARPS; ++x) {
-      q[x] = s_ml[x][lane];
-      t[0] = fmaxf(t[0], q[x].x);
-      t[1] = fmaxf(t[1], q[x].z);
-    }
-    const float b0 = t[0] == -INFINITY ? 0.f : t[0], b1 = t[1] == -INFINITY ? 0.f : t[1];
-#pragma unroll
-    for (int x = 0; x < WARPS; ++x) {
-      const float f0 = ex2(q[x].x - b0), f1 = ex2(q[x].z - b1);
-      l[0] += f0 * q[x].y;
-      l[1] += f1 * q[x].w;
-#pragma unroll
-      for (int i = 0; i < IW; ++i) {
-        const float4 u = s_v[x][i][lane];
-        o[i][0] += f0 * u.x;
-        o[i][1] += f0 * u.y;
-        o[i][2] += f1 * u.z;
-        o[i][3] += f1 * u.w;
+      for (int x = 0; x < WARPS; ++x) {
+        q[x] = s_ml[x][lane];
+        t[0] = fmaxf(t[0], q[x].x);
+        t[1] = fmaxf(t[1], q[x].z);
       }
-    }
+      const float b0 = t[0] == -INFINITY ? 0.f : t[0], b1 = t[1] == -INFINITY ? 0.f : t[1];
+#pragma unroll
+      for (int x = 0; x < WARPS; ++x) {
+        const float f0 = ex2(q[x].x - b0), f1 = ex2(q[x].z - b1);
+        l[0] += f0 * q[x].y;
+        l[1] += f1 * q[x].w;
+#pragma unroll
+        for (int i = 0; i < IW; ++i) {
+          const float4 u = s_v[x][i][lane];
+          o[i][0] += f0 * u.x;
+          o[i][1] += f0 * u.y;
+          o[i][2] += f1 * u.z;
+          o[i][3] += f1 * u.w;
+        }
+      }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
