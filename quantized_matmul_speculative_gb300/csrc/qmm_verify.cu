@@ -89,14 +89,13 @@ __device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
 // on timing.
 //
 // What bounds it: the bytes of the rows read, where there are many sequences
-// (rounds of one row, several clusters an SM so that one's exchange overlaps
+// (rounds of two rows, several clusters an SM so that one's exchange overlaps
 // another's reads); the latency of its two exchanges, where there are few (all
 // rows in one round).  The noise is fetched into L2 meanwhile (fetching the next
-// row too gains nothing).  Nothing may spill: a thread, not a warp, that joined
-// a row's partials cost 6 us more, 8 elements at a time, not 4, of the last pass
-// 10 us.  64 sequences x 5
-// drafts x 128000 fp32 logits: 66 us, 4.0 TB/s of what it would read were no
-// draft refused; 1 x 7 x 32000 bf16: 10.1 us.
+// row too gains nothing).  Nothing may spill: joining a row's partials by a
+// thread, not a warp, cost 6 us more, and 8 elements at a time, not 4, in the
+// last pass 10 us.  64 sequences x 5 drafts x 128000 fp32 logits: 63 us, 4.1 TB/s
+// of what it would read were no draft refused; 1 x 7 x 32000 bf16: 10.0 us.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   using T = typename std::conditional<F32, float, uint16_t>::type;
@@ -344,8 +343,9 @@ cudaError_t launch_verify(VerifyArgs a, cudaStream_t stream) {
   const int sms = device_sm_count();
   a.cluster = 1;
   while (a.cluster < kMaxCluster && static_cast<int64_t>(a.B) * a.cluster <= 2 * sms && a.V > a.cluster * 2048) a.cluster *= 2;
-  // All rows in one round while reading them takes less than the exchanges saved (about 16 MB: 2.5 us).
-  a.round = static_cast<int64_t>(a.B) * (a.k + 1) * a.V * (F32 ? 4 : 2) <= (16 << 20) ? a.k + 1 : 1;
+  // All rows in one round while reading them takes less than the exchanges saved (about 16 MB: 2.5 us), else two:
+  // 64 x 5 x 128000 takes 63.3 us, and 66.1, 66.1, 73.9 with one, three, all.
+  a.round = static_cast<int64_t>(a.B) * (a.k + 1) * a.V * (F32 ? 4 : 2) <= (16 << 20) ? a.k + 1 : 2;
   auto kern = verify_kernel<F32>;
   static std::atomic<uint64_t> ready{0};
   uint64_t bit;

@@ -103,6 +103,20 @@ def test_drawn(B, k, V, dtype):
     check(*problem(B, k, V, dtype, seed=V + B), need=0.7)
 
 
+@pytest.mark.parametrize("greedy", [False, True])
+@pytest.mark.parametrize("B,k,V,dtype", [(24, 6, 40000, torch.float32), (24, 5, 70001, torch.bfloat16)])
+def test_rows_read_in_turn(B, k, V, dtype, greedy):
+    """More than 16 MB of logits: rounds of two rows, the last one of a single row or ending before it."""
+    x, d, q, u, e, T = problem(B, k, V, dtype, seed=5, greedy=greedy)
+    assert x.numel() * x.element_size() > 16 << 20
+    best = x[:, :k].float().argmax(-1).to(torch.int32)
+    d = torch.where(torch.rand(B, k, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda") < 0.8, best, d)
+    lens = torch.arange(B, device="cuda", dtype=torch.int32) % (k + 1)
+    check(x, d, None, u, e, T, need=0.7)
+    check(x, d, None, u * 1e-30, e, T, lens, need=0.7)
+    check(x, d, None, torch.full_like(u, 0.999999), e, T, need=0.7)
+
+
 @pytest.mark.parametrize("B,k,V", [(20, 7, 1000), (4, 5, 32001)])
 def test_ragged_and_certain_drafts(B, k, V):
     x, d, q, u, e, T = problem(B, k, V, seed=2)
