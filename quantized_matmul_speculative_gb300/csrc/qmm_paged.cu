@@ -37,7 +37,7 @@ kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, cons
   const int per_head = c.head_dim / 8, per_row = c.heads * per_head;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (t >= static_cast<int64_t>(B) * M * per_row) return;
-  const int64_t row = t / per_row;  // below 2^20
+  const int64_t row = t >> 31 ? t / per_row : static_cast<uint32_t>(t) / static_cast<uint32_t>(per_row);  // below 2^20
   const int chunk = static_cast<int>(t - row * per_row);
   const uint4 x[2] = {*reinterpret_cast<const uint4*>(kn + row * k_ld + chunk * 8),
                       *reinterpret_cast<const uint4*>(vn + row * v_ld + chunk * 8)};
