@@ -7,7 +7,13 @@
  * The library streams the packed weights from HBM once per call whatever M is,
  * dequantizes each weight group once and reuses it for all M rows.
  *
- * Sources of the definition (page title, section):
+ * and the operators around that product in a batched verify step: quantisation
+ * into the microscaled formats (qmm_quantize_mx), their product for any number of
+ * rows (qmm_matmul_mx), a paged key-value cache (qmm_kv_append) with attention of
+ * 1..16 new rows a sequence over it (qmm_paged_attention), and the verification
+ * of drafted tokens (qmm_verify_draft); each is defined at its declaration.
+ *
+ * Sources of the product's definition (page title, section):
  *   - "MLX quantized_matmul small-M verify kernels", fact "Stock qmv streams
  *     the weight matrix once per input row": the problem (cost linear in M).
  *   - same page, fact "Fix family 1": dequantize each group once into
