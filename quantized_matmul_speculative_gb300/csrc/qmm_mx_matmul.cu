@@ -20,11 +20,13 @@
 // of 50 ns a stage at BN = 256 beside 260 ns of MMAs, the 1000 x 34816 x 5120
 // product took 201 us.)
 //
-// What bounds it: a full stage at BN = 256 brings 48 KB of codes into one SM, in
-// 0.55 us, for 0.19 us of MMAs at the nominal rate; a tile of 20 stages has 1.4 us
-// more to its first and 1.5 us to write.  1000 x 34816 x 5120 nvfp4: 111 us,
-// 3.2 PFLOP/s (a tile a CTA: 131; the activations multicast to the 2 or 4 CTAs of
-// a cluster: 110 and 194, so not done).  8 x 5120 x 5120 mxfp4: 6.1 us, 2.3 TB/s,
+// What bounds it: the scales' way at BN = 256, a stage's taking longer than its
+// 0.26 us of MMAs (without their loads the call took 24 us less, without their
+// stores 12; half the activations' codes changed nothing); a tile of 20 stages has
+// 1.4 us more to its first and 1.5 us to write.  1000 x 34816 x 5120 nvfp4: 97 us,
+// 3.7 PFLOP/s (with the scales of single stages loaded 111, with a tile a CTA too
+// 131; the activations multicast to the 2 or 4 CTAs of a cluster: 110 and 194 for
+// 111, so not done).  8 x 5120 x 5120 mxfp4: 6.1 us, 2.3 TB/s,
 // its latency from first copy to the sum over the cluster.
 //
 // Arithmetic: codes and scales are exact, their products too; the accumulator
@@ -61,7 +63,7 @@ struct MxMatmulArgs {
   int split;    // CTAs of a cluster
   int stages;
   int pitch;    // scale bytes of a row
-  int aligned;  // rows of scales are whole, aligned stages
+  int aligned;  // rows of scales are whole, aligned stages (1), or pairs of them (2)
   uint32_t tmem_cols;
 };
 
@@ -220,39 +222,24 @@ struct ScaleRow {
 // loads' bounds and shifts decided per stage (580 instructions a stage and warp)
 // this alone was the bound, 250 us; with one group, whose chain of load, pass,
 // store and wait takes longer than a stage's MMAs, 149 us.
-template <int SFW, bool ALIGNED, int XB>
-struct ScaleFeed {
+template <int SFW, int XB>
+struct ScaleStage {
   using Words = typename std::conditional<SFW == 4, uint4, uint2>::type;
-  using Row = ScaleRow<SFW, ALIGNED>;
-  Row rows[1 + XB];  // a weight row, activation rows
-  int flip = 0;      // place of the next stage's words
+  int flip = 0;  // place of the next stage's words
   bool ok = true;
-
-  // Load ahead for the tile at (m0, n0), whose first stage is the CTA's it0-th.
-  __device__ __forceinline__ void start(const MxMatmulArgs& a, int m0, int n0, int k_begin, int k_end, int it0) {
-    const int r = threadIdx.x & 127, first = k_begin + (half() ^ (it0 & 1));
-    rows[0].start(a.ws, n0 + r, a.N, a.pitch, first, k_end);
-#pragma unroll
-    for (int b = 0; b < XB; ++b) rows[1 + b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, first, k_end);
-  }
   static __device__ __forceinline__ int half() { return (threadIdx.x - 64) >> 7; }
 
-  template <int U>
-  __device__ __forceinline__ void stage(const MxMatmulArgs& a, unsigned char* pass_all, uint32_t full, uint32_t empty,
-                                        uint32_t columns, int k, int k_end, int it) {
-    if (k >= k_end) return;
+  // The words w of this thread's rows (a weight row, activation rows), of the CTA's it-th stage, into tensor memory.
+  __device__ __forceinline__ void put(const MxMatmulArgs& a, unsigned char* pass_all, uint32_t full, uint32_t empty,
+                                      uint32_t columns, const uint32_t (&w)[1 + XB][SFW], int it) {
     const int r = threadIdx.x & 127, lane = r & 31, s = it % a.stages;
-    const int valid = a.pitch - k * (4 * SFW);
-    const bool wanted = k + kScaleGroups * Row::kAhead < k_end;
     // (two places in turn: a thread that passed the barrier of its next stage has read this one's)
     Words* const pass = reinterpret_cast<Words*>(pass_all) + (half() * 2 + flip) * (1 + XB) * 128;
     flip ^= 1;
 #pragma unroll
     for (int b = 0; b <= XB; ++b) {
-      uint32_t w[SFW];
-      rows[b].template take<U>(w, valid, wanted);
-      if constexpr (SFW == 4) pass[b * 128 + r] = make_uint4(w[0], w[1], w[2], w[3]);
-      else pass[b * 128 + r] = make_uint2(w[0], w[1]);
+      if constexpr (SFW == 4) pass[b * 128 + r] = make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]);
+      else pass[b * 128 + r] = make_uint2(w[b][0], w[b][1]);
     }
     asm volatile("barrier.sync %0, 128;" ::"r"(1 + half()) : "memory");
     // columns: word w of the weights' rows (4), then word w of the activations' (4 XB)
@@ -282,6 +269,33 @@ struct ScaleFeed {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     mbar_arrive(full + s * 8);
   }
+};
+
+template <int SFW, bool ALIGNED, int XB>
+struct ScaleFeed : ScaleStage<SFW, XB> {
+  using ScaleStage<SFW, XB>::half;
+  using Row = ScaleRow<SFW, ALIGNED>;
+  Row rows[1 + XB];  // a weight row, activation rows
+
+  // Load ahead for the tile at (m0, n0), whose first stage is the CTA's it0-th.
+  __device__ __forceinline__ void start(const MxMatmulArgs& a, int m0, int n0, int k_begin, int k_end, int it0) {
+    const int r = threadIdx.x & 127, first = k_begin + (half() ^ (it0 & 1));
+    rows[0].start(a.ws, n0 + r, a.N, a.pitch, first, k_end);
+#pragma unroll
+    for (int b = 0; b < XB; ++b) rows[1 + b].start(a.xs, m0 + b * 128 + r, a.M, a.pitch, first, k_end);
+  }
+
+  template <int U>
+  __device__ __forceinline__ void stage(const MxMatmulArgs& a, unsigned char* pass_all, uint32_t full, uint32_t empty,
+                                        uint32_t columns, int k, int k_end, int it) {
+    if (k >= k_end) return;
+    const int valid = a.pitch - k * (4 * SFW);
+    const bool wanted = k + kScaleGroups * Row::kAhead < k_end;
+    uint32_t w[1 + XB][SFW];
+#pragma unroll
+    for (int b = 0; b <= XB; ++b) rows[b].template take<U>(w[b], valid, wanted);
+    this->put(a, pass_all, full, empty, columns, w, it);
+  }
   // The tile's stages k_begin .. k_end - 1; the first is the CTA's it0-th.
   __device__ __forceinline__ void run(const MxMatmulArgs& a, unsigned char* pass, uint32_t full, uint32_t empty, uint32_t columns,
                                       int k_begin, int k_end, int it0) {
@@ -290,6 +304,54 @@ struct ScaleFeed {
     for (int k = k_begin + group; k < k_end; k += kScaleGroups * Row::kAhead, it += kScaleGroups * Row::kAhead) {
       stage<0>(a, pass, full, empty, columns, k, k_end, it);
       stage<1>(a, pass, full, empty, columns, k + kScaleGroups, k_end, it + kScaleGroups);
+    }
+  }
+};
+
+// The same where a row's stages come in aligned pairs: a thread loads a pair at
+// once (32 bytes for nvfp4, a whole sector of L2), the groups take pairs in turn.
+// Every lane's load is a line of its own, so that half as many of them count:
+// 97 us at 1000 x 34816 x 5120 for 111 (104 with the next pair asked for after
+// the second stage, not the first).
+template <int SFW, int XB>
+struct PairFeed : ScaleStage<SFW, XB> {
+  using ScaleStage<SFW, XB>::half;
+  const uint8_t* next[1 + XB];  // the pair to load next
+  uint32_t c[1 + XB][2 * SFW];
+
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int b = 0; b <= XB; ++b) {
+      if constexpr (SFW == 4)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(c[b][0]), "=r"(c[b][1]), "=r"(c[b][2]), "=r"(c[b][3]), "=r"(c[b][4]), "=r"(c[b][5]),
+                       "=r"(c[b][6]), "=r"(c[b][7]) : "l"(next[b]));
+      else
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c[b][0]), "=r"(c[b][1]), "=r"(c[b][2]), "=r"(c[b][3]) : "l"(next[b]));
+      next[b] += kScaleGroups * 8 * SFW;
+    }
+  }
+  __device__ __forceinline__ void start(const MxMatmulArgs& a, int m0, int n0, int k_begin, int k_end, int it0) {
+    const int r = threadIdx.x & 127, first = k_begin + 2 * (half() ^ ((it0 >> 1) & 1));
+    next[0] = a.ws + static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.pitch + first * (4 * SFW);
+#pragma unroll
+    for (int b = 0; b < XB; ++b)
+      next[1 + b] = a.xs + static_cast<int64_t>(min(m0 + b * 128 + r, a.M - 1)) * a.pitch + first * (4 * SFW);
+    if (first < k_end) load();
+  }
+  // (k_begin, k_end and it0 are even)
+  __device__ __forceinline__ void run(const MxMatmulArgs& a, unsigned char* pass, uint32_t full, uint32_t empty, uint32_t columns,
+                                      int k_begin, int k_end, int it0) {
+    for (int k = k_begin + 2 * (half() ^ ((it0 >> 1) & 1)); k < k_end; k += 2 * kScaleGroups) {
+      uint32_t w[2][1 + XB][SFW];
+#pragma unroll
+      for (int b = 0; b <= XB; ++b)
+#pragma unroll
+        for (int i = 0; i < 2 * SFW; ++i) w[i / SFW][b][i % SFW] = c[b][i];
+      this->put(a, pass, full, empty, columns, w[0], it0 + k - k_begin);
+      if (k + 2 * kScaleGroups < k_end) load();
+      this->put(a, pass, full, empty, columns, w[1], it0 + k - k_begin + 1);
     }
   }
 };
@@ -406,8 +468,7 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
     }
   } else {
     // scales of a tile, the first ones of the next already asked for, then the tile's outputs
-    auto feed = [&](auto aligned) {
-      ScaleFeed<SFW, decltype(aligned)::value, XB> scales;
+    auto feed = [&](auto scales) {
       const uint32_t quarter = static_cast<uint32_t>(warp & 3) << 21;
       unsigned char* const pass = smem + L.scales;
       int it = 0, turn = 0;
@@ -442,8 +503,9 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
         mbar_arrive(free);
       }
     };
-    if (a.aligned) feed(std::true_type{});
-    else feed(std::false_type{});
+    if (XB == 2 && a.aligned == 2) feed(PairFeed<SFW, XB>{});
+    else if (a.aligned) feed(ScaleFeed<SFW, true, XB>{});
+    else feed(ScaleFeed<SFW, false, XB>{});
   }
   __syncwarp();
   __syncthreads();
@@ -539,10 +601,14 @@ cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cud
   // tensor memory's columns (accumulators, then each stage's scales) allow.
   const int budget = a.BN <= 32 ? 113 * 1024 : 227 * 1024, cols = a.BN <= 32 ? 256 : 512;
   const int sf_cols = SFW * 4 * (1 + (a.BN + 127) / 128);
-  // (an even number: a stage's scales always come from one group)
+  // (an even number, and of pairs too: a stage's scales always come from one group)
   a.stages = 2;
   while (a.stages < 8 && GemmSmem(a.BN, a.stages + 2, SFW).total + 1024 <= budget && a.BN + (a.stages + 2) * sf_cols <= cols)
     a.stages += 2;
+  const int pair = 8 * SFW;
+  if (a.BN > 128 && a.split == 1 && a.stages % 4 == 0 && a.K % (2 * kTileK) == 0 && a.pitch % pair == 0 &&
+      ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) & (pair - 1)) == 0)
+    a.aligned = 2;
   a.tmem_cols = cols;
   const int smem = GemmSmem(a.BN, a.stages, SFW).total + 1024;
   CUtensorMap wmap, xmap;

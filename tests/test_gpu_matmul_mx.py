@@ -75,6 +75,18 @@ def test_many_tiles(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("K", [512, 768, 1536, 2560])
+def test_stages_of_a_tile(K, fmt):
+    """Several tiles a CTA, of 2, 3, 6 and 10 stages; scales that start where a pair of stages may, and where not."""
+    x, w = matrix(700, K, fmt, K), matrix(20011, K, fmt, K + 1)
+    y = check(x, w, fmt, torch.bfloat16)
+    for step in (1, 8, 16):
+        moved = torch.zeros(x[1].numel() + 16, dtype=torch.uint8, device="cuda")[step:step + x[1].numel()].view(x[1].shape)
+        moved.copy_(x[1])
+        assert torch.equal(binding.matmul_mx(x[0], moved, *w, fmt), y)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_scale_range(fmt):
     """Small and large scales, the subnormal ones among them."""
     lo, hi = (0, 0x7F) if fmt == "nvfp4" else (64, 190)
