@@ -273,9 +273,8 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
  * null or fp32 [B, M, q_heads], log sum_j exp(scale * q . k_j).  A row that
  * sees no token, and rows i >= m_b: out 0, lse -inf.  What a row does not see
  * never reaches it, whatever is stored there.  Scores, softmax statistics and
- * sums are fp32; probabilities enter the second product as bf16, with their
- * rest as a second operand wherever one token weighs more than about 1/16 of
- * its row (as fp16 for an E4M3 cache).
+ * sums are fp32; probabilities enter the second product as two bf16 operands
+ * that hold 16 of their bits (for an E4M3 cache as one in fp16).
  * workspace: qmm_paged_attention_workspace() bytes, 16-byte aligned, not shared
  * by calls that may run at the same time; contents need no initialisation.
  * Alignment as qmm_kv_append (q and out too).                                 */

@@ -23,8 +23,8 @@
 // What bounds it: a worker's chain load -> scores -> maximum -> weights ->
 // output products, a tile at a time, with two or three warps a scheduler to
 // cover it; then the start (lengths, table, first pieces: about 5 us) and the
-// join.  One row over 65001 tokens, 8 heads x 128 in bf16: 64 us, 4.2 TB/s;
-// 32 ragged sequences x 8 rows: 143 us, 3.8 TB/s; 16 x 4 rows, a window of
+// join.  One row over 65001 tokens, 8 heads x 128 in bf16: 66 us, 4.0 TB/s;
+// 32 ragged sequences x 8 rows: 152 us, 3.6 TB/s; 16 x 4 rows, a window of
 // 4096 tokens, 8 x 64 in E4M3: 57 us; 4 short sequences: 13.6 us.
 #pragma once
 
@@ -769,9 +769,6 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             }
           }
         } else {
-          // Whether some row has a token of more than about 1/16 of its sum so far.
-          bool heavy = false;
-          float tile_top[RPW][2];
 #pragma unroll
           for (int w = 0; w < RPW; ++w) {
             // mask, running maximum, weights 2^(s scale - m)
@@ -793,8 +790,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
               for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-              tile_top[w][r] = top * qf[w].scale[r];
-              top = fmaxf(tile_top[w][r], mx[w][r]);
+              top = fmaxf(top * qf[w].scale[r], mx[w][r]);
               base[r] = top == -INFINITY ? 0.f : top;
               corr[r] = ex2(mx[w][r] - base[r]);
               mx[w][r] = top;
@@ -817,9 +813,6 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
                 s[w][i][2 * r + 1] = ex2(s[w][i][2 * r + 1]);
                 fadd2(sum[w][r][0], sum[w][r][1], s[w][i][2 * r], s[w][i][2 * r + 1]);
               }
-            // (a thread's sum is over a quarter of the columns)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) heavy |= ex2(tile_top[w][r] - base[r]) > 0.25f * (sum[w][r][0] + sum[w][r][1]);
           }
 
           // A token that a row does not see meets it with weight 0, and 0 times its
@@ -842,20 +835,30 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             }
           }
           bad = __any_sync(0xffffffffu, bad);
-          auto values = [&](auto clean, auto with_rest) {
-            constexpr bool kClean = decltype(clean)::value, kRest = decltype(with_rest)::value && !E8;
+          auto values = [&](auto clean) {
+            constexpr bool kClean = decltype(clean)::value;
 #pragma unroll
             for (int t = 0; t < NT / 16; ++t) {
-              // fp16 holds a probability to 11 bits, bf16 to 8 only: where one token weighs much, its rest goes in
-              // as a second operand; else 16 and more roundings of either sign are added
-              uint32_t p[RPW][4], rest[RPW][4];
+              // fp16 holds a weight to 11 bits, which an E4M3 value's 4 leave unseen.  bf16 holds 8, no more than the
+              // output: the weight's upper half goes in as it is and the rest as a second operand, 16 bits together
+              // (66 for 64 us and 152 for 143 us in the two bf16 cases above).
+              // The rest of a weight that is not 0 is not 0 either (its last bit is set first), so that an
+              // infinite value times it is that infinity and not NaN.
+              uint32_t p[RPW][4];
+              [[maybe_unused]] uint32_t rest[RPW][E8 ? 1 : 4];
 #pragma unroll
               for (int w = 0; w < RPW; ++w)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                   const float lo = s[w][2 * t + (x >> 1)][2 * (x & 1)], hi = s[w][2 * t + (x >> 1)][2 * (x & 1) + 1];
-                  p[w][x] = E8 ? pack_f16(lo, hi) : pack_bf16(lo, hi);
-                  rest[w][x] = !kRest ? 0u : pack_bf16(lo - bf16_lo(p[w][x]), hi - bf16_hi(p[w][x]));
+                  if constexpr (E8) {
+                    p[w][x] = pack_f16(lo, hi);
+                  } else {
+                    const uint32_t l = __float_as_uint(lo), h = __float_as_uint(hi);
+                    p[w][x] = __byte_perm(l, h, 0x7632);
+                    rest[w][x] = pack_bf16(__uint_as_float(l | 1u) - __uint_as_float(l & 0xFFFF0000u),
+                                           __uint_as_float(h | 1u) - __uint_as_float(h & 0xFFFF0000u));
+                  }
                 }
 #pragma unroll
               for (int d = 0; d < D / 16; d += E8 ? 2 : 1) {
@@ -869,10 +872,8 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
                   for (int w = 0; w < RPW; ++w) {
                     mma_bf16_16816(o[w][2 * d], p[w], b[0], b[1]);
                     mma_bf16_16816(o[w][2 * d + 1], p[w], b[2], b[3]);
-                    if (kRest) {
-                      mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
-                      mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
-                    }
+                    mma_bf16_16816(o[w][2 * d], rest[w], b[0], b[1]);
+                    mma_bf16_16816(o[w][2 * d + 1], rest[w], b[2], b[3]);
                   }
                 } else {
                   // a chunk's 16 dims come in pairs: even and odd dims become one tile each
@@ -893,10 +894,9 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             }
           };
           if (!bad) {
-            if (E8 || !__any_sync(0xffffffffu, heavy)) values(std::false_type{}, std::false_type{});
-            else values(std::false_type{}, std::true_type{});
+            values(std::false_type{});
           } else {
-            values(std::true_type{}, std::true_type{});
+            values(std::true_type{});
 #pragma unroll 1
             for (int t = 0; t < NT; ++t) {
               if (t % RPI == 0) bad = row_bad(t);
