@@ -274,7 +274,8 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
  * sees no token, and rows i >= m_b: out 0, lse -inf.  What a row does not see
  * never reaches it, whatever is stored there.  Scores, softmax statistics and
  * sums are fp32; probabilities enter the second product as two bf16 operands
- * that hold 16 of their bits (for an E4M3 cache as one in fp16).
+ * that hold 16 of their bits (for an E4M3 cache as one in fp16: 11 bits, fewer
+ * below 2^-29 of the row's largest, none below 2^-40).
  * workspace: qmm_paged_attention_workspace() bytes, 16-byte aligned, not shared
  * by calls that may run at the same time; contents need no initialisation.
  * Alignment as qmm_kv_append (q and out too).                                 */

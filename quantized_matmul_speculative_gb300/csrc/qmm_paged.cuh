@@ -18,7 +18,11 @@
 //
 // The mathematics.  One pass with running maximum m and sum l per row, in
 // base-2 exponents: s = q.k scale log2(e), p = 2^(s - m'), o = o 2^(m - m') +
-// p v, l likewise; o / l and (m + log2 l) ln 2 at the end.
+// p v, l likewise; o / l and (m + log2 l) ln 2 at the end.  An E4M3 cache's m is
+// the maximum less kLift: weights go up to 2^15 then, the upper end of the fp16
+// that they enter the second product in, so that those down to 2^-29 of the
+// row's largest keep 11 bits and only those below 2^-40 vanish (2^-14 and 2^-25
+// without: many tokens far below one vanished from o and not from l).
 //
 // What bounds it: a worker's chain load -> scores -> maximum -> weights ->
 // output products, a tile at a time, with two or three warps a scheduler to
@@ -41,6 +45,7 @@ namespace qmm {
 
 constexpr int kJoinThreads = 128;
 constexpr int kMaxWorkers = 12;  // of a CTA, at most
+constexpr float kLift = 15.f;
 
 struct AttentionArgs {
   qmm_paged_cache c;
@@ -418,6 +423,13 @@ __device__ __forceinline__ void load_query(const AttentionArgs& a, Query<N, E8>&
   }
 }
 
+// The natural logarithm of a row's sum l relative to its m (see above; the lift is taken back first, exactly).
+template <bool E8>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  if constexpr (E8) return (m + kLift + log2f(l * (1.f / (1 << static_cast<int>(kLift))))) * 0.6931471805599453f;
+  else return (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Output column of element e (0, 1) of accumulator tile ot.
 template <bool E8>
 __device__ __forceinline__ int out_col(int ot, int e) {
@@ -790,7 +802,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
               for (int i = 1; i < NT / 8; ++i) top = max3(top, s[w][i][2 * r], s[w][i][2 * r + 1]);
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-              top = fmaxf(top * qf[w].scale[r], mx[w][r]);
+              top = fmaxf(E8 ? fmaf(top, qf[w].scale[r], -kLift) : top * qf[w].scale[r], mx[w][r]);
               base[r] = top == -INFINITY ? 0.f : top;
               corr[r] = ex2(mx[w][r] - base[r]);
               mx[w][r] = top;
@@ -839,7 +851,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
             constexpr bool kClean = decltype(clean)::value;
 #pragma unroll
             for (int t = 0; t < NT / 16; ++t) {
-              // fp16 holds a weight to 11 bits, which an E4M3 value's 4 leave unseen.  bf16 holds 8, no more than the
+              // fp16 holds a weight (up to 2^kLift) to 11 bits, which an E4M3 value's 4 leave unseen.  bf16 holds 8, no more than the
               // output: the weight's upper half goes in as it is and the rest as a second operand, 16 bits together
               // (66 for 64 us and 152 for 143 us in the two bf16 cases above).
               // The rest of a weight that is not 0 is not 0 either (its last bit is set first), so that an
@@ -969,7 +981,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           f[r] = some ? a.v_scale / l : 0.f;
           const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
           to[r] = a.out + at * D;
-          if (a.lse != nullptr && (lane & 3) == 0) a.lse[at] = some ? (mx[w][r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (a.lse != nullptr && (lane & 3) == 0) a.lse[at] = some ? log_sum<E8>(mx[w][r], l) : -INFINITY;
         }
       }
       if (!whole) {
@@ -1137,7 +1149,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
         for (int j = 0; j < IW; ++j)
           *reinterpret_cast<uint32_t*>(to + out_col<false>(i0 + j, 0)) = some ? pack_bf16(o[j][2 * r] * f, o[j][2 * r + 1] * f) : 0u;
       }
-      if (a.lse != nullptr && i0 == 0 && (lane & 3) == 0) a.lse[at] = some ? (t[r] + log2f(l[r])) * 0.6931471805599453f : -INFINITY;
+      if (a.lse != nullptr && i0 == 0 && (lane & 3) == 0) a.lse[at] = some ? log_sum<E8>(t[r], l[r]) : -INFINITY;
     }
   }
 }

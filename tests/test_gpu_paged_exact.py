@@ -79,3 +79,23 @@ def test_infinite_values_that_a_row_sees(D, M, Hq, token):
         assert torch.equal(o1[0, ~sees], o0[0, ~sees])
         rest = torch.arange(D, device="cuda") != 3
         assert torch.equal(o1[..., rest], o0[..., rest])
+
+
+@pytest.mark.parametrize("D,M,Hq", [(64, 1, 4), (64, 4, 8), (128, 1, 1), (256, 1, 2)])
+@pytest.mark.parametrize("n,where", [(3000, 0), (3000, 2999), (40000, 17)])
+def test_light_tokens_of_an_e4m3_cache(D, M, Hq, n, where):
+    """One token leads a row and has value 0; the others, e^-18 (2^-26) of it, are all that the output is made of."""
+    c = Cache([n], 1, D, 16, torch.float8_e4m3fn)
+    q = torch.zeros(1, M, Hq, D, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    j = torch.arange(n, device="cuda")
+    k, v = torch.zeros(n, 1, D, device="cuda"), torch.ones(n, 1, D, device="cuda")
+    k[:, :, 0] = -18.0
+    k[where, :, 0], v[where] = 0.0, 0.0
+    for cache, kv, x in ((c.k, 0, k), (c.v, 1, v)):
+        cache.view(torch.uint8)[c.table[0].long()[j // 16], j % 16] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+        c.dense[0][kv] = x.double()
+    out, lse = binding.paged_attention(q, *c.args(), scale=1.0, return_lse=True)
+    o, l, _, bl = reference(q, c, [M], 1.0, 0, 0)
+    assert ((out.double() - o).abs() <= (2.0**-11 + n * 2.0**-24 + 2.0**-9) * o).all(), (out.flatten()[0].item(), o.flatten()[0].item())
+    assert ((lse.double() - l).abs() <= bl).all()
