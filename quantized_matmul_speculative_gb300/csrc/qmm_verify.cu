@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
   auto value = [](T x) { return fmaxf(F32 ? static_cast<float>(x) : bf16_lo(x), -INFINITY); };  // NaN: -inf
   const float temp = a.temperature[b];
   const bool greedy = !(temp > 0.f);
-  const float c = greedy ? 1.f : fmaxf(1.4426950408889634f / temp, 1e-30f);
+  // (finite, so that the largest logit's 0 times it is 0, and not 0, so that -inf times it is -inf)
+  const float c = greedy ? 1.f : fminf(fmaxf(1.4426950408889634f / temp, 1e-30f), 3e38f);
   int drafts = a.draft_lens != nullptr ? a.draft_lens[b] : a.k;
   drafts = drafts < 0 ? 0 : drafts > a.k ? a.k : drafts;
   // draft tid's logit, draft probability and random number: used after the first round
