@@ -292,8 +292,8 @@ size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int h
  * the drafts were certain, q_i(d_i) = 1), draft i is accepted while
  *     uniform[b, i] * q_i(d_i) < p_i(d_i).
  * After n accepted drafts the next token is the v with the largest
- * w(v) / noise[b, v] (noise fp32 [B, V], exponentially distributed, > 0;
- * the lowest v of equals): w = max(p_n - q_n, 0) where draft n was refused
+ * w(v) / noise[b, v] (noise fp32 [B, V], exponentially distributed, > 0; one
+ * that is NaN or negative counts as +inf; the lowest v of equals): w = max(p_n - q_n, 0) where draft n was refused
  * (w = p_n if that is 0 everywhere), w = p_n where all were accepted.
  * temperature[b] <= 0 or NaN is greedy: a draft is accepted if it is the lowest
  * argmax of its row, and the next token is the argmax of row n.

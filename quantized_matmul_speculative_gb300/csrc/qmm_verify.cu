@@ -285,8 +285,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       }
       const float p = ex2((f - top) * c) * inv;
       const float w = q != nullptr ? p - qi : i == d ? 0.f : p;
-      if (w > 0.f) best_of(v[0], at[0], __fdiv_rn(w, ei), i);
-      if (q != nullptr || d >= 0) best_of(v[1], at[1], p > 0.f ? __fdiv_rn(p, ei) : 0.f, i);
+      // (a noise that is NaN or negative makes 0 of any weight, so that some token is always found)
+      if (w > 0.f) best_of(v[0], at[0], fmaxf(__fdiv_rn(w, ei), 0.f), i);
+      if (q != nullptr || d >= 0) best_of(v[1], at[1], p > 0.f ? fmaxf(__fdiv_rn(p, ei), 0.f) : 0.f, i);
     };
     for (int i = i0 + tid; i < i1; i += 4 * kThreads) {
       float f[4], qi[4], ei[4];
