@@ -323,7 +323,11 @@ def small_m(x, wq, scales, biases, bits: int, group_size: int, out=None, out_dty
 
 # ------------------------------------------------- the operators around the product
 # A call of these takes microseconds on the GPU, so their tensors are checked and
-# allocated by the native module (csrc/qmm_torch.cpp).
+# allocated by the native module (csrc/qmm_torch.cpp).  ``stream`` (a torch stream or
+# a cudaStream_t as an integer; None: the current stream) of each: a call on another
+# stream waits for the work that the current one has been given, and its tensors'
+# memory is not handed out again before it is done; what reads its results on the
+# current stream has to wait for it.
 @functools.lru_cache(maxsize=1)
 def _native():
     import torch  # noqa: F401  (loads the libraries that the module links)

@@ -51,10 +51,11 @@ bool is(const at::Tensor& t, at::ScalarType dtype, at::IntArrayRef shape) {
 }
 const void* ptr(const at::Tensor* t) { return t == nullptr ? nullptr : t->data_ptr(); }
 
-// The device and stream of a call.  Outputs and workspaces come from the
-// current stream's memory; a call on another stream waits for that one (the
-// allocator may have handed out memory it still works on) and has them recorded
-// there, so that they are not handed out again before the call is done.
+// The device and stream of a call.  One rule for a call on another stream than the
+// current one: it waits for what the current one has been given so far (the inputs
+// may still be computed there, and the allocator may hand out memory that it still
+// works on), and every tensor of the call is recorded on the other stream, so that
+// its memory is not handed out again before the call is done.
 class Call {
  public:
   Call(const at::Tensor& first, PyObject* stream)
@@ -62,23 +63,24 @@ class Call {
     if (stream != Py_None) {
       const cudaStream_t s = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
       if (PyErr_Occurred()) throw Refused{nullptr, nullptr};
-      if (s != current_.stream()) run_ = c10::cuda::getStreamFromExternal(s, device_.index());
-    }
-  }
-  void here(const at::Tensor* t) const {
-    if (t != nullptr && t->device() != device_) value_error("all tensors must be on one CUDA device");
-  }
-  at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) {
-    at::Tensor t = at::detail::empty_cuda(shape, dtype, device_, std::nullopt);
-    if (run_.stream() != current_.stream()) {
-      if (!waited_) {
+      if (s != current_.stream()) {
+        run_ = c10::cuda::getStreamFromExternal(s, device_.index());
+        other_ = true;
         at::cuda::CUDAEvent e;
         e.record(current_);
         e.block(run_);
-        waited_ = true;
       }
-      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), run_);
     }
+    here(&first);
+  }
+  void here(const at::Tensor* t) const {
+    if (t == nullptr) return;
+    if (t->device() != device_) value_error("all tensors must be on one CUDA device");
+    if (other_) c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), run_);
+  }
+  at::Tensor empty(at::IntArrayRef shape, at::ScalarType dtype) const {
+    const at::Tensor t = at::detail::empty_cuda(shape, dtype, device_, std::nullopt);
+    here(&t);
     return t;
   }
   void* stream() const { return run_.stream(); }
@@ -91,7 +93,7 @@ class Call {
   }
   c10::Device device_;
   c10::cuda::CUDAStream current_, run_;
-  bool waited_ = false;
+  bool other_ = false;
 };
 
 PyObject* one(const at::Tensor& t) { return THPVariable_Wrap(t); }
