@@ -14,6 +14,7 @@ from pathlib import Path
 import numpy as np
 
 LIBRARY = Path(__file__).resolve().parent / "libqmm.so"
+MODULE = LIBRARY.with_name("_qmm_torch.so")
 
 STATUS = {
     0: "QMM_OK",
@@ -336,7 +337,8 @@ def _native():
     try:
         from . import _qmm_torch
     except ImportError as e:
-        raise RuntimeError("_qmm_torch.so is not built; run __graft_entry__.build() "
+        what = "does not load here" if MODULE.exists() else "is not built"
+        raise RuntimeError(f"{MODULE.name} {what} ({e}); run __graft_entry__.build() "
                            "or quantized_matmul_speculative_gb300/build.py") from e
     return _qmm_torch
 

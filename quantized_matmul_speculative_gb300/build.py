@@ -1,6 +1,10 @@
 """Build libqmm.so (all CUDA kernels and the C ABI) for sm_103a with nvcc, and
 _qmm_torch.so (the native half of the binding for the operators around the product) with g++.
 
+The library needs neither PyTorch nor g++: it is linked first, whatever becomes of
+the module, which is left out where PyTorch is not installed and made again for
+another version of it or of Python.
+
 Each (bits, group size) instantiation of the tensor-core kernels is its own
 translation unit; they compile in parallel.  Objects go to ``_build/`` and the
 library lands next to this file.  A rebuild happens only when a source or
@@ -8,6 +12,8 @@ header is newer than the library.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,6 +29,7 @@ INCLUDE = ROOT / "include"
 BUILD = ROOT / "_build"
 LIBRARY = PKG / "libqmm.so"
 MODULE = PKG / "_qmm_torch.so"
+MODULE_MADE_FOR = BUILD / "qmm_torch.for"  # what module_target() was when the module was linked
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -59,17 +66,39 @@ def _inputs():
     return files
 
 
+def torch_root() -> Path | None:
+    """Folder of the installed PyTorch, without importing it; None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None or spec.origin is None else Path(spec.origin).resolve().parent
+
+
+def module_target() -> str:
+    """The PyTorch and the Python that a module built now is for; empty without PyTorch."""
+    root = torch_root()
+    if root is None:
+        return ""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"{version} {root} {sys.implementation.cache_tag}"
+
+
+def _newer(target: Path) -> bool:
+    return target.exists() and all(f.stat().st_mtime <= target.stat().st_mtime for f in _inputs())
+
+
+def module_up_to_date() -> bool:
+    target = module_target()
+    return not target or (_newer(MODULE) and MODULE_MADE_FOR.exists() and MODULE_MADE_FOR.read_text() == target)
+
+
 def up_to_date() -> bool:
-    if not LIBRARY.exists() or not MODULE.exists():
-        return False
-    lib_t = min(LIBRARY.stat().st_mtime, MODULE.stat().st_mtime)
-    return all(f.stat().st_mtime <= lib_t for f in _inputs())
+    return _newer(LIBRARY) and module_up_to_date()
 
 
 def _torch_paths():
-    import torch
-
-    root = Path(torch.__file__).resolve().parent
+    root = torch_root()
     include = [root / "include", root / "include/torch/csrc/api/include", sysconfig.get_paths()["include"],
                Path(nvcc()).resolve().parent.parent / "include", INCLUDE]
     return [f"-I{p}" for p in include], root / "lib"
@@ -83,9 +112,19 @@ def _run(cmd, what: str):
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> Path:
-    if not force and up_to_date():
-        return LIBRARY
     BUILD.mkdir(exist_ok=True)
+    library, module = force or not _newer(LIBRARY), force or not module_up_to_date()
+    jobs = jobs or min(len(units()), os.cpu_count() or 4)
+    with ThreadPoolExecutor(max_workers=jobs + 1) as ex:
+        module_object = ex.submit(compile_module) if module else None
+        if library:
+            build_library(ex, verbose)
+    if module_object is not None and module_object.result() is not None:  # (raises what the compilation did)
+        link_module(module_object.result())
+    return LIBRARY
+
+
+def build_library(ex: ThreadPoolExecutor, verbose: bool = False):
     cc = nvcc()
 
     def compile_one(unit):
@@ -95,31 +134,33 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             cmd.insert(1, "-Xptxas=-v")
         return obj, _run(cmd, f"nvcc for {obj.name}")
 
-    def compile_module():
-        flags, _ = _torch_paths()
-        obj = BUILD / "qmm_torch.o"
-        _run(["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", str(CSRC / "qmm_torch.cpp"), "-o", str(obj)],
-             f"g++ for {obj.name}")
-        return obj
-
-    jobs = jobs or min(len(units()), os.cpu_count() or 4)
-    with ThreadPoolExecutor(max_workers=jobs) as ex:
-        module = ex.submit(compile_module)
-        results = list(ex.map(compile_one, units()))
-        module_object = module.result()
+    results = list(ex.map(compile_one, units()))
     if verbose:
         for obj, log in results:
             print(f"== {obj.name}\n{log}", file=sys.stderr)
     tmp = LIBRARY.with_name(f"libqmm.{os.getpid()}.tmp.so")
-    cmd = [cc, *ARCH, "-shared", "-o", str(tmp), *[str(o) for o, _ in results]]
-    _run(cmd, "link")
+    _run([cc, *ARCH, "-shared", "-o", str(tmp), *[str(o) for o, _ in results]], "link")
     os.replace(tmp, LIBRARY)
+
+
+def compile_module() -> Path | None:
+    """Object of the native half of the binding; None where there is no PyTorch to build it for."""
+    if not module_target():
+        return None
+    flags, _ = _torch_paths()
+    obj = BUILD / "qmm_torch.o"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", str(CSRC / "qmm_torch.cpp"), "-o", str(obj)],
+         f"g++ for {obj.name}")
+    return obj
+
+
+def link_module(obj: Path):
     _, torch_lib = _torch_paths()
     tmp = MODULE.with_name(f"_qmm_torch.{os.getpid()}.tmp.so")
-    _run(["g++", "-shared", "-o", str(tmp), str(module_object), f"-L{PKG}", "-lqmm", f"-L{torch_lib}", "-ltorch_python",
+    _run(["g++", "-shared", "-o", str(tmp), str(obj), f"-L{PKG}", "-lqmm", f"-L{torch_lib}", "-ltorch_python",
           "-ltorch_cuda", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"], "module link")
     os.replace(tmp, MODULE)
-    return LIBRARY
+    MODULE_MADE_FOR.write_text(module_target())
 
 
 if __name__ == "__main__":
