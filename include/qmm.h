@@ -47,6 +47,12 @@
  * host before anything is launched; a validation failure returns an error and
  * launches nothing.  There is no CPU fallback.  The library allocates no device
  * memory and keeps no per-call state.  X, Wq, scales, biases must not overlap Y.
+ * The small-M calls copy Wq, scales and biases before the stream's preceding
+ * kernels have been waited for, as far as these let their dependents start early
+ * (programmatic dependent launch).  So a kernel that writes weights must not
+ * release its dependents early.  None of this library's does: what
+ * qmm_quantize_mx, qmm_from_ggml and qmm_repack write may be the weights of the
+ * next call on the stream, with nothing in between.
  */
 #ifndef QMM_H_
 #define QMM_H_
@@ -202,7 +208,8 @@ qmm_status qmm_small_m_mx(const void* X, const uint32_t* Wq, const uint8_t* scal
  * the even code, beyond the largest value to the largest; the sign of x stays.
  * s = 0 gives codes 0 (with x's signs).  A group that holds a NaN or an
  * infinity gets a NaN scale (255; nvfp4 0x7F) and codes +0.
- * Wq [R, K*bits/32] and scales [R, K/g] have the layout qmm_small_m_mx reads.
+ * Wq [R, K*bits/32] and scales [R, K/g] have the layout qmm_small_m_mx reads, and
+ * may be the weights of the next call on the stream (see Execution).
  * values: null, or bf16 [R, K]: what the codes stand for, s * value(code) (to
  * nearest even where bf16 cannot hold it: mxfp8 below 2^-130 only).
  * K must be a multiple of 32 (QMM_ERR_SHAPE); X and values are aligned to

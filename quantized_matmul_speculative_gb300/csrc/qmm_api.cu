@@ -19,6 +19,7 @@
 
 #include "../../include/qmm.h"
 #include "qmm_geometry.h"
+#include "qmm_device.cuh"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -731,6 +732,7 @@ ggml_to_affine_kernel(const uint8_t* __restrict__ blocks, int64_t nblk, uint32_t
   const bool vec = (reinterpret_cast<uintptr_t>(Wq) & 15) == 0;
   for (int t = threadIdx.x; t < count; t += kGgmlThreads)
     convert_ggml_block<TYPE>(span + t * kBytes, first + t, Wq, S, B, vec);
+  publish_weights();
 }
 
 }  // namespace qmm

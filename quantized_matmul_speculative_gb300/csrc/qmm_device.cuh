@@ -311,6 +311,19 @@ __device__ __forceinline__ void griddep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// At the end of a kernel that writes weights, by all its threads.  The products copy
+// weights ahead of griddepcontrol.wait, which a grid may do whose prerequisite never
+// issues griddepcontrol.launch_dependents: it starts when all CTAs of that one have
+// completed.  So a kernel that calls this must not release its dependents, and its
+// stores are performed, for the copies' proxy too, before its CTAs exit.  Quantising
+// 34816 x 5120 to nvfp4 takes 121 us with it and 116.5 without (124 with a fence a
+// thread).
+__device__ __forceinline__ void publish_weights() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) __threadfence();
+}
+
 // Vector load of 1, 2 or 4 consecutive 32-bit words from shared memory (the
 // address is aligned to the vector size by construction).
 template <int N>

@@ -151,8 +151,8 @@ qmm_mma_kernel(const MmaParams p) {
   const uint16_t* Bg = p.B;
   const bool gathered = p.rhs != nullptr;
   // Programmatic dependent launch: the next kernel may start now.  Until the
-  // previous one has finished, only the weights (which it cannot have
-  // written) are touched: a plain call pulls its CTA's weight rows and
+  // previous one has finished, only the weights (which it has not written, or
+  // else completed before this one started: publish_weights) are touched: a plain call pulls its CTA's weight rows and
   // scales/biases into L2.  X, the index lists and Y come after the wait.
   griddep_launch_dependents();
   if (!gathered) {

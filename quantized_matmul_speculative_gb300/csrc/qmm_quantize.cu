@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a) {
       }
     }
   }
+  publish_weights();  // (what follows may be the product that reads them)
 }
 
 template <int FMT, bool F32>
