@@ -45,18 +45,21 @@ __device__ __forceinline__ void ld_stream<8>(uint32_t (&d)[8], const uint32_t* p
                : "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7]) : "l"(p + 4));
 }
 
-// Read-only 16-byte load of activations (cached: every CTA of a row tile reads them).
-__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+// 16-byte load of activations (cached: every CTA of a row tile reads them).  The
+// kernel before may write them until griddepcontrol.wait returns: neither a load
+// that the compiler may move nor one of the read-only path, which is for data that
+// nobody writes while the kernel runs.
+__device__ __forceinline__ uint4 ld_after_wait_v4(const void* p) {
   uint4 v;
-  asm("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
   return v;
 }
 
-// Read-only 8-byte load of activations.
-__device__ __forceinline__ uint2 ld_nc_v2(const void* p) {
+// The same, 8 bytes.
+__device__ __forceinline__ uint2 ld_after_wait_v2(const void* p) {
   uint2 v;
-  asm("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
   return v;
 }
 

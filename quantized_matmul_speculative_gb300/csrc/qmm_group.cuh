@@ -82,7 +82,7 @@ struct GroupMath {
         const uint16_t* src =
             X + static_cast<int64_t>(m) * K + static_cast<int64_t>(g0 + j) * GS + (u - unit * CH) * VPW;
 #pragma unroll
-        for (int q8 = 0; q8 < TQ; ++q8) v[b][q8] = (u < ntask) ? ld_nc_v4(src + 8 * q8) : make_uint4(0, 0, 0, 0);
+        for (int q8 = 0; q8 < TQ; ++q8) v[b][q8] = (u < ntask) ? ld_after_wait_v4(src + 8 * q8) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
@@ -136,7 +136,7 @@ struct GroupMath {
         const int j = unit - m * gp;
         const uint16_t* src =
             X + static_cast<int64_t>(m) * Kr + static_cast<int64_t>(g0 + j) * GSR + (u - unit * CH) * 4;
-        v[b] = (u < ntask) ? ld_nc_v2(src) : make_uint2(0, 0);
+        v[b] = (u < ntask) ? ld_after_wait_v2(src) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
@@ -176,7 +176,7 @@ struct GroupMath {
         const int m = static_cast<int>((static_cast<unsigned long long>(unit) * gp_magic) >> 32);
         const int j = unit - m * gp;
         const uint16_t* src = X + static_cast<int64_t>(m) * K + static_cast<int64_t>(g0 + j) * GS + (u - unit * CH) * 4;
-        v[b] = (u < ntask) ? ld_nc_v2(src) : make_uint2(0, 0);
+        v[b] = (u < ntask) ? ld_after_wait_v2(src) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {

@@ -242,7 +242,7 @@ qmm_mma_kernel(const MmaParams p) {
 #pragma unroll
         for (int wc = 0; wc < C::GW; ++wc) {
           uint2 v = make_uint2(0, 0);
-          if (m < M) v = ld_nc_v2(p.X + xrow(m) * (p.K / 2) + k0 / 2 + 4 * wc);
+          if (m < M) v = ld_after_wait_v2(p.X + xrow(m) * (p.K / 2) + k0 / 2 + 4 * wc);
           const uint32_t h0 = bf16x2_times16(v.x), h1 = bf16x2_times16(v.y);
           s += bf16_lo(v.x) + bf16_hi(v.x) + bf16_lo(v.y) + bf16_hi(v.y);
           uint2* d2 = reinterpret_cast<uint2*>(dst + wc * C::VPW);
@@ -254,7 +254,7 @@ qmm_mma_kernel(const MmaParams p) {
 #pragma unroll
         for (int wc = 0; wc < C::GW; ++wc) {
           uint2 v = make_uint2(0, 0);
-          if (m < M) v = ld_nc_v2(p.X + xrow(m) * p.K + k0 + 4 * wc);
+          if (m < M) v = ld_after_wait_v2(p.X + xrow(m) * p.K + k0 + 4 * wc);
           s += bf16_lo(v.x) + bf16_hi(v.x) + bf16_lo(v.y) + bf16_hi(v.y);
           *reinterpret_cast<uint2*>(dst + wc * C::VPW) = make_uint2(prmt_lo(v.x, v.y), prmt_hi(v.x, v.y));
         }
@@ -264,7 +264,7 @@ qmm_mma_kernel(const MmaParams p) {
           uint4 v[C::VPW / 8];
 #pragma unroll
           for (int q = 0; q < C::VPW / 8; ++q) {
-            if (m < M) v[q] = ld_nc_v4(p.X + xrow(m) * p.K + k0 + wc * C::VPW + 8 * q);
+            if (m < M) v[q] = ld_after_wait_v4(p.X + xrow(m) * p.K + k0 + wc * C::VPW + 8 * q);
             else v[q] = make_uint4(0, 0, 0, 0);
           }
           const uint32_t* e = reinterpret_cast<const uint32_t*>(v);  // VPW/2 words of bf16 pairs

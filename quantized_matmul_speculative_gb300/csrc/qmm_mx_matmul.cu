@@ -153,10 +153,10 @@ struct ScaleRow {
         const uint8_t* const p = next + h * 4 * SFW;
         if (ALIGNED || (p >= begin && p + 4 * SFW <= end)) {
           if constexpr (SFW == 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
             w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
           } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
             w[2 * h] = v.x, w[2 * h + 1] = v.y;
           }
         } else {
@@ -165,7 +165,7 @@ struct ScaleRow {
 #pragma unroll 1
           for (int i = 0; i < 4 * SFW; ++i)
             if (p + i >= begin && p + i < end) {
-              const uint32_t byte = static_cast<uint32_t>(__ldg(p + i)) << (8 * (i & 3));
+              const uint32_t byte = static_cast<uint32_t>(p[i]) << (8 * (i & 3));
 #pragma unroll
               for (int x = 0; x < SFW; ++x)
                 if (x == i >> 2) w[h * SFW + x] |= byte;
@@ -323,12 +323,12 @@ struct PairFeed : ScaleStage<SFW, XB> {
 #pragma unroll
     for (int b = 0; b <= XB; ++b) {
       if constexpr (SFW == 4)
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(c[b][0]), "=r"(c[b][1]), "=r"(c[b][2]), "=r"(c[b][3]), "=r"(c[b][4]), "=r"(c[b][5]),
-                       "=r"(c[b][6]), "=r"(c[b][7]) : "l"(next[b]));
+                       "=r"(c[b][6]), "=r"(c[b][7]) : "l"(next[b]) : "memory");
       else
-        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(c[b][0]), "=r"(c[b][1]), "=r"(c[b][2]), "=r"(c[b][3]) : "l"(next[b]));
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c[b][0]), "=r"(c[b][1]), "=r"(c[b][2]), "=r"(c[b][3]) : "l"(next[b]) : "memory");
       next[b] += kScaleGroups * 8 * SFW;
     }
   }

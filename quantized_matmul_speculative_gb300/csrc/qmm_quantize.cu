@@ -40,14 +40,14 @@ struct Eight {
   __device__ __forceinline__ void load(const void* p) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = ld_nc_v4(static_cast<const uint4*>(p) + i);
+      for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = ld_after_wait_v4(static_cast<const uint4*>(p) + i);
     } else {
       uint32_t u[F32 ? 8 : 4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (F32) u[i] = __float_as_uint(__ldg(static_cast<const float*>(p) + i));
-        else if (i & 1) u[i / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16;
-        else u[i / 2] = __ldg(static_cast<const uint16_t*>(p) + i);
+        if constexpr (F32) u[i] = __float_as_uint(static_cast<const float*>(p)[i]);
+        else if (i & 1) u[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16;
+        else u[i / 2] = static_cast<const uint16_t*>(p)[i];
       }
 #pragma unroll
       for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       for (; v + 3 * threads < v1; v += 4 * threads) {
         uint4 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __ldg(xv + v + j * threads);
+        for (int j = 0; j < 4; ++j) w[j] = xv[v + j * threads];
 #pragma unroll
         for (int j = 0; j < 4; j += U) take(w + j, U, v + j * threads);
       }
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (v + j * threads < v1) {
-            w[j] = __ldg(xv + v + j * threads);
+            w[j] = xv[v + j * threads];
             count = j + 1;
           }
 #pragma unroll
@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
       for (int j = 0; j < 4; ++j) {
         const int at_j = min(i + j * kThreads, i1 - 1);  // (again what the last one reads)
         f[j] = value(x[at_j]);
-        qi[j] = q != nullptr ? __ldg(q + at_j) : 0.f;
-        ei[j] = __ldg(e + at_j);
+        qi[j] = q != nullptr ? q[at_j] : 0.f;
+        ei[j] = e[at_j];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) look(min(i + j * kThreads, i1 - 1), f[j], qi[j], ei[j]);
