@@ -413,7 +413,8 @@ __device__ __forceinline__ void load_query(const AttentionArgs& a, Query<N, E8>&
       const int e = static_cast<int>(__float_as_uint(top) >> 23);
       const int up = (e < 30 || e == 255) ? 0 : 14 + 127 - e;  // exponent of the factor
       const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-      f.scale[r] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+      // (not 0 either: a masked score of -inf stays -inf)
+      f.scale[r] = fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1e-30f);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         f.a[kk][r] = pack_f16(bf16_lo(x[kk].x) * f1, bf16_hi(x[kk].x) * f1);

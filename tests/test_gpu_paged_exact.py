@@ -12,7 +12,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from quantized_matmul_speculative_gb300 import binding
-from test_gpu_paged import Cache, queries, reference
+from test_gpu_paged import Cache, check, queries, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,12 @@ def test_light_tokens_of_an_e4m3_cache(D, M, Hq, n, where):
     o, l, _, bl = reference(q, c, [M], 1.0, 0, 0)
     assert ((out.double() - o).abs() <= (2.0**-11 + n * 2.0**-24 + 2.0**-9) * o).all(), (out.flatten()[0].item(), o.flatten()[0].item())
     assert ((lse.double() - l).abs() <= bl).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("scale", [0.0, 1e-38, 1e-28, -1e-28])
+@pytest.mark.parametrize("size", [1e-25, 1e-20, 1.0])
+def test_vanishing_scores(size, scale, dtype):
+    """Queries and scales whose products are nothing beside 1: every row's mean over what it sees, and no more."""
+    c = Cache([77, 3], 2, 128, 16, dtype, seed=6)
+    check(c, (queries(2, 4, 8, 128).float() * size).bfloat16(), scale=scale)
