@@ -277,7 +277,8 @@ qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_
  *     out[b,i,h] = sum_j softmax_j(scale * q[b,i,h] . k[j,h / G]) v[j,h / G],
  * G = q_heads / cache heads (a whole number up to 1024).  q: bf16, row b*M + i q_ld
  * elements apart, q_heads * D contiguous; out: bf16 [B, M, q_heads, D]; lse:
- * null or fp32 [B, M, q_heads], log sum_j exp(scale * q . k_j).  A row that
+ * null or fp32 [B, M, q_heads], log sum_j exp(scale * q . k_j).  scale is finite,
+ * and an E4M3 cache's k_scale times it too (else QMM_ERR_UNSUPPORTED).  A row that
  * sees no token, and rows i >= m_b: out 0, lse -inf.  What a row does not see
  * never reaches it, whatever is stored there.  Scores, softmax statistics and
  * sums are fp32; probabilities enter the second product as two bf16 operands

@@ -147,6 +147,9 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || q_heads / cache->heads > 1024 || window < 0 || sinks < 0 ||
       q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)
     return QMM_ERR_SHAPE;
+  const bool e8 = cache->dtype == QMM_KV_E4M3;
+  const float scale_log2 = scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f);
+  if (!std::isfinite(scale_log2)) return QMM_ERR_UNSUPPORTED;
   if (B == 0 || M == 0) return QMM_OK;
   if (q == nullptr || out == nullptr) return QMM_ERR_NULL;
   if (misaligned(reinterpret_cast<intptr_t>(q), 16) || misaligned(reinterpret_cast<intptr_t>(out), 16) ||
@@ -155,7 +158,6 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
     return QMM_ERR_ALIGN;
   if (workspace == nullptr) return QMM_ERR_NULL;
   if (misaligned(reinterpret_cast<intptr_t>(workspace), 16)) return QMM_ERR_ALIGN;
-  const bool e8 = cache->dtype == QMM_KV_E4M3;
   AttentionArgs a = {};
   a.c = *cache;
   a.q = static_cast<const uint16_t*>(q);
@@ -166,7 +168,7 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   a.G = q_heads / cache->heads;
   a.q_lens = q_lens;
   // at least 1e-30: a masked score of -inf stays -inf, and no finite score of use is told from 0 by less
-  a.scale_log2 = std::fmax(std::fabs(scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f)), 1e-30f);
+  a.scale_log2 = std::fmax(std::fabs(scale_log2), 1e-30f);
   a.negate = scale < 0.f;
   a.v_scale = e8 ? cache->v_scale : 1.f;
   a.window = window;
