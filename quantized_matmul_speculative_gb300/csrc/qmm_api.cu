@@ -342,6 +342,11 @@ qmm_status fail_cuda(cudaError_t e) {
 
 int finish_call(cudaError_t e) { return e == cudaSuccess ? QMM_OK : fail_cuda(e); }
 
+bool injected_short_wait() {
+  const char* inject = std::getenv("QMM_TEST_INJECT");
+  return inject != nullptr && std::strcmp(inject, "short_wait") == 0;
+}
+
 bool injected_launch_failure() {
   const char* inject = std::getenv("QMM_TEST_INJECT");
   return inject != nullptr && std::strcmp(inject, "launch_fail") == 0;

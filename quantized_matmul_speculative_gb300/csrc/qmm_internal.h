@@ -88,6 +88,9 @@ int finish_call(cudaError_t e);
 
 // Host-side fault injection of the error-path tests: launches report an error.
 bool injected_launch_failure();
+// The same, of a wait that runs out: a barrier of the kernel waits for 16 bytes more
+// than its copies bring, with a limit of 100 us.
+bool injected_short_wait();
 
 // Device status word of the paged-cache unit (bit 5: invalid page or length).
 constexpr unsigned int kStatusBadPage = 32u;

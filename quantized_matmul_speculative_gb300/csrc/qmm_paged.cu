@@ -159,6 +159,8 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
   if (workspace == nullptr) return QMM_ERR_NULL;
   if (misaligned(reinterpret_cast<intptr_t>(workspace), 16)) return QMM_ERR_ALIGN;
   AttentionArgs a = {};
+  a.inject = injected_short_wait();
+  a.wait_ns = a.inject ? 100000ull : kWaitLimitNs;
   a.c = *cache;
   a.q = static_cast<const uint16_t*>(q);
   a.q_ld = q_ld;

@@ -67,6 +67,8 @@ struct AttentionArgs {
   int parts;      // workers
   float* part_o;  // [parts][2][RB / 16][D / 8][32 lanes][4], as the MMA leaves them
   float2* part_ml;  // [parts][2][RB]
+  unsigned long long wait_ns;  // limit of a wait for copies
+  int inject;                  // the list's first piece never completes (tests)
   int4* part_seg;   // [parts][2][2] of a part: (b, h, rt, workers that hold the segment; 0: no such part), (the first of them, -, -, -)
 };
 
@@ -591,6 +593,16 @@ struct Stream {
   }
 };
 
+// Waits for the pieces after `slot` and before `next` of a ring, on their way while the one in `slot` is given up.
+// (Not inlined: what it needs would be spilled in the loop that never calls it.)
+static __device__ __noinline__ void drain(uint32_t bars, int slot, int next, int slots, uint32_t phase, unsigned long long wait_ns) {
+  for (int s = slot;;) {
+    s = s + 1 == slots ? 0 : s + 1;
+    if (s == next) return;
+    mbar_wait(bars + s * 8, phase ^ (s < slot), kStatusTimeoutDrain, wait_ns);
+  }
+}
+
 // Rows of segments without tiles: the worker of the sequence's number writes them.
 template <int D>
 __device__ __forceinline__ void empty_rows(const AttentionArgs& a, int worker) {
@@ -650,6 +662,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   const uint32_t bars = sbase + Cfg::OFF_BAR + warp * SLOTS * 8;
   Stream<Cfg, E8> in;
   in.begin(a, cc, sbase + ring_off, bars);
+  if (a.inject && (cc.b | cc.h | cc.rt | cc.kb) == 0 && lane == 0) mbar_expect_tx(bars, 16);
 #pragma unroll 1
   for (int s = 0; s < SLOTS; ++s) in.issue(a, &kmap, &vmap);
 
@@ -661,10 +674,14 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   bool lost = false;
   int slot = 0;        // of the next piece to use
   uint32_t phase = 0;  // of its barrier
-  // A wait that gave up (status bit 0) leaves wrong results, never a hang: later waits are skipped.
+  // A wait that gave up (status bit 0) leaves wrong results, never a hang: the pieces that are still on their way
+  // are waited for (status bit 2 where that gives up too), then no more are asked for and later waits are skipped.
   auto wait = [&]() {
     if (a.box) {
-      if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bars + slot * 8, phase, kStatusTimeoutFull));
+      if (!lost && __any_sync(0xffffffffu, !mbar_wait(bars + slot * 8, phase, kStatusTimeoutFull, a.wait_ns))) {
+        lost = true;
+        drain(bars, slot, in.slot, SLOTS, phase, a.wait_ns);
+      }
     } else {
       cp_async_wait<SLOTS - 1>();
       __syncwarp();
@@ -672,7 +689,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   };
   auto used = [&]() {
     __syncwarp();
-    in.issue(a, &kmap, &vmap);
+    if (!lost) in.issue(a, &kmap, &vmap);
     if (++slot == SLOTS) {
       slot = 0;
       phase ^= 1;
