@@ -65,6 +65,8 @@ struct MxMatmulArgs {
   int pitch;    // scale bytes of a row
   int aligned;  // rows of scales are whole, aligned stages (1), or pairs of them (2)
   uint32_t tmem_cols;
+  unsigned long long wait_ns;  // limit of the waits for a stage
+  int inject;                  // CTA 0's first stage never completes (tests)
 };
 
 // Shared-memory layout (offsets from a 1024-byte aligned start).
@@ -404,6 +406,7 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
     mbar_init(done, 1);
     mbar_init(free, 128 * kScaleGroups);
     fence_mbar_init();
+    if (a.inject && blockIdx.x == 0) mbar_expect_tx(full, 16);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
@@ -420,6 +423,8 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
   // Every role walks the CTA's tiles with a running count of stages, so that the
   // copies for the next tile go on while the last one's outputs are written.  A
   // wait that gave up (a status bit) skips the later ones: wrong results, no hang.
+  // Its role does nothing more to the stages, so that the others give up too, and the
+  // copies under way are waited for (with the limit again) before the CTA ends.
   if (warp == 0) {
     if (lane == 0) {
       bool lost = false;
@@ -436,6 +441,9 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
           tma_load_2d(sbase + s * L.stage + L.x, &xmap, k * (kTileK / 2), m0, full + s * 8);
         }
       }
+      // (the MMAs wait for the same; where one is given up, the limit was time enough for the others)
+      for (int i = max(it - a.stages, 0); i < it; ++i)
+        if (!mbar_wait(full + i % a.stages * 8, (i / a.stages) & 1, kStatusTimeoutDrain, a.wait_ns)) break;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -448,7 +456,8 @@ mx_matmul_kernel(const MxMatmulArgs a, const __grid_constant__ CUtensorMap wmap,
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int k = k_begin; k < k_end; ++k, ++it) {
           const int s = it % a.stages;
-          if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull);
+          if (!lost) lost = !mbar_wait(full + s * 8, (it / a.stages) & 1, kStatusTimeoutFull, a.wait_ns);
+          if (lost) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t base = sbase + s * L.stage;
           const uint32_t sfw = tmem + a.BN + s * (SFW * 4 * (1 + XB)), sfx = sfw + SFW * 4;
@@ -584,6 +593,8 @@ void plan(MxMatmulArgs& a, int sms) {
 template <bool NV>
 cudaError_t launch_mx_matmul(MxMatmulArgs a, const void* Xq, const void* Wq, cudaStream_t stream) {
   if (injected_launch_failure()) return cudaErrorLaunchFailure;
+  a.inject = injected_short_wait();
+  a.wait_ns = a.inject ? 100000ull : kWaitLimitNs;
   constexpr int SFW = NV ? 4 : 2;
   a.ktiles = (a.K + kTileK - 1) / kTileK;
   a.pitch = a.K / (NV ? 16 : 32);

@@ -6,6 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from quantized_matmul_speculative_gb300 import binding
+import test_gpu_matmul_mx as mx
 from test_gpu_paged import Cache, check, queries
 
 pytestmark = pytest.mark.gpu
@@ -26,3 +27,19 @@ def test_attention(monkeypatch, D, M, Hq, lens, dtype):
     monkeypatch.delenv("QMM_TEST_INJECT")
     again, _ = check(c, q)
     assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(8, 300, 1024), (4, 1000, 512), (200, 256, 1024)])
+def test_matmul(monkeypatch, M, N, K, fmt):
+    """The first CTA's products wait in vain for their first stage (which no later one uses again); so does the end of its
+    copies."""
+    x, w = mx.matrix(M, K, fmt, 1), mx.matrix(N, K, fmt, 2)
+    want = mx.check(x, w, fmt, torch.float32)
+    monkeypatch.setenv("QMM_TEST_INJECT", "short_wait")
+    y = binding.matmul_mx(*x, *w, fmt, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 1 | 4
+    assert y.shape == want.shape
+    monkeypatch.delenv("QMM_TEST_INJECT")
+    assert torch.equal(mx.check(x, w, fmt, torch.float32), want)
