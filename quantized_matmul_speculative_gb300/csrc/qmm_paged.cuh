@@ -352,7 +352,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 template <int D, bool E8, int RPW>
 struct AttnCfg {
   // Workers of an SM: as many as their registers allow (spilled ones would go to L2: shared memory takes the
-  // L1's room); seven where eight would have room for two pieces only.
+  // L1's room; only D = 64 with two row tiles spills, 28 bytes a thread in bf16 and 64 in E4M3); seven where eight
+  // would have room for two pieces only.
   static constexpr int WORKERS = D == 256 ? (E8 ? 8 : 7) : D == 64 ? 12 : RPW == 1 ? 10 : 8;
   // Tokens of a tile.  Small ones share a few tokens among more workers and need fewer registers for scores, large
   // ones have less to do beside their products.  D = 64, one row tile, 4 x 1000 tokens and 1 x 65001: 12.4 and 51 us
@@ -462,14 +463,15 @@ __device__ __forceinline__ void cp_async_wait() {
 template <class Cfg, bool E8>
 struct Stream {
   static constexpr int SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
-  static constexpr int CPR = Cfg::ROWB / 16, RPL = (Cfg::TN + 31) / 32, ES = E8 ? 1 : 2, RPI = 32 / CPR;
+  static constexpr int CPR = Cfg::ROWB / 16, ES = E8 ? 1 : 2, RPI = 32 / CPR;
+  static_assert(Cfg::TN <= 32, "a lane finds the page of one token or box of a tile");
   uint32_t ring, bars;  // shared-memory addresses
   Cursor c;             // the segment of the next tile
   int k;
   bool more;            // there is such a tile
   int slot;             // of the next piece
   bool values;          // the next piece is a tile's values
-  int page[RPL], place[RPL], head;  // of the tile that is copied: this lane's tokens (row copies) or boxes
+  int page, place, head;  // of the tile that is copied: this lane's token (row copies) or box
   // Page numbers of the blocks first .. first + 31 of the sequence, a lane each,
   // and of the 32 after them, loaded when the ones before come into use.
   int pages, pages2, first, seq;
@@ -485,22 +487,19 @@ struct Stream {
   // place -1: nobody sees it, page -1: outside the cache.
   __device__ __forceinline__ void find(const AttentionArgs& a) {
     const int lane = threadIdx.x & 31;
-    const int step = a.box ? a.box : 1;                                         // tokens a lane finds the page of
-    const int finders = a.box ? Cfg::TN / a.box : Cfg::TN < 32 ? Cfg::TN : 32;  // lanes that do
+    const int step = a.box ? a.box : 1;                       // tokens a lane finds the page of
+    const int finders = a.box ? Cfg::TN / a.box : Cfg::TN;    // lanes that do
     head = c.h;
     const int t0 = c.tile(k) * Cfg::TN;
-#pragma unroll
-    for (int x = 0; x < RPL; ++x) {
-      const int j = t0 + lane * step + 32 * x;
-      int block = block_of(a, j);
-      place[x] = lane < finders && (x == 0 || !a.box) && seen(a, c, j, step) ? j - block * a.c.page_size : -1;
-      if (place[x] < 0) block = INT_MAX;
-      page[x] = -1;
-      if (c.b == seq && block_of(a, t0) >= first && block_of(a, t0 + Cfg::TN - 1) < first + 32) {
-        const int got = __shfl_sync(0xffffffffu, pages, (block - first) & 31);
-        if (block != INT_MAX) page[x] = got;
-        block = INT_MAX;
-      } else
+    const int j = t0 + lane * step;
+    int block = block_of(a, j);
+    place = lane < finders && seen(a, c, j, step) ? j - block * a.c.page_size : -1;
+    if (place < 0) block = INT_MAX;
+    page = -1;
+    if (c.b == seq && block_of(a, t0) >= first && block_of(a, t0 + Cfg::TN - 1) < first + 32) {
+      const int got = __shfl_sync(0xffffffffu, pages, (block - first) & 31);
+      if (block != INT_MAX) page = got;
+    } else {
       // the lanes' blocks ascend: a window after another until all have been met
       for (;;) {
         const int low = __reduce_min_sync(0xffffffffu, block);
@@ -514,14 +513,14 @@ struct Stream {
         }
         const int got = __shfl_sync(0xffffffffu, pages, (block - first) & 31);
         if (block < first + 32) {
-          page[x] = got;
+          page = got;
           block = INT_MAX;
         }
       }
-      if (place[x] >= 0 && (page[x] < 0 || page[x] >= a.c.num_pages)) {
-        bad_page();
-        page[x] = -1;
-      }
+    }
+    if (place >= 0 && (page < 0 || page >= a.c.num_pages)) {
+      bad_page();
+      page = -1;
     }
     if (++k >= c.ke) {
       more = c.next(a);
@@ -553,35 +552,28 @@ struct Stream {
       if (a.box) {
         const uint32_t full = bars + slot * 8;
         const int per = a.box == 16 ? 1 : SL;  // copies of a box
-        const uint32_t loaded = __ballot_sync(0xffffffffu, place[0] >= 0);
+        const uint32_t loaded = __ballot_sync(0xffffffffu, place >= 0);
         if (lane == 0) mbar_arrive_expect_tx(full, __popc(loaded) * a.box * Cfg::ROWB);
         __syncwarp();
         const int box = lane / per, sl = lane - box * per;  // at most 16 boxes x slices
-        const int p = __shfl_sync(0xffffffffu, page[0], box & 31), s = __shfl_sync(0xffffffffu, place[0], box & 31);
+        const int p = __shfl_sync(0xffffffffu, page, box & 31), s = __shfl_sync(0xffffffffu, place, box & 31);
         if (box * a.box < Cfg::TN && s >= 0) {
           const int token = box * a.box;
           tma_load_5d(base + (token >> 4) * 16 * Cfg::ROWB + sl * 2048 + (token & 15) * ROW, values ? vmap : kmap, 0, s, sl, head,
                       p, full);
         }
       } else {
-        // byte offsets of this lane's tokens from the cache's start, -1: zeros;
-        // they reach the lanes that copy the rows by shuffles
+        // byte offset of this lane's token from the cache's start, -1: zeros; it
+        // reaches the lanes that copy the row by shuffles
         const unsigned long long cache = reinterpret_cast<unsigned long long>(values ? a.c.v : a.c.k);
         const int64_t s_page = values ? a.c.v_page : a.c.k_page, s_token = values ? a.c.v_token : a.c.k_token,
                       s_head = values ? a.c.v_head : a.c.k_head;
-        long long at[RPL];
-#pragma unroll
-        for (int x = 0; x < RPL; ++x)
-          at[x] = place[x] >= 0 && page[x] >= 0 ? (page[x] * s_page + place[x] * s_token + head * s_head) * ES : -1;
+        const long long at = place >= 0 && page >= 0 ? (page * s_page + place * s_token + head * s_head) * ES : -1;
         const int ch = lane % CPR;
 #pragma unroll 4
         for (int g = 0; g < Cfg::TN / RPI; ++g) {
           const int row = g * RPI + lane / CPR;
-          long long r = __shfl_sync(0xffffffffu, at[0], row & 31);
-          if constexpr (RPL == 2) {
-            const long long r2 = __shfl_sync(0xffffffffu, at[1], row & 31);
-            r = row < 32 ? r : r2;
-          }
+          const long long r = __shfl_sync(0xffffffffu, at, row);
           // nothing is read where zeros are filled in
           cp_async_16(base + tile_at<Cfg::ROWB>(row, ch), cache + (r < 0 ? 0 : r) + ch * 16, r >= 0);
         }

@@ -92,10 +92,12 @@ __device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
 // (rounds of two rows, several clusters an SM so that one's exchange overlaps
 // another's reads); the latency of its two exchanges, where there are few (all
 // rows in one round).  The noise is fetched into L2 meanwhile (fetching the next
-// row too gains nothing).  Nothing may spill: joining a row's partials by a
-// thread, not a warp, cost 6 us more, and 8 elements at a time, not 4, in the
-// last pass 10 us.  64 sequences x 5 drafts x 128000 fp32 logits: 63 us, 4.1 TB/s
-// of what it would read were no draft refused; 1 x 7 x 32000 bf16: 10.0 us.
+// row too gains nothing).  Spills in its loops cost most: joining a row's partials
+// by a thread, not a warp, took 6 us more, and 8 elements at a time, not 4, in the
+// last pass 10 us (the bf16 kernel still spills 8 bytes, outside of them).
+// 64 sequences x 5 drafts x 128000 fp32 logits: 64 us for the 108 MB of the rows
+// that it needs and reads (1.7 TB/s; two CTAs of an SM are resident at once, and the
+// longest sequences end alone); 1 x 7 x 32000 bf16: 9.9 us.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   using T = typename std::conditional<F32, float, uint16_t>::type;
@@ -339,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a)
 template <bool F32>
 cudaError_t launch_verify(VerifyArgs a, cudaStream_t stream) {
   if (injected_launch_failure()) return cudaErrorLaunchFailure;
-  // CTAs of a cluster: two to four an SM over all sequences (64 x 5 x 128000:
-  // 66.4 us; one to two 68.1, four to eight 89.9), and no more than one for
-  // every 2048 logits of a row.
+  // CTAs of a cluster: two to four launched for an SM over all sequences, of which
+  // two are resident (64 x 5 x 128000: 66.4 us; one to two 68.1, four to eight
+  // 89.9), and no more than one for every 2048 logits of a row.
   const int sms = device_sm_count();
   a.cluster = 1;
   while (a.cluster < kMaxCluster && static_cast<int64_t>(a.B) * a.cluster <= 2 * sms && a.V > a.cluster * 2048) a.cluster *= 2;
