@@ -23,7 +23,7 @@
 // What bounds it: the scales' way at BN = 256, a stage's taking longer than its
 // 0.26 us of MMAs (without their loads the call took 24 us less, without their
 // stores 12; half the activations' codes changed nothing); a tile of 20 stages has
-// 1.4 us more to its first and 1.5 us to write.  1000 x 34816 x 5120 nvfp4: 93 us,
+// 1.4 us more to its first and 1.5 us to write.  1000 x 34816 x 5120 nvfp4: 94 us,
 // 3.8 PFLOP/s (at 97, with the scales of single stages loaded 111, with a tile a CTA
 // too 131; the activations multicast to the 2 or 4 CTAs of a cluster: 110 and 194 for
 // 111, so not done).  8 x 5120 x 5120 mxfp4: 5.9 us, 2.4 TB/s,

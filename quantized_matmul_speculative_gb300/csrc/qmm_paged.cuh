@@ -28,7 +28,7 @@
 // output products, a tile at a time, with two or three warps a scheduler to
 // cover it; then the start (lengths, table, first pieces: about 5 us) and the
 // join.  One row over 65001 tokens, 8 heads x 128 in bf16: 66 us, 4.0 TB/s;
-// 32 ragged sequences x 8 rows: 152 us, 3.6 TB/s; 16 x 4 rows, a window of
+// 32 ragged sequences x 8 rows: 154 us, 3.5 TB/s; 16 x 4 rows, a window of
 // 4096 tokens, 8 x 64 in E4M3: 57 us; 4 short sequences: 13.6 us.
 #pragma once
 

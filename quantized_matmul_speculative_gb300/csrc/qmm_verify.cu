@@ -95,9 +95,9 @@ __device__ __forceinline__ int ld_dsmem_i32(const int* p, uint32_t rank) {
 // row too gains nothing).  Spills in its loops cost most: joining a row's partials
 // by a thread, not a warp, took 6 us more, and 8 elements at a time, not 4, in the
 // last pass 10 us (the bf16 kernel still spills 8 bytes, outside of them).
-// 64 sequences x 5 drafts x 128000 fp32 logits: 64 us for the 108 MB of the rows
-// that it needs and reads (1.7 TB/s; two CTAs of an SM are resident at once, and the
-// longest sequences end alone); 1 x 7 x 32000 bf16: 9.9 us.
+// 64 sequences x 5 drafts x 128000 fp32 logits: 64 us for 130 MB, of which it needs
+// 108 (2.0 TB/s; two CTAs of an SM are resident at once, and the longest sequences
+// end alone); 1 x 7 x 32000 bf16: 9.9 us.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyArgs a) {
   using T = typename std::conditional<F32, float, uint16_t>::type;
