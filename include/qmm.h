@@ -11,7 +11,11 @@
  * into the microscaled formats (qmm_quantize_mx), their product for any number of
  * rows (qmm_matmul_mx), a paged key-value cache (qmm_kv_append) with attention of
  * 1..16 new rows a sequence over it (qmm_paged_attention), and the verification
- * of drafted tokens (qmm_verify_draft); each is defined at its declaration.
+ * of drafted tokens (qmm_verify_draft); and those of a served layer beside it: the
+ * experts of every token (qmm_route_experts), rotary positions on the way into the
+ * cache (qmm_rope_append), attention of sequences that share a long prefix
+ * (qmm_shared_prefix_attention) and the requests' own low-rank adapters
+ * (qmm_lora_add).  Each is defined at its declaration.
  *
  * Sources of the product's definition (page title, section):
  *   - "MLX quantized_matmul small-M verify kernels", fact "Stock qmv streams
@@ -230,6 +234,45 @@ qmm_status qmm_quantize_mx(const void* X, int x_dtype, int64_t R, int64_t K, int
 qmm_status qmm_matmul_mx(const uint32_t* Xq, const uint8_t* x_scales, const uint32_t* Wq, const uint8_t* w_scales,
                          int M, int N, int K, int format, void* Y, int out_dtype, void* stream);
 
+/* Experts of every token from a router's logits [T, E] (bf16 or fp32, rows ld
+ * elements apart).  With the scores s = softmax(x) or sigmoid(x) and the keys
+ * c = s + bias[e] (bias fp32 [E], null: none; compared in 64 bits)
+ *   the E experts form `groups` groups of neighbours; a group is worth the sum of its
+ *   group_best (1 or 2) best keys, and the top_groups groups worth most are open
+ *   (top_groups == groups: all);
+ *   the k best keys of the open groups are chosen, best first (without a bias the best
+ *   logits), of equals the lowest number;
+ *   weights[t, j] = scale * s, or, with renormalize, scale * s / (sum of the k scores).
+ * The bias chooses; it is not part of the weights.  A NaN logit counts as -inf; an
+ * expert of -inf is chosen last, has weight 0 and adds nothing to its group; +inf
+ * counts as the largest finite number; a NaN key counts as -inf.  Renormalised weights
+ * are ratios of scores however small; where all chosen logits are -inf they are 0.
+ * experts int32 [T, k]: flattened, the list rhs of qmm_gather_small_m for T k <= 256
+ * entries; weights fp32 [T, k].  E <= 512 a multiple of groups <= 32; k <= 32, at most
+ * the experts of top_groups groups.  T == 0 launches nothing.                      */
+typedef enum { QMM_SOFTMAX = 0, QMM_SIGMOID = 1 } qmm_scoring;
+qmm_status qmm_route_experts(const void* logits, int logits_dtype, int64_t ld, const float* bias, int T, int E, int k,
+                             int scoring, int groups, int top_groups, int group_best, int renormalize, float scale,
+                             int32_t* experts, float* weights, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *     Y[t] = base[t] + scales[a] * Bm[a] (A[a] X[t]),  a = adapters[t]
+ * X bf16 [T, K] (rows x_ld apart), A bf16 [L, R, K] and Bm bf16 [L, N, R] contiguous,
+ * adapters int32 [T], scales fp32 [L] (null: 1); base and Y bf16 or fp32 by out_dtype,
+ * rows base_ld and y_ld elements apart; Y may be base (with y_ld == base_ld), and
+ * nothing else may overlap Y.  Sums are fp32, and one rounding to Y's type; the
+ * products with Bm keep 24 bits of A X (16 where Y is bf16).  A row with a negative
+ * number has no adapter: Y[t] = base[t], and X[t] is not read.  A number >= L sets bit 3
+ * of qmm_device_status() and counts as none.  R is a multiple of 8 up to 128 (an adapter
+ * of a smaller rank is padded with zeros), K a multiple of 8, N any; X, A, Bm 16-byte
+ * aligned, x_ld a multiple of 8.  workspace: qmm_lora_workspace(T, L) bytes (it may be
+ * 0, then null will do), 16-byte aligned, not shared by calls that may run at the same
+ * time.  T == 0 or N == 0 launches nothing.                                          */
+qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_t x_ld, const void* A, const void* Bm,
+                        const int32_t* adapters, const float* scales, int T, int N, int K, int R, int L, void* Y,
+                        int64_t y_ld, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+size_t qmm_lora_workspace(int T, int L);
+
 /* A paged key-value cache.  Token j of sequence b lives in page
  * block_table[b][j / page_size] at slot j mod page_size; its key for head h
  * starts at k + page * k_page + slot * k_token + h * k_head (strides in
@@ -271,6 +314,33 @@ typedef struct {
 qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
                          int B, int M, const int32_t* q_lens, void* stream);
 
+/* qmm_kv_append with rotary positions on the way.  A head's elements x[0 .. rot - 1] form
+ * pairs: (x[j], x[j + rot/2]), or with interleaved (x[2j], x[2j + 1]); pair j of a row at
+ * position p turns by t = p * inv_freq[j]:
+ *     (x1, x2) -> factor * (x1 cos t - x2 sin t, x2 cos t + x1 sin t);
+ * elements from rot on stay.  Angles hold at any 32-bit position (inv_freq finite, its
+ * product with p is not rounded); sums are fp32, with one rounding to the output's type.
+ * q (bf16, row b*M + i q_ld elements apart, q_heads * D contiguous) goes to q_out (bf16,
+ * rows q_out_ld apart; it may be q, with q_out_ld == q_ld, and nothing else may overlap
+ * it), the keys to the cache; the values are not turned.  Rows i >= m_b of q_out are 0.
+ * Positions: null, lengths[b] - m_b + i; or int32 [axes][B][M], pair j going by axis 0
+ * for j < sections[0], by axis 1 for the next sections[1], and so on (sections add up
+ * to rot/2; axes <= 4).  They turn only: a key's place in the cache is always that of
+ * its row, as in qmm_kv_append, whose other rules hold too, for any M.  rot is a
+ * multiple of 16 up to D.                                                          */
+typedef struct {
+  const float* inv_freq;    /* device, [rot / 2] */
+  const int32_t* positions; /* device or null */
+  int32_t rot;
+  int32_t axes;
+  int32_t sections[4];
+  int32_t interleaved;
+  float factor;
+} qmm_rope;
+qmm_status qmm_rope_append(const qmm_paged_cache* cache, const qmm_rope* rope, const void* q, int64_t q_ld, int q_heads,
+                           void* q_out, int64_t q_out_ld, const void* k_new, int64_t k_ld, const void* v_new,
+                           int64_t v_ld, int B, int M, const int32_t* q_lens, void* stream);
+
 /* Attention of M = 1..16 new rows of each of B sequences over the cache.  Row
  * i < m_b of sequence b stands at position p = lengths[b] - m_b + i and sees
  * the tokens j <= p with window == 0, or j > p - window, or j < sinks:
@@ -291,6 +361,22 @@ qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int6
                                const int32_t* q_lens, float scale, int window, int sinks, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
 size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int head_dim);
+
+/* qmm_paged_attention of sequences that share their first tokens: tokens
+ * 0 .. P - 1 of every sequence, P = num_prefix_pages * page_size, lie in prefix_pages
+ * (device int32), token P + j of sequence b in page block_table[b][j / page_size]
+ * (max_pages counts the pages of own tokens).  lengths[b] counts all tokens, the prefix
+ * and the new rows among them, and the new rows come after the prefix:
+ * lengths[b] - m_b >= P.  A sequence of length 0, and one with m_b == 0, has no rows; any
+ * other length below P + m_b, or beyond the table, sets bit 5 of qmm_device_status(),
+ * and that sequence's rows see nothing.  Without window and sinks; otherwise arguments,
+ * results and errors are qmm_paged_attention's.  The prefix is read once for all rows.
+ * Probabilities enter the second product with 16 bits for either type of cache.     */
+qmm_status qmm_shared_prefix_attention(const qmm_paged_cache* cache, const int32_t* prefix_pages, int num_prefix_pages,
+                                       const void* q, int64_t q_ld, int B, int M, int q_heads, const int32_t* q_lens,
+                                       float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+size_t qmm_shared_prefix_attention_workspace(int B, int M, int q_heads, int heads, int head_dim);
 
 /* Verification of drafted tokens against the target's logits [B, k+1, V] (bf16
  * or fp32; row i is the target's distribution after i accepted drafts, rows
@@ -359,7 +445,8 @@ int qmm_last_cuda_error(void);                 /* cudaError_t of the last failur
 /* Device status word of the kernels, OR-ed over all kernel units: bit 0 = a
  * consumer gave up waiting for a weight tile, bit 1 = the producer gave up
  * waiting for a free stage, bit 2 = copies still in flight at exit gave up,
- * bit 3 = a gathered call had an invalid index list (see qmm_gather_small_m),
+ * bit 3 = a gathered call had an invalid index list (see qmm_gather_small_m), or
+ * qmm_lora_add an adapter's number out of range,
  * bit 4 = qmm_from_ggml met a block outside its exact range, bit 5 = a paged
  * cache call met an invalid page number or length (see qmm_paged_cache).
  * Every wait is bounded (about 2 s), so a fault shows up here instead of as a

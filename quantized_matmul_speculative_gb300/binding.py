@@ -45,6 +45,14 @@ SIGNATURES = {
     "qmm_paged_attention": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _f32, _i32, _i32, _vp, _vp, _vp,
                                    ctypes.c_size_t, _vp]),
     "qmm_paged_attention_workspace": (ctypes.c_size_t, [_i32, _i32, _i32, _i32, _i32]),
+    "qmm_rope_append": (_i32, [_vp, _vp, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp]),
+    "qmm_shared_prefix_attention": (_i32, [_vp, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]),
+    "qmm_shared_prefix_attention_workspace": (ctypes.c_size_t, [_i32, _i32, _i32, _i32, _i32]),
+    "qmm_route_experts": (_i32, [_vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp]),
+    "qmm_lora_add": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp,
+                            ctypes.c_size_t, _vp]),
+    "qmm_lora_workspace": (ctypes.c_size_t, [_i32, _i32]),
     "qmm_verify_draft": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "qmm_packed_words": (ctypes.c_size_t, [_i64, _i64, _i32]),
     "qmm_pack": (_i32, [_vp, _i64, _i64, _i32, _vp]),
@@ -69,6 +77,13 @@ class PagedCacheStruct(ctypes.Structure):
                 ("num_pages", _i64), ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", _f32),
                 ("v_scale", _f32)]
+
+
+class RopeStruct(ctypes.Structure):
+    """``qmm_rope`` of the header."""
+
+    _fields_ = [("inv_freq", _vp), ("positions", _vp), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32), ("factor", _f32)]
 
 
 class QmmError(RuntimeError):
@@ -417,6 +432,83 @@ def paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens=None, scal
     return _result(_native().paged_attention(q, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, scale,
                                              window, sinks, out, return_lse, workspace, _handle(stream)),
                    "qmm_paged_attention")
+
+
+def rope_append(q, k_new, v_new, k_cache, v_cache, block_table, lengths, inv_freq, q_lens=None, positions=None,
+                sections=None, interleaved: bool = False, factor: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0,
+                out=None, stream=None):
+    """Rotate the new rows' queries and keys, and write keys and values into a paged cache.
+
+    ``q``: bf16 [B, M, q_heads, D]; ``k_new``, ``v_new`` and the cache as in
+    :func:`kv_append`, with any M.  Pair j of a head, its elements j and
+    j + R of the first 2 R (``interleaved``: 2 j and 2 j + 1), turns by the
+    row's position times ``inv_freq`` [R] (fp32, R a multiple of 8); later
+    elements stay.  The position is that in the sequence, or ``positions``
+    [B, M] (int32), or with several axes [axes, B, M], ``sections[i]``
+    neighbouring pairs going by axis i; ``factor`` scales what is turned.
+    Returns the turned queries, bf16 [B, M, q_heads, D] (0 in rows from
+    q_lens on), in ``out`` if given, which may be ``q``."""
+    sections = None if sections is None else tuple(sections)
+    return _result(_native().rope_append(q, k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale,
+                                         inv_freq, positions, sections, interleaved, factor, out, _handle(stream)),
+                   "qmm_rope_append")
+
+
+@functools.lru_cache(maxsize=256)
+def shared_prefix_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
+    """Bytes of workspace that :func:`shared_prefix_attention` needs for these sizes."""
+    return int(lib().qmm_shared_prefix_attention_workspace(B, M, q_heads, heads, head_dim))
+
+
+def shared_prefix_attention(q, k_cache, v_cache, prefix_pages, block_table, lengths, q_lens=None, scale: float | None = None,
+                            k_scale: float = 1.0, v_scale: float = 1.0, out=None, return_lse: bool = False, workspace=None,
+                            stream=None):
+    """Attention as :func:`paged_attention` (without window) of sequences that share a prefix, read once for all of them.
+
+    The tokens of ``prefix_pages`` (int32 [P], full pages) come first in every
+    sequence; ``block_table`` names the pages after them (where it names the
+    prefix too: ``block_table[:, P:]``), and ``lengths`` counts all tokens.
+    The new rows come after the prefix; a sequence of length 0 has none."""
+    return _result(_native().shared_prefix_attention(q, prefix_pages, k_cache, v_cache, block_table, lengths, q_lens, k_scale,
+                                                     v_scale, scale, out, return_lse, workspace, _handle(stream)),
+                   "qmm_shared_prefix_attention")
+
+
+def route_experts(logits, k: int, scoring: str = "softmax", bias=None, groups: int = 1, top_groups: int | None = None,
+                  group_best: int = 2, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """The ``k`` experts of every token and their weights.
+
+    ``logits``: bf16 or fp32 [T, E] (rows may be strided); ``scoring``:
+    ``"softmax"`` or ``"sigmoid"``; ``bias``: fp32 [E], added to the scores for
+    the choice alone.  Of ``groups`` groups of neighbouring experts the
+    ``top_groups`` (None: all) with the largest sums of their ``group_best``
+    best are open.  Returns (experts int32 [T, k], best first, weights fp32
+    [T, k]: ``scale`` times the scores, divided by their sum with
+    ``renormalize``).  ``experts.view(-1)`` is the list ``rhs`` of
+    :func:`gather_small_m`."""
+    modes = {"softmax": 0, "sigmoid": 1}
+    if scoring not in modes:
+        raise ValueError("scoring must be softmax or sigmoid")
+    return _result(_native().route_experts(logits, k, modes[scoring], bias, groups, groups if top_groups is None else top_groups,
+                                           group_best, renormalize, scale, _handle(stream)), "qmm_route_experts")
+
+
+def lora_workspace(T: int, L: int) -> int:
+    """Bytes of workspace that :func:`lora_add` needs for T rows and L adapters."""
+    return int(lib().qmm_lora_workspace(T, L))
+
+
+def lora_add(base, x, a, b, adapters, scales=None, out=None, workspace=None, stream=None):
+    """``base`` plus every row's own low-rank product: row t is base[t] + scales[i] * b[i] (a[i] x[t]), i = adapters[t].
+
+    ``base``: bf16 or fp32 [T, N], the shared projection of ``x`` (bf16
+    [T, K]); ``a``: bf16 [L, R, K]; ``b``: bf16 [L, N, R], R a multiple of 8 up
+    to 128, K of 8; ``adapters``: int32 [T], negative for rows without one,
+    which stay as they are; ``scales``: fp32 [L] (None: 1).  Rows of base, x and
+    out may be strided.  Returns ``out`` (of base's type), which may be
+    ``base``; allocated if not given.  ``workspace``: a uint8 tensor of
+    :func:`lora_workspace` bytes to reuse."""
+    return _result(_native().lora_add(base, x, a, b, adapters, scales, out, workspace, _handle(stream)), "qmm_lora_add")
 
 
 def verify_draft(logits, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens=None, stream=None):

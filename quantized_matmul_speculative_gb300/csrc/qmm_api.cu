@@ -500,6 +500,9 @@ unsigned int qmm_device_status(int clear) {
   v |= read_device_status<8, 128>(clear);
   v |= read_paged_status(clear);
   v |= read_mx_matmul_status(clear);
+  v |= read_rope_status(clear);
+  v |= read_lora_status(clear);
+  v |= read_prefix_status(clear);
   unsigned int g = 0;
   if (cudaMemcpyFromSymbol(&g, qmm::g_qmm_ggml_status, sizeof(g)) != cudaSuccess) return 0xFFFFFFFFu;
   if (clear && g) {

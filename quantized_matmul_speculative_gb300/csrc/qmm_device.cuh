@@ -230,6 +230,16 @@ constexpr unsigned int kStatusTimeoutEmpty = 2u;  // the producer gave up waitin
 constexpr unsigned int kStatusTimeoutDrain = 4u;  // copies still in flight at exit gave up
 constexpr unsigned int kStatusBadGather = 8u;     // a gathered call had an index out of range, or more
                                                   // entries for one expert than its activation tile holds
+// This translation unit's word, read by the host (and cleared).
+static inline unsigned int read_unit_status(int clear) {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_qmm_status, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
+  if (clear && v != 0) {
+    const unsigned int zero = 0;
+    cudaMemcpyToSymbol(g_qmm_status, &zero, sizeof(zero));
+  }
+  return v;
+}
 // Time after which a wait is abandoned (ns).  Far above any legitimate wait.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 

@@ -95,6 +95,10 @@ bool injected_short_wait();
 // Device status word of the paged-cache unit (bit 5: invalid page or length).
 constexpr unsigned int kStatusBadPage = 32u;
 unsigned int read_paged_status(int clear);
+// Device status words of the units of rotation, adapters and attention behind a shared prefix.
+unsigned int read_rope_status(int clear);
+unsigned int read_lora_status(int clear);
+unsigned int read_prefix_status(int clear);
 // Device status word of the microscaled product's unit (bounded waits).
 unsigned int read_mx_matmul_status(int clear);
 

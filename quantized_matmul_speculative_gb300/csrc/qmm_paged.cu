@@ -5,24 +5,31 @@
 #include "qmm_paged.cuh"
 
 namespace qmm {
+
+// Checks that append and attention share; QMM_OK if there is work to launch.
+qmm_status check_cache(const qmm_paged_cache* c, int B, int M, int max_rows) {
+  if (c == nullptr) return QMM_ERR_NULL;
+  if (c->dtype != QMM_KV_BF16 && c->dtype != QMM_KV_E4M3) return QMM_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMM_ERR_UNSUPPORTED;
+  if (B < 0 || B > 65535 || M < 0 || M > max_rows || c->heads < 1 || c->heads > 4096 || c->page_size < 1 || c->max_pages < 0 ||
+      c->num_pages < 0 || c->num_pages > 0x7fffffff || static_cast<int64_t>(c->max_pages) * c->page_size > 0x7fffffff)
+    return QMM_ERR_SHAPE;
+  if (c->table_stride < c->max_pages) return QMM_ERR_SHAPE;
+  if (c->dtype == QMM_KV_E4M3 && !(c->k_scale > 0.f && c->v_scale > 0.f && c->k_scale < INFINITY && c->v_scale < INFINITY))
+    return QMM_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0) return QMM_OK;
+  if (c->lengths == nullptr) return QMM_ERR_NULL;
+  if (c->max_pages > 0 && (c->k == nullptr || c->v == nullptr || c->block_table == nullptr)) return QMM_ERR_NULL;
+  const int64_t per16 = c->dtype == QMM_KV_BF16 ? 8 : 16;
+  if (misaligned(reinterpret_cast<intptr_t>(c->k), 16) || misaligned(reinterpret_cast<intptr_t>(c->v), 16) ||
+      misaligned(c->k_page, per16) || misaligned(c->k_token, per16) || misaligned(c->k_head, per16) ||
+      misaligned(c->v_page, per16) || misaligned(c->v_token, per16) || misaligned(c->v_head, per16) ||
+      misaligned(reinterpret_cast<intptr_t>(c->lengths), 4) || misaligned(reinterpret_cast<intptr_t>(c->block_table), 4))
+    return QMM_ERR_ALIGN;
+  return QMM_OK;
+}
+
 namespace {
-
-// Two E4M3 codes, nearest even and saturating; NaN stays NaN.
-__device__ __forceinline__ uint32_t cvt_e4m3(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Page of token j, or -1 (and the status bit) if the table names none.
-__device__ __forceinline__ int64_t token_page(const qmm_paged_cache& c, int b, int64_t j) {
-  const int64_t p = c.block_table[b * c.table_stride + j / c.page_size];
-  if (p < 0 || p >= c.num_pages) {
-    atomicOr(&g_qmm_status, kStatusBadPage);
-    return -1;
-  }
-  return p;
-}
 
 // cache[page(pos), pos mod page_size, h] = x, as E4M3 e4m3(x / scale).  A copy
 // of 2 + 2 (or 2 + 1) bytes an element, bound by the chain length -> table ->
@@ -66,31 +73,6 @@ kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, cons
   }
 }
 
-bool misaligned(int64_t a, int64_t m) { return (a % m) != 0; }
-
-// Checks that append and attention share; QMM_OK if there is work to launch.
-qmm_status check_cache(const qmm_paged_cache* c, int B, int M) {
-  if (c == nullptr) return QMM_ERR_NULL;
-  if (c->dtype != QMM_KV_BF16 && c->dtype != QMM_KV_E4M3) return QMM_ERR_UNSUPPORTED;
-  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QMM_ERR_UNSUPPORTED;
-  if (B < 0 || B > 65535 || M < 0 || M > 16 || c->heads < 1 || c->heads > 4096 || c->page_size < 1 || c->max_pages < 0 ||
-      c->num_pages < 0 || c->num_pages > 0x7fffffff || static_cast<int64_t>(c->max_pages) * c->page_size > 0x7fffffff)
-    return QMM_ERR_SHAPE;
-  if (c->table_stride < c->max_pages) return QMM_ERR_SHAPE;
-  if (c->dtype == QMM_KV_E4M3 && !(c->k_scale > 0.f && c->v_scale > 0.f && c->k_scale < INFINITY && c->v_scale < INFINITY))
-    return QMM_ERR_UNSUPPORTED;
-  if (B == 0 || M == 0) return QMM_OK;
-  if (c->lengths == nullptr) return QMM_ERR_NULL;
-  if (c->max_pages > 0 && (c->k == nullptr || c->v == nullptr || c->block_table == nullptr)) return QMM_ERR_NULL;
-  const int64_t per16 = c->dtype == QMM_KV_BF16 ? 8 : 16;
-  if (misaligned(reinterpret_cast<intptr_t>(c->k), 16) || misaligned(reinterpret_cast<intptr_t>(c->v), 16) ||
-      misaligned(c->k_page, per16) || misaligned(c->k_token, per16) || misaligned(c->k_head, per16) ||
-      misaligned(c->v_page, per16) || misaligned(c->v_token, per16) || misaligned(c->v_head, per16) ||
-      misaligned(reinterpret_cast<intptr_t>(c->lengths), 4) || misaligned(reinterpret_cast<intptr_t>(c->block_table), 4))
-    return QMM_ERR_ALIGN;
-  return QMM_OK;
-}
-
 }  // namespace
 
 extern template cudaError_t launch_attention<64>(AttentionArgs, bool, int, cudaStream_t);
@@ -118,7 +100,7 @@ using namespace qmm;
 
 qmm_status qmm_kv_append(const qmm_paged_cache* cache, const void* k_new, int64_t k_ld, const void* v_new, int64_t v_ld,
                          int B, int M, const int32_t* q_lens, void* stream) {
-  const qmm_status rc = check_cache(cache, B, M);
+  const qmm_status rc = check_cache(cache, B, M, 16);
   if (rc != QMM_OK) return rc;
   const int64_t width = static_cast<int64_t>(cache->heads) * cache->head_dim;
   if (k_ld < width || v_ld < width) return QMM_ERR_SHAPE;
@@ -142,7 +124,7 @@ size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int h
 qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
                                const int32_t* q_lens, float scale, int window, int sinks, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream) {
-  const qmm_status rc = check_cache(cache, B, M);
+  const qmm_status rc = check_cache(cache, B, M, 16);
   if (rc != QMM_OK) return rc;
   if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || q_heads / cache->heads > 1024 || window < 0 || sinks < 0 ||
       q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)

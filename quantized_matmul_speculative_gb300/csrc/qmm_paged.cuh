@@ -38,8 +38,7 @@
 #include <type_traits>
 
 #include "../../include/qmm.h"
-#include "qmm_device.cuh"
-#include "qmm_internal.h"
+#include "qmm_cache.cuh"
 
 namespace qmm {
 
@@ -79,21 +78,6 @@ inline size_t attention_workspace(int workers, int RB, int D) {
 // Rows of a block: what one warp holds the outputs of.
 inline int attention_row_block(int rows, int D) { return rows <= 16 || D == 256 ? 16 : 32; }
 
-// Tokens of sequence b, clamped to what its block table can hold.
-__device__ __forceinline__ int seq_length(const qmm_paged_cache& c, int b) {
-  const int cap = c.max_pages * c.page_size;
-  int n = c.lengths[b];
-  if (n < 0 || n > cap) {
-    atomicOr(&g_qmm_status, kStatusBadPage);
-    n = n < 0 ? 0 : cap;
-  }
-  return n;
-}
-__device__ __forceinline__ int new_rows(const int32_t* q_lens, int b, int M) {
-  const int m = q_lens != nullptr ? q_lens[b] : M;
-  return m < 0 ? 0 : m > M ? M : m;
-}
-__device__ __forceinline__ void bad_page() { atomicOr(&g_qmm_status, kStatusBadPage); }
 
 // The new row that row gr of a segment belongs to: gr / G (exact for gr * G < 2^32).
 __device__ __forceinline__ int row_of(const AttentionArgs& a, int gr) {

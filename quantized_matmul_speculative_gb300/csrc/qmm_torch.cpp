@@ -264,6 +264,151 @@ PyObject* paged_attention(PyObject* const* a) {
   return with_lse ? two(out, lse) : one(out);
 }
 
+// (q, prefix_pages, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, scale, out, return_lse, workspace,
+//  stream) -> out or (out, lse)
+PyObject* shared_prefix_attention(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[0]), &prefix = tensor(a[1]);
+  if (q.dim() != 4) value_error("q must be [B, M, q_heads, D]");
+  const int64_t B = q.size(0), M = q.size(1), Hq = q.size(2), D = q.size(3);
+  if (prefix.dim() != 1 || prefix.scalar_type() != at::kInt || !prefix.is_contiguous())
+    value_error("prefix_pages must be a contiguous int32 vector");
+  Call call(q, a[13]);
+  call.here(&prefix);
+  const at::Tensor* q_lens;
+  const qmm_paged_cache c = paged_cache(call, a + 2, B, &q_lens);
+  if (D != c.head_dim) value_error("q and the cache must have the same D");
+  const int64_t ld = row_distance(q);
+  const at::Tensor *const given = maybe(a[10]), *const space = maybe(a[12]);
+  call.here(given);
+  call.here(space);
+  if (given != nullptr && !is(*given, at::kBFloat16, q.sizes())) value_error("out must be a contiguous bfloat16 tensor of q's shape");
+  if (space != nullptr && (space->scalar_type() != at::kByte || !space->is_contiguous()))
+    value_error("workspace must be a contiguous uint8 tensor");
+  const at::Tensor out = given != nullptr ? *given : call.empty(q.sizes(), at::kBFloat16);
+  at::Tensor lse;
+  const bool with_lse = PyObject_IsTrue(a[11]);
+  if (with_lse) lse = call.empty({B, M, Hq}, at::kFloat);
+  const int b = narrow(B), m = narrow(M), hq = narrow(Hq);
+  const at::Tensor ws =
+      space != nullptr
+          ? *space
+          : call.empty({static_cast<int64_t>(qmm_shared_prefix_attention_workspace(b, m, hq, c.heads, c.head_dim))}, at::kByte);
+  const float scale = a[9] == Py_None ? 1.f / std::sqrt(static_cast<float>(D)) : static_cast<float>(real(a[9]));
+  const qmm_status rc = qmm_shared_prefix_attention(
+      &c, static_cast<const int32_t*>(prefix.data_ptr()), narrow(prefix.size(0)), q.data_ptr(), ld, b, m, hq,
+      static_cast<const int32_t*>(ptr(q_lens)), scale, out.data_ptr(), with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+      ws.data_ptr(), ws.numel(), call.stream());
+  if (rc != QMM_OK) return status(rc);
+  return with_lse ? two(out, lse) : one(out);
+}
+
+// (q, k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens, k_scale, v_scale, inv_freq, positions, sections,
+//  interleaved, factor, out, stream) -> out
+PyObject* rope_append(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &freq = tensor(a[10]);
+  if (q.dim() != 4) value_error("q must be [B, M, q_heads, D]");
+  if (k.dim() != 4 || k.sizes() != v.sizes()) value_error("k_new and v_new must be [B, M, heads, D] of one shape");
+  const int64_t B = q.size(0), M = q.size(1), Hq = q.size(2), D = q.size(3);
+  if (k.size(0) != B || k.size(1) != M || k.size(3) != D) value_error("q and k_new must have the same B, M and D");
+  if (freq.dim() != 1 || freq.scalar_type() != at::kFloat || !freq.is_contiguous())
+    value_error("inv_freq must be a contiguous float32 vector");
+  const at::Tensor *const positions = maybe(a[11]), *const given = maybe(a[15]);
+  Call call(q, a[16]);
+  for (const at::Tensor* t : {&k, &v, &freq, positions, given}) call.here(t);
+  const at::Tensor* q_lens;
+  const qmm_paged_cache c = paged_cache(call, a + 3, B, &q_lens);
+  if (k.size(2) != c.heads || D != c.head_dim) value_error("k_new and the cache must have the same heads and D");
+  qmm_rope r = {};
+  r.inv_freq = static_cast<const float*>(freq.data_ptr());
+  r.rot = narrow(2 * freq.size(0));
+  r.axes = 1;
+  r.sections[0] = r.rot / 2;
+  if (positions != nullptr) {
+    const int64_t dims = positions->dim();
+    if (positions->scalar_type() != at::kInt || !positions->is_contiguous() || (dims != 2 && dims != 3) ||
+        positions->size(dims - 2) != B || positions->size(dims - 1) != M)
+      value_error("positions must be contiguous int32 [B, M] or [axes, B, M]");
+    r.positions = static_cast<const int32_t*>(positions->data_ptr());
+    r.axes = dims == 3 ? narrow(positions->size(0)) : 1;
+  }
+  if (a[12] != Py_None) {
+    if (positions == nullptr) value_error("sections go with positions");
+    if (!PyTuple_Check(a[12]) || PyTuple_GET_SIZE(a[12]) != r.axes || r.axes > 4)
+      value_error("sections must be a tuple of as many numbers as positions has axes, at most 4");
+    for (int i = 0; i < r.axes; ++i) r.sections[i] = narrow(integer(PyTuple_GET_ITEM(a[12], i)));
+  } else if (r.axes != 1) {
+    value_error("several axes need sections");
+  }
+  r.interleaved = PyObject_IsTrue(a[13]);
+  r.factor = static_cast<float>(real(a[14]));
+  if (given != nullptr && given->sizes() != q.sizes()) value_error("out must have q's shape");
+  const at::Tensor out = given != nullptr ? *given : call.empty(q.sizes(), at::kBFloat16);
+  const qmm_status rc =
+      qmm_rope_append(&c, &r, q.data_ptr(), row_distance(q), narrow(Hq), out.data_ptr(), row_distance(out), k.data_ptr(),
+                      row_distance(k), v.data_ptr(), row_distance(v), narrow(B), narrow(M),
+                      static_cast<const int32_t*>(ptr(q_lens)), call.stream());
+  return rc == QMM_OK ? one(out) : status(rc);
+}
+
+// (logits, k, sigmoid, bias, groups, top_groups, group_best, renormalize, scale, stream) -> (experts, weights)
+PyObject* route_experts(PyObject* const* a) {
+  const at::Tensor& x = tensor(a[0]);
+  const bool f32 = x.scalar_type() == at::kFloat;
+  if (x.dim() != 2 || (!f32 && x.scalar_type() != at::kBFloat16)) type_error("logits must be a bfloat16 or float32 matrix");
+  const int64_t T = x.size(0), E = x.size(1);
+  if (E > 1 && x.stride(1) != 1) value_error("the elements of a row of logits must be contiguous");
+  const at::Tensor* const bias = maybe(a[3]);
+  if (bias != nullptr && !is(*bias, at::kFloat, {E})) value_error("bias must be contiguous float32 [E]");
+  Call call(x, a[9]);
+  call.here(bias);
+  const int k = narrow(integer(a[1]));
+  const at::Tensor experts = call.empty({T, k}, at::kInt), weights = call.empty({T, k}, at::kFloat);
+  const qmm_status rc = qmm_route_experts(
+      x.data_ptr(), f32 ? QMM_OUT_F32 : QMM_OUT_BF16, T > 1 ? x.stride(0) : E, static_cast<const float*>(ptr(bias)), narrow(T),
+      narrow(E), k, PyObject_IsTrue(a[2]) ? QMM_SIGMOID : QMM_SOFTMAX, narrow(integer(a[4])), narrow(integer(a[5])),
+      narrow(integer(a[6])), PyObject_IsTrue(a[7]), static_cast<float>(real(a[8])), static_cast<int32_t*>(experts.data_ptr()),
+      static_cast<float*>(weights.data_ptr()), call.stream());
+  return rc == QMM_OK ? two(experts, weights) : status(rc);
+}
+
+// (base, x, a, b, adapters, scales, out, workspace, stream) -> out
+PyObject* lora_add(PyObject* const* a) {
+  const at::Tensor &base = tensor(a[0]), &x = tensor(a[1]), &A = tensor(a[2]), &Bm = tensor(a[3]), &ids = tensor(a[4]);
+  const at::Tensor *const scales = maybe(a[5]), *const given = maybe(a[6]), *const space = maybe(a[7]);
+  const bool f32 = base.scalar_type() == at::kFloat;
+  if (base.dim() != 2 || (!f32 && base.scalar_type() != at::kBFloat16)) type_error("base must be a bfloat16 or float32 matrix");
+  if (x.dim() != 2 || x.scalar_type() != at::kBFloat16) type_error("x must be a bfloat16 matrix");
+  if (A.dim() != 3 || Bm.dim() != 3) value_error("a and b must be [L, R, K] and [L, N, R]");
+  const int64_t T = base.size(0), N = base.size(1), K = x.size(1), L = A.size(0), R = A.size(1);
+  if (!is(A, at::kBFloat16, {L, R, K}) || !is(Bm, at::kBFloat16, {L, N, R}))
+    value_error("a and b must be contiguous bfloat16 [L, R, K] and [L, N, R]");
+  if (x.size(0) != T) value_error("x and base must have as many rows");
+  if (!is(ids, at::kInt, {T})) value_error("adapters must be contiguous int32 [T]");
+  if (scales != nullptr && !is(*scales, at::kFloat, {L})) value_error("scales must be contiguous float32 [L]");
+  const auto distance = [](const at::Tensor& t) {
+    const int64_t rows = t.size(0), n = t.size(1), ld = rows > 1 ? t.stride(0) : n;
+    if ((n > 1 && t.stride(1) != 1) || ld < n) value_error("the elements of a row must be contiguous, and rows apart");
+    return ld;
+  };
+  if (given != nullptr && (given->sizes() != base.sizes() || given->scalar_type() != base.scalar_type()))
+    value_error("out must have base's shape and dtype");
+  if (space != nullptr && (space->scalar_type() != at::kByte || !space->is_contiguous()))
+    value_error("workspace must be a contiguous uint8 tensor");
+  Call call(base, a[8]);
+  for (const at::Tensor* t : {&x, &A, &Bm, &ids, scales, given, space}) call.here(t);
+  const at::Tensor out = given != nullptr ? *given : call.empty(base.sizes(), base.scalar_type());
+  const int64_t need = static_cast<int64_t>(qmm_lora_workspace(narrow(T), narrow(L)));
+  at::Tensor ws;
+  if (space != nullptr) ws = *space;
+  else if (need > 0) ws = call.empty({need}, at::kByte);
+  const qmm_status rc = qmm_lora_add(
+      base.data_ptr(), distance(base), x.data_ptr(), distance(x), A.data_ptr(), Bm.data_ptr(),
+      static_cast<const int32_t*>(ids.data_ptr()), static_cast<const float*>(ptr(scales)), narrow(T), narrow(N), narrow(K),
+      narrow(R), narrow(L), out.data_ptr(), distance(out), f32 ? QMM_OUT_F32 : QMM_OUT_BF16,
+      ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, call.stream());
+  return rc == QMM_OK ? one(out) : status(rc);
+}
+
 // (logits, draft_tokens, draft_probs, uniform, noise, temperature, draft_lens, stream) -> (tokens, accepted)
 PyObject* verify_draft(PyObject* const* a) {
   const at::Tensor& logits = tensor(a[0]);
@@ -311,7 +456,9 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 #define ENTRY(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(quantize_mx, 8),       ENTRY(matmul_mx, 9),    ENTRY(kv_append, 10),
-                         ENTRY(paged_attention, 15),  ENTRY(verify_draft, 8), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(paged_attention, 15),  ENTRY(verify_draft, 8), ENTRY(shared_prefix_attention, 14),
+                         ENTRY(rope_append, 17),      ENTRY(route_experts, 10), ENTRY(lora_add, 9),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
