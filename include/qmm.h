@@ -371,7 +371,8 @@ size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int h
  * other length below P + m_b, or beyond the table, sets bit 5 of qmm_device_status(),
  * and that sequence's rows see nothing.  Without window and sinks; otherwise arguments,
  * results and errors are qmm_paged_attention's.  The prefix is read once for all rows.
- * Probabilities enter the second product with 16 bits for either type of cache.     */
+ * Probabilities enter the second product with 16 bits (for an E4M3 cache as one fp16
+ * operand: 11 bits, fewer below 2^-25 of the row's largest, none below 2^-36).       */
 qmm_status qmm_shared_prefix_attention(const qmm_paged_cache* cache, const int32_t* prefix_pages, int num_prefix_pages,
                                        const void* q, int64_t q_ld, int B, int M, int q_heads, const int32_t* q_lens,
                                        float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,

@@ -53,7 +53,10 @@ def units():
     """(source, object, extra flags) for every translation unit."""
     out = [(CSRC / f"{name}.cu", BUILD / f"{name}.o", []) for name in PLAIN_UNITS]
     for d in HEAD_DIMS:
-        out.append((CSRC / "qmm_paged_inst.cu", BUILD / f"qmm_paged_d{d}.o", [f"-DQMM_HEAD_DIM={d}"]))
+        for behind in ("false", "true"):
+            out.append((CSRC / "qmm_paged_inst.cu", BUILD / f"qmm_paged_d{d}_{behind}.o",
+                        [f"-DQMM_HEAD_DIM={d}", f"-DQMM_BEHIND={behind}"]))
+        out.append((CSRC / "qmm_prefix_inst.cu", BUILD / f"qmm_prefix_d{d}.o", [f"-DQMM_HEAD_DIM={d}"]))
     for bits, gs in MMA_INSTANCES:
         out.append((CSRC / "qmm_mma_inst.cu", BUILD / f"qmm_mma_b{bits}_g{gs}.o",
                     [f"-DQMM_BITS={bits}", f"-DQMM_GS={gs}"]))

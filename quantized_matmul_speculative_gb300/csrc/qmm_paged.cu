@@ -75,21 +75,84 @@ kv_append_kernel(const qmm_paged_cache c, const uint16_t* kn, int64_t k_ld, cons
 
 }  // namespace
 
-extern template cudaError_t launch_attention<64>(AttentionArgs, bool, int, cudaStream_t);
-extern template cudaError_t launch_attention<128>(AttentionArgs, bool, int, cudaStream_t);
-extern template cudaError_t launch_attention<256>(AttentionArgs, bool, int, cudaStream_t);
-extern template unsigned int read_attention_status<64>(int);
-extern template unsigned int read_attention_status<128>(int);
-extern template unsigned int read_attention_status<256>(int);
+extern template cudaError_t launch_attention<64, false>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<64, false>(int);
+extern template cudaError_t launch_attention<64, true>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<64, true>(int);
+extern template cudaError_t launch_attention<128, false>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<128, false>(int);
+extern template cudaError_t launch_attention<128, true>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<128, true>(int);
+extern template cudaError_t launch_attention<256, false>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<256, false>(int);
+extern template cudaError_t launch_attention<256, true>(AttentionArgs, bool, int, cudaStream_t);
+extern template unsigned int read_attention_status<256, true>(int);
 
 unsigned int read_paged_status(int clear) {
-  unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_qmm_status, sizeof(v)) != cudaSuccess) return 0xFFFFFFFFu;
-  if (clear && v != 0) {
-    const unsigned int zero = 0;
-    cudaMemcpyToSymbol(g_qmm_status, &zero, sizeof(zero));
-  }
-  return v | read_attention_status<64>(clear) | read_attention_status<128>(clear) | read_attention_status<256>(clear);
+  return read_unit_status(clear) | read_attention_status<64, false>(clear) | read_attention_status<128, false>(clear) |
+         read_attention_status<256, false>(clear) | read_attention_status<64, true>(clear) | read_attention_status<128, true>(clear) |
+         read_attention_status<256, true>(clear);
+}
+
+qmm_status run_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
+                         const int32_t* q_lens, float scale, int window, int sinks, void* out, float* out32, float* lse, int skip,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const qmm_status rc = check_cache(cache, B, M, 16);
+  if (rc != QMM_OK) return rc;
+  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || q_heads / cache->heads > 1024 || window < 0 || sinks < 0 ||
+      q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)
+    return QMM_ERR_SHAPE;
+  const bool e8 = cache->dtype == QMM_KV_E4M3;
+  const float scale_log2 = scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f);
+  if (!std::isfinite(scale_log2)) return QMM_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0) return QMM_OK;
+  if (q == nullptr || (out == nullptr && out32 == nullptr)) return QMM_ERR_NULL;
+  if (misaligned(reinterpret_cast<intptr_t>(q), 16) || misaligned(reinterpret_cast<intptr_t>(out), 16) ||
+      misaligned(q_ld, 8) || misaligned(reinterpret_cast<intptr_t>(lse), 4) ||
+      misaligned(reinterpret_cast<intptr_t>(q_lens), 4))
+    return QMM_ERR_ALIGN;
+  if (workspace == nullptr) return QMM_ERR_NULL;
+  if (misaligned(reinterpret_cast<intptr_t>(workspace), 16)) return QMM_ERR_ALIGN;
+  AttentionArgs a = {};
+  a.inject = injected_short_wait();
+  a.wait_ns = a.inject ? 100000ull : kWaitLimitNs;
+  a.c = *cache;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_ld = q_ld;
+  a.B = B;
+  a.M = M;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->heads;
+  a.q_lens = q_lens;
+  // at least 1e-30: a masked score of -inf stays -inf, and no finite score of use is told from 0 by less
+  a.scale_log2 = std::fmax(std::fabs(scale_log2), 1e-30f);
+  a.negate = scale < 0.f;
+  a.v_scale = e8 ? cache->v_scale : 1.f;
+  a.window = window;
+  a.sinks = window != 0 ? sinks : 0;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.out32 = out32;
+  a.lse = lse;
+  a.skip = skip;
+  a.RB = attention_row_block(M * a.G, cache->head_dim);
+  a.RT = (M * a.G + a.RB - 1) / a.RB;
+  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
+  // (places of the list of tiles are numbered in 32 bits; a tile holds 16 tokens at least)
+  if (static_cast<int64_t>(B) * cache->heads * a.RT * (static_cast<int64_t>(cache->max_pages) * cache->page_size / 16 + 1 + kLead) >
+      0x7fffffff)
+    return QMM_ERR_SHAPE;
+  const int ctas = device_sm_count();
+  const size_t workers = static_cast<size_t>(ctas) * kMaxWorkers;
+  if (workspace_bytes < attention_workspace(static_cast<int>(workers), a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + workers * 2 * a.RB * cache->head_dim);
+  a.part_seg = reinterpret_cast<int4*>(a.part_ml + workers * 2 * a.RB);
+  const bool behind = out32 != nullptr;
+  const auto launch = cache->head_dim == 64    ? (behind ? launch_attention<64, true> : launch_attention<64, false>)
+                      : cache->head_dim == 128 ? (behind ? launch_attention<128, true> : launch_attention<128, false>)
+                                               : (behind ? launch_attention<256, true> : launch_attention<256, false>);
+  const cudaError_t e = launch(a, e8, ctas, stream);
+  return static_cast<qmm_status>(finish_call(e));
 }
 
 }  // namespace qmm
@@ -124,59 +187,8 @@ size_t qmm_paged_attention_workspace(int B, int M, int q_heads, int heads, int h
 qmm_status qmm_paged_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
                                const int32_t* q_lens, float scale, int window, int sinks, void* out, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream) {
-  const qmm_status rc = check_cache(cache, B, M, 16);
-  if (rc != QMM_OK) return rc;
-  if (q_heads < 1 || q_heads > 65535 || q_heads % cache->heads != 0 || q_heads / cache->heads > 1024 || window < 0 || sinks < 0 ||
-      q_ld < static_cast<int64_t>(q_heads) * cache->head_dim)
-    return QMM_ERR_SHAPE;
-  const bool e8 = cache->dtype == QMM_KV_E4M3;
-  const float scale_log2 = scale * 1.4426950408889634f * (e8 ? cache->k_scale : 1.f);
-  if (!std::isfinite(scale_log2)) return QMM_ERR_UNSUPPORTED;
-  if (B == 0 || M == 0) return QMM_OK;
-  if (q == nullptr || out == nullptr) return QMM_ERR_NULL;
-  if (misaligned(reinterpret_cast<intptr_t>(q), 16) || misaligned(reinterpret_cast<intptr_t>(out), 16) ||
-      misaligned(q_ld, 8) || misaligned(reinterpret_cast<intptr_t>(lse), 4) ||
-      misaligned(reinterpret_cast<intptr_t>(q_lens), 4))
-    return QMM_ERR_ALIGN;
-  if (workspace == nullptr) return QMM_ERR_NULL;
-  if (misaligned(reinterpret_cast<intptr_t>(workspace), 16)) return QMM_ERR_ALIGN;
-  AttentionArgs a = {};
-  a.inject = injected_short_wait();
-  a.wait_ns = a.inject ? 100000ull : kWaitLimitNs;
-  a.c = *cache;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_ld = q_ld;
-  a.B = B;
-  a.M = M;
-  a.Hq = q_heads;
-  a.G = q_heads / cache->heads;
-  a.q_lens = q_lens;
-  // at least 1e-30: a masked score of -inf stays -inf, and no finite score of use is told from 0 by less
-  a.scale_log2 = std::fmax(std::fabs(scale_log2), 1e-30f);
-  a.negate = scale < 0.f;
-  a.v_scale = e8 ? cache->v_scale : 1.f;
-  a.window = window;
-  a.sinks = window != 0 ? sinks : 0;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.lse = lse;
-  a.RB = attention_row_block(M * a.G, cache->head_dim);
-  a.RT = (M * a.G + a.RB - 1) / a.RB;
-  a.g_magic = a.G == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
-  // (places of the list of tiles are numbered in 32 bits; a tile holds 16 tokens at least)
-  if (static_cast<int64_t>(B) * cache->heads * a.RT * (static_cast<int64_t>(cache->max_pages) * cache->page_size / 16 + 1 + kLead) >
-      0x7fffffff)
-    return QMM_ERR_SHAPE;
-  const int ctas = device_sm_count();
-  const size_t workers = static_cast<size_t>(ctas) * kMaxWorkers;
-  if (workspace_bytes < attention_workspace(static_cast<int>(workers), a.RB, cache->head_dim)) return QMM_ERR_SHAPE;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + workers * 2 * a.RB * cache->head_dim);
-  a.part_seg = reinterpret_cast<int4*>(a.part_ml + workers * 2 * a.RB);
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->head_dim == 64    ? launch_attention<64>(a, e8, ctas, st)
-                        : cache->head_dim == 128 ? launch_attention<128>(a, e8, ctas, st)
-                                                 : launch_attention<256>(a, e8, ctas, st);
-  return static_cast<qmm_status>(finish_call(e));
+  return run_attention(cache, q, q_ld, B, M, q_heads, q_lens, scale, window, sinks, out, nullptr, lse, 0, workspace,
+                       workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -57,7 +57,9 @@ struct AttentionArgs {
   float v_scale;
   int window, sinks;
   __nv_bfloat16* out;
+  float* out32;      // behind a prefix the outputs go there, unrounded
   float* lse;
+  int skip;          // tokens of that prefix, which the lengths count
   int box;        // tokens of a TMA box (8 or 16); 0: copied row by row
   int page_log2;  // of the page size, or -1
   int RB, RT;     // rows of a row block (16 or 32), row blocks of a segment's M * G rows
@@ -78,6 +80,20 @@ inline size_t attention_workspace(int workers, int RB, int D) {
 // Rows of a block: what one warp holds the outputs of.
 inline int attention_row_block(int rows, int D) { return rows <= 16 || D == 256 ? 16 : 32; }
 
+
+// Tokens of sequence b that its table holds; behind a prefix 0 (and, unless it is empty or has no new rows, the
+// status bit) where its new rows do not come after the prefix.
+template <bool BEHIND>
+__device__ __forceinline__ int own_length(const AttentionArgs& a, int b) {
+  if constexpr (!BEHIND) return seq_length(a.c, b);
+  const int m = new_rows(a.q_lens, b, a.M), n = a.c.lengths[b], own = n - a.skip;
+  if (n == 0 || m == 0) return 0;
+  if (n < 0 || own < m || own > a.c.max_pages * a.c.page_size) {
+    bad_page();
+    return 0;
+  }
+  return own;
+}
 
 // The new row that row gr of a segment belongs to: gr / G (exact for gr * G < 2^32).
 __device__ __forceinline__ int row_of(const AttentionArgs& a, int gr) {
@@ -126,8 +142,9 @@ constexpr int kLead = 4;
 __device__ __forceinline__ int places(const Visible& v) { return v.tiles > 0 ? v.tiles + kLead : 0; }
 
 // Places of one head of sequence b, over its row blocks.
+template <bool BEHIND>
 __device__ __forceinline__ int head_places(const AttentionArgs& a, int b) {
-  const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
+  const int L = own_length<BEHIND>(a, b), m = new_rows(a.q_lens, b, a.M);
   int n = 0;
   for (int rt = 0; rt < a.RT; ++rt) n += places(visible(a, L, m, rt));
   return n;
@@ -161,6 +178,7 @@ struct Shares {
 };
 
 // A worker's share of the list, segment by segment.
+template <bool BEHIND>
 struct Cursor {
   int u, end;  // place of the list that this segment begins at; end of the share
   int b, h, rt;
@@ -169,12 +187,12 @@ struct Cursor {
   Visible v;
 
   __device__ __forceinline__ void load(const AttentionArgs& a) {
-    L = seq_length(a.c, b);
+    L = own_length<BEHIND>(a, b);
     m = new_rows(a.q_lens, b, a.M);
   }
   // Places of sequence s over all heads.
   static __device__ __forceinline__ int seq_places(const AttentionArgs& a, int s) {
-    return s < a.B ? head_places(a, s) * a.c.heads : 0;
+    return s < a.B ? head_places<BEHIND>(a, s) * a.c.heads : 0;
   }
   // The first segment with tiles in this worker's share (every lane of the warp
   // calls); false: none.  T: the list's places.
@@ -207,7 +225,7 @@ struct Cursor {
       before += __shfl_sync(0xffffffffu, inc, 31);
     }
     load(a);
-    const int per_head = max(head_places(a, b), 1);
+    const int per_head = max(head_places<BEHIND>(a, b), 1);
     h = (start - before) / per_head;
     u = before + h * per_head;
     for (rt = 0; rt < a.RT - 1; ++rt) {
@@ -425,8 +443,19 @@ __device__ __forceinline__ int out_col(int ot, int e) {
   return E8 ? (ot >> 1) * 16 + 4 * c + 2 * e + (ot & 1) : ot * 8 + 2 * c + e;
 }
 
+// Unrounded outputs: two neighbouring columns of one tile (E4M3: four, of two tiles in turn), times f, or 0.
+template <bool E8>
+__device__ __forceinline__ void store_f32(float* to, float x0, float x1, float y0, float y1, float f, bool some) {
+  if constexpr (E8) {
+    *reinterpret_cast<float4*>(to) = some ? make_float4(x0 * f, y0 * f, x1 * f, y1 * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    *reinterpret_cast<float2*>(to) = some ? make_float2(x0 * f, x1 * f) : make_float2(0.f, 0.f);
+  }
+}
+
 // Whether some row of queries sees one of the tokens j .. j + count - 1.
-__device__ __forceinline__ bool seen(const AttentionArgs& a, const Cursor& p, int j, int count) {
+template <class C>
+__device__ __forceinline__ bool seen(const AttentionArgs& a, const C& p, int j, int count) {
   return j < p.v.hi && (j + count > p.v.first || j < a.sinks);
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -444,13 +473,13 @@ __device__ __forceinline__ void cp_async_wait() {
 // out, and what tokens past the length hold is dealt with where the values are
 // used.  Any other page size: 16-byte asynchronous copies of the tokens' rows;
 // tokens that nobody sees and those of pages outside the cache become zeros.
-template <class Cfg, bool E8>
+template <class Cfg, bool E8, bool BEHIND>
 struct Stream {
   static constexpr int SL = Cfg::ROWB >= 128 ? Cfg::ROWB / 128 : 1, ROW = Cfg::ROWB >= 128 ? 128 : 64;
   static constexpr int CPR = Cfg::ROWB / 16, ES = E8 ? 1 : 2, RPI = 32 / CPR;
   static_assert(Cfg::TN <= 32, "a lane finds the page of one token or box of a tile");
   uint32_t ring, bars;  // shared-memory addresses
-  Cursor c;             // the segment of the next tile
+  Cursor<BEHIND> c;     // the segment of the next tile
   int k;
   bool more;            // there is such a tile
   int slot;             // of the next piece
@@ -511,7 +540,7 @@ struct Stream {
       k = c.kb;
     }
   }
-  __device__ __forceinline__ void begin(const AttentionArgs& a, const Cursor& at, uint32_t ring_addr, uint32_t bar_addr) {
+  __device__ __forceinline__ void begin(const AttentionArgs& a, const Cursor<BEHIND>& at, uint32_t ring_addr, uint32_t bar_addr) {
     ring = ring_addr;
     bars = bar_addr;
     c = at;
@@ -580,12 +609,12 @@ static __device__ __noinline__ void drain(uint32_t bars, int slot, int next, int
 }
 
 // Rows of segments without tiles: the worker of the sequence's number writes them.
-template <int D>
+template <int D, bool BEHIND>
 __device__ __forceinline__ void empty_rows(const AttentionArgs& a, int worker) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int b = worker; b < a.B; b += a.parts) {
-    const int L = seq_length(a.c, b), m = new_rows(a.q_lens, b, a.M);
+    const int L = own_length<BEHIND>(a, b), m = new_rows(a.q_lens, b, a.M);
 #pragma unroll 1
     for (int rt = 0; rt < a.RT; ++rt) {
       if (visible(a, L, m, rt).tiles != 0) continue;
@@ -594,14 +623,20 @@ __device__ __forceinline__ void empty_rows(const AttentionArgs& a, int worker) {
       for (int x = lane; x < per_head * a.c.heads; x += 32) {
         const int h = x / per_head, gr = r0 + (x - h * per_head) / (D / 8), col = (x % (D / 8)) * 8, i = row_of(a, gr);
         const int64_t at = (static_cast<int64_t>(b) * a.M + i) * a.Hq + h * a.G + gr - i * a.G;
-        *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
+        if constexpr (BEHIND) {
+          *reinterpret_cast<uint4*>(a.out32 + at * D + col) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(a.out32 + at * D + col + 4) = make_uint4(0, 0, 0, 0);
+        } else {
+          *reinterpret_cast<uint4*>(a.out + at * D + col) = make_uint4(0, 0, 0, 0);
+        }
         if (col == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
       }
     }
   }
 }
 
-template <int D, bool E8, int RPW>
+// BEHIND: behind a prefix, with unrounded outputs (see AttentionArgs).
+template <int D, bool E8, int RPW, bool BEHIND>
 __global__ void __launch_bounds__(AttnCfg<D, E8, RPW>::THREADS, 1)
 attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using Cfg = AttnCfg<D, E8, RPW>;
@@ -619,12 +654,12 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  Cursor cc;
+  Cursor<BEHIND> cc;
   int T;
   if (lane < 2) a.part_seg[(worker * 2 + lane) * 2] = make_int4(0, 0, 0, 0);
   __syncwarp();
   if (!cc.begin(a, worker, T)) {
-    empty_rows<D>(a, worker);
+    empty_rows<D, BEHIND>(a, worker);
     return;
   }
   {
@@ -636,7 +671,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
   }
   const int ring_off = warp * SLOTS * Cfg::TILEB;
   const uint32_t bars = sbase + Cfg::OFF_BAR + warp * SLOTS * 8;
-  Stream<Cfg, E8> in;
+  Stream<Cfg, E8, BEHIND> in;
   in.begin(a, cc, sbase + ring_off, bars);
   if (a.inject && (cc.b | cc.h | cc.rt | cc.kb) == 0 && lane == 0) mbar_expect_tx(bars, 16);
 #pragma unroll 1
@@ -959,7 +994,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
 #pragma unroll
     for (int w = 0; w < RPW; ++w) {
       float f[2];
-      __nv_bfloat16* to[2];
+      typename std::conditional<BEHIND, float, __nv_bfloat16>::type* to[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float l = sum[w][r][0] + sum[w][r][1];
@@ -974,7 +1009,8 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           const bool some = i < cc.m && l != 0.f;  // NaN sums count
           f[r] = some ? a.v_scale / l : 0.f;
           const int64_t at = (static_cast<int64_t>(cc.b) * a.M + i) * a.Hq + cc.h * a.G + gr - i * a.G;
-          to[r] = a.out + at * D;
+          if constexpr (BEHIND) to[r] = a.out32 + at * D;
+          else to[r] = a.out + at * D;
           if (a.lse != nullptr && (lane & 3) == 0) a.lse[at] = some ? log_sum<E8>(mx[w][r], l) : -INFINITY;
         }
       }
@@ -990,7 +1026,10 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
           for (int i = 0; i < D / 8; i += E8 ? 2 : 1) {
             // (a row without weight: 0 whatever the accumulators hold)
             const bool some = f[r] != 0.f;
-            if constexpr (E8) {
+            if constexpr (BEHIND) {
+              store_f32<E8>(to[r] + out_col<E8>(i, 0), o[w][i][2 * r], o[w][i][2 * r + 1],
+                            E8 ? o[w][i + E8][2 * r] : 0.f, E8 ? o[w][i + E8][2 * r + 1] : 0.f, f[r], some);
+            } else if constexpr (E8) {
               uint2 u = make_uint2(0u, 0u);
               if (some) u = make_uint2(pack_bf16(o[w][i][2 * r] * f[r], o[w][i + 1][2 * r] * f[r]),
                                        pack_bf16(o[w][i][2 * r + 1] * f[r], o[w][i + 1][2 * r + 1] * f[r]));
@@ -1005,7 +1044,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
     }
   } while (cc.next(a));
   if (!a.box) cp_async_wait<0>();
-  empty_rows<D>(a, worker);
+  empty_rows<D, BEHIND>(a, worker);
 }
 
 // Combines the parts of segments that several workers share.  A segment's
@@ -1015,7 +1054,7 @@ attention_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap
 // has an item of its own; of more, the warps share the parts of an item and are
 // added in order through shared memory.  (One warp an item for any number: 25 us
 // of the 72 us that one 65001-token row took, in 152 parts a head.)
-template <int D, bool E8>
+template <int D, bool E8, bool BEHIND>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs a) {
   constexpr int IW = 2, PER = D / 8 / IW, WARPS = kJoinThreads / 32;
   __shared__ float4 s_v[WARPS][IW][32];
@@ -1133,7 +1172,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
       const float f = some ? a.v_scale / l[r] : 0.f;
       const int64_t at = (static_cast<int64_t>(seg.x) * a.M + i) * a.Hq + seg.y * a.G + gr - i * a.G;
       __nv_bfloat16* const to = a.out + at * D;
-      if constexpr (E8) {
+      if constexpr (BEHIND) {
+        float* const to32 = a.out32 + at * D;
+        if constexpr (E8) {
+          store_f32<true>(to32 + out_col<true>(i0, 0), o[0][2 * r], o[0][2 * r + 1], o[1][2 * r], o[1][2 * r + 1], f, some);
+        } else {
+#pragma unroll
+          for (int j = 0; j < IW; ++j)
+            store_f32<false>(to32 + out_col<false>(i0 + j, 0), o[j][2 * r], o[j][2 * r + 1], 0.f, 0.f, f, some);
+        }
+      } else if constexpr (E8) {
         static_assert(IW == 2, "an E4M3 cache's output tiles come in pairs");
         uint2 p = make_uint2(0u, 0u);
         if (some) p = make_uint2(pack_bf16(o[0][2 * r] * f, o[1][2 * r] * f), pack_bf16(o[0][2 * r + 1] * f, o[1][2 * r + 1] * f));
@@ -1148,11 +1196,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttentionArgs 
   }
 }
 
+// Checks and launches of qmm_paged_attention (qmm_paged.cu).  With out32 the tokens come
+// behind a prefix of `skip` (see AttentionArgs).
+qmm_status run_attention(const qmm_paged_cache* cache, const void* q, int64_t q_ld, int B, int M, int q_heads,
+                         const int32_t* q_lens, float scale, int window, int sinks, void* out, float* out32, float* lse, int skip,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 // Launcher of one head size (qmm_paged_inst.cu): the attention kernel, of at most
 // `ctas` CTAs, then the join.
-template <int D>
+template <int D, bool BEHIND>
 cudaError_t launch_attention(AttentionArgs a, bool e8, int ctas, cudaStream_t stream);
-template <int D>
+template <int D, bool BEHIND>
 unsigned int read_attention_status(int clear);
 
 }  // namespace qmm

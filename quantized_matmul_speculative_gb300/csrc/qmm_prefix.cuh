@@ -1,0 +1,837 @@
+// Attention of a batch of sequences over a prefix that they share, on the tensor cores
+// (qmm_shared_prefix_attention, include/qmm.h).
+//
+// The work.  For one key-value head the rows of all sequences (new rows x the G query
+// heads of the head, without those that do not exist) meet the same keys, so they form
+// tiles of 128 rows, and one copy of a key and value tile serves 256 of them.  A segment
+// is a pair of row tiles of one head; its prefix is cut into tiles of TN tokens; the
+// tiles of all segments form one list, of which every CTA takes an equal, contiguous
+// share.  What a CTA leaves of a segment (maximum, sum, unnormalised output of its share)
+// is a part; a second kernel adds a row's parts to the sequence's own tokens' attention,
+// which the paged kernel (qmm_paged.cuh) has left unrounded.
+//
+// A CTA.  Two lanes, each a warpgroup with a thread a row, and a row tile of scores and
+// of outputs in tensor memory.  In a pair both lanes take every token tile, each with
+// rows of its own; a row tile without a partner is both lanes', which take the token
+// tiles in turn, so that one lane's exponentials run beside the other's products either
+// way.  One thread issues the products, in the order
+//   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ..   of jobs (token tile, lane)
+// where job j's scores go to buffer j mod 2, whose probabilities PV(j - 2) has read (the
+// tensor cores work in order).  Warps of their own copy keys and values, a ring of pieces:
+// by TMA where boxes of 8 tokens divide a page and the cache is bf16, else through
+// registers (E4M3 becomes fp16 there) or by 16-byte asynchronous copies.
+// D = 256: the outputs of one row tile fill half the tensor memory, so there is one lane,
+// with two buffers of scores.
+//
+// The mathematics.  As in qmm_paged.cuh: s = q.k scale log2(e), p = 2^(s - m), sums and
+// outputs in fp32.  m is not the running maximum but follows it where that has grown by
+// more than kSlack (a factor 2^kSlack that fp32 has room for), so that the outputs in
+// tensor memory are seldom scaled.  bf16: p enters the second product as two operands of
+// 16 bits together; the probabilities of a chunk of 32 tokens replace its scores, upper
+// halves in 16 columns, lower ones in the next 16.  E4M3: as one fp16 operand relative to
+// the maximum less kLiftE8 in base 2, so that weights from 2^-25 of the largest on keep 11
+// bits and none below 2^-36 remain.
+#pragma once
+
+#include <climits>
+
+#include "qmm_cache.cuh"
+
+namespace qmm {
+
+constexpr int kRows = 128;        // of a tile
+constexpr int kLoadWarps = 4;
+constexpr int kMaxStarts = 440;   // sequences whose first rows a CTA lists; of more, rows that do not exist are computed too
+constexpr float kSlack = 8.f, kSlackE8 = 4.f, kLiftE8 = 11.f;
+
+struct PrefixArgs {
+  qmm_paged_cache c;
+  const int32_t* prefix;  // pages
+  int tokens;             // of the prefix
+  const uint16_t* q;
+  int64_t q_ld;
+  int B, M, Hq, G;
+  const int32_t* q_lens;
+  float scale_log2;       // |scale| log2(e), times k_scale for an E4M3 cache; > 0
+  int negate;
+  float v_scale;
+  int box;                // tokens of a TMA box; 0: copied by threads
+  int page_log2;          // of the page size, or -1
+  int ctas;
+  float4* part_o;         // [parts][lanes][D / 4][128 rows], part: segment + CTA
+  float2* part_ml;        // [parts][lanes][128]: (m, sum)
+  int* starts;            // [B + 1]: first token row of every sequence
+  const float* own_o;     // [B][M][Hq][D], the own tokens' outputs
+  const float* own_lse;   // [B][M][Hq]
+  __nv_bfloat16* out;
+  float* lse;
+  unsigned long long wait_ns;
+  int inject;
+};
+
+template <int D, bool E8>
+struct PrefixCfg {
+  static constexpr int TN = D == 256 ? 64 : 128;   // tokens of a tile
+  static constexpr int LANES = D == 256 ? 1 : 2;
+  static constexpr int SLICES = D / 64;            // of 128 bytes of a row
+  static constexpr int PIECE = TN * D * 2, QB = kRows * D * 2;
+  static constexpr int MISC = 3072;                // barriers, starts, alignment
+  static constexpr int FIT = (232448 - MISC - LANES * QB) / PIECE, SLOTS = FIT > 8 ? 8 : FIT;
+  static constexpr int OFF_Q = SLOTS * PIECE, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 256;
+  static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
+  static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps;
+  static constexpr int O_COL = 256;                // scores in columns 0 .. 2 TN - 1, outputs from 256 on
+  static_assert(SLOTS >= 4 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
+};
+
+// New rows of sequence b that exist (0 where they do not come behind the prefix).
+__device__ __forceinline__ int rows_of(const PrefixArgs& a, int b) {
+  const int m = new_rows(a.q_lens, b, a.M), n = a.c.lengths[b], own = n - a.tokens;
+  return n <= 0 || own < m || own > a.c.max_pages * a.c.page_size ? 0 : m;
+}
+
+// How a CTA sees the list.
+struct PrefixList {
+  int rows, tiles, pairs, tiles_n;  // rows of a head, row tiles, segments of a head, token tiles
+  int ctas;                         // with a share: no more than there are units, so that every share holds one
+  long long units;
+  template <class Cfg>
+  static __device__ __forceinline__ PrefixList make(const PrefixArgs& a, int token_rows) {
+    PrefixList l;
+    l.rows = token_rows * a.G;
+    l.tiles = (l.rows + kRows - 1) / kRows;
+    l.pairs = (l.tiles + Cfg::LANES - 1) / Cfg::LANES;
+    l.tiles_n = (a.tokens + Cfg::TN - 1) / Cfg::TN;
+    l.units = static_cast<long long>(a.c.heads) * l.pairs * l.tiles_n;
+    l.ctas = l.units < a.ctas ? static_cast<int>(l.units) : a.ctas;
+    return l;
+  }
+  __device__ __forceinline__ long long begin(int cta) const { return cta < ctas ? units * cta / ctas : units; }
+  // the CTA whose share holds unit u
+  __device__ __forceinline__ int holder(long long u) const {
+    int c = static_cast<int>(u * ctas / units);
+    while (c + 1 < ctas && begin(c + 1) <= u) ++c;
+    while (c > 0 && begin(c) > u) --c;
+    return c;
+  }
+};
+
+// One segment of a CTA's share.
+struct PrefixSegment {
+  int s, h, pair, kb, ke;  // segment, head, pair of row tiles, token tiles
+  bool split;              // one row tile, the token tiles taken in turn (two lanes only)
+  __device__ __forceinline__ PrefixSegment(const PrefixList& l, long long u, long long end, int lanes) {
+    s = static_cast<int>(u / l.tiles_n);
+    h = s / l.pairs;
+    pair = s - h * l.pairs;
+    kb = static_cast<int>(u - static_cast<long long>(s) * l.tiles_n);
+    const long long left = end - u;
+    ke = left < l.tiles_n - kb ? kb + static_cast<int>(left) : l.tiles_n;
+    split = lanes == 2 && 2 * pair + 1 >= l.tiles;
+  }
+  __device__ __forceinline__ int jobs(int lanes) const { return (ke - kb) * (lanes == 2 && !split ? 2 : 1); }
+  // of one lane of two
+  __device__ __forceinline__ int lane_jobs(int lane) const { return split ? (ke - kb + 1 - lane) / 2 : ke - kb; }
+};
+
+// Sequence of token row tr: the last one that starts at or before it.
+__device__ __forceinline__ int sequence_of(const int* starts, int B, int tr) {
+  int lo = 0, hi = B;  // starts[lo] <= tr < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= tr) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---- tensor memory and products ----
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead_bytes, uint32_t stride_bytes) {
+  // 128-byte swizzle; leading offset: between slices (read for outputs wider than one), stride: between groups of 8 rows
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(lead_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(stride_bytes >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)) : "memory");
+}
+__device__ __forceinline__ void mma_commit_to(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld32(float (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
+        "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]),
+        "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
+  uint32_t u[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[16 * h + i]);
+    tmem_st16(addr + 16 * h, u);
+  }
+}
+__device__ __forceinline__ float exp2_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_of3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(v));
+  return r;
+}
+// (x0, x1) = (x0, x1) * f - c as a packed pair.
+__device__ __forceinline__ void scale_less(float& x0, float& x1, float f, float c) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 d, {%3, %3};\n"
+      " fma.rn.f32x2 a, a, b, d;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(f), "f"(-c));
+}
+__device__ __forceinline__ void add_pair(float& s0, float& s1, float x0, float x1) {
+  asm("{\n .reg .b64 a, c;\n mov.b64 a, {%0, %1};\n mov.b64 c, {%2, %3};\n add.rn.f32x2 a, a, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_box(uint32_t dst, const void* tmap, int token, int slice, int head, int page, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(tmap), "r"(0), "r"(token), "r"(slice), "r"(head), "r"(page), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_16(uint32_t dst, unsigned long long src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+
+// Byte of 16-byte chunk c (of D / 8) of row r in a tile of `rows` rows: slices of 128
+// bytes of the rows, chunks permuted as the 128-byte swizzle wants them.
+__device__ __forceinline__ uint32_t swizzled(int r, int c, int rows) {
+  return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// ---- the roles of a CTA's warps ----
+template <int D, bool E8>
+struct PrefixRoles {
+  using Cfg = PrefixCfg<D, E8>;
+  static constexpr int TN = Cfg::TN, LANES = Cfg::LANES, SLOTS = Cfg::SLOTS;
+  const PrefixArgs& a;
+  const PrefixList l;
+  unsigned char* smem;
+  uint32_t sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem;
+  const int* starts;
+  long long begin, end;
+
+  // --- copies ---
+  __device__ __forceinline__ int page_of(int j, int& place) const {
+    const int block = a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
+    place = j - block * a.c.page_size;
+    const int p = a.prefix[block];
+    if (p < 0 || p >= a.c.num_pages) {
+      bad_page();
+      return -1;
+    }
+    return p;
+  }
+
+  __device__ __forceinline__ void load_tma(const CUtensorMap* kmap, const CUtensorMap* vmap) {
+    const int lane = threadIdx.x & 31;
+    bool lost = false;
+    int it = 0;
+    const int groups = TN / a.box, boxes = groups * Cfg::SLICES;
+    for (long long u = begin; u < end && !lost;) {
+      const PrefixSegment g(l, u, end, LANES);
+      for (int t = g.kb; t < g.ke && !lost; ++t) {
+        // the pages of the tile's boxes, a lane each (16 at most); outside the prefix and the cache: zeros
+        int page = a.c.num_pages, place = 0;
+        const int j = t * TN + lane * a.box;
+        if (lane < groups && j < a.tokens) {
+          const int p = page_of(j, place);
+          if (p >= 0) page = p;
+        }
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int slot = it % SLOTS;
+          if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+          lost = __any_sync(0xffffffffu, lost);
+          if (lost) break;
+          if (lane == 0) mbar_arrive_expect_tx(full + slot * 8, Cfg::PIECE);
+          __syncwarp();
+          for (int x0 = 0; x0 < boxes; x0 += 32) {
+            const int x = x0 + lane, box = x % groups, slice = x / groups;
+            const int pg = __shfl_sync(0xffffffffu, page, box), pl = __shfl_sync(0xffffffffu, place, box);
+            if (x < boxes)
+              tma_box(sbase + slot * Cfg::PIECE + slice * TN * 128 + box * a.box * 128, kv ? vmap : kmap, pl, slice, g.h, pg,
+                      full + slot * 8);
+          }
+        }
+      }
+      u += g.ke - g.kb;
+    }
+    // (the products wait for the same; where one is given up, the limit was time enough for the others)
+    for (int i = max(it - SLOTS, 0); i < it; ++i)
+      if (__any_sync(0xffffffffu, !mbar_wait(full + i % SLOTS * 8, (i / SLOTS) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
+  }
+
+  // By threads, for pages that no box divides: bf16, rows by 16-byte asynchronous copies, kLag pieces under way.
+  __device__ __forceinline__ void load_rows() {
+    constexpr int CPR = D / 8, STEP = 32 * kLoadWarps / CPR, kLag = 2;  // chunks of a row; rows between a thread's
+    const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
+    bool lost = false;
+    int it = 0;
+    for (long long u = begin; u < end && !lost;) {
+      const PrefixSegment g(l, u, end, LANES);
+      for (int t = g.kb; t < g.ke && !lost; ++t)
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int slot = it % SLOTS;
+          if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+          if (lost) break;
+          const unsigned long long cache = reinterpret_cast<unsigned long long>(kv ? a.c.v : a.c.k);
+          for (int r = r0; r < TN; r += STEP) {
+            int place = 0;
+            const int j = t * TN + r, p = j < a.tokens ? page_of(j, place) : -1;
+            const int64_t at = kv ? p * a.c.v_page + place * a.c.v_token + g.h * a.c.v_head
+                                  : p * a.c.k_page + place * a.c.k_token + g.h * a.c.k_head;
+            copy_16(sbase + slot * Cfg::PIECE + swizzled(r, ch, TN), cache + (p >= 0 ? (at + ch * 8) * 2 : 0), p >= 0);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (it >= kLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+            fence_async_shared();
+            mbar_arrive(full + (it - kLag) % SLOTS * 8);
+          }
+        }
+      u += g.ke - g.kb;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    fence_async_shared();
+    if (!lost)
+      for (int i = max(it - kLag, 0); i < it; ++i) mbar_arrive(full + i % SLOTS * 8);
+  }
+
+  // E4M3 through registers, the next piece's loads ahead of a piece's conversion.
+  __device__ __forceinline__ void load_e4m3() {
+    constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = TN / STEP;  // 16-byte chunks of a row; of a thread
+    const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
+    bool lost = false;
+    int it = 0;
+    uint4 k[N], v[N];
+    auto fetch = [&](uint4 (&to)[N], const int (&page)[N], const int (&place)[N], int h, bool values) {
+      const uint8_t* const cache = static_cast<const uint8_t*>(values ? a.c.v : a.c.k);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        to[i] = make_uint4(0, 0, 0, 0);
+        if (page[i] >= 0)
+          to[i] = ld_after_wait_v4(cache + (values ? page[i] * a.c.v_page + place[i] * a.c.v_token + h * a.c.v_head
+                                                   : page[i] * a.c.k_page + place[i] * a.c.k_token + h * a.c.k_head) +
+                                   ch * 16);
+      }
+    };
+    auto put = [&](const uint4 (&from)[N]) {
+      const int slot = it % SLOTS;
+      if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+      if (lost) return;
+      unsigned char* const piece = smem + slot * Cfg::PIECE;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t w[4] = {from[i].x, from[i].y, from[i].z, from[i].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[2 * e] = e4m3x2_f16x2(w[e]);
+          o[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
+        }
+        const int r = r0 + i * STEP;
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch, TN)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1, TN)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_async_shared();
+      mbar_arrive(full + slot * 8);
+      ++it;
+    };
+    int page[N], place[N];
+    auto find = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int j = t * TN + r0 + i * STEP;
+        place[i] = 0;
+        page[i] = j < a.tokens ? page_of(j, place[i]) : -1;
+      }
+    };
+    long long u = begin;
+    if (u >= end) return;
+    PrefixSegment g(l, u, end, LANES);
+    int t = g.kb;
+    find(t);
+    fetch(k, page, place, g.h, false);
+    while (!lost) {
+      fetch(v, page, place, g.h, true);
+      put(k);
+      if (lost) break;
+      bool more = true;
+      if (++t == g.ke) {
+        u += g.ke - g.kb;
+        more = u < end;
+        if (more) {
+          g = PrefixSegment(l, u, end, LANES);
+          t = g.kb;
+        }
+      }
+      if (more) {
+        find(t);
+        fetch(k, page, place, g.h, false);
+      }
+      put(v);
+      if (!more) break;
+    }
+  }
+
+  // --- products, by one thread ---
+  __device__ __forceinline__ void multiply() {
+    constexpr uint32_t kType = E8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 sums
+    constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((TN >> 3) << 17) | ((kRows >> 4) << 24);
+    constexpr uint32_t kPV = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kRows >> 4) << 24);
+    bool lost = false;
+    int it = 0;               // the segment's first piece
+    int n[2] = {0, 0};        // jobs of a buffer so far
+    int nq[2] = {0, 0};       // query tiles of a lane so far
+    auto wait = [&](uint32_t bar, int phase) {
+      if (!lost) lost = !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns);
+    };
+    for (long long u = begin; u < end && !lost;) {
+      const PrefixSegment g(l, u, end, LANES);
+      const int J = g.jobs(LANES);
+      const bool pair = LANES == 2 && !g.split;
+      auto second = [&](int j) {  // PV(j)
+        const int t = pair ? j >> 1 : j, piece = it + 2 * t + 1, slot = piece % SLOTS, buf = j & 1, o = LANES == 2 ? buf : 0;
+        if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
+        // (the buffer's job j is its n-th but one, or its last)
+        wait(p_full + buf * 8, n[buf] - 1);
+        if (lost) return;
+        tmem_after();
+        const uint32_t v = sbase + slot * Cfg::PIECE, p = tmem + buf * TN, d = tmem + Cfg::O_COL + o * D;
+#pragma unroll
+        for (int x = 0; x < TN / 16; ++x) {
+          const uint64_t b = tile_desc(v + x * 2048, TN * 128, 1024);
+          const uint32_t at = p + (x >> 1) * 32 + (x & 1) * 8;
+          mma_ts(d, at, b, kPV, x > 0 || j >= LANES);
+          if constexpr (!E8) mma_ts(d, at + 16, b, kPV, true);
+        }
+        if (!pair || (j & 1)) mma_commit_to(empty + slot * 8);
+        if (LANES == 1) mma_commit_to(pv_done);
+        if (j + LANES >= J) mma_commit_to(o_full + o * 8);
+      };
+      for (int j = 0; j < J && !lost; ++j) {
+        if (j >= 2) second(j - 2);
+        const int t = pair ? j >> 1 : j, piece = it + 2 * t, slot = piece % SLOTS, buf = j & 1, lane = LANES == 2 ? buf : 0;
+        if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
+        if (j < LANES) wait(q_full + lane * 8, nq[lane]++);
+        if (lost) break;
+        tmem_after();
+        const uint32_t k = sbase + slot * Cfg::PIECE, q = sbase + Cfg::OFF_Q + lane * Cfg::QB;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ss(tmem + buf * TN, tile_desc(q + (x >> 2) * kRows * 128 + (x & 3) * 32, 16, 1024),
+                 tile_desc(k + (x >> 2) * TN * 128 + (x & 3) * 32, 16, 1024), kS, x > 0);
+        if (!pair || (j & 1)) mma_commit_to(empty + slot * 8);
+        mma_commit_to(s_full + buf * 8);
+        ++n[buf];
+      }
+      for (int j = max(J - 2, 0); j < J && !lost; ++j) second(j);
+      it += 2 * (g.ke - g.kb);
+      u += g.ke - g.kb;
+    }
+    // all products are done before the tensor memory is given back
+    mma_commit_to(fin);
+    mbar_wait(fin, 0, kStatusTimeoutDrain, a.wait_ns);
+  }
+
+  // --- rows: queries, probabilities, outputs; a thread a row ---
+  __device__ __forceinline__ float load_query(const PrefixSegment& g, int lane, int row) {
+    const int r = (LANES == 2 ? (g.split ? 2 * g.pair : 2 * g.pair + lane) : g.pair) * kRows + row;
+    const uint16_t* src = nullptr;
+    if (r < l.rows) {
+      const int tr = r / a.G;
+      int at = tr;  // of the B x M rows
+      if (a.B <= kMaxStarts) {
+        const int b = sequence_of(starts, a.B, tr);
+        at = b * a.M + tr - starts[b];
+      }
+      src = a.q + at * a.q_ld + static_cast<int64_t>(g.h * a.G + r - tr * a.G) * D;
+    }
+    unsigned char* const tile = smem + Cfg::OFF_Q + lane * Cfg::QB;
+    const uint32_t flip = a.negate ? 0x80008000u : 0u;
+    float scale = a.scale_log2, f = 1.f;
+    if constexpr (E8) {
+      // fp16, scaled by a power of two so that the row's largest element lies in [2^14, 2^15); 0, tiny and infinite rows stay
+      float top = 0.f;
+      if (src != nullptr)
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 x = ld_after_wait_v4(src + c * 8);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        }
+      const int e = static_cast<int>(__float_as_uint(top) >> 23), up = (e < 30 || e == 255) ? 0 : 14 + 127 - e;
+      f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+      scale = fmaxf(scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1e-30f);
+    }
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (src != nullptr) {
+        x = ld_after_wait_v4(src + c * 8);
+        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+        if constexpr (E8)
+          x = make_uint4(f16x2_of(bf16_lo(x.x) * f, bf16_hi(x.x) * f), f16x2_of(bf16_lo(x.y) * f, bf16_hi(x.y) * f),
+                         f16x2_of(bf16_lo(x.z) * f, bf16_hi(x.z) * f), f16x2_of(bf16_lo(x.w) * f, bf16_hi(x.w) * f));
+      }
+      *reinterpret_cast<uint4*>(tile + swizzled(row, c, kRows)) = x;
+    }
+    fence_async_shared();
+    mbar_arrive(q_full + lane * 8);
+    return scale;
+  }
+
+  __device__ __forceinline__ void rows() {
+    const int lane = threadIdx.x >> 7, row = threadIdx.x & 127;
+    const uint32_t mine = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;  // this warp's quarter of the tensor memory's lanes
+    const uint32_t o_at = tmem + Cfg::O_COL + lane * D + mine;
+    bool lost = false;
+    int n[2] = {0, 0};  // jobs of a buffer so far
+    int n_o = 0, n_pv = 0;
+    auto wait = [&](uint32_t bar, int phase) {
+      if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns));
+      tmem_after();
+    };
+    for (long long u = begin; u < end;) {
+      const PrefixSegment g(l, u, end, LANES);
+      u += g.ke - g.kb;
+      const int jobs = LANES == 2 ? g.lane_jobs(lane) : g.ke - g.kb;
+      const int64_t part = (static_cast<int64_t>(g.s) + blockIdx.x) * LANES + lane;
+      float m = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+      if (jobs > 0 && !lost) {
+        const float scale = load_query(g, lane, row);
+        for (int j = 0; j < jobs; ++j) {
+          const int buf = LANES == 2 ? lane : j & 1;
+          const int t = LANES == 2 && g.split ? g.kb + 2 * j + lane : g.kb + j;
+          const int valid = a.tokens - t * TN;  // of the tile's columns, if fewer than TN
+          const uint32_t s_at = tmem + buf * TN + mine;
+          wait(s_full + buf * 8, n[buf]++);
+          if (lost) break;
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < TN; c += 64) {
+            float x[32], y[32];
+            tmem_ld32(x, s_at + c);
+            tmem_ld32(y, s_at + c + 32);
+            tmem_loaded();
+            if (valid < TN) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (c + i >= valid) x[i] = -INFINITY;
+                if (c + 32 + i >= valid) y[i] = -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = max_of3(top, x[i], y[i]);
+          }
+          top *= scale;
+          const float want = E8 ? top - kLiftE8 : top;
+          const bool grown = want > m + (E8 ? kSlackE8 : kSlack) || m == -INFINITY;
+          float f = 1.f;
+          if (grown) {
+            f = exp2_of(m - (want == -INFINITY ? 0.f : want));
+            m = want;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            if (LANES == 1) wait(pv_done, n_pv - 1);  // (of two lanes, the one's products end before its next scores)
+            sum0 *= f;
+            sum1 *= f;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              float x[32];
+              tmem_ld32(x, o_at + c);
+              tmem_loaded();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] *= f;
+              tmem_st32(o_at + c, x);
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int c = 0; c < TN; c += 32) {
+            float x[32];
+            tmem_ld32(x, s_at + c);
+            tmem_loaded();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              scale_less(x[i], x[i + 1], scale, base);
+              x[i] = exp2_of(x[i]);
+              x[i + 1] = exp2_of(x[i + 1]);
+            }
+            if (valid < TN) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c + i >= valid) x[i] = 0.f;
+            }
+            uint32_t p[16];
+            if constexpr (E8) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                add_pair(sum0, sum1, x[2 * i], x[2 * i + 1]);
+                p[i] = f16x2_of(x[2 * i], x[2 * i + 1]);
+              }
+              tmem_st16(s_at + c, p);
+            } else {
+              // the upper half of a probability as it is, the rest as a second operand; the rest of one that is not 0 is not 0
+              // either (its last bit is set first), so that an infinite value times it is that infinity and not NaN
+              uint32_t rest[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float lo = x[2 * i], hi = x[2 * i + 1];
+                add_pair(sum0, sum1, lo, hi);
+                const uint32_t bl = __float_as_uint(lo), bh = __float_as_uint(hi);
+                p[i] = __byte_perm(bl, bh, 0x7632);
+                rest[i] = bf16x2_of(__uint_as_float(bl | 1u) - __uint_as_float(bl & 0xFFFF0000u),
+                                    __uint_as_float(bh | 1u) - __uint_as_float(bh & 0xFFFF0000u));
+              }
+              tmem_st16(s_at + c, p);
+              tmem_st16(s_at + c + 16, rest);
+            }
+          }
+          tmem_stored();
+          tmem_before();
+          mbar_arrive(p_full + buf * 8);
+          ++n_pv;
+        }
+        wait(o_full + lane * 8, n_o++);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          tmem_ld32(x, o_at + c);
+          tmem_loaded();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            a.part_o[(part * (D / 4) + c / 4 + i) * kRows + row] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+        tmem_before();
+      }
+      a.part_ml[part * kRows + row] = make_float2(m, sum0 + sum1);
+    }
+  }
+};
+
+template <int D, bool E8>
+__global__ void __launch_bounds__(PrefixCfg<D, E8>::THREADS, 1)
+prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using Cfg = PrefixCfg<D, E8>;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t full = sbase + Cfg::OFF_BAR, empty = full + Cfg::SLOTS * 8, s_full = empty + Cfg::SLOTS * 8, p_full = s_full + 16,
+                 q_full = p_full + 16, o_full = q_full + 16, pv_done = o_full + 16, fin = pv_done + 8;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + Cfg::SLOTS * 16 + 80);
+  int* const starts = reinterpret_cast<int*>(smem + Cfg::OFF_STARTS);
+  int* const s_sum = reinterpret_cast<int*>(smem + Cfg::OFF_Q);  // (before the queries)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::SLOTS; ++s) {
+      mbar_init(full + s * 8, a.box ? 1 : 32 * kLoadWarps);
+      mbar_init(empty + s * 8, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i * 8, 1);
+      mbar_init(p_full + i * 8, 128);
+      mbar_init(q_full + i * 8, 128);
+      mbar_init(o_full + i * 8, 1);
+    }
+    mbar_init(pv_done, 1);
+    mbar_init(fin, 1);
+    fence_mbar_init();
+    if (a.inject && blockIdx.x == 0) mbar_expect_tx(full, 16);
+  }
+  if (warp == Cfg::WG / 32) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  // the sequences' first token rows
+  int token_rows = a.B * a.M;
+  if (a.B <= kMaxStarts) {
+    // (a thread takes neighbouring sequences, at most two)
+    constexpr int kPer = (kMaxStarts + Cfg::THREADS - 1) / Cfg::THREADS;
+    int m[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = threadIdx.x * kPer + i;
+      m[i] = b < a.B ? rows_of(a, b) : 0;
+      mine += m[i];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, s);
+      if (lane >= s) inc += o;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    __syncthreads();
+    int before = inc - mine;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    token_rows = 0;
+    for (int w = 0; w < Cfg::THREADS / 32; ++w) token_rows += s_sum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int b = threadIdx.x * kPer + i;
+      if (b < a.B) {
+        starts[b] = before;
+        if (blockIdx.x == 0) a.starts[b] = before;
+      }
+      before += m[i];
+    }
+    if (threadIdx.x == 0) {
+      starts[a.B] = token_rows;
+      if (blockIdx.x == 0) a.starts[a.B] = token_rows;
+    }
+  } else if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b <= a.B; b += Cfg::THREADS) a.starts[b] = b * a.M;
+  }
+  tmem_before();
+  __syncthreads();
+  tmem_after();
+  const uint32_t tmem = *tmem_slot;
+  const PrefixList l = PrefixList::make<Cfg>(a, token_rows);
+  PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem, starts,
+                       l.begin(blockIdx.x), l.begin(blockIdx.x + 1)};
+  if (warp < Cfg::WG / 32) {
+    r.rows();
+  } else if (warp == Cfg::WG / 32) {
+    if (lane == 0) r.multiply();
+  } else if (E8) {
+    r.load_e4m3();
+  } else if (a.box == 0) {
+    r.load_rows();
+  } else if (warp == Cfg::WG / 32 + 1) {
+    r.load_tma(&kmap, &vmap);
+  }
+  __syncwarp();
+  tmem_before();
+  __syncthreads();
+  tmem_after();
+  if (warp == Cfg::WG / 32) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// Adds a row's parts and its own tokens' share, in the order of the list.  A CTA takes a
+// head and a few neighbouring rows of the B x M x G of it, a thread four of their columns.
+constexpr int kPrefixJoinThreads = 256;
+template <int D, bool E8>
+__global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixArgs a) {
+  using Cfg = PrefixCfg<D, E8>;
+  constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int blocks = (a.B * a.M * a.G + ROWS - 1) / ROWS;
+  const int h = blockIdx.x / blocks, x = (blockIdx.x - h * blocks) * ROWS + threadIdx.x % ROWS, col = threadIdx.x / ROWS;
+  if (x >= a.B * a.M * a.G) return;
+  const int tr = x / a.G, b = tr / a.M, i = tr - b * a.M;
+  const int64_t at = static_cast<int64_t>(tr) * a.Hq + h * a.G + x - tr * a.G;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lse = -INFINITY;
+  if (i < rows_of(a, b)) {
+    const float own_lse = a.own_lse[at];
+    const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
+    const float own_m = own_lse * 1.4426950408889634f;
+    float top = own_m;
+    int first = 0, parts = 0, lanes = 1;
+    int64_t p0 = 0;  // (part, lane) of the first
+    int r = 0;
+    if (a.tokens > 0) {
+      const PrefixList l = PrefixList::make<Cfg>(a, a.starts[a.B]);
+      r = (a.starts[b] + i) * a.G + x - tr * a.G;
+      const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair;
+      r -= tile * kRows;
+      const long long u0 = static_cast<long long>(s) * l.tiles_n;
+      first = l.holder(u0);
+      parts = l.holder(u0 + l.tiles_n - 1) - first + 1;
+      const bool split = Cfg::LANES == 2 && 2 * pair + 1 >= l.tiles;
+      lanes = split ? 2 : 1;
+      p0 = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
+    }
+    // (a part's lanes lie next to each other, parts LANES apart)
+    const int n = parts * lanes, step = lanes == 2 ? 1 : Cfg::LANES;
+    for (int p = 0; p < n; ++p) top = fmaxf(top, a.part_ml[(p0 + p * step) * kRows + r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float w = own_lse == -INFINITY ? 0.f : exp2_of(own_m - ref);
+    float sum = w;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+      const int64_t at_part = p0 + p * step;
+      const float2 ml = a.part_ml[at_part * kRows + r];
+      if (ml.y == 0.f) continue;  // (a lane without a tile leaves no output)
+      const float4 v = a.part_o[(at_part * COLS + col) * kRows + r];
+      const float f = exp2_of(ml.x - ref);
+      sum += f * ml.y;
+      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+    }
+    if (sum != 0.f) {
+      const float f = a.v_scale / sum, g = w / sum;
+      o = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      if (w != 0.f) o.x += own.x * g, o.y += own.y * g, o.z += own.z * g, o.w += own.w * g;
+      lse = (ref + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+  *reinterpret_cast<uint2*>(a.out + at * D + col * 4) = make_uint2(bf16x2_of(o.x, o.y), bf16x2_of(o.z, o.w));
+  if (col == 0 && a.lse != nullptr) a.lse[at] = lse;
+}
+
+// Segments of a call at most, whatever exists of its rows.
+inline int64_t prefix_segments(int64_t rows, int heads, int D) {
+  const int64_t tiles = (rows + kRows - 1) / kRows;
+  return heads * (D == 256 ? tiles : (tiles + 1) / 2);
+}
+
+// Launchers of one head size (qmm_prefix_inst.cu).
+template <int D>
+cudaError_t launch_prefix(const PrefixArgs& a, bool e8, cudaStream_t stream);
+template <int D>
+cudaError_t launch_prefix_join(const PrefixArgs& a, bool e8, cudaStream_t stream);
+template <int D>
+unsigned int read_prefix_unit(int clear);
+
+}  // namespace qmm

@@ -3,7 +3,9 @@
 Bounds, from its roundings: a score is an fp32 sum of D exact products, off by at most d = (D + 8) 2^-24 scale sum|q k|;
 probabilities enter the second product with 16 bits (2^-16) after an exponential (2^-21), and sums of up to some hundred
 terms in a chain (tiles of 128, then parts) add 2^-16; so with P = sum_j p_j |v_j| the output is off by at most
-(2^-14 + 2 d) P + 2^-8 |o| (the last for the bf16 output), and the log-sum-exp by d + 2^-16 + 2^-20 |lse|."""
+(2^-14 + 2 d) P + 2^-8 |o| (the last for the bf16 output), and the log-sum-exp by d + 2^-16 + 2^-20 |lse|.
+An E4M3 cache's probabilities enter that product in fp16, 11 bits, whose rounding is off by at most eps / 2 = 2^-11 of each:
+(2^-11 + 2^-14 + 2 d) P there."""
 import math
 
 import pytest
@@ -57,7 +59,8 @@ def reference(q, s, rows, scale):
 
         o[b, :m] = back(p @ v.transpose(1, 2))
         lse[b, :m] = back(torch.logsumexp(x, -1))[..., 0]
-        bo[b, :m] = back((2.0**-14 + 2 * d)[..., None] * (p @ v.abs().transpose(1, 2))) + 2.0**-8 * o[b, :m].abs()
+        weight = 2.0**-14 + (2.0**-11 if s.k.dtype == E4M3 else 0.0)
+        bo[b, :m] = back((weight + 2 * d)[..., None] * (p @ v.abs().transpose(1, 2))) + 2.0**-8 * o[b, :m].abs()
         bl[b, :m] = back(d)[..., 0] + 2.0**-16 + 2.0**-20 * lse[b, :m].abs()
     return o, lse, bo, bl
 
@@ -65,7 +68,10 @@ def reference(q, s, rows, scale):
 def check(q, s, rows=None, scale=None, **more):
     B, M, Hq, D = q.shape
     q_lens = None if rows is None else torch.tensor(rows, dtype=torch.int32, device="cuda")
-    out, lse = binding.shared_prefix_attention(q, *s.args(), q_lens=q_lens, scale=scale, return_lse=True, **s.c.scales(), **more)
+    size = binding.shared_prefix_attention_workspace(B, M, Hq, s.k.shape[2], D)
+    workspace = torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # NaN wherever it is read before it is written
+    out, lse = binding.shared_prefix_attention(q, *s.args(), q_lens=q_lens, scale=scale, return_lse=True, workspace=workspace,
+                                               **s.c.scales(), **more)
     torch.cuda.synchronize()
     assert binding.device_status() == 0
     rows = [M] * B if rows is None else rows
