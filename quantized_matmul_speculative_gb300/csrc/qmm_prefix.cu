@@ -97,6 +97,7 @@ qmm_status qmm_shared_prefix_attention(const qmm_paged_cache* cache, const int32
   a.page_log2 = (cache->page_size & (cache->page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(cache->page_size)) : -1;
   const int tile = D == 256 ? 64 : 128;
   const int64_t units = prefix_segments(static_cast<int64_t>(B) * M * a.G, cache->heads, D) * ((a.tokens + tile - 1) / tile);
+  if (units > 0x7fffff00) return QMM_ERR_SHAPE;  // (numbered in 32 bits)
   a.ctas = units < device_sm_count() ? static_cast<int>(units) : device_sm_count();
   a.part_o = reinterpret_cast<float4*>(ws + space.part_o);
   a.part_ml = reinterpret_cast<float2*>(ws + space.part_ml);

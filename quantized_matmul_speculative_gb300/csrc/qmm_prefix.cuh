@@ -40,8 +40,8 @@
 namespace qmm {
 
 constexpr int kRows = 128;        // of a tile
-constexpr int kLoadWarps = 4;
-constexpr int kMaxStarts = 440;   // sequences whose first rows a CTA lists; of more, rows that do not exist are computed too
+constexpr int kLoadWarps = 3;   // (12 warps in all: a thread may have 168 registers, of 13 and more 128)
+constexpr int kMaxStarts = 400;   // sequences whose first rows a CTA lists; of more, rows that do not exist are computed too
 constexpr float kSlack = 8.f, kSlackE8 = 4.f, kLiftE8 = 11.f;
 
 struct PrefixArgs {
@@ -80,6 +80,7 @@ struct PrefixCfg {
   static constexpr int OFF_Q = SLOTS * PIECE, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 256;
   static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
   static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps;
+  static constexpr int ROW_REGS = E8 ? 192 : 208, OTHER_REGS = E8 ? 120 : 88;
   static constexpr int O_COL = 256;                // scores in columns 0 .. 2 TN - 1, outputs from 256 on
   static_assert(SLOTS >= 4 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
 };
@@ -94,7 +95,7 @@ __device__ __forceinline__ int rows_of(const PrefixArgs& a, int b) {
 struct PrefixList {
   int rows, tiles, pairs, tiles_n;  // rows of a head, row tiles, segments of a head, token tiles
   int ctas;                         // with a share: no more than there are units, so that every share holds one
-  long long units;
+  int units, each, more;            // units of a share; how many of the first shares hold one more
   template <class Cfg>
   static __device__ __forceinline__ PrefixList make(const PrefixArgs& a, int token_rows) {
     PrefixList l;
@@ -102,17 +103,17 @@ struct PrefixList {
     l.tiles = (l.rows + kRows - 1) / kRows;
     l.pairs = (l.tiles + Cfg::LANES - 1) / Cfg::LANES;
     l.tiles_n = (a.tokens + Cfg::TN - 1) / Cfg::TN;
-    l.units = static_cast<long long>(a.c.heads) * l.pairs * l.tiles_n;
-    l.ctas = l.units < a.ctas ? static_cast<int>(l.units) : a.ctas;
+    l.units = a.c.heads * l.pairs * l.tiles_n;
+    l.ctas = min(l.units, a.ctas);
+    l.each = l.ctas > 0 ? l.units / l.ctas : 0;
+    l.more = l.units - l.each * l.ctas;
     return l;
   }
-  __device__ __forceinline__ long long begin(int cta) const { return cta < ctas ? units * cta / ctas : units; }
+  __device__ __forceinline__ int begin(int cta) const { return cta < ctas ? cta * each + min(cta, more) : units; }
   // the CTA whose share holds unit u
-  __device__ __forceinline__ int holder(long long u) const {
-    int c = static_cast<int>(u * ctas / units);
-    while (c + 1 < ctas && begin(c + 1) <= u) ++c;
-    while (c > 0 && begin(c) > u) --c;
-    return c;
+  __device__ __forceinline__ int holder(int u) const {
+    const int long_ones = more * (each + 1);
+    return u < long_ones ? u / (each + 1) : more + (u - long_ones) / each;
   }
 };
 
@@ -120,13 +121,12 @@ struct PrefixList {
 struct PrefixSegment {
   int s, h, pair, kb, ke;  // segment, head, pair of row tiles, token tiles
   bool split;              // one row tile, the token tiles taken in turn (two lanes only)
-  __device__ __forceinline__ PrefixSegment(const PrefixList& l, long long u, long long end, int lanes) {
-    s = static_cast<int>(u / l.tiles_n);
+  __device__ __forceinline__ PrefixSegment(const PrefixList& l, int u, int end, int lanes) {
+    s = u / l.tiles_n;
     h = s / l.pairs;
     pair = s - h * l.pairs;
-    kb = static_cast<int>(u - static_cast<long long>(s) * l.tiles_n);
-    const long long left = end - u;
-    ke = left < l.tiles_n - kb ? kb + static_cast<int>(left) : l.tiles_n;
+    kb = u - s * l.tiles_n;
+    ke = min(l.tiles_n, kb + end - u);
     split = lanes == 2 && 2 * pair + 1 >= l.tiles;
   }
   __device__ __forceinline__ int jobs(int lanes) const { return (ke - kb) * (lanes == 2 && !split ? 2 : 1); }
@@ -218,6 +218,13 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   asm("{\n .reg .b16 h;\n cvt.u16.u32 h, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}" : "=r"(r) : "r"(v));
   return r;
 }
+// (x0, x1) = x - (1 - 2^-20) (x's upper 16 bits), as a packed pair.
+__device__ __forceinline__ void rest_of(float& x0, float& x1) {
+  const uint32_t h0 = __float_as_uint(x0) & 0xFFFF0000u, h1 = __float_as_uint(x1) & 0xFFFF0000u;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 d, {%4, %4};\n"
+      " fma.rn.f32x2 a, b, d, a;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x0), "+f"(x1) : "f"(__uint_as_float(h0)), "f"(__uint_as_float(h1)), "f"(-(1.f - 1.f / 1048576.f)));
+}
 // (x0, x1) = (x0, x1) * f - c as a packed pair.
 __device__ __forceinline__ void scale_less(float& x0, float& x1, float f, float c) {
   asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 d, {%3, %3};\n"
@@ -254,7 +261,7 @@ struct PrefixRoles {
   unsigned char* smem;
   uint32_t sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem;
   const int* starts;
-  long long begin, end;
+  int begin, end;
 
   // --- copies ---
   __device__ __forceinline__ int page_of(int j, int& place) const {
@@ -273,7 +280,7 @@ struct PrefixRoles {
     bool lost = false;
     int it = 0;
     const int groups = TN / a.box, boxes = groups * Cfg::SLICES;
-    for (long long u = begin; u < end && !lost;) {
+    for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       for (int t = g.kb; t < g.ke && !lost; ++t) {
         // the pages of the tile's boxes, a lane each (16 at most); outside the prefix and the cache: zeros
@@ -312,7 +319,7 @@ struct PrefixRoles {
     const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
     bool lost = false;
     int it = 0;
-    for (long long u = begin; u < end && !lost;) {
+    for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       for (int t = g.kb; t < g.ke && !lost; ++t)
         for (int kv = 0; kv < 2; ++kv, ++it) {
@@ -344,7 +351,7 @@ struct PrefixRoles {
 
   // E4M3 through registers, the next piece's loads ahead of a piece's conversion.
   __device__ __forceinline__ void load_e4m3() {
-    constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = TN / STEP;  // 16-byte chunks of a row; of a thread
+    constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = (TN + STEP - 1) / STEP;  // 16-byte chunks of a row; of a thread
     const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
     bool lost = false;
     int it = 0;
@@ -375,6 +382,7 @@ struct PrefixRoles {
           o[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
         }
         const int r = r0 + i * STEP;
+        if (r >= TN) break;
         *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch, TN)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1, TN)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
@@ -388,10 +396,10 @@ struct PrefixRoles {
       for (int i = 0; i < N; ++i) {
         const int j = t * TN + r0 + i * STEP;
         place[i] = 0;
-        page[i] = j < a.tokens ? page_of(j, place[i]) : -1;
+        page[i] = r0 + i * STEP < TN && j < a.tokens ? page_of(j, place[i]) : -1;
       }
     };
-    long long u = begin;
+    int u = begin;
     if (u >= end) return;
     PrefixSegment g(l, u, end, LANES);
     int t = g.kb;
@@ -431,7 +439,7 @@ struct PrefixRoles {
     auto wait = [&](uint32_t bar, int phase) {
       if (!lost) lost = !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns);
     };
-    for (long long u = begin; u < end && !lost;) {
+    for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       const int J = g.jobs(LANES);
       const bool pair = LANES == 2 && !g.split;
@@ -527,119 +535,127 @@ struct PrefixRoles {
     return scale;
   }
 
+  // The scores of the 32 columns from c on that are tokens, the others -inf.
+  __device__ __forceinline__ static void cut(float (&x)[32], int c, int valid) {
+    if (valid < c + 32)
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i >= valid) x[i] = -INFINITY;
+  }
+  // 32 scores to probabilities, to the columns that held the scores; their sums.
+  __device__ __forceinline__ static void weigh(float (&x)[32], uint32_t at, float scale, float base, float& sum0, float& sum1) {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      scale_less(x[2 * i], x[2 * i + 1], scale, base);
+      x[2 * i] = exp2_of(x[2 * i]);
+      x[2 * i + 1] = exp2_of(x[2 * i + 1]);
+      add_pair(sum0, sum1, x[2 * i], x[2 * i + 1]);
+      if constexpr (E8) p[i] = f16x2_of(x[2 * i], x[2 * i + 1]);
+      else p[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+    }
+    tmem_st16(at, p);
+    if constexpr (!E8) {
+      // The upper half of a probability goes in as it is, the rest as a second operand: x - hi (1 - 2^-20), which is 0 for x = 0
+      // alone, so that an infinite value times it is that infinity and not NaN; the 2^-20 of x is below the 16 bits' own rounding.
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        rest_of(x[2 * i], x[2 * i + 1]);
+        p[i] = bf16x2_of(x[2 * i], x[2 * i + 1]);
+      }
+      tmem_st16(at + 16, p);
+    }
+  }
+
   __device__ __forceinline__ void rows() {
     const int lane = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t mine = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;  // this warp's quarter of the tensor memory's lanes
     const uint32_t o_at = tmem + Cfg::O_COL + lane * D + mine;
     bool lost = false;
-    int n[2] = {0, 0};  // jobs of a buffer so far
-    int n_o = 0, n_pv = 0;
+    int n[2] = {0, 0};    // jobs of a buffer so far
+    int n_o[2] = {0, 0};  // segments of a lane so far
+    int n_pv = 0;
     auto wait = [&](uint32_t bar, int phase) {
       if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns));
       tmem_after();
     };
-    for (long long u = begin; u < end;) {
+    auto jobs_of = [&](const PrefixSegment& g, int x) { return LANES == 2 ? g.lane_jobs(x) : g.ke - g.kb; };
+    float scale = 0.f;
+    if (begin < end) {
+      const PrefixSegment g(l, begin, end, LANES);
+      if (jobs_of(g, lane) > 0) scale = load_query(g, lane, row);
+    }
+    for (int u = begin; u < end;) {
       const PrefixSegment g(l, u, end, LANES);
       u += g.ke - g.kb;
-      const int jobs = LANES == 2 ? g.lane_jobs(lane) : g.ke - g.kb;
-      const int64_t part = (static_cast<int64_t>(g.s) + blockIdx.x) * LANES + lane;
+      const int jobs = jobs_of(g, lane);
       float m = -INFINITY, sum0 = 0.f, sum1 = 0.f;
-      if (jobs > 0 && !lost) {
-        const float scale = load_query(g, lane, row);
-        for (int j = 0; j < jobs; ++j) {
-          const int buf = LANES == 2 ? lane : j & 1;
-          const int t = LANES == 2 && g.split ? g.kb + 2 * j + lane : g.kb + j;
-          const int valid = a.tokens - t * TN;  // of the tile's columns, if fewer than TN
-          const uint32_t s_at = tmem + buf * TN + mine;
-          wait(s_full + buf * 8, n[buf]++);
-          if (lost) break;
-          float top = -INFINITY;
+#pragma unroll 1
+      for (int j = 0; j < jobs; ++j) {
+        const int buf = LANES == 2 ? lane : j & 1;
+        const int t = LANES == 2 && g.split ? g.kb + 2 * j + lane : g.kb + j;
+        const int valid = a.tokens - t * TN;  // of the tile's columns, if fewer than TN
+        const uint32_t s_at = tmem + buf * TN + mine;
+        wait(s_full + buf * 8, n[buf]++);
+        if (lost) break;
+        // all scores of the row at once
+        float x[TN / 32][32];
 #pragma unroll
-          for (int c = 0; c < TN; c += 64) {
-            float x[32], y[32];
-            tmem_ld32(x, s_at + c);
-            tmem_ld32(y, s_at + c + 32);
-            tmem_loaded();
-            if (valid < TN) {
+        for (int c = 0; c < TN / 32; ++c) tmem_ld32(x[c], s_at + c * 32);
+        tmem_loaded();
+        if (valid < TN)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (c + i >= valid) x[i] = -INFINITY;
-                if (c + 32 + i >= valid) y[i] = -INFINITY;
-              }
-            }
+          for (int c = 0; c < TN / 32; ++c) cut(x[c], c * 32, valid);
+        float top = fmaxf(x[0][0], x[0][1]), top1 = fmaxf(x[1][0], x[1][1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = max_of3(top, x[i], y[i]);
+        for (int c = 0; c < TN / 32; c += 2)
+#pragma unroll
+          for (int i = c == 0 ? 2 : 0; i < 32; i += 2) {
+            top = max_of3(top, x[c][i], x[c][i + 1]);
+            top1 = max_of3(top1, x[c + 1][i], x[c + 1][i + 1]);
           }
-          top *= scale;
-          const float want = E8 ? top - kLiftE8 : top;
-          const bool grown = want > m + (E8 ? kSlackE8 : kSlack) || m == -INFINITY;
-          float f = 1.f;
-          if (grown) {
-            f = exp2_of(m - (want == -INFINITY ? 0.f : want));
-            m = want;
-          }
-          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-            if (LANES == 1) wait(pv_done, n_pv - 1);  // (of two lanes, the one's products end before its next scores)
-            sum0 *= f;
-            sum1 *= f;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              float x[32];
-              tmem_ld32(x, o_at + c);
-              tmem_loaded();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] *= f;
-              tmem_st32(o_at + c, x);
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int c = 0; c < TN; c += 32) {
-            float x[32];
-            tmem_ld32(x, s_at + c);
-            tmem_loaded();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              scale_less(x[i], x[i + 1], scale, base);
-              x[i] = exp2_of(x[i]);
-              x[i + 1] = exp2_of(x[i + 1]);
-            }
-            if (valid < TN) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c + i >= valid) x[i] = 0.f;
-            }
-            uint32_t p[16];
-            if constexpr (E8) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                add_pair(sum0, sum1, x[2 * i], x[2 * i + 1]);
-                p[i] = f16x2_of(x[2 * i], x[2 * i + 1]);
-              }
-              tmem_st16(s_at + c, p);
-            } else {
-              // the upper half of a probability as it is, the rest as a second operand; the rest of one that is not 0 is not 0
-              // either (its last bit is set first), so that an infinite value times it is that infinity and not NaN
-              uint32_t rest[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float lo = x[2 * i], hi = x[2 * i + 1];
-                add_pair(sum0, sum1, lo, hi);
-                const uint32_t bl = __float_as_uint(lo), bh = __float_as_uint(hi);
-                p[i] = __byte_perm(bl, bh, 0x7632);
-                rest[i] = bf16x2_of(__uint_as_float(bl | 1u) - __uint_as_float(bl & 0xFFFF0000u),
-                                    __uint_as_float(bh | 1u) - __uint_as_float(bh & 0xFFFF0000u));
-              }
-              tmem_st16(s_at + c, p);
-              tmem_st16(s_at + c + 16, rest);
-            }
-          }
-          tmem_stored();
-          tmem_before();
-          mbar_arrive(p_full + buf * 8);
-          ++n_pv;
+        top = fmaxf(top, top1) * scale;
+        const float want = E8 ? top - kLiftE8 : top;
+        const bool grown = want > m + (E8 ? kSlackE8 : kSlack) || m == -INFINITY;
+        float f = 1.f;
+        if (grown) {
+          f = exp2_of(m - (want == -INFINITY ? 0.f : want));
+          m = want;
         }
-        wait(o_full + lane * 8, n_o++);
+        const float base = m == -INFINITY ? 0.f : m;
+        const bool again = j > 0 && __any_sync(0xffffffffu, f != 1.f);
+        if (again) {
+          sum0 *= f;
+          sum1 *= f;
+        }
+#pragma unroll
+        for (int c = 0; c < TN / 32; ++c) weigh(x[c], s_at + c * 32, scale, base, sum0, sum1);
+        if (again) {
+          if (LANES == 1) wait(pv_done, n_pv - 1);  // (of two lanes, the one's products end before its next scores)
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tmem_ld32(x[0], o_at + c);
+            tmem_loaded();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[0][i] *= f;
+            tmem_st32(o_at + c, x[0]);
+          }
+        }
+        tmem_stored();
+        tmem_before();
+        mbar_arrive(p_full + buf * 8);
+        ++n_pv;
+      }
+      // the next segment's queries, whose scores may begin beside this one's end
+      if (u < end) {
+        const PrefixSegment next(l, u, end, LANES);
+        if (jobs_of(next, lane) > 0 && !lost) scale = load_query(next, lane, row);
+      }
+      const bool both = LANES == 2 && g.split;
+      const float sum = sum0 + sum1;
+      if (!both) {
+        const int64_t part = (static_cast<int64_t>(g.s) + blockIdx.x) * LANES + lane;
+        wait(o_full + lane * 8, n_o[lane]);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float x[32];
@@ -649,9 +665,44 @@ struct PrefixRoles {
           for (int i = 0; i < 8; ++i)
             a.part_o[(part * (D / 4) + c / 4 + i) * kRows + row] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
-        tmem_before();
+        a.part_ml[part * kRows + row] = make_float2(m, sum);
+      } else {
+        // one part of both lanes' outputs, which lie in the same lanes of tensor memory: a lane adds half of the columns
+        const int64_t part = (static_cast<int64_t>(g.s) + blockIdx.x) * LANES;
+        a.part_ml[(part + lane) * kRows + row] = make_float2(m, sum);  // (shared memory is full)
+        __threadfence_block();
+        asm volatile("barrier.sync 1, 256;" ::: "memory");
+        const float2 other = __ldcg(&a.part_ml[(part + (lane ^ 1)) * kRows + row]);
+        const bool second = g.lane_jobs(1) > 0;
+        wait(o_full, n_o[0]);
+        if (second) wait(o_full + 8, n_o[1]);
+        const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+        const float f_mine = exp2_of(m - ref), f_other = exp2_of(other.x - ref);
+        const float f0 = lane == 0 ? f_mine : f_other, f1 = lane == 0 ? f_other : f_mine;
+        const uint32_t at = tmem + Cfg::O_COL + mine + lane * (D / 2);
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          float x[32], y[32];
+          tmem_ld32(x, at + c);
+          if (second) tmem_ld32(y, at + D + c);
+          tmem_loaded();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] *= f0;
+            if (second) x[i] = fmaf(y[i], f1, x[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            a.part_o[(part * (D / 4) + lane * (D / 8) + c / 4 + i) * kRows + row] =
+                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+        asm volatile("barrier.sync 1, 256;" ::: "memory");  // both have read both
+        if (lane == 0) a.part_ml[part * kRows + row] = make_float2(top, fmaf(sum, f_mine, other.y * f_other));
       }
-      a.part_ml[part * kRows + row] = make_float2(m, sum0 + sum1);
+      if (LANES == 1) ++n_o[0];
+      else
+        for (int x = 0; x < 2; ++x) n_o[x] += g.lane_jobs(x) > 0;
+      tmem_before();
     }
   }
 };
@@ -738,6 +789,13 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const PrefixList l = PrefixList::make<Cfg>(a, token_rows);
   PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem, starts,
                        l.begin(blockIdx.x), l.begin(blockIdx.x + 1)};
+  // Two lanes: a thread that holds a row of 128 scores takes registers of the others' (of the 384 x 168 of the launch,
+  // 256 x 208 + 128 x 88; an E4M3 cache's copying threads hold two pieces' chunks: 256 x 192 + 128 x 120).
+  if constexpr (Cfg::LANES == 2) {
+    static_assert(256 * Cfg::ROW_REGS + 128 * Cfg::OTHER_REGS <= 384 * 168, "registers of the launch");
+    if (warp < Cfg::WG / 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::ROW_REGS));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::OTHER_REGS));
+  }
   if (warp < Cfg::WG / 32) {
     r.rows();
   } else if (warp == Cfg::WG / 32) {
@@ -777,7 +835,7 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
     const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
     const float own_m = own_lse * 1.4426950408889634f;
     float top = own_m;
-    int first = 0, parts = 0, lanes = 1;
+    int first = 0, parts = 0;
     int64_t p0 = 0;  // (part, lane) of the first
     int r = 0;
     if (a.tokens > 0) {
@@ -785,25 +843,23 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
       r = (a.starts[b] + i) * a.G + x - tr * a.G;
       const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair;
       r -= tile * kRows;
-      const long long u0 = static_cast<long long>(s) * l.tiles_n;
+      const int u0 = s * l.tiles_n;
       first = l.holder(u0);
       parts = l.holder(u0 + l.tiles_n - 1) - first + 1;
       const bool split = Cfg::LANES == 2 && 2 * pair + 1 >= l.tiles;
-      lanes = split ? 2 : 1;
       p0 = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
     }
-    // (a part's lanes lie next to each other, parts LANES apart)
-    const int n = parts * lanes, step = lanes == 2 ? 1 : Cfg::LANES;
-    for (int p = 0; p < n; ++p) top = fmaxf(top, a.part_ml[(p0 + p * step) * kRows + r].x);
+    constexpr int step = Cfg::LANES;
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_ml[(p0 + p * step) * kRows + r].x);
     const float ref = top == -INFINITY ? 0.f : top;
     const float w = own_lse == -INFINITY ? 0.f : exp2_of(own_m - ref);
     float sum = w;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int p = 0; p < n; ++p) {
+    for (int p = 0; p < parts; ++p) {
       const int64_t at_part = p0 + p * step;
       const float2 ml = a.part_ml[at_part * kRows + r];
-      if (ml.y == 0.f) continue;  // (a lane without a tile leaves no output)
       const float4 v = a.part_o[(at_part * COLS + col) * kRows + r];
       const float f = exp2_of(ml.x - ref);
       sum += f * ml.y;
