@@ -80,7 +80,6 @@ struct PrefixCfg {
   static constexpr int OFF_Q = SLOTS * PIECE, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 256;
   static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
   static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps;
-  static constexpr int ROW_REGS = E8 ? 192 : 208, OTHER_REGS = E8 ? 120 : 88;
   static constexpr int O_COL = 256;                // scores in columns 0 .. 2 TN - 1, outputs from 256 on
   static_assert(SLOTS >= 4 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
 };
@@ -434,8 +433,8 @@ struct PrefixRoles {
     constexpr uint32_t kPV = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kRows >> 4) << 24);
     bool lost = false;
     int it = 0;               // the segment's first piece
-    int n[2] = {0, 0};        // jobs of a buffer so far
-    int nq[2] = {0, 0};       // query tiles of a lane so far
+    uint32_t p_phase = 0;     // of the buffers' next probabilities, a bit each
+    uint32_t q_phase = 0;     // of the lanes' next query tiles
     auto wait = [&](uint32_t bar, int phase) {
       if (!lost) lost = !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns);
     };
@@ -446,8 +445,8 @@ struct PrefixRoles {
       auto second = [&](int j) {  // PV(j)
         const int t = pair ? j >> 1 : j, piece = it + 2 * t + 1, slot = piece % SLOTS, buf = j & 1, o = LANES == 2 ? buf : 0;
         if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
-        // (the buffer's job j is its n-th but one, or its last)
-        wait(p_full + buf * 8, n[buf] - 1);
+        wait(p_full + buf * 8, p_phase >> buf);
+        p_phase ^= 1u << buf;
         if (lost) return;
         tmem_after();
         const uint32_t v = sbase + slot * Cfg::PIECE, p = tmem + buf * TN, d = tmem + Cfg::O_COL + o * D;
@@ -466,7 +465,10 @@ struct PrefixRoles {
         if (j >= 2) second(j - 2);
         const int t = pair ? j >> 1 : j, piece = it + 2 * t, slot = piece % SLOTS, buf = j & 1, lane = LANES == 2 ? buf : 0;
         if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
-        if (j < LANES) wait(q_full + lane * 8, nq[lane]++);
+        if (j < LANES) {
+          wait(q_full + lane * 8, q_phase >> lane);
+          q_phase ^= 1u << lane;
+        }
         if (lost) break;
         tmem_after();
         const uint32_t k = sbase + slot * Cfg::PIECE, q = sbase + Cfg::OFF_Q + lane * Cfg::QB;
@@ -476,7 +478,6 @@ struct PrefixRoles {
                  tile_desc(k + (x >> 2) * TN * 128 + (x & 3) * 32, 16, 1024), kS, x > 0);
         if (!pair || (j & 1)) mma_commit_to(empty + slot * 8);
         mma_commit_to(s_full + buf * 8);
-        ++n[buf];
       }
       for (int j = max(J - 2, 0); j < J && !lost; ++j) second(j);
       it += 2 * (g.ke - g.kb);
@@ -572,9 +573,9 @@ struct PrefixRoles {
     const uint32_t mine = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;  // this warp's quarter of the tensor memory's lanes
     const uint32_t o_at = tmem + Cfg::O_COL + lane * D + mine;
     bool lost = false;
-    int n[2] = {0, 0};    // jobs of a buffer so far
-    int n_o[2] = {0, 0};  // segments of a lane so far
-    int n_pv = 0;
+    int n_jobs = 0;            // of this lane so far
+    int n_o = 0, n_other = 0;  // segments with jobs of this lane, and of the other one
+    uint32_t phases = 0;       // one lane's buffers of scores
     auto wait = [&](uint32_t bar, int phase) {
       if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns));
       tmem_after();
@@ -596,24 +597,31 @@ struct PrefixRoles {
         const int t = LANES == 2 && g.split ? g.kb + 2 * j + lane : g.kb + j;
         const int valid = a.tokens - t * TN;  // of the tile's columns, if fewer than TN
         const uint32_t s_at = tmem + buf * TN + mine;
-        wait(s_full + buf * 8, n[buf]++);
+        wait(s_full + buf * 8, LANES == 2 ? n_jobs : phases >> buf);
+        phases ^= 1u << buf;
         if (lost) break;
-        // all scores of the row at once
-        float x[TN / 32][32];
-#pragma unroll
-        for (int c = 0; c < TN / 32; ++c) tmem_ld32(x[c], s_at + c * 32);
-        tmem_loaded();
-        if (valid < TN)
-#pragma unroll
-          for (int c = 0; c < TN / 32; ++c) cut(x[c], c * 32, valid);
-        float top = fmaxf(x[0][0], x[0][1]), top1 = fmaxf(x[1][0], x[1][1]);
-#pragma unroll
-        for (int c = 0; c < TN / 32; c += 2)
-#pragma unroll
-          for (int i = c == 0 ? 2 : 0; i < 32; i += 2) {
-            top = max_of3(top, x[c][i], x[c][i + 1]);
-            top1 = max_of3(top1, x[c + 1][i], x[c + 1][i + 1]);
+        // The row's largest score, then its probabilities, 64 columns at a time, which are read twice (with all 128 in registers,
+        // or with half of them kept, some of those were spilled).
+        float x0[32], x1[32];
+        float top = -INFINITY, top1 = -INFINITY;
+        auto scores = [&](int c) {
+          tmem_ld32(x0, s_at + c);
+          tmem_ld32(x1, s_at + c + 32);
+          tmem_loaded();
+          if (valid < TN) {
+            cut(x0, c, valid);
+            cut(x1, c + 32, valid);
           }
+        };
+#pragma unroll 1
+        for (int c = 0; c < TN; c += 64) {
+          scores(c);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            top = max_of3(top, x0[i], x0[i + 1]);
+            top1 = max_of3(top1, x1[i], x1[i + 1]);
+          }
+        }
         top = fmaxf(top, top1) * scale;
         const float want = E8 ? top - kLiftE8 : top;
         const bool grown = want > m + (E8 ? kSlackE8 : kSlack) || m == -INFINITY;
@@ -628,23 +636,27 @@ struct PrefixRoles {
           sum0 *= f;
           sum1 *= f;
         }
-#pragma unroll
-        for (int c = 0; c < TN / 32; ++c) weigh(x[c], s_at + c * 32, scale, base, sum0, sum1);
+#pragma unroll 1
+        for (int c = 0; c < TN; c += 64) {
+          if (TN > 64) scores(c);
+          weigh(x0, s_at + c, scale, base, sum0, sum1);
+          weigh(x1, s_at + c + 32, scale, base, sum0, sum1);
+        }
         if (again) {
-          if (LANES == 1) wait(pv_done, n_pv - 1);  // (of two lanes, the one's products end before its next scores)
+          if (LANES == 1) wait(pv_done, n_jobs - 1);  // (of two lanes, the one's products end before its next scores)
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
-            tmem_ld32(x[0], o_at + c);
+            tmem_ld32(x0, o_at + c);
             tmem_loaded();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[0][i] *= f;
-            tmem_st32(o_at + c, x[0]);
+            for (int i = 0; i < 32; ++i) x0[i] *= f;
+            tmem_st32(o_at + c, x0);
           }
         }
         tmem_stored();
         tmem_before();
         mbar_arrive(p_full + buf * 8);
-        ++n_pv;
+        ++n_jobs;
       }
       // the next segment's queries, whose scores may begin beside this one's end
       if (u < end) {
@@ -655,7 +667,7 @@ struct PrefixRoles {
       const float sum = sum0 + sum1;
       if (!both) {
         const int64_t part = (static_cast<int64_t>(g.s) + blockIdx.x) * LANES + lane;
-        wait(o_full + lane * 8, n_o[lane]);
+        wait(o_full + lane * 8, n_o);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float x[32];
@@ -674,8 +686,8 @@ struct PrefixRoles {
         asm volatile("barrier.sync 1, 256;" ::: "memory");
         const float2 other = __ldcg(&a.part_ml[(part + (lane ^ 1)) * kRows + row]);
         const bool second = g.lane_jobs(1) > 0;
-        wait(o_full, n_o[0]);
-        if (second) wait(o_full + 8, n_o[1]);
+        wait(o_full, lane == 0 ? n_o : n_other);
+        if (second) wait(o_full + 8, lane == 0 ? n_other : n_o);
         const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
         const float f_mine = exp2_of(m - ref), f_other = exp2_of(other.x - ref);
         const float f0 = lane == 0 ? f_mine : f_other, f1 = lane == 0 ? f_other : f_mine;
@@ -699,9 +711,8 @@ struct PrefixRoles {
         asm volatile("barrier.sync 1, 256;" ::: "memory");  // both have read both
         if (lane == 0) a.part_ml[part * kRows + row] = make_float2(top, fmaf(sum, f_mine, other.y * f_other));
       }
-      if (LANES == 1) ++n_o[0];
-      else
-        for (int x = 0; x < 2; ++x) n_o[x] += g.lane_jobs(x) > 0;
+      n_o += jobs > 0;
+      if (LANES == 2) n_other += g.lane_jobs(lane ^ 1) > 0;
       tmem_before();
     }
   }
@@ -789,13 +800,6 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const PrefixList l = PrefixList::make<Cfg>(a, token_rows);
   PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem, starts,
                        l.begin(blockIdx.x), l.begin(blockIdx.x + 1)};
-  // Two lanes: a thread that holds a row of 128 scores takes registers of the others' (of the 384 x 168 of the launch,
-  // 256 x 208 + 128 x 88; an E4M3 cache's copying threads hold two pieces' chunks: 256 x 192 + 128 x 120).
-  if constexpr (Cfg::LANES == 2) {
-    static_assert(256 * Cfg::ROW_REGS + 128 * Cfg::OTHER_REGS <= 384 * 168, "registers of the launch");
-    if (warp < Cfg::WG / 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::ROW_REGS));
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::OTHER_REGS));
-  }
   if (warp < Cfg::WG / 32) {
     r.rows();
   } else if (warp == Cfg::WG / 32) {
