@@ -160,6 +160,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)) : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mma_commit_to(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -426,65 +431,83 @@ struct PrefixRoles {
     }
   }
 
-  // --- products, by one thread ---
+  // --- products: one warp, whose loop is uniform (the products' descriptors are made in uniform registers) and of which
+  // one thread issues them (with all of it in that thread's branch a product took 112 cycles to issue, and 64 to do) ---
   __device__ __forceinline__ void multiply() {
     constexpr uint32_t kType = E8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 sums
     constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((TN >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t kPV = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) | ((D >> 3) << 17) | ((kRows >> 4) << 24);
+    const bool leader = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = tile_desc(sbase + Cfg::OFF_Q, 16, 1024), k_desc = tile_desc(sbase, 16, 1024),
+                   v_desc = tile_desc(sbase, TN * 128, 1024);
     bool lost = false;
     int it = 0;               // the segment's first piece
     uint32_t p_phase = 0;     // of the buffers' next probabilities, a bit each
     uint32_t q_phase = 0;     // of the lanes' next query tiles
     auto wait = [&](uint32_t bar, int phase) {
-      if (!lost) lost = !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns);
+      if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns));
+    };
+    auto commit = [&](uint32_t bar) {
+      if (leader) mma_commit_to(bar);
     };
     for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       const int J = g.jobs(LANES);
       const bool pair = LANES == 2 && !g.split;
-      auto second = [&](int j) {  // PV(j)
-        const int t = pair ? j >> 1 : j, piece = it + 2 * t + 1, slot = piece % SLOTS, buf = j & 1, o = LANES == 2 ? buf : 0;
-        if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
-        wait(p_full + buf * 8, p_phase >> buf);
-        p_phase ^= 1u << buf;
-        if (lost) return;
-        tmem_after();
-        const uint32_t v = sbase + slot * Cfg::PIECE, p = tmem + buf * TN, d = tmem + Cfg::O_COL + o * D;
+      // S(j) for j < J, after PV(j - 2); then the last two
+#pragma unroll 1
+      for (int j = 0; j < J + 2 && !lost; ++j) {
+        const int buf = j & 1, o = LANES == 2 ? buf : 0;
+        {
+          const int i = j - 2;  // PV(i)
+          if (i >= 0 && i < J) {
+            const int piece = it + 2 * (pair ? i >> 1 : i) + 1, slot = piece % SLOTS;
+            if (!pair || !buf) wait(full + slot * 8, piece / SLOTS);
+            wait(p_full + buf * 8, p_phase >> buf);
+            p_phase ^= 1u << buf;
+            if (lost) break;
+            tmem_after();
+            const uint64_t v = v_desc + slot * (Cfg::PIECE >> 4);
+            const uint32_t p = tm + buf * TN, d = tm + Cfg::O_COL + o * D;
+            const bool more = i >= LANES;
+            if (leader) {
 #pragma unroll
-        for (int x = 0; x < TN / 16; ++x) {
-          const uint64_t b = tile_desc(v + x * 2048, TN * 128, 1024);
-          const uint32_t at = p + (x >> 1) * 32 + (x & 1) * 8;
-          mma_ts(d, at, b, kPV, x > 0 || j >= LANES);
-          if constexpr (!E8) mma_ts(d, at + 16, b, kPV, true);
+              for (int x = 0; x < TN / 16; ++x) {
+                mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * (2048 >> 4), kPV, x > 0 || more);
+                if constexpr (!E8) mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * (2048 >> 4), kPV, true);
+              }
+            }
+            if (!pair || buf) commit(empty + slot * 8);
+            if (LANES == 1) commit(pv_done);
+            if (i + LANES >= J) commit(o_full + o * 8);
+          }
         }
-        if (!pair || (j & 1)) mma_commit_to(empty + slot * 8);
-        if (LANES == 1) mma_commit_to(pv_done);
-        if (j + LANES >= J) mma_commit_to(o_full + o * 8);
-      };
-      for (int j = 0; j < J && !lost; ++j) {
-        if (j >= 2) second(j - 2);
-        const int t = pair ? j >> 1 : j, piece = it + 2 * t, slot = piece % SLOTS, buf = j & 1, lane = LANES == 2 ? buf : 0;
-        if (!pair || !(j & 1)) wait(full + slot * 8, piece / SLOTS);
-        if (j < LANES) {
-          wait(q_full + lane * 8, q_phase >> lane);
-          q_phase ^= 1u << lane;
-        }
-        if (lost) break;
-        tmem_after();
-        const uint32_t k = sbase + slot * Cfg::PIECE, q = sbase + Cfg::OFF_Q + lane * Cfg::QB;
+        if (j < J) {
+          const int piece = it + 2 * (pair ? j >> 1 : j), slot = piece % SLOTS;
+          if (!pair || !buf) wait(full + slot * 8, piece / SLOTS);
+          if (j < LANES) {
+            wait(q_full + o * 8, q_phase >> o);
+            q_phase ^= 1u << o;
+          }
+          if (lost) break;
+          tmem_after();
+          const uint64_t k = k_desc + slot * (Cfg::PIECE >> 4), q = q_desc + o * (Cfg::QB >> 4);
+          const uint32_t d = tm + buf * TN;
+          if (leader) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)
-          mma_ss(tmem + buf * TN, tile_desc(q + (x >> 2) * kRows * 128 + (x & 3) * 32, 16, 1024),
-                 tile_desc(k + (x >> 2) * TN * 128 + (x & 3) * 32, 16, 1024), kS, x > 0);
-        if (!pair || (j & 1)) mma_commit_to(empty + slot * 8);
-        mma_commit_to(s_full + buf * 8);
+            for (int x = 0; x < D / 16; ++x)
+              mma_ss(d, q + (((x >> 2) * kRows * 128 + (x & 3) * 32) >> 4), k + (((x >> 2) * TN * 128 + (x & 3) * 32) >> 4), kS, x > 0);
+          }
+          if (!pair || buf) commit(empty + slot * 8);
+          commit(s_full + buf * 8);
+        }
       }
-      for (int j = max(J - 2, 0); j < J && !lost; ++j) second(j);
       it += 2 * (g.ke - g.kb);
       u += g.ke - g.kb;
     }
     // all products are done before the tensor memory is given back
-    mma_commit_to(fin);
+    commit(fin);
     mbar_wait(fin, 0, kStatusTimeoutDrain, a.wait_ns);
   }
 
@@ -655,7 +678,8 @@ struct PrefixRoles {
         }
         tmem_stored();
         tmem_before();
-        mbar_arrive(p_full + buf * 8);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + buf * 8);
         ++n_jobs;
       }
       // the next segment's queries, whose scores may begin beside this one's end
@@ -738,7 +762,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i * 8, 1);
-      mbar_init(p_full + i * 8, 128);
+      mbar_init(p_full + i * 8, 4);
       mbar_init(q_full + i * 8, 128);
       mbar_init(o_full + i * 8, 1);
     }
@@ -803,7 +827,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   if (warp < Cfg::WG / 32) {
     r.rows();
   } else if (warp == Cfg::WG / 32) {
-    if (lane == 0) r.multiply();
+    r.multiply();
   } else if (E8) {
     r.load_e4m3();
   } else if (a.box == 0) {
