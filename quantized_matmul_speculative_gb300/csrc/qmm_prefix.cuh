@@ -260,6 +260,7 @@ template <int D, bool E8>
 struct PrefixRoles {
   using Cfg = PrefixCfg<D, E8>;
   static constexpr int TN = Cfg::TN, LANES = Cfg::LANES, SLOTS = Cfg::SLOTS;
+  static constexpr int HALVES = TN / 64;  // of a tile's probabilities, handed over one after the other
   const PrefixArgs& a;
   const PrefixList l;
   unsigned char* smem;
@@ -279,21 +280,31 @@ struct PrefixRoles {
     return p;
   }
 
+  // A tile's boxes: the page of each (what lies outside the prefix and the cache reads as zeros) and its place there, in the
+  // first lanes.  A tile has at most 16 along its tokens.
+  __device__ __forceinline__ void find_boxes(int t, int& page, int& place) const {
+    const int lane = threadIdx.x & 31, j = t * TN + lane * a.box;
+    page = a.c.num_pages;
+    place = 0;
+    if (lane * a.box < TN && j < a.tokens) {
+      const int p = page_of(j, place);
+      if (p >= 0) page = p;
+    }
+  }
   __device__ __forceinline__ void load_tma(const CUtensorMap* kmap, const CUtensorMap* vmap) {
     const int lane = threadIdx.x & 31;
     bool lost = false;
     int it = 0;
     const int groups = TN / a.box, boxes = groups * Cfg::SLICES;
+    int page = 0, place = 0;
+    if (begin < end) find_boxes(PrefixSegment(l, begin, end, LANES).kb, page, place);
     for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
+      u += g.ke - g.kb;
       for (int t = g.kb; t < g.ke && !lost; ++t) {
-        // the pages of the tile's boxes, a lane each (16 at most); outside the prefix and the cache: zeros
-        int page = a.c.num_pages, place = 0;
-        const int j = t * TN + lane * a.box;
-        if (lane < groups && j < a.tokens) {
-          const int p = page_of(j, place);
-          if (p >= 0) page = p;
-        }
+        // the next tile's page numbers are on their way while this one's copies are issued
+        int page2 = 0, place2 = 0;
+        if (t + 1 < g.ke || u < end) find_boxes(t + 1 < g.ke ? t + 1 : 0, page2, place2);
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int slot = it % SLOTS;
           if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
@@ -309,8 +320,9 @@ struct PrefixRoles {
                       full + slot * 8);
           }
         }
+        page = page2;
+        place = place2;
       }
-      u += g.ke - g.kb;
     }
     // (the products wait for the same; where one is given up, the limit was time enough for the others)
     for (int i = max(it - SLOTS, 0); i < it; ++i)
@@ -464,20 +476,23 @@ struct PrefixRoles {
           if (i >= 0 && i < J) {
             const int piece = it + 2 * (pair ? i >> 1 : i) + 1, slot = piece % SLOTS;
             if (!pair || !buf) wait(full + slot * 8, piece / SLOTS);
-            wait(p_full + buf * 8, p_phase >> buf);
-            p_phase ^= 1u << buf;
-            if (lost) break;
-            tmem_after();
             const uint64_t v = v_desc + slot * (Cfg::PIECE >> 4);
             const uint32_t p = tm + buf * TN, d = tm + Cfg::O_COL + o * D;
             const bool more = i >= LANES;
-            if (leader) {
 #pragma unroll
-              for (int x = 0; x < TN / 16; ++x) {
-                mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * (2048 >> 4), kPV, x > 0 || more);
-                if constexpr (!E8) mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * (2048 >> 4), kPV, true);
+            for (int half = 0; half < HALVES; ++half) {
+              wait(p_full + (buf * 2 + half) * 8, p_phase >> buf);
+              tmem_after();
+              if (leader && !lost) {
+#pragma unroll
+                for (int x = half * 4; x < half * 4 + 4; ++x) {
+                  mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * (2048 >> 4), kPV, x > 0 || more);
+                  if constexpr (!E8) mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * (2048 >> 4), kPV, true);
+                }
               }
             }
+            p_phase ^= 1u << buf;
+            if (lost) break;
             if (!pair || buf) commit(empty + slot * 8);
             if (LANES == 1) commit(pv_done);
             if (i + LANES >= J) commit(o_full + o * 8);
@@ -658,28 +673,29 @@ struct PrefixRoles {
         if (again) {
           sum0 *= f;
           sum1 *= f;
-        }
-#pragma unroll 1
-        for (int c = 0; c < TN; c += 64) {
-          if (TN > 64) scores(c);
-          weigh(x0, s_at + c, scale, base, sum0, sum1);
-          weigh(x1, s_at + c + 32, scale, base, sum0, sum1);
-        }
-        if (again) {
           if (LANES == 1) wait(pv_done, n_jobs - 1);  // (of two lanes, the one's products end before its next scores)
+          float y[32];
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
-            tmem_ld32(x0, o_at + c);
+            tmem_ld32(y, o_at + c);
             tmem_loaded();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x0[i] *= f;
-            tmem_st32(o_at + c, x0);
+            for (int i = 0; i < 32; ++i) y[i] *= f;
+            tmem_st32(o_at + c, y);
           }
         }
-        tmem_stored();
-        tmem_before();
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + buf * 8);
+        // 64 columns' probabilities at a time, so that the products with the first begin beside the second
+#pragma unroll 1
+        for (int half = 0; half < HALVES; ++half) {
+          const int c = half * 64;
+          scores(c);
+          weigh(x0, s_at + c, scale, base, sum0, sum1);
+          weigh(x1, s_at + c + 32, scale, base, sum0, sum1);
+          tmem_stored();
+          tmem_before();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) mbar_arrive(p_full + (buf * 2 + half) * 8);
+        }
         ++n_jobs;
       }
       // the next segment's queries, whose scores may begin beside this one's end
@@ -750,8 +766,8 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   unsigned char* const smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
   const uint32_t full = sbase + Cfg::OFF_BAR, empty = full + Cfg::SLOTS * 8, s_full = empty + Cfg::SLOTS * 8, p_full = s_full + 16,
-                 q_full = p_full + 16, o_full = q_full + 16, pv_done = o_full + 16, fin = pv_done + 8;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + Cfg::SLOTS * 16 + 80);
+                 q_full = p_full + 32, o_full = q_full + 16, pv_done = o_full + 16, fin = pv_done + 8;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + Cfg::SLOTS * 16 + 96);
   int* const starts = reinterpret_cast<int*>(smem + Cfg::OFF_STARTS);
   int* const s_sum = reinterpret_cast<int*>(smem + Cfg::OFF_Q);  // (before the queries)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -762,7 +778,8 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i * 8, 1);
-      mbar_init(p_full + i * 8, 4);
+      mbar_init(p_full + i * 16, 4);
+      mbar_init(p_full + i * 16 + 8, 4);
       mbar_init(q_full + i * 8, 128);
       mbar_init(o_full + i * 8, 1);
     }
