@@ -265,13 +265,14 @@ qmm_status qmm_route_experts(const void* logits, int logits_dtype, int64_t ld, c
  * number has no adapter: Y[t] = base[t], and X[t] is not read.  A number >= L sets bit 3
  * of qmm_device_status() and counts as none.  R is a multiple of 8 up to 128 (an adapter
  * of a smaller rank is padded with zeros), K a multiple of 8, N any; X, A, Bm 16-byte
- * aligned, x_ld a multiple of 8.  workspace: qmm_lora_workspace(T, L) bytes (it may be
- * 0, then null will do), 16-byte aligned, not shared by calls that may run at the same
- * time.  T == 0 or N == 0 launches nothing.                                          */
+ * aligned, x_ld a multiple of 8.  At most some 65000 tiles of rows: T / 16 plus the
+ * smaller of T and L + 1, or T / 64 where that is 32 rows an adapter (QMM_ERR_SHAPE).
+ * workspace: qmm_lora_workspace(T, L, R) bytes, 16-byte aligned, not shared by calls that
+ * may run at the same time.  T == 0 or N == 0 launches nothing.                      */
 qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_t x_ld, const void* A, const void* Bm,
                         const int32_t* adapters, const float* scales, int T, int N, int K, int R, int L, void* Y,
                         int64_t y_ld, int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
-size_t qmm_lora_workspace(int T, int L);
+size_t qmm_lora_workspace(int T, int L, int R);
 
 /* A paged key-value cache.  Token j of sequence b lives in page
  * block_table[b][j / page_size] at slot j mod page_size; its key for head h

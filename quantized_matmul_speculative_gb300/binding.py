@@ -52,7 +52,7 @@ SIGNATURES = {
     "qmm_route_experts": (_i32, [_vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp]),
     "qmm_lora_add": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i32, _vp,
                             ctypes.c_size_t, _vp]),
-    "qmm_lora_workspace": (ctypes.c_size_t, [_i32, _i32]),
+    "qmm_lora_workspace": (ctypes.c_size_t, [_i32, _i32, _i32]),
     "qmm_verify_draft": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "qmm_packed_words": (ctypes.c_size_t, [_i64, _i64, _i32]),
     "qmm_pack": (_i32, [_vp, _i64, _i64, _i32, _vp]),
@@ -493,9 +493,9 @@ def route_experts(logits, k: int, scoring: str = "softmax", bias=None, groups: i
                                            group_best, renormalize, scale, _handle(stream)), "qmm_route_experts")
 
 
-def lora_workspace(T: int, L: int) -> int:
-    """Bytes of workspace that :func:`lora_add` needs for T rows and L adapters."""
-    return int(lib().qmm_lora_workspace(T, L))
+def lora_workspace(T: int, L: int, R: int) -> int:
+    """Bytes of workspace that :func:`lora_add` needs for T rows and L adapters of rank R."""
+    return int(lib().qmm_lora_workspace(T, L, R))
 
 
 def lora_add(base, x, a, b, adapters, scales=None, out=None, workspace=None, stream=None):

@@ -397,7 +397,7 @@ PyObject* lora_add(PyObject* const* a) {
   Call call(base, a[8]);
   for (const at::Tensor* t : {&x, &A, &Bm, &ids, scales, given, space}) call.here(t);
   const at::Tensor out = given != nullptr ? *given : call.empty(base.sizes(), base.scalar_type());
-  const int64_t need = static_cast<int64_t>(qmm_lora_workspace(narrow(T), narrow(L)));
+  const int64_t need = static_cast<int64_t>(qmm_lora_workspace(narrow(T), narrow(L), narrow(R)));
   at::Tensor ws;
   if (space != nullptr) ws = *space;
   else if (need > 0) ws = call.empty({need}, at::kByte);

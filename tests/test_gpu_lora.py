@@ -65,7 +65,14 @@ def test_requests(rows, dtype):
     check(problem(ids, 7, 16, 320, 272, dtype, seed=len(ids)))
 
 
-@pytest.mark.parametrize("T,L", [(50, 64), (333, 5), (1500, 100), (5000, 40), (700, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [16, 24, 32, 64, 96, 128])
+def test_many_rows_an_adapter(R, dtype):
+    """Tiles of 16, 32 or 64 rows, full and not."""
+    check(problem([0] * 130 + [-1] * 40 + [1] * 65 + [2] * 3 + [0] * 31, 3, R, 448, 600, dtype, seed=R))
+
+
+@pytest.mark.parametrize("T,L", [(50, 64), (333, 5), (1500, 100), (5000, 40), (700, 1), (600, 5000)])
 def test_rows_in_any_order(T, L):
     g = torch.Generator().manual_seed(T)
     ids = torch.randint(-1, L, (T,), generator=g).tolist()
@@ -147,12 +154,25 @@ def test_what_is_not_finite_stays_in_its_row():
     assert torch.equal(got[[1, 3]], want[[1, 3]])
 
 
-def test_results_do_not_depend_on_the_other_rows():
+def test_some_of_the_rows():
+    """The same rows with more or fewer others, which changes how they are tiled, and repeated exactly."""
     p = problem([0, 1, 2, 0, 1, 1] * 60, 3, 32, 512, 300, seed=3)
     want = check(p)
+    assert torch.equal(binding.lora_add(**p), want)
     for rows in ([0], [5], list(range(3)), list(range(100, 290))):
-        q = {**p, "base": p["base"][rows], "x": p["x"][rows], "adapters": p["adapters"][rows]}
-        assert torch.equal(binding.lora_add(**q), want[rows])
+        check({**p, "base": p["base"][rows], "x": p["x"][rows], "adapters": p["adapters"][rows]})
+
+
+def test_workspace():
+    """One that is reused, holding NaN."""
+    for T in (7, 300):
+        p = problem([0, 1, -1, 1, 0, 2, 1] * (T // 7), 3, 16, 512, 300, torch.float32, seed=4)
+        want = check(p)
+        ws = torch.full((binding.lora_workspace(len(p["x"]), 3, 16),), 255, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            assert torch.equal(binding.lora_add(**p, workspace=ws), want)
+        with pytest.raises(binding.QmmError):
+            binding.lora_add(**p, workspace=ws[:-256])
 
 
 def test_refusals():

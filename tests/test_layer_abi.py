@@ -85,8 +85,10 @@ def test_lora(lib):  # noqa: F811
                         ({"X": P + 8}, ALIGN), ({"A": P + 8}, ALIGN), ({"Bm": P + 8}, ALIGN), ({"x_ld": 68}, ALIGN),
                         ({"adapters": P + 2}, ALIGN), ({"scales": P + 2}, ALIGN), ({"T": 0}, OK), ({"N": 0}, OK)):
         assert call(lib.qmm_lora_add, good, changes) == rc, changes
-    many = dict(good, T=100000)
-    need = lib.qmm_lora_workspace(100000, 3)
-    if need > 0:
-        for changes, rc in (({"ws": None}, NULL), ({"ws": P + 8}, ALIGN), ({"ws_bytes": need - 1}, SHAPE)):
-            assert call(lib.qmm_lora_add, many, changes) == rc, changes
+    need = lib.qmm_lora_workspace(5, 3, 16)
+    assert need > 0 and lib.qmm_lora_workspace(100000, 3, 16) > need
+    for changes, rc in (({"ws": None}, NULL), ({"ws": P + 8}, ALIGN), ({"ws_bytes": need - 1}, SHAPE),
+                        ({"T": 2**23, "L": 1, "ws_bytes": 2**50}, SHAPE)):
+        assert call(lib.qmm_lora_add, good, changes) == rc, changes
+    for sizes in ((0, 3, 16), (5, -1, 16), (5, 3, 0), (5, 3, 136)):
+        assert lib.qmm_lora_workspace(*sizes) == 0
