@@ -2,20 +2,21 @@
 //
 // A warp takes a token; its lanes hold the row, LPG neighbouring lanes a group (the
 // largest power of two of which all groups fit into the warp), each up to PER
-// neighbouring experts of it, so that lower lanes and places are lower experts.  The k
-// best are taken one after another: a maximum of ordered keys over the warp, the first
-// lane that holds it, the first of its places.
+// neighbouring experts of it, so that lower lanes and places are lower experts.
 //
-// The mathematics.  Keys of score + bias are compared in 64 bits, where two that lie
-// close together decide whole numbers.  They are computed in 32 bits first: a score is
-// then off by at most a few 2^-24 (expf, a sum and a division), a key by another
-// rounding of itself, so that a gap of kGap (1 + |key|) = 2^-19 (1 + |key|) between all
-// neighbours down to the first expert that is left out, and between the last group taken
-// and the first left, shows that 64 bits would choose the same.  Else (about one token
-// in a thousand) the warp does the token again in 64 bits.  Without a bias the logits
-// are the keys, exactly.
+// The mathematics.  What orders the experts (logits, or scores with the bias) is put on a
+// scale of 2^23 steps between the row's least and greatest, with the expert's number, the
+// lowest first, in the 9 bits below: one unsigned key each, no two alike.  Every lane sorts
+// its own keys once; then k + 1 rounds take the largest of the lanes' first ones.  Neighbours
+// of that order that are nearer than the steps' and the scores' own errors (or than one
+// step, where logits are compared) may be in the wrong order, unless they are the same
+// logit with the same bias: then, in some tokens of a thousand, the warp does the token again
+// in 64 bits, one maximum after another.  The errors: a sigmoid from the approximate
+// exponential and reciprocal is off by 4 2^-24, a softmax by 24 2^-24 (exponentials 2 units in
+// the last place each, a sum of 512 in 31 + 5 steps), a key's own rounding is |key| 2^-24; so
+// two keys more than kGap (1 + |key|) apart are in their order, with kGap 2^-20 and 2^-18.
 //
-// What bounds it: instructions of the k rounds, and one launch for few tokens.
+// What bounds it: instructions, some 400 a token of 256 experts; one launch for few tokens.
 #include <cfloat>
 #include <climits>
 
@@ -27,7 +28,7 @@ namespace qmm {
 namespace {
 
 constexpr int kRouteWarps = 8;
-constexpr float kGap = 1.f / (1 << 18);
+constexpr float kGapSigmoid = 1.f / (1 << 20), kGapSoftmax = 1.f / (1 << 18);
 
 struct RouteArgs {
   const void* x;
@@ -54,137 +55,69 @@ __device__ __forceinline__ unsigned long long ordered(double v) {
 __device__ __forceinline__ float value_of(uint32_t u) {
   return u == 0 ? -INFINITY : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
-__device__ __forceinline__ double value_of(unsigned long long u) {
-  return u == 0 ? -static_cast<double>(INFINITY) : __longlong_as_double(u >> 63 ? u & ~(1ull << 63) : ~u);
-}
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<unsigned long long>(hi) << 32 | lo;
 }
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
-template <class F>
-__device__ __forceinline__ F sigmoid(F x) {
-  const F e = exp_of(x < F(0) ? x : -x);
-  return (x < F(0) ? e : F(1)) / (F(1) + e);
-}
+__device__ __forceinline__ float warp_max(float v) { return value_of(warp_max(ordered(v))); }
 template <class F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
   for (int s = 16; s > 0; s /= 2) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
-template <class F>
-struct KeyOf { using type = uint32_t; };
-template <>
-struct KeyOf<double> { using type = unsigned long long; };
+__device__ __forceinline__ float sigmoid_of(float x) {
+  const float e = expf(x < 0.f ? x : -x);
+  return (x < 0.f ? e : 1.f) / (1.f + e);
+}
+// The same within 4 2^-24, absolutely.
+__device__ __forceinline__ float sigmoid_near(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+// NaN logits count as -inf, +inf as the largest number.
+__device__ __forceinline__ float clean(float x) { return x == x ? fminf(x, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float logit_of(const RouteArgs& a, int64_t t, int e) {
+  return clean(a.f32 ? static_cast<const float*>(a.x)[t * a.ld + e]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[t * a.ld + e]));
+}
 
-// A token's choice, with keys in F: lane j < k gets the j-th expert and its logit.
-// False: F does not tell two neighbours apart.  x: the lane's logits, in F's range
-// (-inf for an expert that is out); `top` the row's largest, or 0 if that is -inf.
+// The best one or two of v[0 .. PER - 1] and of the neighbouring lanes of a group.
 template <class F, int PER>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[PER], float top, const float (&bias)[PER], int first,
-                                       int mine, int& expert, float& logit, F& total) {
-  using Key = typename KeyOf<F>::type;
-  const int lane = threadIdx.x & 31;
-  const bool biased = a.bias != nullptr, grouped = a.top_groups < a.groups;
-  const bool by_sum = grouped && a.group_best == 2;
-  const bool scores = biased || by_sum || (!a.sigmoid && !a.renormalize);
-  Key key[PER];   // order of the experts
-  F worth[PER];   // of an expert in its group
-  total = F(1);
-  if (!a.sigmoid && scores) {
-    F s = F(0);
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i < mine) s += exp_of(F(x[i]) - F(top));
-    total = warp_sum(s);
-  }
+__device__ __forceinline__ F group_worth(const RouteArgs& a, const F (&v)[PER]) {
+  F best = -F(INFINITY), second = -F(INFINITY);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    F v = F(x[i]);
-    worth[i] = v;
-    if ((biased || by_sum) && x[i] != -INFINITY) {
-      worth[i] = (a.sigmoid ? sigmoid(v) : exp_of(v - F(top)) / total) + (biased ? F(bias[i]) : F(0));
-      if (biased) v = worth[i];
-    }
-    key[i] = i < mine ? ordered(v) : Key(0);
+    second = v[i] > best ? best : v[i] > second ? v[i] : second;
+    best = v[i] > best ? v[i] : best;
   }
-  bool apart = true;
-  // whether lo is below hi in any precision (or both are -inf)
-  auto told = [&](F hi, F lo) {
-    return sizeof(F) == 8 || hi - lo > F(kGap) * (F(1) + fabs(hi)) || (hi == lo && hi == -F(INFINITY));
-  };
-  if (grouped) {
-    // the group's best one or two keys, over its lanes
-    F best = -F(INFINITY), second = -F(INFINITY);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const F v = i < mine && worth[i] == worth[i] ? worth[i] : -F(INFINITY);
-      second = v > best ? best : v > second ? v : second;
-      best = v > best ? v : best;
-    }
-    for (int s = 1; s < (1 << a.lpg_log2); s *= 2) {
-      const F b = __shfl_xor_sync(0xffffffffu, best, s), c = __shfl_xor_sync(0xffffffffu, second, s);
-      second = b > best ? (best > c ? best : c) : (b > second ? b : second);
-      best = b > best ? b : best;
-    }
-    const F sum = a.group_best == 2 && second > -F(INFINITY) ? best + second : best;
-    Key g = lane < a.groups << a.lpg_log2 ? ordered(sum) : Key(0);
-    bool in = false;
-    F last = F(0);
-    for (int j = 0; j < a.top_groups; ++j) {
-      const Key m = warp_max(g);
-      const int at = __ffs(__ballot_sync(0xffffffffu, g == m)) - 1;
-      if (lane >> a.lpg_log2 == at >> a.lpg_log2) {
-        in = true;
-        g = Key(0);
-      }
-      last = value_of(m);
-    }
-    if ((biased || by_sum) && !told(last, value_of(warp_max(g)))) apart = false;
-    if (!in)
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = Key(0);
+  for (int s = 1; s < (1 << a.lpg_log2); s *= 2) {
+    const F b = __shfl_xor_sync(0xffffffffu, best, s), c = __shfl_xor_sync(0xffffffffu, second, s);
+    second = b > best ? (best > c ? best : c) : (b > second ? b : second);
+    best = b > best ? b : best;
   }
-  F before = F(0);
-  int e_before = 0;
-  float v_before = 0.f;
-  const int rounds = sizeof(F) == 4 && biased ? a.k + 1 : a.k;  // with the first one that is left out
-  for (int j = 0; j < rounds; ++j) {
-    Key m = key[0];
-    int at = 0;
-    float xv = x[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i)
-      if (key[i] > m) {
-        m = key[i];
-        at = i;
-        xv = x[i];
-      }
-    const Key top_key = warp_max(m);
-    const int src = __ffs(__ballot_sync(0xffffffffu, m == top_key)) - 1;
-    const int e = __shfl_sync(0xffffffffu, first + at, src);
-    const float v = __shfl_sync(0xffffffffu, xv, src);
-    if (biased && sizeof(F) == 4) {
-      if (j > 0 && top_key != 0 && !told(before, value_of(top_key)) && !(v == v_before && a.bias[e] == a.bias[e_before]))
-        apart = false;
-      before = value_of(top_key);
-      e_before = e;
-      v_before = v;
+  return a.group_best == 2 && second > -F(INFINITY) ? best + second : best;
+}
+
+// Whether this lane's group is open, from its groups' worths; `last` the least that is, `left` the best that is not.
+template <class Key>
+__device__ __forceinline__ bool open_groups(const RouteArgs& a, Key worth, Key& last, Key& left) {
+  const int lane = threadIdx.x & 31;
+  bool in = false;
+  for (int j = 0; j < a.top_groups; ++j) {
+    last = warp_max(worth);
+    const int at = __ffs(__ballot_sync(0xffffffffu, worth == last)) - 1;
+    if (lane >> a.lpg_log2 == at >> a.lpg_log2) {
+      in = true;
+      worth = Key(0);
     }
-    if (lane == j && j < a.k) {
-      expert = e;
-      logit = v;
-    }
-    if (lane == src)
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == at) key[i] = Key(0);
   }
-  return apart;
+  left = warp_max(worth);
+  return in;
 }
 
 // A lane's `mine` logits from `first` on; those of a group's neighbouring lanes lie
@@ -223,7 +156,99 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int firs
     }
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) x[i] = x[i] == x[i] ? fminf(x[i], FLT_MAX) : -INFINITY;
+  for (int i = 0; i < PER; ++i) x[i] = clean(x[i]);
+}
+
+struct Lanes {  // this lane's experts: `mine` from `first` on
+  int first, mine;
+  bool real;  // of a group
+  __device__ __forceinline__ explicit Lanes(const RouteArgs& a) {
+    const int lane = threadIdx.x & 31, group = lane >> a.lpg_log2, inside = (lane & ((1 << a.lpg_log2) - 1)) * a.per;
+    real = group < a.groups;
+    first = group * a.size + inside;
+    mine = real ? min(a.per, a.size - inside) : 0;
+  }
+};
+
+// A token's choice in 64 bits: lane j < k gets the j-th expert.
+template <int PER>
+__device__ __noinline__ int choose_exactly(const RouteArgs& a, int64_t t) {
+  using Key = unsigned long long;
+  const int lane = threadIdx.x & 31;
+  const Lanes l(a);
+  const bool biased = a.bias != nullptr, grouped = a.top_groups < a.groups, by_sum = grouped && a.group_best == 2;
+  float x[PER];
+  load_row(a, t, l.first, l.mine, x);
+  Key key[PER];
+  double worth[PER];
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
+  top = warp_max(top);
+  double total = 1.0;
+  if (!a.sigmoid && (biased || by_sum)) {
+    double s = 0.0;
+    for (int i = 0; i < PER; ++i)
+      if (i < l.mine && x[i] != -INFINITY) s += exp(static_cast<double>(x[i]) - top);
+    total = warp_sum(s);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    double v = x[i];
+    worth[i] = v;
+    if ((biased || by_sum) && x[i] != -INFINITY) {
+      const double e = exp(a.sigmoid ? (v < 0.0 ? v : -v) : v - top);
+      worth[i] = a.sigmoid ? (v < 0.0 ? e : 1.0) / (1.0 + e) : e / total;
+      if (biased) worth[i] += a.bias[l.first + i];
+      worth[i] = worth[i] == worth[i] ? worth[i] : -static_cast<double>(INFINITY);
+      if (biased) v = worth[i];
+    }
+    key[i] = i < l.mine ? ordered(v) : Key(0);
+  }
+  if (grouped) {
+    const Key of_group = ordered(group_worth(a, worth));  // (every lane takes part in it)
+    Key last, left;
+    if (!open_groups(a, l.real ? of_group : Key(0), last, left))
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = Key(0);
+  }
+  int expert = 0;
+  for (int j = 0; j < a.k; ++j) {
+    Key m = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+      if (key[i] > m) {
+        m = key[i];
+        at = i;
+      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, m == warp_max(m))) - 1;
+    const int e = __shfl_sync(0xffffffffu, l.first + at, src);
+    if (lane == j) expert = e;
+    if (lane == src)
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == at) key[i] = Key(0);
+  }
+  return expert;
+}
+
+// Descending, by merging odd and even places.
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+            v[i + j] = hi;
+            v[i + j + k] = lo;
+          }
 }
 
 template <int PER>
@@ -233,32 +258,99 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  const int group = lane >> a.lpg_log2, sub = lane & ((1 << a.lpg_log2) - 1);
-  const int inside = sub * a.per, first = group * a.size + inside;
-  const int mine = group < a.groups ? min(a.per, a.size - inside) : 0;
-  float x[PER], bias[PER];
-  load_row(a, t, first, mine, x);
+  const Lanes l(a);
+  const bool biased = a.bias != nullptr, grouped = a.top_groups < a.groups, by_sum = grouped && a.group_best == 2;
+  const float gap = a.sigmoid ? kGapSigmoid : kGapSoftmax;
+  float x[PER];
+  load_row(a, t, l.first, l.mine, x);
+  float top = x[0];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) bias[i] = a.bias != nullptr && i < mine ? a.bias[first + i] : 0.f;
-  float top = -INFINITY;
+  for (int i = 1; i < PER; ++i) top = fmaxf(top, x[i]);
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float total = 1.f;
+  if (!a.sigmoid && (biased || by_sum || !a.renormalize)) {
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
-  top = value_of(warp_max(ordered(top)));
-  if (top == -INFINITY) top = 0.f;
-
-  int expert = 0;
-  float logit = -INFINITY, total;
-  if (!choose<float>(a, x, top, bias, first, mine, expert, logit, total)) {
-    double exact_total;
-    choose<double>(a, x, top, bias, first, mine, expert, logit, exact_total);
+    for (int i = 0; i < PER; ++i) s += expf(x[i] - ref);  // (0 for experts that do not exist)
+    total = warp_sum(s);
+  }
+  // what orders the experts, and what they are worth in their groups (x stays, where it is neither, only -inf or not)
+  float worth[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    worth[i] = x[i];
+    if ((biased || by_sum) && x[i] != -INFINITY) {
+      float v = a.sigmoid ? sigmoid_near(x[i]) : expf(x[i] - ref) / total;
+      if (biased) {
+        v += a.bias[l.first + i];
+        v = v == v ? v : -INFINITY;
+        x[i] = v;
+      }
+      worth[i] = v;
+    }
+  }
+  bool apart = true, open = l.real;
+  if (grouped) {
+    const uint32_t of_group = ordered(group_worth(a, worth));  // (every lane takes part in it)
+    uint32_t last, left;
+    open = open_groups(a, l.real ? of_group : 0u, last, left);
+    const float hi = value_of(last), lo = value_of(left);
+    if (biased || by_sum) apart = hi - lo > 2.f * gap * (1.f + fabsf(hi)) || (hi == lo && hi == -INFINITY);
+  }
+  // the scale: 2 .. 2^23 - 2; 1 for -inf
+  float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    hi = fmaxf(hi, x[i]);
+    if (x[i] != -INFINITY) lo = fminf(lo, x[i]);
+  }
+  hi = warp_max(hi);
+  lo = -warp_max(-lo);
+  const float range = hi - lo;
+  apart = apart && range < FLT_MAX / 2;  // (also where all are -inf)
+  const float unit = range > 0.f ? 8388600.f / range : 0.f;
+  apart = apart && unit < FLT_MAX;
+  const uint32_t margin = biased ? static_cast<uint32_t>(fminf(gap * (1.f + fmaxf(fabsf(hi), fabsf(lo))) * unit, 8388608.f)) + 4u : 1u;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t step = x[i] == -INFINITY ? 1u : 2u + static_cast<uint32_t>((x[i] - lo) * unit);
+    key[i] = open && i < l.mine ? step << 9 | (511u - (l.first + i)) : 0u;
+  }
+  sort_down(key);
+  uint32_t mine = 0, next = 0;
+  for (int j = 0; j <= a.k; ++j) {
+    next = warp_max(key[0]);
+    if (lane == j) mine = next;
+    const bool taken = key[0] == next;
+#pragma unroll
+    for (int i = 0; i + 1 < PER; ++i) key[i] = taken ? key[i + 1] : key[i];
+    if (taken) key[PER - 1] = 0u;
+  }
+  int expert = 511 - static_cast<int>(mine & 511u);
+  float logit = lane < a.k ? logit_of(a, t, expert) : 0.f;
+  {
+    // neighbours of the order, down to the first that is left out
+    const uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1), below = lane == a.k - 1 ? next : after;
+    bool told = true;
+    if (lane < a.k && below != 0 && (mine >> 9) - (below >> 9) < margin) {
+      const int e = 511 - static_cast<int>(below & 511u);
+      told = logit_of(a, t, e) == logit && (!biased || a.bias[e] == a.bias[expert] || logit == -INFINITY);
+    }
+    apart = __all_sync(0xffffffffu, told) && apart;
+  }
+  if (!apart) {
+    expert = choose_exactly<PER>(a, t);
+    if (lane < a.k) logit = logit_of(a, t, expert);
   }
   // the weights, from the k logits
-  const float best = value_of(warp_max(ordered(lane < a.k ? logit : -INFINITY)));
+  const float best = warp_max(lane < a.k ? logit : -INFINITY);
   float w = 0.f;
   if (lane < a.k && logit != -INFINITY) {
     // (sigmoids below 2^-43 are exponentials, whose ratios do not depend on the largest)
     if (a.renormalize && (!a.sigmoid || best < -30.f)) w = expf(logit - best);
-    else w = a.sigmoid ? sigmoid(logit) : expf(logit - top) / total;
+    else w = a.sigmoid ? sigmoid_of(logit) : expf(logit - ref) / total;
   }
   if (a.renormalize) {
     const float sum = warp_sum(w);
