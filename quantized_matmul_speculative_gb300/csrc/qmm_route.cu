@@ -27,7 +27,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kRouteWarps = 8;
+constexpr int kRouteWarps = 4;
 constexpr float kGapSigmoid = 1.f / (1 << 20), kGapSoftmax = 1.f / (1 << 18);
 
 struct RouteArgs {
@@ -120,43 +120,45 @@ __device__ __forceinline__ bool open_groups(const RouteArgs& a, Key worth, Key& 
   return in;
 }
 
-// A lane's `mine` logits from `first` on; those of a group's neighbouring lanes lie
-// behind them, so that whole 16-byte chunks serve the usual sizes.
+// `mine` of a row's values from `first` on, others -inf.  Those of a group's neighbouring
+// lanes lie behind them, so that whole 16-byte chunks serve the usual sizes.
 template <int PER>
-__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int first, int mine, float (&x)[PER]) {
+__device__ __forceinline__ void load_floats(const float* row, int mine, float (&x)[PER]) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) x[i] = -INFINITY;
-  if (mine <= 0) return;
-  if (a.f32) {
-    const float* const row = static_cast<const float*>(a.x) + t * a.ld + first;
-    if (PER % 4 == 0 && mine == PER && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+  if (PER % 4 == 0 && mine == PER && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
 #pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        const uint4 u = ld_after_wait_v4(row + 4 * i);
-        x[4 * i] = __uint_as_float(u.x), x[4 * i + 1] = __uint_as_float(u.y);
-        x[4 * i + 2] = __uint_as_float(u.z), x[4 * i + 3] = __uint_as_float(u.w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i < mine) x[i] = row[i];
+    for (int i = 0; i < PER / 4; ++i) {
+      const uint4 u = ld_after_wait_v4(row + 4 * i);
+      x[4 * i] = __uint_as_float(u.x), x[4 * i + 1] = __uint_as_float(u.y);
+      x[4 * i + 2] = __uint_as_float(u.z), x[4 * i + 3] = __uint_as_float(u.w);
     }
   } else {
-    const __nv_bfloat16* const row = static_cast<const __nv_bfloat16*>(a.x) + t * a.ld + first;
-    if (PER % 4 == 0 && mine == PER && (reinterpret_cast<uintptr_t>(row) & 7) == 0) {
 #pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        const uint2 u = ld_after_wait_v2(row + 4 * i);
-        x[4 * i] = bf16_lo(u.x), x[4 * i + 1] = bf16_hi(u.x), x[4 * i + 2] = bf16_lo(u.y), x[4 * i + 3] = bf16_hi(u.y);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i < mine) x[i] = __bfloat162float(row[i]);
-    }
+    for (int i = 0; i < PER; ++i)
+      if (i < mine) x[i] = row[i];
+  }
+}
+template <int PER>
+__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int first, int mine, float (&x)[PER]) {
+  if (a.f32) {
+    load_floats(static_cast<const float*>(a.x) + t * a.ld + first, mine, x);
+    return;
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) x[i] = clean(x[i]);
+  for (int i = 0; i < PER; ++i) x[i] = -INFINITY;
+  const __nv_bfloat16* const row = static_cast<const __nv_bfloat16*>(a.x) + t * a.ld + first;
+  if (PER % 4 == 0 && mine == PER && (reinterpret_cast<uintptr_t>(row) & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < PER / 4; ++i) {
+      const uint2 u = ld_after_wait_v2(row + 4 * i);
+      x[4 * i] = bf16_lo(u.x), x[4 * i + 1] = bf16_hi(u.x), x[4 * i + 2] = bf16_lo(u.y), x[4 * i + 3] = bf16_hi(u.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i < mine) x[i] = __bfloat162float(row[i]);
+  }
 }
 
 struct Lanes {  // this lane's experts: `mine` from `first` on
@@ -179,6 +181,8 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, int64_t t) {
   const bool biased = a.bias != nullptr, grouped = a.top_groups < a.groups, by_sum = grouped && a.group_best == 2;
   float x[PER];
   load_row(a, t, l.first, l.mine, x);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = clean(x[i]);
   Key key[PER];
   double worth[PER];
   float top = -INFINITY;
@@ -251,44 +255,39 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {
           }
 }
 
+// One token, by its warp.
 template <int PER>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const Lanes l(a);
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, const Lanes& l, const float (&bias)[PER],
+                                            float (&x)[PER]) {
   const bool biased = a.bias != nullptr, grouped = a.top_groups < a.groups, by_sum = grouped && a.group_best == 2;
   const float gap = a.sigmoid ? kGapSigmoid : kGapSoftmax;
-  float x[PER];
-  load_row(a, t, l.first, l.mine, x);
-  float top = x[0];
+  float ref = 0.f, total = 1.f;
+  if (!a.sigmoid) {
+    float top = x[0];
 #pragma unroll
-  for (int i = 1; i < PER; ++i) top = fmaxf(top, x[i]);
-  top = warp_max(top);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float total = 1.f;
-  if (!a.sigmoid && (biased || by_sum || !a.renormalize)) {
-    float s = 0.f;
+    for (int i = 1; i < PER; ++i) top = fmaxf(top, x[i]);
+    top = warp_max(top);
+    ref = top == -INFINITY ? 0.f : top;
+    if (biased || by_sum || !a.renormalize) {
+      float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s += expf(x[i] - ref);  // (0 for experts that do not exist)
-    total = warp_sum(s);
-  }
-  // what orders the experts, and what they are worth in their groups (x stays, where it is neither, only -inf or not)
-  float worth[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    worth[i] = x[i];
-    if ((biased || by_sum) && x[i] != -INFINITY) {
-      float v = a.sigmoid ? sigmoid_near(x[i]) : expf(x[i] - ref) / total;
-      if (biased) {
-        v += a.bias[l.first + i];
-        v = v == v ? v : -INFINITY;
-        x[i] = v;
-      }
-      worth[i] = v;
+      for (int i = 0; i < PER; ++i) s += expf(x[i] - ref);  // (0 for experts that do not exist)
+      total = warp_sum(s);
     }
+  }
+  // what orders the experts, and what they are worth in their groups
+  float worth[PER];
+  if (biased || by_sum) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      float v = a.sigmoid ? sigmoid_near(x[i]) : expf(x[i] - ref) / total;
+      if (biased) v += bias[i];
+      worth[i] = x[i] != -INFINITY && v == v ? v : -INFINITY;
+      if (biased) x[i] = worth[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) worth[i] = x[i];
   }
   bool apart = true, open = l.real;
   if (grouped) {
@@ -363,9 +362,30 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteArgs
 }
 
 template <int PER>
+__global__ void __launch_bounds__(32 * kRouteWarps, PER <= 8 ? 5 : 2) route_kernel(const __grid_constant__ RouteArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, step_t = gridDim.x * kRouteWarps;
+  int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const Lanes l(a);
+  float bias[PER], x[PER], ahead[PER];
+  if (a.bias != nullptr) load_floats(a.bias + l.first, l.mine, bias);
+  load_row(a, t, l.first, l.mine, ahead);
+  // a warp's tokens, the next one's logits under way
+  for (; t < a.T; t += step_t) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = clean(ahead[i]);
+    if (t + step_t < a.T) load_row(a, t + step_t, l.first, l.mine, ahead);
+    route_token(a, t, lane, l, bias, x);
+  }
+}
+
+template <int PER>
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
-  return launch_dependent(route_kernel<PER>, dim3(static_cast<unsigned>((a.T + kRouteWarps - 1) / kRouteWarps)),
-                          32 * kRouteWarps, 0, stream, a);
+  // as many CTAs as the SMs hold, each warp with every so manieth token
+  const int ctas = (a.T + kRouteWarps - 1) / kRouteWarps, most = (PER <= 8 ? 5 : 2) * device_sm_count();
+  return launch_dependent(route_kernel<PER>, dim3(ctas < most ? ctas : most), 32 * kRouteWarps, 0, stream, a);
 }
 
 }  // namespace
