@@ -76,12 +76,14 @@ struct PrefixCfg {
   static constexpr int SLICES = D / 64;            // of 128 bytes of a row
   static constexpr int PIECE = TN * D * 2, QB = kRows * D * 2;
   static constexpr int MISC = 3072;                // barriers, starts, alignment
-  static constexpr int FIT = (232448 - MISC - LANES * QB) / PIECE, SLOTS = FIT > 8 ? 8 : FIT;
-  static constexpr int OFF_Q = SLOTS * PIECE, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 256;
+  // an E4M3 cache's pieces as they lie there, on their way to fp16
+  static constexpr int RAW = TN * D, RAWS = !E8 ? 0 : D == 64 ? 8 : 4;
+  static constexpr int FIT = (232448 - MISC - LANES * QB - RAWS * RAW) / PIECE, SLOTS = FIT > 8 ? 8 : FIT;
+  static constexpr int OFF_RAW = SLOTS * PIECE, OFF_Q = OFF_RAW + RAWS * RAW, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 384;
   static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
   static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps;
   static constexpr int O_COL = 256;                // scores in columns 0 .. 2 TN - 1, outputs from 256 on
-  static_assert(SLOTS >= 4 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
+  static_assert(SLOTS >= 3 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
 };
 
 // New rows of sequence b that exist (0 where they do not come behind the prefix).
@@ -264,7 +266,7 @@ struct PrefixRoles {
   const PrefixArgs& a;
   const PrefixList l;
   unsigned char* smem;
-  uint32_t sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem;
+  uint32_t sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, raw_full, raw_empty, tmem;
   const int* starts;
   int begin, end;
 
@@ -293,9 +295,13 @@ struct PrefixRoles {
   }
   __device__ __forceinline__ void load_tma(const CUtensorMap* kmap, const CUtensorMap* vmap) {
     const int lane = threadIdx.x & 31;
+    // (to the ring of pieces, or of an E4M3 cache's raw ones, whose rows are half as long)
+    constexpr int RING = E8 ? Cfg::RAWS : SLOTS, BYTES = E8 ? Cfg::RAW : Cfg::PIECE, OFF = E8 ? Cfg::OFF_RAW : 0;
+    constexpr int ROW = E8 && D == 64 ? 64 : 128, SLICES = E8 ? (D + 127) / 128 : Cfg::SLICES;
+    const uint32_t f = E8 ? raw_full : full, e = E8 ? raw_empty : empty;
     bool lost = false;
     int it = 0;
-    const int groups = TN / a.box, boxes = groups * Cfg::SLICES;
+    const int groups = TN / a.box, boxes = groups * SLICES;
     int page = 0, place = 0;
     if (begin < end) find_boxes(PrefixSegment(l, begin, end, LANES).kb, page, place);
     for (int u = begin; u < end && !lost;) {
@@ -306,18 +312,18 @@ struct PrefixRoles {
         int page2 = 0, place2 = 0;
         if (t + 1 < g.ke || u < end) find_boxes(t + 1 < g.ke ? t + 1 : 0, page2, place2);
         for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int slot = it % SLOTS;
-          if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+          const int slot = it % RING;
+          if (it >= RING) lost = !mbar_wait(e + slot * 8, ((it / RING) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
           lost = __any_sync(0xffffffffu, lost);
           if (lost) break;
-          if (lane == 0) mbar_arrive_expect_tx(full + slot * 8, Cfg::PIECE);
+          if (lane == 0) mbar_arrive_expect_tx(f + slot * 8, BYTES);
           __syncwarp();
           for (int x0 = 0; x0 < boxes; x0 += 32) {
             const int x = x0 + lane, box = x % groups, slice = x / groups;
             const int pg = __shfl_sync(0xffffffffu, page, box), pl = __shfl_sync(0xffffffffu, place, box);
             if (x < boxes)
-              tma_box(sbase + slot * Cfg::PIECE + slice * TN * 128 + box * a.box * 128, kv ? vmap : kmap, pl, slice, g.h, pg,
-                      full + slot * 8);
+              tma_box(sbase + OFF + slot * BYTES + slice * TN * ROW + box * a.box * ROW, kv ? vmap : kmap, pl, slice, g.h, pg,
+                      f + slot * 8);
           }
         }
         page = page2;
@@ -325,8 +331,42 @@ struct PrefixRoles {
       }
     }
     // (the products wait for the same; where one is given up, the limit was time enough for the others)
-    for (int i = max(it - SLOTS, 0); i < it; ++i)
-      if (__any_sync(0xffffffffu, !mbar_wait(full + i % SLOTS * 8, (i / SLOTS) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
+    for (int i = max(it - RING, 0); i < it; ++i)
+      if (__any_sync(0xffffffffu, !mbar_wait(f + i % RING * 8, (i / RING) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
+  }
+
+  // Raw pieces to fp16, by the other copying warps.
+  __device__ __forceinline__ void convert() {
+    constexpr int CPR = D / 16, THREADS = 32 * (kLoadWarps - 1), STEP = THREADS / CPR;
+    const int x = threadIdx.x - Cfg::WG - 64, ch = x % CPR, r0 = x / CPR, lane = threadIdx.x & 31;
+    const int pieces = 2 * (end - begin);
+    for (int it = 0; it < pieces; ++it) {
+      const int from = it % Cfg::RAWS, to = it % SLOTS;
+      bool lost = !mbar_wait(raw_full + from * 8, (it / Cfg::RAWS) & 1, kStatusTimeoutFull, a.wait_ns);
+      if (it >= SLOTS) lost = lost || !mbar_wait(empty + to * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+      if (__any_sync(0xffffffffu, lost)) return;
+      const unsigned char* const raw = smem + Cfg::OFF_RAW + from * Cfg::RAW;
+      unsigned char* const piece = smem + to * Cfg::PIECE;
+#pragma unroll 4
+      for (int r = r0; r < TN; r += STEP) {
+        const int at = D == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : (ch >> 3) * TN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(raw + at);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint4 o[2];
+        o[0] = make_uint4(e4m3x2_f16x2(w[0]), e4m3x2_f16x2(w[0] >> 16), e4m3x2_f16x2(w[1]), e4m3x2_f16x2(w[1] >> 16));
+        o[1] = make_uint4(e4m3x2_f16x2(w[2]), e4m3x2_f16x2(w[2] >> 16), e4m3x2_f16x2(w[3]), e4m3x2_f16x2(w[3] >> 16));
+        // (of a row's two slices, which lie in the same banks, one half's chunks are stored in the other order)
+        const int odd = (ch >> 2) & 1;
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + odd, TN)) = odd ? o[1] : o[0];
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1 - odd, TN)) = odd ? o[0] : o[1];
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(raw_empty + from * 8);
+        mbar_arrive(full + to * 8);
+      }
+    }
   }
 
   // By threads, for pages that no box divides: bf16, rows by 16-byte asynchronous copies, kLag pieces under way.
@@ -768,12 +808,13 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const uint32_t full = sbase + Cfg::OFF_BAR, empty = full + Cfg::SLOTS * 8, s_full = empty + Cfg::SLOTS * 8, p_full = s_full + 16,
                  q_full = p_full + 32, o_full = q_full + 16, pv_done = o_full + 16, fin = pv_done + 8;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_BAR + Cfg::SLOTS * 16 + 96);
+  const uint32_t raw_full = sbase + Cfg::OFF_BAR + Cfg::SLOTS * 16 + 112, raw_empty = raw_full + Cfg::RAWS * 8;
   int* const starts = reinterpret_cast<int*>(smem + Cfg::OFF_STARTS);
   int* const s_sum = reinterpret_cast<int*>(smem + Cfg::OFF_Q);  // (before the queries)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::SLOTS; ++s) {
-      mbar_init(full + s * 8, a.box ? 1 : 32 * kLoadWarps);
+      mbar_init(full + s * 8, !a.box ? 32 * kLoadWarps : E8 ? kLoadWarps - 1 : 1);
       mbar_init(empty + s * 8, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -785,8 +826,12 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
     }
     mbar_init(pv_done, 1);
     mbar_init(fin, 1);
+    for (int s = 0; s < Cfg::RAWS; ++s) {
+      mbar_init(raw_full + s * 8, 1);
+      mbar_init(raw_empty + s * 8, kLoadWarps - 1);
+    }
     fence_mbar_init();
-    if (a.inject && blockIdx.x == 0) mbar_expect_tx(full, 16);
+    if (a.inject && blockIdx.x == 0) mbar_expect_tx(E8 ? raw_full : full, 16);
   }
   if (warp == Cfg::WG / 32) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "r"(512u) : "memory");
@@ -839,18 +884,19 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   tmem_after();
   const uint32_t tmem = *tmem_slot;
   const PrefixList l = PrefixList::make<Cfg>(a, token_rows);
-  PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, tmem, starts,
+  PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, raw_full, raw_empty, tmem, starts,
                        l.begin(blockIdx.x), l.begin(blockIdx.x + 1)};
   if (warp < Cfg::WG / 32) {
     r.rows();
   } else if (warp == Cfg::WG / 32) {
     r.multiply();
-  } else if (E8) {
-    r.load_e4m3();
   } else if (a.box == 0) {
-    r.load_rows();
+    if constexpr (E8) r.load_e4m3();
+    else r.load_rows();
   } else if (warp == Cfg::WG / 32 + 1) {
     r.load_tma(&kmap, &vmap);
+  } else {
+    if constexpr (E8) r.convert();
   }
   __syncwarp();
   tmem_before();
@@ -875,46 +921,55 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
   const int64_t at = static_cast<int64_t>(tr) * a.Hq + h * a.G + x - tr * a.G;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float lse = -INFINITY;
+  // (the own tokens' share is on its way beside what says whether there is a row)
+  const float own_lse = a.own_lse[at];
+  const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
   if (i < rows_of(a, b)) {
-    const float own_lse = a.own_lse[at];
-    const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
-    const float own_m = own_lse * 1.4426950408889634f;
-    float top = own_m;
-    int first = 0, parts = 0;
-    int64_t p0 = 0;  // (part, lane) of the first
-    int r = 0;
+    // running maximum, sum and output over the row's parts, four under way at a time
+    float top = own_lse * 1.4426950408889634f, sum = own_lse == -INFINITY ? 0.f : 1.f;
+    float4 acc = sum != 0.f ? own : o;
     if (a.tokens > 0) {
       const PrefixList l = PrefixList::make<Cfg>(a, a.starts[a.B]);
-      r = (a.starts[b] + i) * a.G + x - tr * a.G;
-      const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair;
+      int r = (a.starts[b] + i) * a.G + x - tr * a.G;
+      const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair, u0 = s * l.tiles_n;
       r -= tile * kRows;
-      const int u0 = s * l.tiles_n;
-      first = l.holder(u0);
-      parts = l.holder(u0 + l.tiles_n - 1) - first + 1;
+      const int first = l.holder(u0), parts = l.holder(u0 + l.tiles_n - 1) - first + 1;
       const bool split = Cfg::LANES == 2 && 2 * pair + 1 >= l.tiles;
-      p0 = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
-    }
-    constexpr int step = Cfg::LANES;
-#pragma unroll 8
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, a.part_ml[(p0 + p * step) * kRows + r].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float w = own_lse == -INFINITY ? 0.f : exp2_of(own_m - ref);
-    float sum = w;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const int64_t at_part = p0 + p * step;
-      const float2 ml = a.part_ml[at_part * kRows + r];
-      const float4 v = a.part_o[(at_part * COLS + col) * kRows + r];
-      const float f = exp2_of(ml.x - ref);
-      sum += f * ml.y;
-      acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+      const int64_t p0 = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
+      for (int p = 0; p < parts; p += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p + k < parts) {
+            const int64_t at_part = p0 + (p + k) * Cfg::LANES;
+            ml[k] = a.part_ml[at_part * kRows + r];
+            v[k] = a.part_o[(at_part * COLS + col) * kRows + r];
+          }
+        }
+        float t = top;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t = fmaxf(t, ml[k].x);
+        const float ref = t == -INFINITY ? 0.f : t, f = exp2_of(top - ref);
+        top = t;
+        sum *= f;
+        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (p + k >= parts) break;
+          const float g = exp2_of(ml[k].x - ref);
+          sum += g * ml[k].y;
+          const float gv = g * a.v_scale;  // (what the own tokens' outputs have been scaled by already)
+          acc.x += gv * v[k].x, acc.y += gv * v[k].y, acc.z += gv * v[k].z, acc.w += gv * v[k].w;
+        }
+      }
     }
     if (sum != 0.f) {
-      const float f = a.v_scale / sum, g = w / sum;
+      const float f = 1.f / sum;
       o = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-      if (w != 0.f) o.x += own.x * g, o.y += own.y * g, o.z += own.z * g, o.w += own.w * g;
-      lse = (ref + log2f(sum)) * 0.6931471805599453f;
+      lse = (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
   *reinterpret_cast<uint2*>(a.out + at * D + col * 4) = make_uint2(bf16x2_of(o.x, o.y), bf16x2_of(o.z, o.w));

@@ -280,7 +280,7 @@ extern "C" qmm_status qmm_rope_append(const qmm_paged_cache* cache, const qmm_ro
   if (rc != QMM_OK) return rc;
   const int64_t width = static_cast<int64_t>(cache->heads) * cache->head_dim, q_width = static_cast<int64_t>(q_heads) * cache->head_dim;
   if (q_heads < 1 || q_heads > 65535 || k_ld < width || v_ld < width || q_ld < q_width || q_out_ld < q_width ||
-      static_cast<int64_t>(B) * M > 0x7fffffff || rope->rot < 0 || rope->rot > cache->head_dim || rope->rot % 16 != 0)
+      static_cast<int64_t>(B) * M > 0x7fff0000 || rope->rot < 0 || rope->rot > cache->head_dim || rope->rot % 16 != 0)
     return QMM_ERR_SHAPE;
   if (rope->positions != nullptr) {
     if (rope->axes < 1 || rope->axes > 4) return QMM_ERR_UNSUPPORTED;
