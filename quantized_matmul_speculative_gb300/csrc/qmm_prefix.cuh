@@ -282,15 +282,16 @@ struct PrefixRoles {
     return p;
   }
 
-  // A tile's boxes: the page of each (what lies outside the prefix and the cache reads as zeros) and its place there, in the
-  // first lanes.  A tile has at most 16 along its tokens.
-  __device__ __forceinline__ void find_boxes(int t, int& page, int& place) const {
+  // A tile's boxes along its tokens, 16 at most, one a lane: the entry of the prefix's table and the place in that page.  The
+  // entry is looked at when its turn comes, so that it may be on its way until then.
+  __device__ __forceinline__ void find_boxes(int t, int& entry, int& place) const {
     const int lane = threadIdx.x & 31, j = t * TN + lane * a.box;
-    page = a.c.num_pages;
+    entry = INT_MIN;  // outside the prefix
     place = 0;
     if (lane * a.box < TN && j < a.tokens) {
-      const int p = page_of(j, place);
-      if (p >= 0) page = p;
+      const int block = a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
+      place = j - block * a.c.page_size;
+      entry = a.prefix[block];
     }
   }
   __device__ __forceinline__ void load_tma(const CUtensorMap* kmap, const CUtensorMap* vmap) {
@@ -301,16 +302,20 @@ struct PrefixRoles {
     const uint32_t f = E8 ? raw_full : full, e = E8 ? raw_empty : empty;
     bool lost = false;
     int it = 0;
-    const int groups = TN / a.box, boxes = groups * SLICES;
-    int page = 0, place = 0;
-    if (begin < end) find_boxes(PrefixSegment(l, begin, end, LANES).kb, page, place);
+    const int groups = TN / a.box, boxes = groups * SLICES, groups_log2 = 31 - __clz(groups);  // (box is a power of two)
+    int entry = 0, place = 0;
+    if (begin < end) find_boxes(PrefixSegment(l, begin, end, LANES).kb, entry, place);
     for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       u += g.ke - g.kb;
       for (int t = g.kb; t < g.ke && !lost; ++t) {
         // the next tile's page numbers are on their way while this one's copies are issued
-        int page2 = 0, place2 = 0;
-        if (t + 1 < g.ke || u < end) find_boxes(t + 1 < g.ke ? t + 1 : 0, page2, place2);
+        int entry2 = 0, place2 = 0;
+        if (t + 1 < g.ke || u < end) find_boxes(t + 1 < g.ke ? t + 1 : 0, entry2, place2);
+        // (what lies outside the prefix and the cache is outside the tensor and reads as zeros)
+        const bool none = entry < 0 || entry >= a.c.num_pages;
+        if (none && entry != INT_MIN) bad_page();
+        const int page = none ? static_cast<int>(a.c.num_pages) : entry;
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int slot = it % RING;
           if (it >= RING) lost = !mbar_wait(e + slot * 8, ((it / RING) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
@@ -319,14 +324,14 @@ struct PrefixRoles {
           if (lane == 0) mbar_arrive_expect_tx(f + slot * 8, BYTES);
           __syncwarp();
           for (int x0 = 0; x0 < boxes; x0 += 32) {
-            const int x = x0 + lane, box = x % groups, slice = x / groups;
+            const int x = x0 + lane, slice = x >> groups_log2, box = x & (groups - 1);
             const int pg = __shfl_sync(0xffffffffu, page, box), pl = __shfl_sync(0xffffffffu, place, box);
             if (x < boxes)
               tma_box(sbase + OFF + slot * BYTES + slice * TN * ROW + box * a.box * ROW, kv ? vmap : kmap, pl, slice, g.h, pg,
                       f + slot * 8);
           }
         }
-        page = page2;
+        entry = entry2;
         place = place2;
       }
     }
@@ -347,7 +352,7 @@ struct PrefixRoles {
       if (__any_sync(0xffffffffu, lost)) return;
       const unsigned char* const raw = smem + Cfg::OFF_RAW + from * Cfg::RAW;
       unsigned char* const piece = smem + to * Cfg::PIECE;
-#pragma unroll 4
+#pragma unroll 8
       for (int r = r0; r < TN; r += STEP) {
         const int at = D == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : (ch >> 3) * TN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
         const uint4 u = *reinterpret_cast<const uint4*>(raw + at);
