@@ -40,7 +40,8 @@
 namespace qmm {
 
 constexpr int kRows = 128;        // of a tile
-constexpr int kLoadWarps = 3;   // (12 warps in all: a thread may have 168 registers, of 13 and more 128)
+constexpr int kLoadWarps = 3;     // (12 warps in all: a thread may have 168 registers, of 13 and more 128)
+constexpr int kConvertWarps = 4;  // more for an E4M3 cache
 constexpr int kMaxStarts = 400;   // sequences whose first rows a CTA lists; of more, rows that do not exist are computed too
 constexpr float kSlack = 8.f, kSlackE8 = 4.f, kLiftE8 = 11.f;
 
@@ -81,7 +82,10 @@ struct PrefixCfg {
   static constexpr int FIT = (232448 - MISC - LANES * QB - RAWS * RAW) / PIECE, SLOTS = FIT > 8 ? 8 : FIT;
   static constexpr int OFF_RAW = SLOTS * PIECE, OFF_Q = OFF_RAW + RAWS * RAW, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 384;
   static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
-  static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps;
+  static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps + (E8 ? 32 * kConvertWarps : 0);
+  // E4M3, two lanes: of the launch's 512 x 128 registers, 256 x 168 for the threads with rows and 256 x 88 for the others
+  static constexpr bool MOVE_REGS = E8 && LANES == 2;
+  static constexpr int ROW_REGS = 168, OTHER_REGS = 88;
   static constexpr int O_COL = 256;                // scores in columns 0 .. 2 TN - 1, outputs from 256 on
   static_assert(SLOTS >= 3 && SMEM <= 232448 && O_COL + LANES * D <= 512 && 2 * TN <= O_COL, "room of an SM");
 };
@@ -295,14 +299,11 @@ struct PrefixRoles {
     }
   }
   __device__ __forceinline__ void load_tma(const CUtensorMap* kmap, const CUtensorMap* vmap) {
-    const int lane = threadIdx.x & 31;
-    // (to the ring of pieces, or of an E4M3 cache's raw ones, whose rows are half as long)
-    constexpr int RING = E8 ? Cfg::RAWS : SLOTS, BYTES = E8 ? Cfg::RAW : Cfg::PIECE, OFF = E8 ? Cfg::OFF_RAW : 0;
-    constexpr int ROW = E8 && D == 64 ? 64 : 128, SLICES = E8 ? (D + 127) / 128 : Cfg::SLICES;
-    const uint32_t f = E8 ? raw_full : full, e = E8 ? raw_empty : empty;
+    // (a warp asks for one box after another, 110 cycles each: the copying warps share them)
+    const int lane = threadIdx.x & 31, loader = (threadIdx.x - Cfg::WG - 32) >> 5;
     bool lost = false;
     int it = 0;
-    const int groups = TN / a.box, boxes = groups * SLICES, groups_log2 = 31 - __clz(groups);  // (box is a power of two)
+    const int groups = TN / a.box, boxes = groups * Cfg::SLICES, groups_log2 = 31 - __clz(groups);  // (box is a power of two)
     int entry = 0, place = 0;
     if (begin < end) find_boxes(PrefixSegment(l, begin, end, LANES).kb, entry, place);
     for (int u = begin; u < end && !lost;) {
@@ -317,18 +318,18 @@ struct PrefixRoles {
         if (none && entry != INT_MIN) bad_page();
         const int page = none ? static_cast<int>(a.c.num_pages) : entry;
         for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int slot = it % RING;
-          if (it >= RING) lost = !mbar_wait(e + slot * 8, ((it / RING) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+          const int slot = it % SLOTS;
+          if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
           lost = __any_sync(0xffffffffu, lost);
           if (lost) break;
-          if (lane == 0) mbar_arrive_expect_tx(f + slot * 8, BYTES);
+          if (loader == 0 && lane == 0) mbar_arrive_expect_tx(full + slot * 8, Cfg::PIECE);
           __syncwarp();
-          for (int x0 = 0; x0 < boxes; x0 += 32) {
-            const int x = x0 + lane, slice = x >> groups_log2, box = x & (groups - 1);
+          for (int x0 = 0; x0 < boxes; x0 += 32 * kLoadWarps) {
+            const int x = x0 + lane * kLoadWarps + loader, slice = x >> groups_log2, box = x & (groups - 1);
             const int pg = __shfl_sync(0xffffffffu, page, box), pl = __shfl_sync(0xffffffffu, place, box);
             if (x < boxes)
-              tma_box(sbase + OFF + slot * BYTES + slice * TN * ROW + box * a.box * ROW, kv ? vmap : kmap, pl, slice, g.h, pg,
-                      f + slot * 8);
+              tma_box(sbase + slot * Cfg::PIECE + slice * TN * 128 + box * a.box * 128, kv ? vmap : kmap, pl, slice, g.h, pg,
+                      full + slot * 8);
           }
         }
         entry = entry2;
@@ -336,42 +337,8 @@ struct PrefixRoles {
       }
     }
     // (the products wait for the same; where one is given up, the limit was time enough for the others)
-    for (int i = max(it - RING, 0); i < it; ++i)
-      if (__any_sync(0xffffffffu, !mbar_wait(f + i % RING * 8, (i / RING) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
-  }
-
-  // Raw pieces to fp16, by the other copying warps.
-  __device__ __forceinline__ void convert() {
-    constexpr int CPR = D / 16, THREADS = 32 * (kLoadWarps - 1), STEP = THREADS / CPR;
-    const int x = threadIdx.x - Cfg::WG - 64, ch = x % CPR, r0 = x / CPR, lane = threadIdx.x & 31;
-    const int pieces = 2 * (end - begin);
-    for (int it = 0; it < pieces; ++it) {
-      const int from = it % Cfg::RAWS, to = it % SLOTS;
-      bool lost = !mbar_wait(raw_full + from * 8, (it / Cfg::RAWS) & 1, kStatusTimeoutFull, a.wait_ns);
-      if (it >= SLOTS) lost = lost || !mbar_wait(empty + to * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
-      if (__any_sync(0xffffffffu, lost)) return;
-      const unsigned char* const raw = smem + Cfg::OFF_RAW + from * Cfg::RAW;
-      unsigned char* const piece = smem + to * Cfg::PIECE;
-#pragma unroll 8
-      for (int r = r0; r < TN; r += STEP) {
-        const int at = D == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : (ch >> 3) * TN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        const uint4 u = *reinterpret_cast<const uint4*>(raw + at);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint4 o[2];
-        o[0] = make_uint4(e4m3x2_f16x2(w[0]), e4m3x2_f16x2(w[0] >> 16), e4m3x2_f16x2(w[1]), e4m3x2_f16x2(w[1] >> 16));
-        o[1] = make_uint4(e4m3x2_f16x2(w[2]), e4m3x2_f16x2(w[2] >> 16), e4m3x2_f16x2(w[3]), e4m3x2_f16x2(w[3] >> 16));
-        // (of a row's two slices, which lie in the same banks, one half's chunks are stored in the other order)
-        const int odd = (ch >> 2) & 1;
-        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + odd, TN)) = odd ? o[1] : o[0];
-        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1 - odd, TN)) = odd ? o[0] : o[1];
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(raw_empty + from * 8);
-        mbar_arrive(full + to * 8);
-      }
-    }
+    for (int i = max(it - SLOTS, 0); i < it; ++i)
+      if (__any_sync(0xffffffffu, !mbar_wait(full + i % SLOTS * 8, (i / SLOTS) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
   }
 
   // By threads, for pages that no box divides: bf16, rows by 16-byte asynchronous copies, kLag pieces under way.
@@ -410,81 +377,96 @@ struct PrefixRoles {
       for (int i = max(it - kLag, 0); i < it; ++i) mbar_arrive(full + i % SLOTS * 8);
   }
 
-  // E4M3 through registers, the next piece's loads ahead of a piece's conversion.
-  __device__ __forceinline__ void load_e4m3() {
-    constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = (TN + STEP - 1) / STEP;  // 16-byte chunks of a row; of a thread
+  // E4M3: rows by 16-byte asynchronous copies to the ring of raw pieces, whatever the page size (boxes of 8 tokens took a warp
+  // 110 cycles each to ask for).
+  static __device__ __forceinline__ uint32_t raw_at(int r, int ch) {
+    return D == 64 ? r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) : (ch >> 3) * TN * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  }
+  __device__ __forceinline__ void copy_raw() {
+    constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = (TN + STEP - 1) / STEP;
     const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
-    bool lost = false;
-    int it = 0;
-    uint4 k[N], v[N];
-    auto fetch = [&](uint4 (&to)[N], const int (&page)[N], const int (&place)[N], int h, bool values) {
-      const uint8_t* const cache = static_cast<const uint8_t*>(values ? a.c.v : a.c.k);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        to[i] = make_uint4(0, 0, 0, 0);
-        if (page[i] >= 0)
-          to[i] = ld_after_wait_v4(cache + (values ? page[i] * a.c.v_page + place[i] * a.c.v_token + h * a.c.v_head
-                                                   : page[i] * a.c.k_page + place[i] * a.c.k_token + h * a.c.k_head) +
-                                   ch * 16);
-      }
-    };
-    auto put = [&](const uint4 (&from)[N]) {
-      const int slot = it % SLOTS;
-      if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
-      if (lost) return;
-      unsigned char* const piece = smem + slot * Cfg::PIECE;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t w[4] = {from[i].x, from[i].y, from[i].z, from[i].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[2 * e] = e4m3x2_f16x2(w[e]);
-          o[2 * e + 1] = e4m3x2_f16x2(w[e] >> 16);
-        }
-        const int r = r0 + i * STEP;
-        if (r >= TN) break;
-        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch, TN)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1, TN)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_async_shared();
-      mbar_arrive(full + slot * 8);
-      ++it;
-    };
-    int page[N], place[N];
+    int entry[N], place[N];  // the tile's rows of this thread: the prefix's entry (INT_MIN: no row), and the place in that page
     auto find = [&](int t) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int j = t * TN + r0 + i * STEP;
+        const int r = r0 + i * STEP, j = t * TN + r;
+        entry[i] = INT_MIN;
         place[i] = 0;
-        page[i] = r0 + i * STEP < TN && j < a.tokens ? page_of(j, place[i]) : -1;
-      }
-    };
-    int u = begin;
-    if (u >= end) return;
-    PrefixSegment g(l, u, end, LANES);
-    int t = g.kb;
-    find(t);
-    fetch(k, page, place, g.h, false);
-    while (!lost) {
-      fetch(v, page, place, g.h, true);
-      put(k);
-      if (lost) break;
-      bool more = true;
-      if (++t == g.ke) {
-        u += g.ke - g.kb;
-        more = u < end;
-        if (more) {
-          g = PrefixSegment(l, u, end, LANES);
-          t = g.kb;
+        if (r < TN && j < a.tokens) {
+          const int block = a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
+          place[i] = j - block * a.c.page_size;
+          entry[i] = a.prefix[block];
         }
       }
-      if (more) {
-        find(t);
-        fetch(k, page, place, g.h, false);
+    };
+    bool lost = false;
+    int it = 0;
+    if (begin < end) find(PrefixSegment(l, begin, end, LANES).kb);
+    for (int u = begin; u < end && !lost;) {
+      const PrefixSegment g(l, u, end, LANES);
+      u += g.ke - g.kb;
+      for (int t = g.kb; t < g.ke && !lost; ++t) {
+        int page[N], at[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const bool none = entry[i] < 0 || entry[i] >= a.c.num_pages;
+          if (none && entry[i] != INT_MIN) bad_page();
+          page[i] = none ? -1 : entry[i];
+          at[i] = place[i];
+        }
+        // (the next tile's entries are on their way while this one's copies are issued)
+        if (t + 1 < g.ke || u < end) find(t + 1 < g.ke ? t + 1 : 0);
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int slot = it % Cfg::RAWS;
+          if (it >= Cfg::RAWS) lost = !mbar_wait(raw_empty + slot * 8, ((it / Cfg::RAWS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+          if (lost) break;
+          const unsigned long long cache = reinterpret_cast<unsigned long long>(kv ? a.c.v : a.c.k) + ch * 16;
+          const int64_t s_page = kv ? a.c.v_page : a.c.k_page, s_token = kv ? a.c.v_token : a.c.k_token,
+                        head = g.h * (kv ? a.c.v_head : a.c.k_head);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = r0 + i * STEP;
+            if (r < TN)
+              copy_16(sbase + Cfg::OFF_RAW + slot * Cfg::RAW + raw_at(r, ch),
+                      cache + (page[i] >= 0 ? page[i] * s_page + at[i] * s_token + head : 0), page[i] >= 0);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full + slot * 8) : "memory");
+        }
       }
-      put(v);
-      if (!more) break;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+
+  // Raw pieces to fp16, by warps of their own.
+  __device__ __forceinline__ void convert() {
+    constexpr int CPR = D / 16, STEP = 32 * kConvertWarps / CPR;
+    const int x = threadIdx.x - Cfg::WG - 32 - 32 * kLoadWarps, ch = x % CPR, r0 = x / CPR, lane = threadIdx.x & 31;
+    const int pieces = 2 * (end - begin);
+    for (int it = 0; it < pieces; ++it) {
+      const int from = it % Cfg::RAWS, to = it % SLOTS;
+      bool lost = !mbar_wait(raw_full + from * 8, (it / Cfg::RAWS) & 1, kStatusTimeoutFull, a.wait_ns);
+      if (it >= SLOTS) lost = lost || !mbar_wait(empty + to * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
+      if (__any_sync(0xffffffffu, lost)) return;
+      const unsigned char* const raw = smem + Cfg::OFF_RAW + from * Cfg::RAW;
+      unsigned char* const piece = smem + to * Cfg::PIECE;
+#pragma unroll
+      for (int r = r0; r < TN; r += STEP) {
+        const uint4 u = *reinterpret_cast<const uint4*>(raw + raw_at(r, ch));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint4 o[2];
+        o[0] = make_uint4(e4m3x2_f16x2(w[0]), e4m3x2_f16x2(w[0] >> 16), e4m3x2_f16x2(w[1]), e4m3x2_f16x2(w[1] >> 16));
+        o[1] = make_uint4(e4m3x2_f16x2(w[2]), e4m3x2_f16x2(w[2] >> 16), e4m3x2_f16x2(w[3]), e4m3x2_f16x2(w[3] >> 16));
+        // (of a row's two slices, which lie in the same banks, one half's chunks are stored in the other order)
+        const int odd = (ch >> 2) & 1;
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + odd, TN)) = odd ? o[1] : o[0];
+        *reinterpret_cast<uint4*>(piece + swizzled(r, 2 * ch + 1 - odd, TN)) = odd ? o[0] : o[1];
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(raw_empty + from * 8);
+        mbar_arrive(full + to * 8);
+      }
     }
   }
 
@@ -819,7 +801,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::SLOTS; ++s) {
-      mbar_init(full + s * 8, !a.box ? 32 * kLoadWarps : E8 ? kLoadWarps - 1 : 1);
+      mbar_init(full + s * 8, E8 ? kConvertWarps : a.box ? 1 : 32 * kLoadWarps);
       mbar_init(empty + s * 8, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -832,8 +814,8 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
     mbar_init(pv_done, 1);
     mbar_init(fin, 1);
     for (int s = 0; s < Cfg::RAWS; ++s) {
-      mbar_init(raw_full + s * 8, 1);
-      mbar_init(raw_empty + s * 8, kLoadWarps - 1);
+      mbar_init(raw_full + s * 8, 32 * kLoadWarps);
+      mbar_init(raw_empty + s * 8, kConvertWarps);
     }
     fence_mbar_init();
     if (a.inject && blockIdx.x == 0) mbar_expect_tx(E8 ? raw_full : full, 16);
@@ -891,17 +873,22 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const PrefixList l = PrefixList::make<Cfg>(a, token_rows);
   PrefixRoles<D, E8> r{a, l, smem, sbase, full, empty, s_full, p_full, q_full, o_full, pv_done, fin, raw_full, raw_empty, tmem, starts,
                        l.begin(blockIdx.x), l.begin(blockIdx.x + 1)};
+  if constexpr (Cfg::MOVE_REGS) {
+    static_assert(256 * Cfg::ROW_REGS + 256 * Cfg::OTHER_REGS <= 512 * 128 && Cfg::THREADS == 512, "registers of the launch");
+    if (warp < Cfg::WG / 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::ROW_REGS));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::OTHER_REGS));
+  }
   if (warp < Cfg::WG / 32) {
     r.rows();
   } else if (warp == Cfg::WG / 32) {
     r.multiply();
+  } else if constexpr (E8) {
+    if (warp <= Cfg::WG / 32 + kLoadWarps) r.copy_raw();
+    else r.convert();
   } else if (a.box == 0) {
-    if constexpr (E8) r.load_e4m3();
-    else r.load_rows();
-  } else if (warp == Cfg::WG / 32 + 1) {
-    r.load_tma(&kmap, &vmap);
+    r.load_rows();
   } else {
-    if constexpr (E8) r.convert();
+    r.load_tma(&kmap, &vmap);
   }
   __syncwarp();
   tmem_before();

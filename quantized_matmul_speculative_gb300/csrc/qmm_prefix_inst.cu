@@ -22,7 +22,7 @@ static cudaError_t launch_main(PrefixArgs a, cudaStream_t stream) {
   // boxes of the largest size that divides page and tile, down to the 8 rows of the swizzle
   CUtensorMap kmap = {}, vmap = {};
   a.box = 0;
-  if (a.c.num_pages > 0)
+  if (!E8 && a.c.num_pages > 0)
     for (int box = Cfg::TN; box >= 8 && a.box == 0; box /= 2)
       if (a.c.page_size % box == 0) a.box = box;
   if (a.box != 0 && (!cache_map(&kmap, a.c, false, a.box, 1) || !cache_map(&vmap, a.c, true, a.box, 1))) a.box = 0;
