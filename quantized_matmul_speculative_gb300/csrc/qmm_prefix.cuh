@@ -533,7 +533,7 @@ struct PrefixRoles {
             q_phase ^= 1u << o;
           }
           if (lost) break;
-          tmem_after();
+          // (no fence: the operands are in shared memory, and PV(j - 2), issued after one, has read what lies in the buffer)
           const uint64_t k = k_desc + slot * (Cfg::PIECE >> 4), q = q_desc + o * (Cfg::QB >> 4);
           const uint32_t d = tm + buf * TN;
           if (leader) {
