@@ -121,6 +121,14 @@ def test_long():
     check(queries(33, 8, 8, 64), s)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+def test_many_sequences(dtype):
+    """More than a CTA lists the first rows of (rows that do not exist are computed then, and not written)."""
+    own = [1 + b % 7 for b in range(430)]
+    s = Shared(11, own, 1, 64, 16, dtype, seed=13)
+    check(queries(430, 2, 2, 64), s, [min(1 + b % 2, own[b]) for b in range(430)])
+
+
 def test_empty_prefix_and_empty_sequences():
     s = Shared(0, [5, 30, 17], 2, 128, 16)
     check(queries(3, 4, 4, 128), s, [4, 4, 1])
