@@ -45,13 +45,14 @@ struct LoraArgs {
   int T, N, K, R, L, f32;
   int rows_log2;   // of a tile: 4, 5 or 6
   int tiles;       // at most
-  int slices;      // of K
-  int column_ctas; // of a tile
+  int slices;      // of K at most
+  int sms;
   int in_place, vector;  // Y is base; rows of base and Y in 16-byte pieces
   float* part;     // [slices][tiles][rows][R]
   // of more than kPairRows rows:
   int* plan_rows;  // [tiles][rows]: row, or -1
-  int* plan_ids;   // [tiles]: adapter, L (none), or -1 (no such tile)
+  int* plan_ids;   // [tiles]: adapter, or L (none)
+  int* plan_total; // tiles that there are
   int* counts;     // [L + 1]: an adapter's rows, then its first tile
   int* place;      // [T]
 };
@@ -63,51 +64,68 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& a, int t) {
   return id < 0 || id >= a.L ? a.L : id;
 }
 
-// Rows and adapter of tile q, by all threads of a CTA; false: there is no such tile.
-// (Read from L2, as the second kernel does this before it waits for the first one.)
+// The tiles, as all threads of a CTA see them.  (Read from L2, as the second kernel does
+// this before it waits for the first one.)
 struct Tile {
   __align__(16) int ids[kPairRows];
   int rows[64];
   int leaders[kLoraWarps];
   int id, rank;
 };
-__device__ __forceinline__ bool find_tile(const LoraArgs& a, int q, Tile& s) {
-  const int t = threadIdx.x, R = 1 << a.rows_log2;
-  if (a.T > kPairRows) {
-    const int id = __ldcg(&a.plan_ids[q]);
-    if (id < 0) return false;
-    if (t == 0) s.id = id;
-    if (t < R) s.rows[t] = __ldcg(&a.plan_rows[q * R + t]);
+struct Tiles {
+  Tile& s;
+  int total;               // tiles that there are
+  int id, rank, number;    // of this thread's row: its adapter, place there, and the tile that it begins (-1: none)
+  __device__ __forceinline__ Tiles(const LoraArgs& a, Tile& shared) : s(shared) {
+    const int t = threadIdx.x, R = 1 << a.rows_log2;
+    if (a.T > kPairRows) {
+      total = __ldcg(a.plan_total);
+      return;
+    }
+    id = t < a.T ? adapter_of(a, t) : -1;
+    s.ids[t] = id;
     __syncthreads();
-    return true;
-  }
-  const int id = t < a.T ? adapter_of(a, t) : -1;
-  s.ids[t] = id;
-  if (t < R) s.rows[t] = -1;
-  if (t == 0) s.rank = -1;
-  __syncthreads();
-  int rank = 0;
+    rank = 0;
 #pragma unroll 4
-  for (int i = 0; i < a.T; i += 4) {
-    const int4 o = *reinterpret_cast<const int4*>(s.ids + i);
-    rank += (o.x == id && i < t) + (o.y == id && i + 1 < t) + (o.z == id && i + 2 < t) + (o.w == id && i + 3 < t);
+    for (int i = 0; i < a.T; i += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(s.ids + i);
+      rank += (o.x == id && i < t) + (o.y == id && i + 1 < t) + (o.z == id && i + 2 < t) + (o.w == id && i + 3 < t);
+    }
+    // the rows that tiles begin with, which number them
+    const bool leads = t < a.T && (rank & (R - 1)) == 0;
+    const unsigned who = __ballot_sync(0xffffffffu, leads);
+    if ((t & 31) == 0) s.leaders[t >> 5] = __popc(who);
+    __syncthreads();
+    int before = __popc(who & ((1u << (t & 31)) - 1));
+    total = 0;
+    for (int w = 0; w < kLoraWarps; ++w) {
+      if (w < t >> 5) before += s.leaders[w];
+      total += s.leaders[w];
+    }
+    number = leads ? before : -1;
   }
-  // the row that a tile begins with; tiles are numbered by these
-  const bool leads = t < a.T && (rank & (R - 1)) == 0;
-  const unsigned who = __ballot_sync(0xffffffffu, leads);
-  if ((t & 31) == 0) s.leaders[t >> 5] = __popc(who);
-  __syncthreads();
-  int number = __popc(who & ((1u << (t & 31)) - 1));
-  for (int w = 0; w < t >> 5; ++w) number += s.leaders[w];
-  if (leads && number == q) {
-    s.id = id;
-    s.rank = rank;
+  // Rows and adapter of tile q < total, in shared memory.
+  __device__ __forceinline__ void select(const LoraArgs& a, int q) {
+    const int t = threadIdx.x, R = 1 << a.rows_log2;
+    __syncthreads();  // (the tile before has been read)
+    if (a.T > kPairRows) {
+      if (t == 0) s.id = __ldcg(&a.plan_ids[q]);
+      if (t < R) s.rows[t] = __ldcg(&a.plan_rows[q * R + t]);
+    } else {
+      if (t < R) s.rows[t] = -1;
+      if (number == q) {
+        s.id = id;
+        s.rank = rank;
+      }
+      __syncthreads();
+      if (t < a.T && id == s.id && rank >= s.rank && rank < s.rank + R) s.rows[rank - s.rank] = t;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  if (s.rank < 0) return false;
-  if (t < a.T && id == s.id && rank >= s.rank && rank < s.rank + R) s.rows[rank - s.rank] = t;
-  __syncthreads();
-  return true;
+};
+// Slices of K that the tiles' H is computed in: about two CTAs an SM, each warp with four blocks of 32 of K or more.
+__device__ __forceinline__ int slices_of(const LoraArgs& a, int total) {
+  return max(1, min(a.slices, (2 * a.sms + total - 1) / max(total, 1)));
 }
 
 // Sorts the rows by adapter: one CTA.
@@ -120,7 +138,6 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraArgs 
   int* const counts = a.L < kPlanCounts ? s_counts : a.counts;
   for (int i = threadIdx.x; i <= a.L; i += kPlanThreads) counts[i] = 0;
   for (int i = threadIdx.x; i < a.tiles * R; i += kPlanThreads) a.plan_rows[i] = -1;
-  for (int i = threadIdx.x; i < a.tiles; i += kPlanThreads) a.plan_ids[i] = -1;
   if (threadIdx.x == 0) s_base = 0;
   __threadfence_block();
   __syncthreads();
@@ -148,6 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) lora_plan_kernel(const LoraArgs 
     if (threadIdx.x == kPlanThreads - 1) s_base = before + n;
     __syncthreads();
   }
+  if (threadIdx.x == 0) *a.plan_total = s_base;
   __threadfence_block();
   __syncthreads();
   for (int t = threadIdx.x; t < a.T; t += kPlanThreads) {
@@ -165,57 +183,62 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
   __shared__ float h[WR][16][NT * 8 + 4];
   griddep_wait();
   griddep_launch_dependents();
-  const int q = blockIdx.y, slice = blockIdx.x;
-  if (!find_tile(a, q, tile) || tile.id >= a.L) return;
+  Tiles tiles(a, tile);
+  const int slices = slices_of(a, tiles.total);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int wr = warp % WR, kw = warp / WR;
-  const int blocks = (a.K + 31) / 32, b0 = blocks * slice / a.slices, b1 = blocks * (slice + 1) / a.slices;
-  const int r0 = tile.rows[wr * 16 + g], r1 = tile.rows[wr * 16 + 8 + g];
-  const uint16_t* const x0 = a.x + (r0 < 0 ? 0 : r0) * a.x_ld + 8 * c;
-  const uint16_t* const x1 = a.x + (r1 < 0 ? 0 : r1) * a.x_ld + 8 * c;
-  const uint16_t* const w0 = a.A + (static_cast<int64_t>(tile.id) * a.R + g) * a.K + 8 * c;
+  const int wr = warp % WR, kw = warp / WR, blocks = (a.K + 31) / 32;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  float acc[NT][4] = {};
-  constexpr int U = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks whose loads are under way together
-  if (tile.rows[wr * 16] >= 0)
-    for (int b = b0 + kw; b < b1; b += KW * U) {
-      uint4 u[U], v[U], w[U][NT];
+  for (int unit = blockIdx.x; unit < tiles.total * slices; unit += gridDim.x) {
+    const int q = unit / slices, slice = unit - q * slices;
+    tiles.select(a, q);
+    if (tile.id >= a.L) continue;
+    const int b0 = blocks * slice / slices, b1 = blocks * (slice + 1) / slices;
+    const int r0 = tile.rows[wr * 16 + g], r1 = tile.rows[wr * 16 + 8 + g];
+    const uint16_t* const x0 = a.x + (r0 < 0 ? 0 : r0) * a.x_ld + 8 * c;
+    const uint16_t* const x1 = a.x + (r1 < 0 ? 0 : r1) * a.x_ld + 8 * c;
+    const uint16_t* const w0 = a.A + (static_cast<int64_t>(tile.id) * a.R + g) * a.K + 8 * c;
+    float acc[NT][4] = {};
+    constexpr int U = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks whose loads are under way together
+    if (tile.rows[wr * 16] >= 0)
+      for (int b = b0 + kw; b < b1; b += KW * U) {
+        uint4 u[U], v[U], w[U][NT];
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = (b + i * KW) * 32;
-        const bool in = b + i * KW < b1 && k + 8 * c < a.K;
-        u[i] = in && r0 >= 0 ? ld_after_wait_v4(x0 + k) : none;
-        v[i] = in && r1 >= 0 ? ld_after_wait_v4(x1 + k) : none;
+        for (int i = 0; i < U; ++i) {
+          const int k = (b + i * KW) * 32;
+          const bool in = b + i * KW < b1 && k + 8 * c < a.K;
+          u[i] = in && r0 >= 0 ? ld_after_wait_v4(x0 + k) : none;
+          v[i] = in && r1 >= 0 ? ld_after_wait_v4(x1 + k) : none;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            w[i][j] = in && j * 8 < a.R ? ld_after_wait_v4(w0 + static_cast<int64_t>(j * 8) * a.K + k) : none;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const uint32_t f0[4] = {u[i].x, v[i].x, u[i].y, v[i].y}, f1[4] = {u[i].z, v[i].z, u[i].w, v[i].w};
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            mma_bf16_16816(acc[j], f0, w[i][j].x, w[i][j].y);
+            mma_bf16_16816(acc[j], f1, w[i][j].z, w[i][j].w);
+          }
+        }
+      }
+    // in the order of the warps
+    for (int s = 0; s < KW; ++s) {
+      if (kw == s)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          w[i][j] = in && j * 8 < a.R ? ld_after_wait_v4(w0 + static_cast<int64_t>(j * 8) * a.K + k) : none;
-      }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint32_t f0[4] = {u[i].x, v[i].x, u[i].y, v[i].y}, f1[4] = {u[i].z, v[i].z, u[i].w, v[i].w};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          mma_bf16_16816(acc[j], f0, w[i][j].x, w[i][j].y);
-          mma_bf16_16816(acc[j], f1, w[i][j].z, w[i][j].w);
-        }
-      }
+          for (int e = 0; e < 4; ++e) {
+            float& to = h[wr][g + 8 * (e >> 1)][j * 8 + 2 * c + (e & 1)];
+            to = s == 0 ? acc[j][e] : to + acc[j][e];
+          }
+      __syncthreads();
     }
-  // in the order of the warps
-  for (int s = 0; s < KW; ++s) {
-    if (kw == s)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float& to = h[wr][g + 8 * (e >> 1)][j * 8 + 2 * c + (e & 1)];
-          to = s == 0 ? acc[j][e] : to + acc[j][e];
-        }
-    __syncthreads();
-  }
-  float* const out = a.part + ((static_cast<int64_t>(slice) * a.tiles + q) << ROWS_LOG2) * a.R;
-  for (int i = threadIdx.x; i < (a.R << ROWS_LOG2); i += kLoraThreads) {
-    const int r = i / a.R, k = i - r * a.R;
-    out[i] = h[r >> 4][r & 15][k];
+    float* const out = a.part + ((static_cast<int64_t>(slice) * a.tiles + q) << ROWS_LOG2) * a.R;
+    for (int i = threadIdx.x; i < (a.R << ROWS_LOG2); i += kLoraThreads) {
+      const int r = i / a.R, k = i - r * a.R;
+      out[i] = h[r >> 4][r & 15][k];
+    }
   }
 }
 
@@ -274,136 +297,142 @@ __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_
   constexpr int RAW = sizeof(T) == 4 ? 2 : 1;  // 16-byte pieces of 8 columns
   __shared__ Tile tile;
   __shared__ __align__(16) __nv_bfloat16 h[TERMS][ROWS][PITCH];
-  const int q = blockIdx.y;
-  if (!find_tile(a, q, tile)) {
-    griddep_wait();
-    griddep_launch_dependents();
-    return;
-  }
   const T* const base = static_cast<const T*>(a.base);
   T* const y = static_cast<T*>(a.y);
-  const int groups = (a.N + 31) / 32;
-  const int n0 = groups * blockIdx.x / a.column_ctas, n1 = groups * (blockIdx.x + 1) / a.column_ctas;
-  if (tile.id >= a.L) {
-    griddep_wait();
-    griddep_launch_dependents();
-    // rows without an adapter, bit for bit
-    if (a.in_place) return;
-    const int first = n0 * 32, count = min(n1 * 32, a.N) - first;
-    for (int r = 0; r < ROWS; ++r) {
-      const int t = tile.rows[r];
-      if (t < 0) break;
-      constexpr int P = 16 / sizeof(T);
-      if (a.vector) {
-        for (int i = threadIdx.x * P; i < count; i += kLoraThreads * P) {
-          const int64_t from = t * a.base_ld + first + i, to = t * a.y_ld + first + i;
-          if (i + P <= count) *reinterpret_cast<uint4*>(y + to) = ld_after_wait_v4(base + from);
-          else
-            for (int e = 0; i + e < count; ++e) y[to + e] = base[from + e];
-        }
-      } else {
-        for (int i = threadIdx.x; i < count; i += kLoraThreads) y[t * a.y_ld + first + i] = base[t * a.base_ld + first + i];
-      }
-    }
-    return;
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int wr = warp % WR, nw = warp / WR;
-  const int row[2] = {tile.rows[wr * 16 + g], tile.rows[wr * 16 + 8 + g]};
-  const uint16_t* const w0 = a.B + static_cast<int64_t>(tile.id) * a.N * a.R + 4 * STEPS * c;
-  const int valid = a.R - 4 * STEPS * c;
-  uint2 w[4][STEPS];  // a thread's ranks of the group's 32 rows of B
-  auto fetch = [&](int group) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = group * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-      load_ranks<STEPS, FULL, (WR > 1)>(w[j], w0 + static_cast<int64_t>(n) * a.R, group < n1 && n < a.N ? valid : 0);
-    }
-  };
-  const bool some = tile.rows[wr * 16] >= 0;  // of this warp's rows
-  int group = n0 + nw;
-  if (WR == 1) fetch(group);
-  griddep_wait();
-  griddep_launch_dependents();
-  if (WR > 1 && some) fetch(group);
-  // the tile's H: slices added in order, scaled, as bf16 terms
-  const float scale = a.scales != nullptr ? a.scales[tile.id] : 1.f;
-  for (int i = threadIdx.x; i < ROWS * STEPS * 4; i += kLoraThreads) {
-    const int r = i / (STEPS * 4), k = (i - r * STEPS * 4) * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (k < a.R && tile.rows[r] >= 0)
-#pragma unroll 4
-      for (int s = 0; s < a.slices; ++s) {
-        const uint4 u = ld_after_wait_v4(a.part + (((static_cast<int64_t>(s) * a.tiles + q) << ROWS_LOG2) + r) * a.R + k);
-        v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y), v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
-      }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float rest = v[e] * scale;
-#pragma unroll
-      for (int term = 0; term < TERMS; ++term) {
-        // (towards zero but for the last, so that no finite number becomes infinite)
-        const __nv_bfloat16 top = term + 1 < TERMS ? __float2bfloat16_rz(rest) : __float2bfloat16_rn(rest);
-        h[term][r][k + e] = top;
-        // (what is not finite stays in the first term: infinity less itself would be NaN in every column)
-        rest = fabsf(rest) <= 3.4028235e38f ? rest - __bfloat162float(top) : 0.f;
-      }
-    }
-  }
-  __syncthreads();
-  if (!some) return;
-#pragma unroll 1
-  for (; group < n1; group += NW) {
-    const int n = group * 32 + 8 * c;
-    const bool whole = a.vector && n + 8 <= a.N;
-    uint4 b[2][RAW];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int i = 0; i < RAW; ++i)
-        if (row[r] >= 0 && whole) b[r][i] = ld_after_wait_v4(base + row[r] * a.base_ld + n + i * 4);
-    float acc[4][4] = {};
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int term = TERMS - 1; term >= 0; --term) {
-        const int k = 4 * STEPS * c + 4 * s;
-        const uint2 lo = *reinterpret_cast<const uint2*>(&h[term][wr * 16 + g][k]);
-        const uint2 hi = *reinterpret_cast<const uint2*>(&h[term][wr * 16 + 8 + g][k]);
-        const uint32_t f[4] = {lo.x, hi.x, lo.y, hi.y};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_bf16_16816(acc[j], f, w[j][s].x, w[j][s].y);
-      }
-    fetch(group + NW);  // under way while this group is written
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (row[r] < 0) continue;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc[i >> 1][2 * r + (i & 1)];
-      T* const to = y + row[r] * a.y_ld + n;
-      if (whole) {
-        if constexpr (RAW == 2) {
-          const uint4 u = b[r][0], z = b[r][RAW - 1];
-          const uint32_t words[8] = {u.x, u.y, u.z, u.w, z.x, z.y, z.z, z.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(words[i]);
-        } else {
-          const uint32_t words[4] = {b[r][0].x, b[r][0].y, b[r][0].z, b[r][0].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] += bf16_lo(words[i]);
-            v[2 * i + 1] += bf16_hi(words[i]);
+  Tiles tiles(a, tile);
+  const int slices = slices_of(a, tiles.total);
+  // an equal, contiguous share of all tiles' groups of 32 columns
+  const int groups = (a.N + 31) / 32;
+  const int64_t units = static_cast<int64_t>(tiles.total) * groups, end = units * (blockIdx.x + 1) / gridDim.x;
+  bool waited = false;
+  for (int64_t u = units * blockIdx.x / gridDim.x; u < end;) {
+    const int q = static_cast<int>(u / groups), n0 = static_cast<int>(u - static_cast<int64_t>(q) * groups);
+    const int n1 = static_cast<int>(end - u < groups - n0 ? n0 + (end - u) : groups);
+    u += n1 - n0;
+    tiles.select(a, q);
+    if (tile.id >= a.L) {
+      if (!waited) griddep_wait();
+      waited = true;
+      // rows without an adapter, bit for bit
+      if (a.in_place) continue;
+      const int first = n0 * 32, count = min(n1 * 32, a.N) - first;
+      for (int r = 0; r < ROWS; ++r) {
+        const int t = tile.rows[r];
+        if (t < 0) break;
+        constexpr int P = 16 / sizeof(T);
+        if (a.vector) {
+          for (int i = threadIdx.x * P; i < count; i += kLoraThreads * P) {
+            const int64_t from = t * a.base_ld + first + i, to = t * a.y_ld + first + i;
+            if (i + P <= count) *reinterpret_cast<uint4*>(y + to) = ld_after_wait_v4(base + from);
+            else
+              for (int e = 0; i + e < count; ++e) y[to + e] = base[from + e];
           }
+        } else {
+          for (int i = threadIdx.x; i < count; i += kLoraThreads) y[t * a.y_ld + first + i] = base[t * a.base_ld + first + i];
         }
-        store8(to, v);
-      } else {
+      }
+      continue;
+    }
+    const int row[2] = {tile.rows[wr * 16 + g], tile.rows[wr * 16 + 8 + g]};
+    const uint16_t* const w0 = a.B + static_cast<int64_t>(tile.id) * a.N * a.R + 4 * STEPS * c;
+    const int valid = a.R - 4 * STEPS * c;
+    uint2 w[4][STEPS];  // a thread's ranks of the group's 32 rows of B
+    auto fetch = [&](int group) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < a.N) to[i] = static_cast<T>(widen(base[row[r] * a.base_ld + n + i]) + v[i]);
+      for (int j = 0; j < 4; ++j) {
+        const int n = group * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+        load_ranks<STEPS, FULL, (WR > 1)>(w[j], w0 + static_cast<int64_t>(n) * a.R, group < n1 && n < a.N ? valid : 0);
+      }
+    };
+    const bool some = tile.rows[wr * 16] >= 0;  // of this warp's rows
+    int group = n0 + nw;
+    if (WR == 1) fetch(group);
+    if (!waited) griddep_wait();
+    waited = true;
+    if (WR > 1 && some) fetch(group);
+    // the tile's H: slices added in order, scaled, as bf16 terms
+    const float scale = a.scales != nullptr ? a.scales[tile.id] : 1.f;
+    for (int i = threadIdx.x; i < ROWS * STEPS * 4; i += kLoraThreads) {
+      const int r = i / (STEPS * 4), k = (i - r * STEPS * 4) * 4;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (k < a.R && tile.rows[r] >= 0)
+#pragma unroll 4
+        for (int s = 0; s < slices; ++s) {
+          const uint4 u = ld_after_wait_v4(a.part + (((static_cast<int64_t>(s) * a.tiles + q) << ROWS_LOG2) + r) * a.R + k);
+          v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y), v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
+        }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float rest = v[e] * scale;
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          // (towards zero but for the last, so that no finite number becomes infinite)
+          const __nv_bfloat16 top = term + 1 < TERMS ? __float2bfloat16_rz(rest) : __float2bfloat16_rn(rest);
+          h[term][r][k + e] = top;
+          // (what is not finite stays in the first term: infinity less itself would be NaN in every column)
+          rest = fabsf(rest) <= 3.4028235e38f ? rest - __bfloat162float(top) : 0.f;
+        }
+      }
+    }
+    __syncthreads();
+    if (some)
+#pragma unroll 1
+    for (; group < n1; group += NW) {
+      const int n = group * 32 + 8 * c;
+      const bool whole = a.vector && n + 8 <= a.N;
+      uint4 b[2][RAW];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < RAW; ++i)
+          if (row[r] >= 0 && whole) b[r][i] = ld_after_wait_v4(base + row[r] * a.base_ld + n + i * 4);
+      float acc[4][4] = {};
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int term = TERMS - 1; term >= 0; --term) {
+          const int k = 4 * STEPS * c + 4 * s;
+          const uint2 lo = *reinterpret_cast<const uint2*>(&h[term][wr * 16 + g][k]);
+          const uint2 hi = *reinterpret_cast<const uint2*>(&h[term][wr * 16 + 8 + g][k]);
+          const uint32_t f[4] = {lo.x, hi.x, lo.y, hi.y};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_bf16_16816(acc[j], f, w[j][s].x, w[j][s].y);
+        }
+      fetch(group + NW);  // under way while this group is written
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (row[r] < 0) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[i >> 1][2 * r + (i & 1)];
+        T* const to = y + row[r] * a.y_ld + n;
+        if (whole) {
+          if constexpr (RAW == 2) {
+            const uint4 u = b[r][0], z = b[r][RAW - 1];
+            const uint32_t words[8] = {u.x, u.y, u.z, u.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(words[i]);
+          } else {
+            const uint32_t words[4] = {b[r][0].x, b[r][0].y, b[r][0].z, b[r][0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] += bf16_lo(words[i]);
+              v[2 * i + 1] += bf16_hi(words[i]);
+            }
+          }
+          store8(to, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n + i < a.N) to[i] = static_cast<T>(widen(base[row[r] * a.base_ld + n + i]) + v[i]);
+        }
       }
     }
   }
+  if (!waited) griddep_wait();
+  griddep_launch_dependents();
 }
 
 // How T rows on up to L adapters are tiled.
@@ -421,7 +450,7 @@ struct LoraPlan {
   int64_t part_floats(int R) const { return kMaxSlices * (tiles << rows_log2) * R; }
 };
 struct LoraSpace {
-  size_t part, rows, ids, counts, place, total;
+  size_t part, rows, ids, total_tiles, counts, place, total;
   LoraSpace(int T, int L, int R) {
     const LoraPlan p(T, L, R);
     size_t at = 0;
@@ -434,6 +463,7 @@ struct LoraSpace {
     const bool planned = T > kPairRows;
     rows = room(planned ? static_cast<size_t>(p.tiles << p.rows_log2) * 4 : 0);
     ids = room(planned ? static_cast<size_t>(p.tiles) * 4 : 0);
+    total_tiles = room(planned ? 4 : 0);
     counts = room(planned ? (static_cast<size_t>(L) + 1) * 4 : 0);
     place = room(planned ? static_cast<size_t>(T) * 4 : 0);
     total = at;
@@ -449,7 +479,8 @@ cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
               : nt <= 4          ? lora_shrink_kernel<4, 4>
               : nt <= 8          ? lora_shrink_kernel<8, 4>
                                  : lora_shrink_kernel<16, 4>;
-  return launch_dependent(kern, dim3(a.slices, a.tiles), kLoraThreads, 0, stream, a);
+  const int64_t units = static_cast<int64_t>(a.slices) * a.tiles;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(std::min<int64_t>(units, 2 * a.sms))), kLoraThreads, 0, stream, a);
 }
 template <class T>
 cudaError_t launch_expand(const LoraArgs& a, cudaStream_t stream) {
@@ -464,7 +495,10 @@ cudaError_t launch_expand(const LoraArgs& a, cudaStream_t stream) {
               : R < 64           ? lora_expand_kernel<T, 4, 4, false>
               : R == 128         ? lora_expand_kernel<T, 8, 4, true>
                                  : lora_expand_kernel<T, 8, 4, false>;
-  return launch_dependent(kern, dim3(a.column_ctas, a.tiles), kLoraThreads, 0, stream, a);
+  // as many CTAs as the SMs hold, each warp with 32 columns or more
+  const int64_t warps = kLoraWarps >> (a.rows_log2 - 4), units = static_cast<int64_t>(a.tiles) * ((a.N + 31) / 32);
+  const int64_t ctas = std::min<int64_t>((units + warps - 1) / warps, (a.R <= 32 ? 3 : 2) * a.sms);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kLoraThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -526,15 +560,12 @@ qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_
   a.in_place = base == Y && base_ld == y_ld;
   a.vector = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(Y)) % 16) == 0 && base_ld * es % 16 == 0 &&
              y_ld * es % 16 == 0;
-  // CTAs: about three an SM for H, each warp with four blocks of 32 of K or more; about six for Y, each warp with 32
-  // columns or more
-  const int sms = device_sm_count(), row_warps = (1 << a.rows_log2) / 16, warps = kLoraWarps / row_warps;
-  const int blocks = (K + 31) / 32, groups = (N + 31) / 32;
-  a.slices = std::max(1, std::min({kMaxSlices, blocks / (4 * warps), (3 * sms + a.tiles - 1) / a.tiles}));
-  a.column_ctas = std::max(1, std::min((groups + warps - 1) / warps, (6 * sms + a.tiles - 1) / a.tiles));
+  a.sms = device_sm_count();
+  a.slices = std::max(1, std::min(kMaxSlices, (K + 31) / 32 / (4 * (kLoraWarps >> (a.rows_log2 - 4)))));
   a.part = reinterpret_cast<float*>(ws + space.part);
   a.plan_rows = reinterpret_cast<int*>(ws + space.rows);
   a.plan_ids = reinterpret_cast<int*>(ws + space.ids);
+  a.plan_total = reinterpret_cast<int*>(ws + space.total_tiles);
   a.counts = reinterpret_cast<int*>(ws + space.counts);
   a.place = reinterpret_cast<int*>(ws + space.place);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
