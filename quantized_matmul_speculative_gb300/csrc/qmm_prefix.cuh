@@ -34,6 +34,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "qmm_cache.cuh"
 
@@ -471,7 +472,23 @@ struct PrefixRoles {
   }
 
   // --- products: one warp, whose loop is uniform (the products' descriptors are made in uniform registers) and of which
-  // one thread issues them (with all of it in that thread's branch a product took 112 cycles to issue, and 64 to do) ---
+  // one thread issues them (with all of it in that thread's branch a product took 112 cycles to issue, and 64 to do).  A
+  // job's way through this warp is on both lanes' path, so that it is kept short: slots and phases are counted, not
+  // computed, and a wait that is over costs one test. ---
+  struct Place {  // of the next key (or value) piece
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void next() {  // they take turns
+      slot += 2;
+      if (slot >= SLOTS) {
+        slot -= SLOTS;
+        phase ^= 1;
+      }
+    }
+  };
+  static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t phase, unsigned long long wait_ns) {
+    return mbar_wait(bar, phase, kStatusTimeoutFull, wait_ns);
+  }
   __device__ __forceinline__ void multiply() {
     constexpr uint32_t kType = E8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 sums
     constexpr uint32_t kS = (1u << 4) | (kType << 7) | (kType << 10) | ((TN >> 3) << 17) | ((kRows >> 4) << 24);
@@ -480,76 +497,83 @@ struct PrefixRoles {
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t q_desc = tile_desc(sbase + Cfg::OFF_Q, 16, 1024), k_desc = tile_desc(sbase, 16, 1024),
                    v_desc = tile_desc(sbase, TN * 128, 1024);
-    bool lost = false;
-    int it = 0;               // the segment's first piece
+    bool lost = false;  // after a wait that gave up nothing more is issued or waited for
+    Place key = {0, 0}, value = {1, 0};
     uint32_t p_phase = 0;     // of the buffers' next probabilities, a bit each
     uint32_t q_phase = 0;     // of the lanes' next query tiles
-    auto wait = [&](uint32_t bar, int phase) {
-      if (!lost) lost = __any_sync(0xffffffffu, !mbar_wait(bar, phase & 1, kStatusTimeoutFull, a.wait_ns));
+    auto wait = [&](uint32_t bar, uint32_t phase) {
+      if (!lost && !mbar_try_wait(bar, phase & 1, 20000u)) lost = !wait_long(bar, phase & 1, a.wait_ns);
     };
     auto commit = [&](uint32_t bar) {
-      if (leader) mma_commit_to(bar);
+      if (leader && !lost) mma_commit_to(bar);
     };
-    for (int u = begin; u < end && !lost;) {
+    // PV(i) of a segment of J jobs; jobs of buffer BUF.  In a pair both lanes use a piece, else one job.
+    auto second = [&](auto buf_of, bool pair, int i, int J) {
+      constexpr int BUF = decltype(buf_of)::value, O = LANES == 2 ? BUF : 0;
+      const bool first_use = !pair || BUF == 0, last_use = !pair || BUF == 1;
+      if (first_use) wait(full + value.slot * 8, value.phase);
+      const uint64_t v = v_desc + value.slot * (Cfg::PIECE >> 4);
+      const uint32_t p = tm + BUF * TN, d = tm + Cfg::O_COL + O * D;
+      const bool more = i >= LANES;
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half) {
+        wait(p_full + (BUF * 2 + half) * 8, p_phase >> BUF);
+        tmem_after();
+        if (leader && !lost) {
+#pragma unroll
+          for (int x = half * 4; x < half * 4 + 4; ++x) {
+            mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * (2048 >> 4), kPV, x > 0 || more);
+            if constexpr (!E8) mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * (2048 >> 4), kPV, true);
+          }
+        }
+      }
+      p_phase ^= 1u << BUF;
+      if (last_use) {
+        commit(empty + value.slot * 8);
+        value.next();
+      }
+      if (LANES == 1) commit(pv_done);
+      if (i + LANES >= J) commit(o_full + O * 8);
+    };
+    // S(j)
+    auto first = [&](auto buf_of, bool pair, int j) {
+      constexpr int BUF = decltype(buf_of)::value, O = LANES == 2 ? BUF : 0;
+      const bool first_use = !pair || BUF == 0, last_use = !pair || BUF == 1;
+      if (first_use) wait(full + key.slot * 8, key.phase);
+      if (j < LANES) {
+        wait(q_full + O * 8, q_phase >> O);
+        q_phase ^= 1u << O;
+      }
+      // (no fence: the operands are in shared memory, and PV(j - 2), issued after one, has read what lies in the buffer)
+      const uint64_t k = k_desc + key.slot * (Cfg::PIECE >> 4), q = q_desc + O * (Cfg::QB >> 4);
+      if (leader && !lost) {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+          mma_ss(tm + BUF * TN, q + (((x >> 2) * kRows * 128 + (x & 3) * 32) >> 4), k + (((x >> 2) * TN * 128 + (x & 3) * 32) >> 4),
+                 kS, x > 0);
+      }
+      if (last_use) {
+        commit(empty + key.slot * 8);
+        key.next();
+      }
+      commit(s_full + BUF * 8);
+    };
+    for (int u = begin; u < end;) {
       const PrefixSegment g(l, u, end, LANES);
+      u += g.ke - g.kb;
       const int J = g.jobs(LANES);
       const bool pair = LANES == 2 && !g.split;
       // S(j) for j < J, after PV(j - 2); then the last two
 #pragma unroll 1
-      for (int j = 0; j < J + 2 && !lost; ++j) {
-        const int buf = j & 1, o = LANES == 2 ? buf : 0;
-        {
-          const int i = j - 2;  // PV(i)
-          if (i >= 0 && i < J) {
-            const int piece = it + 2 * (pair ? i >> 1 : i) + 1, slot = piece % SLOTS;
-            if (!pair || !buf) wait(full + slot * 8, piece / SLOTS);
-            const uint64_t v = v_desc + slot * (Cfg::PIECE >> 4);
-            const uint32_t p = tm + buf * TN, d = tm + Cfg::O_COL + o * D;
-            const bool more = i >= LANES;
-#pragma unroll
-            for (int half = 0; half < HALVES; ++half) {
-              wait(p_full + (buf * 2 + half) * 8, p_phase >> buf);
-              tmem_after();
-              if (leader && !lost) {
-#pragma unroll
-                for (int x = half * 4; x < half * 4 + 4; ++x) {
-                  mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8, v + x * (2048 >> 4), kPV, x > 0 || more);
-                  if constexpr (!E8) mma_ts(d, p + (x >> 1) * 32 + (x & 1) * 8 + 16, v + x * (2048 >> 4), kPV, true);
-                }
-              }
-            }
-            p_phase ^= 1u << buf;
-            if (lost) break;
-            if (!pair || buf) commit(empty + slot * 8);
-            if (LANES == 1) commit(pv_done);
-            if (i + LANES >= J) commit(o_full + o * 8);
-          }
-        }
-        if (j < J) {
-          const int piece = it + 2 * (pair ? j >> 1 : j), slot = piece % SLOTS;
-          if (!pair || !buf) wait(full + slot * 8, piece / SLOTS);
-          if (j < LANES) {
-            wait(q_full + o * 8, q_phase >> o);
-            q_phase ^= 1u << o;
-          }
-          if (lost) break;
-          // (no fence: the operands are in shared memory, and PV(j - 2), issued after one, has read what lies in the buffer)
-          const uint64_t k = k_desc + slot * (Cfg::PIECE >> 4), q = q_desc + o * (Cfg::QB >> 4);
-          const uint32_t d = tm + buf * TN;
-          if (leader) {
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              mma_ss(d, q + (((x >> 2) * kRows * 128 + (x & 3) * 32) >> 4), k + (((x >> 2) * TN * 128 + (x & 3) * 32) >> 4), kS, x > 0);
-          }
-          if (!pair || buf) commit(empty + slot * 8);
-          commit(s_full + buf * 8);
-        }
+      for (int j = 0; j < J + 2; j += 2) {
+        if (j >= 2) second(std::integral_constant<int, 0>{}, pair, j - 2, J);
+        if (j < J) first(std::integral_constant<int, 0>{}, pair, j);
+        if (j >= 2 && j - 1 < J) second(std::integral_constant<int, 1>{}, pair, j - 1, J);
+        if (j + 1 < J) first(std::integral_constant<int, 1>{}, pair, j + 1);
       }
-      it += 2 * (g.ke - g.kb);
-      u += g.ke - g.kb;
     }
     // all products are done before the tensor memory is given back
-    commit(fin);
+    if (leader) mma_commit_to(fin);
     mbar_wait(fin, 0, kStatusTimeoutDrain, a.wait_ns);
   }
 
@@ -900,62 +924,78 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
 // Adds a row's parts and its own tokens' share, in the order of the list.  A CTA takes a
 // head and a few neighbouring rows of the B x M x G of it, a thread four of their columns.
 constexpr int kPrefixJoinThreads = 256;
-template <int D, bool E8>
+// AHEAD parts are under way at a time: 8 where the CTAs are few, 4 where many of them
+// cover for each other (32 x 1 rows, 20 parts each: 8.4 us with 8, 11.7 with 4; 64 x 8, 5
+// parts: 14.4 and 11.8).
+template <int D, bool E8, int AHEAD>
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixArgs a) {
   using Cfg = PrefixCfg<D, E8>;
   constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS;
+  // where the CTA's rows are: place among the B x M x q_heads (-1: none), their first part (that lane's), how many, row there
+  __shared__ int64_t s_at[ROWS], s_part[ROWS];
+  __shared__ int s_parts[ROWS], s_row[ROWS];
+  __shared__ bool s_real[ROWS];
   griddep_wait();
   griddep_launch_dependents();
-  const int blocks = (a.B * a.M * a.G + ROWS - 1) / ROWS;
-  const int h = blockIdx.x / blocks, x = (blockIdx.x - h * blocks) * ROWS + threadIdx.x % ROWS, col = threadIdx.x / ROWS;
-  if (x >= a.B * a.M * a.G) return;
-  const int tr = x / a.G, b = tr / a.M, i = tr - b * a.M;
-  const int64_t at = static_cast<int64_t>(tr) * a.Hq + h * a.G + x - tr * a.G;
+  if (threadIdx.x < ROWS) {
+    const int all = a.B * a.M * a.G, blocks = (all + ROWS - 1) / ROWS;
+    const int h = blockIdx.x / blocks, x = (blockIdx.x - h * blocks) * ROWS + threadIdx.x;
+    const int tr = x / a.G, b = tr / a.M, i = tr - b * a.M;
+    s_at[threadIdx.x] = x < all ? static_cast<int64_t>(tr) * a.Hq + h * a.G + x - tr * a.G : -1;
+    s_parts[threadIdx.x] = 0;
+    const bool real = x < all && i < rows_of(a, b);
+    s_real[threadIdx.x] = real;
+    if (real && a.tokens > 0) {
+      const PrefixList l = PrefixList::make<Cfg>(a, a.starts[a.B]);
+      const int r = (a.starts[b] + i) * a.G + x - tr * a.G;
+      const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair, u0 = s * l.tiles_n;
+      const int first = l.holder(u0);
+      const bool split = Cfg::LANES == 2 && 2 * pair + 1 >= l.tiles;
+      s_part[threadIdx.x] = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
+      s_parts[threadIdx.x] = l.holder(u0 + l.tiles_n - 1) - first + 1;
+      s_row[threadIdx.x] = r - tile * kRows;
+    }
+  }
+  __syncthreads();
+  const int mine = threadIdx.x % ROWS, col = threadIdx.x / ROWS;
+  const int64_t at = s_at[mine];
+  if (at < 0) return;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float lse = -INFINITY;
-  // (the own tokens' share is on its way beside what says whether there is a row)
-  const float own_lse = a.own_lse[at];
-  const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
-  if (i < rows_of(a, b)) {
-    // running maximum, sum and output over the row's parts, four under way at a time
+  if (s_real[mine]) {
+    // running maximum, sum and output over the row's parts, some under way at a time
+    const float own_lse = a.own_lse[at];
+    const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
     float top = own_lse * 1.4426950408889634f, sum = own_lse == -INFINITY ? 0.f : 1.f;
     float4 acc = sum != 0.f ? own : o;
-    if (a.tokens > 0) {
-      const PrefixList l = PrefixList::make<Cfg>(a, a.starts[a.B]);
-      int r = (a.starts[b] + i) * a.G + x - tr * a.G;
-      const int tile = r / kRows, pair = tile / Cfg::LANES, s = h * l.pairs + pair, u0 = s * l.tiles_n;
-      r -= tile * kRows;
-      const int first = l.holder(u0), parts = l.holder(u0 + l.tiles_n - 1) - first + 1;
-      const bool split = Cfg::LANES == 2 && 2 * pair + 1 >= l.tiles;
-      const int64_t p0 = (static_cast<int64_t>(s) + first) * Cfg::LANES + (Cfg::LANES == 2 && !split ? tile & 1 : 0);
-      for (int p = 0; p < parts; p += 4) {
-        float2 ml[4];
-        float4 v[4];
+    const int parts = s_parts[mine], r = s_row[mine];
+    const int64_t p0 = s_part[mine];
+    for (int p = 0; p < parts; p += AHEAD) {
+      float2 ml[AHEAD];
+      float4 v[AHEAD];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
-          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (p + k < parts) {
-            const int64_t at_part = p0 + (p + k) * Cfg::LANES;
-            ml[k] = a.part_ml[at_part * kRows + r];
-            v[k] = a.part_o[(at_part * COLS + col) * kRows + r];
-          }
+      for (int k = 0; k < AHEAD; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p + k < parts) {
+          const int64_t at_part = p0 + (p + k) * Cfg::LANES;
+          ml[k] = a.part_ml[at_part * kRows + r];
+          v[k] = a.part_o[(at_part * COLS + col) * kRows + r];
         }
-        float t = top;
+      }
+      float t = top;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t = fmaxf(t, ml[k].x);
-        const float ref = t == -INFINITY ? 0.f : t, f = exp2_of(top - ref);
-        top = t;
-        sum *= f;
-        acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+      for (int k = 0; k < AHEAD; ++k) t = fmaxf(t, ml[k].x);
+      const float ref = t == -INFINITY ? 0.f : t, f = exp2_of(top - ref);
+      top = t;
+      sum *= f;
+      acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (p + k >= parts) break;
-          const float g = exp2_of(ml[k].x - ref);
-          sum += g * ml[k].y;
-          const float gv = g * a.v_scale;  // (what the own tokens' outputs have been scaled by already)
-          acc.x += gv * v[k].x, acc.y += gv * v[k].y, acc.z += gv * v[k].z, acc.w += gv * v[k].w;
-        }
+      for (int k = 0; k < AHEAD; ++k) {
+        if (p + k >= parts) break;
+        const float g = exp2_of(ml[k].x - ref), gv = g * a.v_scale;  // (what the own tokens' outputs have been scaled by already)
+        sum += g * ml[k].y;
+        acc.x += gv * v[k].x, acc.y += gv * v[k].y, acc.z += gv * v[k].z, acc.w += gv * v[k].w;
       }
     }
     if (sum != 0.f) {

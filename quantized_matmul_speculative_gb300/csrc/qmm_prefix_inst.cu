@@ -38,8 +38,10 @@ template <int D>
 cudaError_t launch_prefix_join(const PrefixArgs& a, bool e8, cudaStream_t stream) {
   constexpr int ROWS = kPrefixJoinThreads / (D / 4);
   const int64_t ctas = a.c.heads * ((static_cast<int64_t>(a.B) * a.M * a.G + ROWS - 1) / ROWS);
-  return launch_dependent(e8 ? prefix_join_kernel<D, true> : prefix_join_kernel<D, false>, dim3(static_cast<unsigned>(ctas)),
-                          kPrefixJoinThreads, 0, stream, a);
+  const bool few = ctas <= 4 * device_sm_count();
+  auto kern = e8 ? (few ? prefix_join_kernel<D, true, 8> : prefix_join_kernel<D, true, 4>)
+                 : (few ? prefix_join_kernel<D, false, 8> : prefix_join_kernel<D, false, 4>);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kPrefixJoinThreads, 0, stream, a);
 }
 
 template <int D>
