@@ -111,14 +111,15 @@ qmm_status qmm_shared_prefix_attention(const qmm_paged_cache* cache, const int32
   a.inject = injected_short_wait();
   a.wait_ns = a.inject ? 100000ull : kWaitLimitNs;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // (the own tokens first: they have limits of their own, beyond which nothing is launched)
+  const qmm_status own = run_attention(cache, q, q_ld, B, M, q_heads, q_lens, scale, 0, 0, nullptr, own_o, own_lse, a.tokens,
+                                       ws + space.attention, workspace_bytes - space.attention, st);
+  if (own != QMM_OK) return own;
   if (a.tokens > 0) {
     const auto launch = D == 64 ? launch_prefix<64> : D == 128 ? launch_prefix<128> : launch_prefix<256>;
     const cudaError_t e = launch(a, e8, st);
     if (e != cudaSuccess) return static_cast<qmm_status>(finish_call(e));
   }
-  const qmm_status own = run_attention(cache, q, q_ld, B, M, q_heads, q_lens, scale, 0, 0, nullptr, own_o, own_lse, a.tokens,
-                                       ws + space.attention, workspace_bytes - space.attention, st);
-  if (own != QMM_OK) return own;
   const auto join = D == 64 ? launch_prefix_join<64> : D == 128 ? launch_prefix_join<128> : launch_prefix_join<256>;
   return static_cast<qmm_status>(finish_call(join(a, e8, st)));
 }

@@ -395,7 +395,7 @@ extern "C" qmm_status qmm_route_experts(const void* logits, int logits_dtype, in
                                         int scoring, int groups, int top_groups, int group_best, int renormalize, float scale,
                                         int32_t* experts, float* weights, void* stream) {
   using namespace qmm;
-  if (T < 0 || E < 1 || E > 512 || k < 1 || k > 32 || ld < E || groups < 1 || groups > 32 || E % groups != 0 ||
+  if (T < 0 || T > 0x7fff0000 || E < 1 || E > 512 || k < 1 || k > 32 || ld < E || groups < 1 || groups > 32 || E % groups != 0 ||
       top_groups < 1 || top_groups > groups || k > top_groups * (E / groups))
     return QMM_ERR_SHAPE;
   if ((logits_dtype != QMM_OUT_BF16 && logits_dtype != QMM_OUT_F32) || (scoring != QMM_SOFTMAX && scoring != QMM_SIGMOID) ||

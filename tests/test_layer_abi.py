@@ -11,7 +11,7 @@ from test_ops_abi import ALIGN, CACHES, NULL, OK, SHAPE, UNSUPPORTED, P, cache, 
 def test_route(lib):  # noqa: F811
     good = dict(logits=P, dtype=0, ld=64, bias=None, T=4, E=64, k=8, scoring=0, groups=8, top_groups=4, group_best=2,
                 renormalize=1, scale=1.0, experts=P, weights=P, stream=None)
-    for changes, rc in (({"T": -1}, SHAPE), ({"E": 0}, SHAPE), ({"E": 520, "ld": 520}, SHAPE), ({"k": 0}, SHAPE), ({"k": 33}, SHAPE),
+    for changes, rc in (({"T": -1}, SHAPE), ({"T": 2**31 - 1}, SHAPE), ({"E": 0}, SHAPE), ({"E": 520, "ld": 520}, SHAPE), ({"k": 0}, SHAPE), ({"k": 33}, SHAPE),
                         ({"ld": 63}, SHAPE), ({"groups": 0}, SHAPE), ({"groups": 7}, SHAPE), ({"groups": 64}, SHAPE),
                         ({"top_groups": 0}, SHAPE), ({"top_groups": 9}, SHAPE), ({"k": 9, "top_groups": 1}, SHAPE),
                         ({"dtype": 2}, UNSUPPORTED), ({"scoring": 2}, UNSUPPORTED), ({"group_best": 0}, UNSUPPORTED),
