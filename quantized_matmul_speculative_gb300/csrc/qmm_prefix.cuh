@@ -597,7 +597,7 @@ struct PrefixRoles {
       // fp16, scaled by a power of two so that the row's largest element lies in [2^14, 2^15); 0, tiny and infinite rows stay
       float top = 0.f;
       if (src != nullptr)
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
           const uint4 x = ld_after_wait_v4(src + c * 8);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -608,7 +608,7 @@ struct PrefixRoles {
       f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
       scale = fmaxf(scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 1e-30f);
     }
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < D / 8; ++c) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (src != nullptr) {
