@@ -28,6 +28,7 @@ namespace qmm {
 namespace {
 
 constexpr int kRouteWarps = 4;
+constexpr float kMasked = -1.2676506e30f;  // -2^100
 constexpr float kGapSigmoid = 1.f / (1 << 20), kGapSoftmax = 1.f / (1 << 18);
 
 struct RouteArgs {
@@ -297,12 +298,12 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
     const float hi = value_of(last), lo = value_of(left);
     if (biased || by_sum) apart = hi - lo > 2.f * gap * (1.f + fabsf(hi)) || (hi == lo && hi == -INFINITY);
   }
-  // the scale: 2 .. 2^23 - 2; 1 for -inf
+  // the scale: 2 .. 2^23 - 2 from the least that is not masked by a very large negative number; 1 for -inf
   float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     hi = fmaxf(hi, x[i]);
-    if (x[i] != -INFINITY) lo = fminf(lo, x[i]);
+    if (x[i] > kMasked) lo = fminf(lo, x[i]);
   }
   hi = warp_max(hi);
   lo = -warp_max(-lo);
@@ -314,7 +315,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const uint32_t step = x[i] == -INFINITY ? 1u : 2u + static_cast<uint32_t>((x[i] - lo) * unit);
+    const uint32_t step = x[i] == -INFINITY ? 1u : 2u + __float2uint_rz((x[i] - lo) * unit);  // (2 below lo)
     key[i] = open && i < l.mine ? step << 9 | (511u - (l.first + i)) : 0u;
   }
   sort_down(key);

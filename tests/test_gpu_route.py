@@ -218,3 +218,17 @@ def test_feeds_the_gathered_product():
             bound = 1e-3 * (x[t].float().abs().sum() * 0.02 * 8)  # both within 1e-3 of sum |x w|
             assert ((y[t * k + j] - one[0]).abs() <= bound).all()
     assert binding.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_masked_by_the_lowest_value(scoring, dtype):
+    """Experts masked by the type's lowest value are off the scale of the others, which keep their order."""
+    x = logits(48, 96, dtype, 17)
+    x[::2, ::2] = torch.finfo(dtype).min
+    x[1::4, 5:] = torch.finfo(dtype).min  # fewer than k left: the lowest numbers of the masked
+    x[3] = -math.inf
+    x[3, 4] = torch.finfo(dtype).min
+    for b in (None, torch.linspace(-0.4, 0.4, 96, device="cuda")):
+        check(x, 8, scoring, b)
+        check(x, 8, scoring, b, groups=8, top_groups=3, group_best=1, renormalize=False)
