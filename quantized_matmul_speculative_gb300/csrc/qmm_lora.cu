@@ -20,6 +20,7 @@
 // What bounds it: HBM for many adapters, two launches and their loads' latency for few rows.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/qmm.h"
 #include "qmm_device.cuh"
@@ -31,6 +32,7 @@ namespace {
 constexpr int kLoraThreads = 256, kLoraWarps = kLoraThreads / 32;
 constexpr int kMaxRank = 128;
 constexpr int kPairRows = kLoraThreads;  // rows up to which all pairs are compared
+constexpr int kTurnPitch = 36;           // floats, of 32 columns
 constexpr int kMaxSlices = 8;            // of K, over CTAs
 constexpr int kPlanThreads = 1024, kPlanCounts = 4096;
 
@@ -47,7 +49,7 @@ struct LoraArgs {
   int tiles;       // at most
   int slices;      // of K at most
   int sms;
-  int in_place, vector;  // Y is base; rows of base and Y in 16-byte pieces
+  int in_place;    // Y is base
   float* part;     // [slices][tiles][rows][R]
   // of more than kPairRows rows:
   int* plan_rows;  // [tiles][rows]: row, or -1
@@ -242,11 +244,18 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
   }
 }
 
-template <class T>
-__device__ __forceinline__ float widen(T v) {
-  if constexpr (sizeof(T) == 4) return v;
-  else return __bfloat162float(v);
+// A piece of base.
+__device__ __forceinline__ void load_piece(uint4& v, const void* p) { v = ld_after_wait_v4(p); }
+__device__ __forceinline__ void load_piece(float& v, const float* p) {
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
 }
+__device__ __forceinline__ void load_piece(__nv_bfloat16& v, const __nv_bfloat16* p) {
+  uint16_t u;
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(u) : "l"(p) : "memory");
+  v = __ushort_as_bfloat16(u);
+}
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void store8(float* to, const float (&v)[8]) {
   reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -288,15 +297,42 @@ __device__ __forceinline__ void load_ranks(uint2 (&w)[STEPS], const uint16_t* p,
   }
 }
 
+// `count` columns from `first` on of rows without an adapter, bit for bit, four rows under way at a time.
+template <class T, int ROWS, bool VEC>
+__device__ __forceinline__ void copy_rows(const LoraArgs& a, const int* rows, int first, int count) {
+  constexpr int P = VEC ? 16 / sizeof(T) : 1;
+  using Piece = std::conditional_t<VEC, uint4, T>;
+  const T* const base = static_cast<const T*>(a.base) + first;
+  T* const y = static_cast<T*>(a.y) + first;
+#pragma unroll 1
+  for (int r = 0; r < ROWS && rows[r] >= 0; r += 4) {
+#pragma unroll 1
+    for (int i = threadIdx.x * P; i < count; i += kLoraThreads * P) {
+      Piece u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (rows[r + k] >= 0) load_piece(u[k], base + rows[r + k] * a.base_ld + i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (rows[r + k] >= 0) *reinterpret_cast<Piece*>(y + rows[r + k] * a.y_ld + i) = u[k];
+    }
+  }
+}
+
 // Y of a tile's share of columns, 32 at a time a warp (its 16 rows).  STEPS k16 steps of
-// ranks, FULL if R is 16 STEPS; thread c of four holds ranks 4 STEPS c on.
-template <class T, int STEPS, int ROWS_LOG2, bool FULL>
+// ranks, FULL if R is 16 STEPS; thread c of four holds ranks 4 STEPS c on.  VEC: the rows of
+// base and Y are pieces of 16 bytes, and a thread adds 8 neighbouring columns of two rows;
+// else the products are turned in shared memory and a thread adds a column of 16 rows, so
+// that a warp's 32 elements of a row are neighbours (784 rows of 9919 columns: 42 us with
+// the elements of VEC's order one by one).
+template <class T, int STEPS, int ROWS_LOG2, bool FULL, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_kernel(const LoraArgs a) {
   constexpr int ROWS = 1 << ROWS_LOG2, WR = ROWS / 16, NW = kLoraWarps / WR, TERMS = sizeof(T) == 4 ? 3 : 2;
   constexpr int PITCH = STEPS * 16 + 8;  // (an odd number of 16 bytes: the eight rows of a load in different banks)
   constexpr int RAW = sizeof(T) == 4 ? 2 : 1;  // 16-byte pieces of 8 columns
   __shared__ Tile tile;
   __shared__ __align__(16) __nv_bfloat16 h[TERMS][ROWS][PITCH];
+  __shared__ __align__(16) float turned[VEC ? 1 : kLoraWarps][16][kTurnPitch];
   const T* const base = static_cast<const T*>(a.base);
   T* const y = static_cast<T*>(a.y);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -315,24 +351,7 @@ __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_
     if (tile.id >= a.L) {
       if (!waited) griddep_wait();
       waited = true;
-      // rows without an adapter, bit for bit
-      if (a.in_place) continue;
-      const int first = n0 * 32, count = min(n1 * 32, a.N) - first;
-      for (int r = 0; r < ROWS; ++r) {
-        const int t = tile.rows[r];
-        if (t < 0) break;
-        constexpr int P = 16 / sizeof(T);
-        if (a.vector) {
-          for (int i = threadIdx.x * P; i < count; i += kLoraThreads * P) {
-            const int64_t from = t * a.base_ld + first + i, to = t * a.y_ld + first + i;
-            if (i + P <= count) *reinterpret_cast<uint4*>(y + to) = ld_after_wait_v4(base + from);
-            else
-              for (int e = 0; i + e < count; ++e) y[to + e] = base[from + e];
-          }
-        } else {
-          for (int i = threadIdx.x; i < count; i += kLoraThreads) y[t * a.y_ld + first + i] = base[t * a.base_ld + first + i];
-        }
-      }
+      if (!a.in_place) copy_rows<T, ROWS, VEC>(a, tile.rows, n0 * 32, min(n1 * 32, a.N) - n0 * 32);
       continue;
     }
     const int row[2] = {tile.rows[wr * 16 + g], tile.rows[wr * 16 + 8 + g]};
@@ -381,13 +400,12 @@ __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_
 #pragma unroll 1
     for (; group < n1; group += NW) {
       const int n = group * 32 + 8 * c;
-      const bool whole = a.vector && n + 8 <= a.N;
       uint4 b[2][RAW];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int i = 0; i < RAW; ++i)
-          if (row[r] >= 0 && whole) b[r][i] = ld_after_wait_v4(base + row[r] * a.base_ld + n + i * 4);
+          if (VEC && row[r] >= 0 && n < a.N) b[r][i] = ld_after_wait_v4(base + row[r] * a.base_ld + n + i * 4);
       float acc[4][4] = {};
 #pragma unroll
       for (int s = 0; s < STEPS; ++s)
@@ -401,14 +419,13 @@ __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_
           for (int j = 0; j < 4; ++j) mma_bf16_16816(acc[j], f, w[j][s].x, w[j][s].y);
         }
       fetch(group + NW);  // under way while this group is written
+      if constexpr (VEC) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (row[r] < 0) continue;
-        float v[8];
+        for (int r = 0; r < 2; ++r) {
+          if (row[r] < 0 || n >= a.N) continue;
+          float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[i >> 1][2 * r + (i & 1)];
-        T* const to = y + row[r] * a.y_ld + n;
-        if (whole) {
+          for (int i = 0; i < 8; ++i) v[i] = acc[i >> 1][2 * r + (i & 1)];
           if constexpr (RAW == 2) {
             const uint4 u = b[r][0], z = b[r][RAW - 1];
             const uint32_t words[8] = {u.x, u.y, u.z, u.w, z.x, z.y, z.z, z.w};
@@ -422,12 +439,30 @@ __global__ void __launch_bounds__(kLoraThreads, STEPS <= 2 ? 3 : 2) lora_expand_
               v[2 * i + 1] += bf16_hi(words[i]);
             }
           }
-          store8(to, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n + i < a.N) to[i] = static_cast<T>(widen(base[row[r] * a.base_ld + n + i]) + v[i]);
+          store8(y + row[r] * a.y_ld + n, v);
         }
+      } else {
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4*>(&turned[warp][g + 8 * r][8 * c + i]) =
+                make_float4(acc[i >> 1][2 * r], acc[i >> 1][2 * r + 1], acc[(i >> 1) + 1][2 * r], acc[(i >> 1) + 1][2 * r + 1]);
+        __syncwarp();
+        const int column = group * 32 + lane;
+        const int* const rows = tile.rows + wr * 16;
+        if (column < a.N)
+#pragma unroll 1
+          for (int i = 0; i < 16; i += 8) {
+            T v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (rows[i + k] >= 0) load_piece(v[k], base + rows[i + k] * a.base_ld + column);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (rows[i + k] >= 0) y[rows[i + k] * a.y_ld + column] = static_cast<T>(widen(v[k]) + turned[warp][i + k][lane]);
+          }
       }
     }
   }
@@ -482,22 +517,22 @@ cudaError_t launch_shrink(const LoraArgs& a, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(a.slices) * a.tiles;
   return launch_dependent(kern, dim3(static_cast<unsigned>(std::min<int64_t>(units, 2 * a.sms))), kLoraThreads, 0, stream, a);
 }
-template <class T>
+template <class T, bool VEC>
 cudaError_t launch_expand(const LoraArgs& a, cudaStream_t stream) {
   const int R = a.R;
-  auto kern = a.rows_log2 == 6   ? (R == 32 ? lora_expand_kernel<T, 2, 6, true> : lora_expand_kernel<T, 4, 6, true>)
-              : a.rows_log2 == 5 ? lora_expand_kernel<T, 8, 5, true>
-              : R == 16          ? lora_expand_kernel<T, 1, 4, true>
-              : R < 16           ? lora_expand_kernel<T, 1, 4, false>
-              : R == 32          ? lora_expand_kernel<T, 2, 4, true>
-              : R < 32           ? lora_expand_kernel<T, 2, 4, false>
-              : R == 64          ? lora_expand_kernel<T, 4, 4, true>
-              : R < 64           ? lora_expand_kernel<T, 4, 4, false>
-              : R == 128         ? lora_expand_kernel<T, 8, 4, true>
-                                 : lora_expand_kernel<T, 8, 4, false>;
-  // as many CTAs as the SMs hold, each warp with 32 columns or more
-  const int64_t warps = kLoraWarps >> (a.rows_log2 - 4), units = static_cast<int64_t>(a.tiles) * ((a.N + 31) / 32);
-  const int64_t ctas = std::min<int64_t>((units + warps - 1) / warps, (a.R <= 32 ? 3 : 2) * a.sms);
+  auto kern = a.rows_log2 == 6   ? (R == 32 ? lora_expand_kernel<T, 2, 6, true, VEC> : lora_expand_kernel<T, 4, 6, true, VEC>)
+              : a.rows_log2 == 5 ? lora_expand_kernel<T, 8, 5, true, VEC>
+              : R == 16          ? lora_expand_kernel<T, 1, 4, true, VEC>
+              : R < 16           ? lora_expand_kernel<T, 1, 4, false, VEC>
+              : R == 32          ? lora_expand_kernel<T, 2, 4, true, VEC>
+              : R < 32           ? lora_expand_kernel<T, 2, 4, false, VEC>
+              : R == 64          ? lora_expand_kernel<T, 4, 4, true, VEC>
+              : R < 64           ? lora_expand_kernel<T, 4, 4, false, VEC>
+              : R == 128         ? lora_expand_kernel<T, 8, 4, true, VEC>
+                                 : lora_expand_kernel<T, 8, 4, false, VEC>;
+  // as many CTAs as the SMs hold, each warp with 32 columns or more, but tiles apart (8 tiles of 21 columns: 15.7 us in one CTA)
+  const int64_t warps = kLoraWarps >> (a.rows_log2 - 4), groups = (a.N + 31) / 32;
+  const int64_t ctas = std::min<int64_t>(a.tiles * ((groups + warps - 1) / warps), (a.R <= 32 ? 3 : 2) * a.sms);
   return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kLoraThreads, 0, stream, a);
 }
 
@@ -558,8 +593,8 @@ qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_
   a.rows_log2 = plan.rows_log2;
   a.tiles = static_cast<int>(plan.tiles);
   a.in_place = base == Y && base_ld == y_ld;
-  a.vector = ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(Y)) % 16) == 0 && base_ld * es % 16 == 0 &&
-             y_ld * es % 16 == 0;
+  const bool vector = N % 8 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(Y)) % 16) == 0 &&
+                      base_ld * es % 16 == 0 && y_ld * es % 16 == 0;
   a.sms = device_sm_count();
   a.slices = std::max(1, std::min(kMaxSlices, (K + 31) / 32 / (4 * (kLoraWarps >> (a.rows_log2 - 4)))));
   a.part = reinterpret_cast<float*>(ws + space.part);
@@ -572,7 +607,9 @@ qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_
   cudaError_t e = cudaSuccess;
   if (T > kPairRows) e = launch_dependent(lora_plan_kernel, dim3(1), kPlanThreads, 0, st, a);
   if (e == cudaSuccess) e = launch_shrink(a, st);
-  if (e == cudaSuccess) e = a.f32 ? launch_expand<float>(a, st) : launch_expand<__nv_bfloat16>(a, st);
+  if (e == cudaSuccess)
+    e = a.f32 ? (vector ? launch_expand<float, true>(a, st) : launch_expand<float, false>(a, st))
+              : (vector ? launch_expand<__nv_bfloat16, true>(a, st) : launch_expand<__nv_bfloat16, false>(a, st));
   return static_cast<qmm_status>(finish_call(e));
 }
 
