@@ -924,17 +924,18 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
 // Adds a row's parts and its own tokens' share, in the order of the list.  A CTA takes a
 // head and a few neighbouring rows of the B x M x G of it, a thread four of their columns.
 constexpr int kPrefixJoinThreads = 256;
-// AHEAD parts are under way at a time: 8 where the CTAs are few, 4 where many of them
-// cover for each other (32 x 1 rows, 20 parts each: 8.4 us with 8, 11.7 with 4; 64 x 8, 5
-// parts: 14.4 and 11.8).
-template <int D, bool E8, int AHEAD>
+// Where the CTAs are few, SPLIT threads have eight parts each under way and are then added
+// in order; where many CTAs cover for each other, one thread has four.
+template <int D, bool E8, int SPLIT>
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixArgs a) {
   using Cfg = PrefixCfg<D, E8>;
-  constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS;
+  constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS / SPLIT, AHEAD = SPLIT > 1 ? 8 : 4;
   // where the CTA's rows are: place among the B x M x q_heads (-1: none), their first part (that lane's), how many, row there
   __shared__ int64_t s_at[ROWS], s_part[ROWS];
   __shared__ int s_parts[ROWS], s_row[ROWS];
   __shared__ bool s_real[ROWS];
+  __shared__ float4 s_acc[SPLIT][SPLIT > 1 ? ROWS * COLS : 1];
+  __shared__ float2 s_sum[SPLIT][SPLIT > 1 ? ROWS * COLS : 1];
   griddep_wait();
   griddep_launch_dependents();
   if (threadIdx.x < ROWS) {
@@ -957,20 +958,24 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
     }
   }
   __syncthreads();
-  const int mine = threadIdx.x % ROWS, col = threadIdx.x / ROWS;
+  const int place = threadIdx.x % (ROWS * COLS), turn = threadIdx.x / (ROWS * COLS);
+  const int mine = place % ROWS, col = place / ROWS;
   const int64_t at = s_at[mine];
-  if (at < 0) return;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lse = -INFINITY;
-  if (s_real[mine]) {
-    // running maximum, sum and output over the row's parts, some under way at a time
-    const float own_lse = a.own_lse[at];
-    const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
-    float top = own_lse * 1.4426950408889634f, sum = own_lse == -INFINITY ? 0.f : 1.f;
-    float4 acc = sum != 0.f ? own : o;
+  const bool real = at >= 0 && s_real[mine];
+  // running maximum, sum and output over the row's parts, some under way at a time
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float top = -INFINITY, sum = 0.f;
+  if (real) {
+    if (turn == 0) {
+      const float own_lse = a.own_lse[at];
+      const float4 own = reinterpret_cast<const float4*>(a.own_o)[at * COLS + col];
+      top = own_lse * 1.4426950408889634f;
+      sum = own_lse == -INFINITY ? 0.f : 1.f;
+      if (sum != 0.f) acc = own;
+    }
     const int parts = s_parts[mine], r = s_row[mine];
     const int64_t p0 = s_part[mine];
-    for (int p = 0; p < parts; p += AHEAD) {
+    for (int p = turn * AHEAD; p < parts; p += SPLIT * AHEAD) {
       float2 ml[AHEAD];
       float4 v[AHEAD];
 #pragma unroll
@@ -998,11 +1003,37 @@ __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const P
         acc.x += gv * v[k].x, acc.y += gv * v[k].y, acc.z += gv * v[k].z, acc.w += gv * v[k].w;
       }
     }
-    if (sum != 0.f) {
-      const float f = 1.f / sum;
-      o = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-      lse = (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  if constexpr (SPLIT > 1) {
+    s_acc[turn][place] = acc;
+    s_sum[turn][place] = make_float2(top, sum);
+    __syncthreads();
+    if (turn != 0) return;
+    float2 ml[SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) {
+      ml[k] = s_sum[k][place];
+      top = fmaxf(top, ml[k].x);
     }
+    const float ref = top == -INFINITY ? 0.f : top;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) {
+      const float g = exp2_of(ml[k].x - ref);
+      const float4 v = s_acc[k][place];
+      if (ml[k].y == 0.f) continue;
+      sum += g * ml[k].y;
+      acc.x += g * v.x, acc.y += g * v.y, acc.z += g * v.z, acc.w += g * v.w;
+    }
+  }
+  if (at < 0) return;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float lse = -INFINITY;
+  if (sum != 0.f) {
+    const float f = 1.f / sum;
+    o = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    lse = (top + log2f(sum)) * 0.6931471805599453f;
   }
   *reinterpret_cast<uint2*>(a.out + at * D + col * 4) = make_uint2(bf16x2_of(o.x, o.y), bf16x2_of(o.z, o.w));
   if (col == 0 && a.lse != nullptr) a.lse[at] = lse;
