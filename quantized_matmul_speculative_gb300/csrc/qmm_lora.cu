@@ -125,9 +125,12 @@ struct Tiles {
     __syncthreads();
   }
 };
-// Slices of K that the tiles' H is computed in: about two CTAs an SM, each warp with four blocks of 32 of K or more.
+// Blocks of 32 of K whose loads a warp has under way together, for so many n8 tiles of ranks.
+__host__ __device__ constexpr int blocks_together(int nt) { return nt <= 2 ? 4 : nt <= 4 ? 2 : 1; }
+// Slices of K that the tiles' H is computed in: up to two CTAs an SM at once (more of them than there is room for: 54.2
+// us for 64 x 4 rows of rank 64 on 34816 x 5120, and 51.3), each warp with that many blocks or more.
 __device__ __forceinline__ int slices_of(const LoraArgs& a, int total) {
-  return max(1, min(a.slices, (2 * a.sms + total - 1) / max(total, 1)));
+  return max(1, min(a.slices, 2 * a.sms / max(total, 1)));
 }
 
 // Sorts the rows by adapter: one CTA.
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
     const uint16_t* const x1 = a.x + (r1 < 0 ? 0 : r1) * a.x_ld + 8 * c;
     const uint16_t* const w0 = a.A + (static_cast<int64_t>(tile.id) * a.R + g) * a.K + 8 * c;
     float acc[NT][4] = {};
-    constexpr int U = NT <= 2 ? 4 : NT <= 4 ? 2 : 1;  // blocks whose loads are under way together
+    constexpr int U = blocks_together(NT);
     if (tile.rows[wr * 16] >= 0)
       for (int b = b0 + kw; b < b1; b += KW * U) {
         uint4 u[U], v[U], w[U][NT];
@@ -596,7 +599,7 @@ qmm_status qmm_lora_add(const void* base, int64_t base_ld, const void* X, int64_
   const bool vector = N % 8 == 0 && ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(Y)) % 16) == 0 &&
                       base_ld * es % 16 == 0 && y_ld * es % 16 == 0;
   a.sms = device_sm_count();
-  a.slices = std::max(1, std::min(kMaxSlices, (K + 31) / 32 / (4 * (kLoraWarps >> (a.rows_log2 - 4)))));
+  a.slices = std::max(1, std::min(kMaxSlices, (K + 31) / 32 / (blocks_together(R / 8) * (kLoraWarps >> (a.rows_log2 - 4)))));
   a.part = reinterpret_cast<float*>(ws + space.part);
   a.plan_rows = reinterpret_cast<int*>(ws + space.rows);
   a.plan_ids = reinterpret_cast<int*>(ws + space.ids);
