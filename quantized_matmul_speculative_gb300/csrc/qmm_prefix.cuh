@@ -924,12 +924,15 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
 // Adds a row's parts and its own tokens' share, in the order of the list.  A CTA takes a
 // head and a few neighbouring rows of the B x M x G of it, a thread four of their columns.
 constexpr int kPrefixJoinThreads = 256;
-// Where the CTAs are few, SPLIT threads have eight parts each under way and are then added
-// in order; where many CTAs cover for each other, one thread has four.
-template <int D, bool E8, int SPLIT>
+// AHEAD parts are under way at a time: 4 where many CTAs cover for each other, 8 where the
+// CTAs are few (64 x 8 rows, 5 parts: 11.8 us with 4, 14.4 with 8; 32 x 1 rows, 20 parts:
+// 11.7 and 8.4).  Where they are fewer than the SMs, SPLIT threads share a row's parts, which
+// are then added in order (32 x 1: 6.5 us, 2 x 16 of 5 heads, 76 parts: 8 us, and 13.2
+// without; but 9 x 16 of 7 heads, a part each: 8.8 and 5.2).
+template <int D, bool E8, int SPLIT, int AHEAD>
 __global__ void __launch_bounds__(kPrefixJoinThreads) prefix_join_kernel(const PrefixArgs a) {
   using Cfg = PrefixCfg<D, E8>;
-  constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS / SPLIT, AHEAD = SPLIT > 1 ? 8 : 4;
+  constexpr int COLS = D / 4, ROWS = kPrefixJoinThreads / COLS / SPLIT;
   // where the CTA's rows are: place among the B x M x q_heads (-1: none), their first part (that lane's), how many, row there
   __shared__ int64_t s_at[ROWS], s_part[ROWS];
   __shared__ int s_parts[ROWS], s_row[ROWS];

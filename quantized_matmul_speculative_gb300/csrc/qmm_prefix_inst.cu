@@ -34,15 +34,20 @@ cudaError_t launch_prefix(const PrefixArgs& a, bool e8, cudaStream_t stream) {
   return e8 ? launch_main<D, true>(a, stream) : launch_main<D, false>(a, stream);
 }
 
+template <int D, int SPLIT, int AHEAD>
+cudaError_t launch_join(const PrefixArgs& a, bool e8, cudaStream_t stream) {
+  constexpr int ROWS = kPrefixJoinThreads / (D / 4) / SPLIT;
+  const int64_t ctas = a.c.heads * ((static_cast<int64_t>(a.B) * a.M * a.G + ROWS - 1) / ROWS);
+  return launch_dependent(e8 ? prefix_join_kernel<D, true, SPLIT, AHEAD> : prefix_join_kernel<D, false, SPLIT, AHEAD>,
+                          dim3(static_cast<unsigned>(ctas)), kPrefixJoinThreads, 0, stream, a);
+}
 template <int D>
 cudaError_t launch_prefix_join(const PrefixArgs& a, bool e8, cudaStream_t stream) {
   constexpr int ROWS = kPrefixJoinThreads / (D / 4);
-  const int64_t rows = static_cast<int64_t>(a.B) * a.M * a.G;
-  const bool few = a.c.heads * ((rows + ROWS - 1) / ROWS) <= 4 * device_sm_count();
-  auto kern = e8 ? (few ? prefix_join_kernel<D, true, 4> : prefix_join_kernel<D, true, 1>)
-                 : (few ? prefix_join_kernel<D, false, 4> : prefix_join_kernel<D, false, 1>);
-  const int mine = few ? ROWS / 4 : ROWS;
-  return launch_dependent(kern, dim3(static_cast<unsigned>(a.c.heads * ((rows + mine - 1) / mine))), kPrefixJoinThreads, 0, stream, a);
+  const int64_t ctas = a.c.heads * ((static_cast<int64_t>(a.B) * a.M * a.G + ROWS - 1) / ROWS);
+  return ctas <= device_sm_count()       ? launch_join<D, 4, 8>(a, e8, stream)
+         : ctas <= 4 * device_sm_count() ? launch_join<D, 1, 8>(a, e8, stream)
+                                         : launch_join<D, 1, 4>(a, e8, stream);
 }
 
 template <int D>
