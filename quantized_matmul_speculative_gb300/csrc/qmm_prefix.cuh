@@ -276,17 +276,6 @@ struct PrefixRoles {
   int begin, end;
 
   // --- copies ---
-  __device__ __forceinline__ int page_of(int j, int& place) const {
-    const int block = a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
-    place = j - block * a.c.page_size;
-    const int p = a.prefix[block];
-    if (p < 0 || p >= a.c.num_pages) {
-      bad_page();
-      return -1;
-    }
-    return p;
-  }
-
   // A tile's boxes along its tokens, 16 at most, one a lane: the entry of the prefix's table and the place in that page.  The
   // entry is looked at when its turn comes, so that it may be on its way until then.
   __device__ __forceinline__ void find_boxes(int t, int& entry, int& place) const {
@@ -342,27 +331,73 @@ struct PrefixRoles {
       if (__any_sync(0xffffffffu, !mbar_wait(full + i % SLOTS * 8, (i / SLOTS) & 1, kStatusTimeoutDrain, a.wait_ns))) break;
   }
 
-  // By threads, for pages that no box divides: bf16, rows by 16-byte asynchronous copies, kLag pieces under way.
+  // A thread's rows of a tile, each STEP-th from r0 on: the prefix's entries (INT_MIN: no token), and the places in their pages.
+  template <int N, int STEP>
+  struct Rows {
+    int page[N], place[N];
+    __device__ __forceinline__ void find(const PrefixArgs& a, int t, int r0) {
+      const int size = a.c.page_size, j0 = t * TN + r0;
+      int block = a.page_log2 >= 0 ? j0 >> a.page_log2 : j0 / size, at = j0 - block * size;
+      const int step = a.page_log2 >= 0 ? STEP >> a.page_log2 : STEP / size, rest = STEP - step * size;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        page[i] = r0 + i * STEP < TN && j0 + i * STEP < a.tokens ? a.prefix[block] : INT_MIN;
+        place[i] = at;
+        block += step;
+        at += rest;
+        if (at >= size) {
+          at -= size;
+          ++block;
+        }
+      }
+    }
+    // Entries that are no pages become -1.
+    __device__ __forceinline__ void check(const PrefixArgs& a) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (page[i] < 0 || page[i] >= a.c.num_pages) {
+          if (page[i] != INT_MIN) bad_page();
+          page[i] = -1;
+        }
+    }
+  };
+
+  // bf16 pages that no box divides: rows by 16-byte asynchronous copies, kLag pieces under way.  The next tile's entries are on
+  // their way while this one's copies are issued (looked up one by one: 239 us for 32 x 1 rows behind 32768 pages of a token).
   __device__ __forceinline__ void load_rows() {
-    constexpr int CPR = D / 8, STEP = 32 * kLoadWarps / CPR, kLag = 2;  // chunks of a row; rows between a thread's
+    constexpr int CPR = D / 8, STEP = 32 * kLoadWarps / CPR, N = (TN + STEP - 1) / STEP, kLag = 2;  // chunks of a row; rows between a thread's
     const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
+    const bool alike = a.c.k_page == a.c.v_page && a.c.k_token == a.c.v_token && a.c.k_head == a.c.v_head;
+    Rows<N, STEP> next;
+    uint32_t to[N];  // in a piece
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i] = swizzled(r0 + i * STEP, ch, TN);
     bool lost = false;
     int it = 0;
+    if (begin < end) next.find(a, PrefixSegment(l, begin, end, LANES).kb, r0);
     for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
-      for (int t = g.kb; t < g.ke && !lost; ++t)
+      u += g.ke - g.kb;
+      for (int t = g.kb; t < g.ke && !lost; ++t) {
+        Rows<N, STEP> rows = next;
+        rows.check(a);
+        if (t + 1 < g.ke || u < end) next.find(a, t + 1 < g.ke ? t + 1 : 0, r0);
+        int64_t from[N];
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int slot = it % SLOTS;
           if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
           if (lost) break;
-          const unsigned long long cache = reinterpret_cast<unsigned long long>(kv ? a.c.v : a.c.k);
-          for (int r = r0; r < TN; r += STEP) {
-            int place = 0;
-            const int j = t * TN + r, p = j < a.tokens ? page_of(j, place) : -1;
-            const int64_t at = kv ? p * a.c.v_page + place * a.c.v_token + g.h * a.c.v_head
-                                  : p * a.c.k_page + place * a.c.k_token + g.h * a.c.k_head;
-            copy_16(sbase + slot * Cfg::PIECE + swizzled(r, ch, TN), cache + (p >= 0 ? (at + ch * 8) * 2 : 0), p >= 0);
+          if (kv == 0 || !alike) {
+            const int64_t s_page = kv ? a.c.v_page : a.c.k_page, s_token = kv ? a.c.v_token : a.c.k_token;
+#pragma unroll
+            for (int i = 0; i < N; ++i) from[i] = rows.page[i] < 0 ? 0 : (rows.page[i] * s_page + rows.place[i] * s_token) * 2;
           }
+          const unsigned long long cache =
+              reinterpret_cast<unsigned long long>(kv ? a.c.v : a.c.k) + (g.h * (kv ? a.c.v_head : a.c.k_head) + ch * 8) * 2;
+          const uint32_t piece = sbase + slot * Cfg::PIECE;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (r0 + i * STEP < TN) copy_16(piece + to[i], cache + from[i], rows.page[i] >= 0);
           asm volatile("cp.async.commit_group;" ::: "memory");
           if (it >= kLag) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
@@ -370,7 +405,7 @@ struct PrefixRoles {
             mbar_arrive(full + (it - kLag) % SLOTS * 8);
           }
         }
-      u += g.ke - g.kb;
+      }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     fence_async_shared();
@@ -386,37 +421,18 @@ struct PrefixRoles {
   __device__ __forceinline__ void copy_raw() {
     constexpr int CPR = D / 16, STEP = 32 * kLoadWarps / CPR, N = (TN + STEP - 1) / STEP;
     const int x = threadIdx.x - Cfg::WG - 32, ch = x % CPR, r0 = x / CPR;
-    int entry[N], place[N];  // the tile's rows of this thread: the prefix's entry (INT_MIN: no row), and the place in that page
-    auto find = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int r = r0 + i * STEP, j = t * TN + r;
-        entry[i] = INT_MIN;
-        place[i] = 0;
-        if (r < TN && j < a.tokens) {
-          const int block = a.page_log2 >= 0 ? j >> a.page_log2 : j / a.c.page_size;
-          place[i] = j - block * a.c.page_size;
-          entry[i] = a.prefix[block];
-        }
-      }
-    };
+    Rows<N, STEP> next;
     bool lost = false;
     int it = 0;
-    if (begin < end) find(PrefixSegment(l, begin, end, LANES).kb);
+    if (begin < end) next.find(a, PrefixSegment(l, begin, end, LANES).kb, r0);
     for (int u = begin; u < end && !lost;) {
       const PrefixSegment g(l, u, end, LANES);
       u += g.ke - g.kb;
       for (int t = g.kb; t < g.ke && !lost; ++t) {
-        int page[N], at[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const bool none = entry[i] < 0 || entry[i] >= a.c.num_pages;
-          if (none && entry[i] != INT_MIN) bad_page();
-          page[i] = none ? -1 : entry[i];
-          at[i] = place[i];
-        }
+        Rows<N, STEP> rows = next;
+        rows.check(a);
         // (the next tile's entries are on their way while this one's copies are issued)
-        if (t + 1 < g.ke || u < end) find(t + 1 < g.ke ? t + 1 : 0);
+        if (t + 1 < g.ke || u < end) next.find(a, t + 1 < g.ke ? t + 1 : 0, r0);
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int slot = it % Cfg::RAWS;
           if (it >= Cfg::RAWS) lost = !mbar_wait(raw_empty + slot * 8, ((it / Cfg::RAWS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
@@ -429,7 +445,7 @@ struct PrefixRoles {
             const int r = r0 + i * STEP;
             if (r < TN)
               copy_16(sbase + Cfg::OFF_RAW + slot * Cfg::RAW + raw_at(r, ch),
-                      cache + (page[i] >= 0 ? page[i] * s_page + at[i] * s_token + head : 0), page[i] >= 0);
+                      cache + (rows.page[i] >= 0 ? rows.page[i] * s_page + rows.place[i] * s_token + head : 0), rows.page[i] >= 0);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full + slot * 8) : "memory");
         }
