@@ -57,7 +57,7 @@ struct PrefixArgs {
   float scale_log2;       // |scale| log2(e), times k_scale for an E4M3 cache; > 0
   int negate;
   float v_scale;
-  int box;                // tokens of a TMA box; 0: copied by threads
+  int box;                // tokens of a TMA box
   int page_log2;          // of the page size, or -1
   int ctas;
   float4* part_o;         // [parts][lanes][D / 4][128 rows], part: segment + CTA
@@ -351,6 +351,10 @@ struct PrefixRoles {
         }
       }
     }
+    __device__ __forceinline__ void offsets(int64_t (&from)[N], int64_t s_page, int64_t s_token) const {
+#pragma unroll
+      for (int i = 0; i < N; ++i) from[i] = page[i] < 0 ? 0 : page[i] * s_page + place[i] * s_token;
+    }
     // Entries that are no pages become -1.
     __device__ __forceinline__ void check(const PrefixArgs& a) {
 #pragma unroll
@@ -387,11 +391,7 @@ struct PrefixRoles {
           const int slot = it % SLOTS;
           if (it >= SLOTS) lost = !mbar_wait(empty + slot * 8, ((it / SLOTS) & 1) ^ 1, kStatusTimeoutEmpty, a.wait_ns);
           if (lost) break;
-          if (kv == 0 || !alike) {
-            const int64_t s_page = kv ? a.c.v_page : a.c.k_page, s_token = kv ? a.c.v_token : a.c.k_token;
-#pragma unroll
-            for (int i = 0; i < N; ++i) from[i] = rows.page[i] < 0 ? 0 : (rows.page[i] * s_page + rows.place[i] * s_token) * 2;
-          }
+          if (kv == 0 || !alike) rows.offsets(from, (kv ? a.c.v_page : a.c.k_page) * 2, (kv ? a.c.v_token : a.c.k_token) * 2);
           const unsigned long long cache =
               reinterpret_cast<unsigned long long>(kv ? a.c.v : a.c.k) + (g.h * (kv ? a.c.v_head : a.c.k_head) + ch * 8) * 2;
           const uint32_t piece = sbase + slot * Cfg::PIECE;
@@ -825,7 +825,8 @@ struct PrefixRoles {
   }
 };
 
-template <int D, bool E8>
+// BOXES: bf16 pages that TMA boxes divide.
+template <int D, bool E8, bool BOXES>
 __global__ void __launch_bounds__(PrefixCfg<D, E8>::THREADS, 1)
 prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using Cfg = PrefixCfg<D, E8>;
@@ -841,7 +842,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::SLOTS; ++s) {
-      mbar_init(full + s * 8, E8 ? kConvertWarps : a.box ? 1 : 32 * kLoadWarps);
+      mbar_init(full + s * 8, E8 ? kConvertWarps : BOXES ? 1 : 32 * kLoadWarps);
       mbar_init(empty + s * 8, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -925,10 +926,10 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ CUtensorMap kmap, cons
   } else if constexpr (E8) {
     if (warp <= Cfg::WG / 32 + kLoadWarps) r.copy_raw();
     else r.convert();
-  } else if (a.box == 0) {
-    r.load_rows();
-  } else {
+  } else if constexpr (BOXES) {
     r.load_tma(&kmap, &vmap);
+  } else {
+    r.load_rows();
   }
   __syncwarp();
   tmem_before();

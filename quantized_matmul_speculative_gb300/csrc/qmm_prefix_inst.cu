@@ -8,10 +8,10 @@
 
 namespace qmm {
 
-template <int D, bool E8>
-static cudaError_t launch_main(PrefixArgs a, cudaStream_t stream) {
+template <int D, bool E8, bool BOXES>
+static cudaError_t launch_copies(const PrefixArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
   using Cfg = PrefixCfg<D, E8>;
-  auto kern = prefix_kernel<D, E8>;
+  auto kern = prefix_kernel<D, E8, BOXES>;
   static std::atomic<uint64_t> ready{0};
   uint64_t bit;
   if (first_on_device(ready, &bit)) {
@@ -19,14 +19,22 @@ static cudaError_t launch_main(PrefixArgs a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  // boxes of the largest size that divides page and tile, down to the 8 rows of the swizzle
+  return launch_dependent(kern, dim3(a.ctas), Cfg::THREADS, Cfg::SMEM, stream, a, kmap, vmap);
+}
+template <int D, bool E8>
+static cudaError_t launch_main(PrefixArgs a, cudaStream_t stream) {
   CUtensorMap kmap = {}, vmap = {};
   a.box = 0;
-  if (!E8 && a.c.num_pages > 0)
-    for (int box = Cfg::TN; box >= 8 && a.box == 0; box /= 2)
-      if (a.c.page_size % box == 0) a.box = box;
-  if (a.box != 0 && (!cache_map(&kmap, a.c, false, a.box, 1) || !cache_map(&vmap, a.c, true, a.box, 1))) a.box = 0;
-  return launch_dependent(kern, dim3(a.ctas), Cfg::THREADS, Cfg::SMEM, stream, a, kmap, vmap);
+  if constexpr (!E8) {
+    // boxes of the largest size that divides page and tile, down to the 8 rows of the swizzle
+    if (a.c.num_pages > 0)
+      for (int box = PrefixCfg<D, E8>::TN; box >= 8 && a.box == 0; box /= 2)
+        if (a.c.page_size % box == 0) a.box = box;
+    if (a.box != 0 && cache_map(&kmap, a.c, false, a.box, 1) && cache_map(&vmap, a.c, true, a.box, 1))
+      return launch_copies<D, E8, true>(a, kmap, vmap, stream);
+    a.box = 0;
+  }
+  return launch_copies<D, E8, false>(a, kmap, vmap, stream);
 }
 
 template <int D>
