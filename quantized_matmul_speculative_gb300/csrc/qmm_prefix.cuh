@@ -18,8 +18,9 @@
 //   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ..   of jobs (token tile, lane)
 // where job j's scores go to buffer j mod 2, whose probabilities PV(j - 2) has read (the
 // tensor cores work in order).  Warps of their own copy keys and values, a ring of pieces:
-// by TMA where boxes of 8 tokens divide a page and the cache is bf16, else through
-// registers (E4M3 becomes fp16 there) or by 16-byte asynchronous copies.
+// by TMA where boxes of 8 tokens divide a page and the cache is bf16, else by 16-byte
+// asynchronous copies, which of E4M3 go to a ring of their own and are turned into fp16 by
+// further warps.
 // D = 256: the outputs of one row tile fill half the tensor memory, so there is one lane,
 // with two buffers of scores.
 //
@@ -31,6 +32,13 @@
 // halves in 16 columns, lower ones in the next 16.  E4M3: as one fp16 operand relative to
 // the maximum less kLiftE8 in base 2, so that weights from 2^-25 of the largest on keep 11
 // bits and none below 2^-36 remain.
+//
+// What bounds it.  bf16, 64 x 8 rows of 8 x 4 heads x 128 behind 16384 tokens: the products, 85
+// of 148 us with own tokens and joins; a pair of row tiles times 128 tokens takes 4260 cycles,
+// in which the warp that issues them is busy throughout.  32 x 1 rows behind 32768: 37 of 73
+// us, a tile's chain from scores to weights to products, 3.6 TB/s.  E4M3, 48 x 4 rows of
+// 8 x 8 heads x 64 behind 20016: 67 of 104 us, the instructions of the copying, converting and
+// row warps.  4 x 1 behind 2048: 9 of 25 us, the first pages, copies and products in turn.
 #pragma once
 
 #include <climits>
@@ -77,11 +85,11 @@ struct PrefixCfg {
   static constexpr int LANES = D == 256 ? 1 : 2;
   static constexpr int SLICES = D / 64;            // of 128 bytes of a row
   static constexpr int PIECE = TN * D * 2, QB = kRows * D * 2;
-  static constexpr int MISC = 3072;                // barriers, starts, alignment
+  static constexpr int BARS = 384, MISC = BARS + (kMaxStarts + 1) * 4 + 1024;  // barriers; and starts, alignment
   // an E4M3 cache's pieces as they lie there, on their way to fp16
   static constexpr int RAW = TN * D, RAWS = !E8 ? 0 : D == 64 ? 8 : 4;
   static constexpr int FIT = (232448 - MISC - LANES * QB - RAWS * RAW) / PIECE, SLOTS = FIT > 8 ? 8 : FIT;
-  static constexpr int OFF_RAW = SLOTS * PIECE, OFF_Q = OFF_RAW + RAWS * RAW, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + 384;
+  static constexpr int OFF_RAW = SLOTS * PIECE, OFF_Q = OFF_RAW + RAWS * RAW, OFF_BAR = OFF_Q + LANES * QB, OFF_STARTS = OFF_BAR + BARS;
   static constexpr int SMEM = OFF_STARTS + (kMaxStarts + 1) * 4 + 1024;
   static constexpr int WG = 128 * LANES, THREADS = WG + 32 + 32 * kLoadWarps + (E8 ? 32 * kConvertWarps : 0);
   // E4M3, two lanes: of the launch's 512 x 128 registers, 256 x 168 for the threads with rows and 256 x 88 for the others
