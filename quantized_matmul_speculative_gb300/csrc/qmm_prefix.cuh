@@ -33,12 +33,14 @@
 // the maximum less kLiftE8 in base 2, so that weights from 2^-25 of the largest on keep 11
 // bits and none below 2^-36 remain.
 //
-// What bounds it.  bf16, 64 x 8 rows of 8 x 4 heads x 128 behind 16384 tokens: the products, 85
-// of 148 us with own tokens and joins; a pair of row tiles times 128 tokens takes 4260 cycles,
-// in which the warp that issues them is busy throughout.  32 x 1 rows behind 32768: 37 of 73
-// us, a tile's chain from scores to weights to products, 3.6 TB/s.  E4M3, 48 x 4 rows of
-// 8 x 8 heads x 64 behind 20016: 67 of 104 us, the instructions of the copying, converting and
-// row warps.  4 x 1 behind 2048: 9 of 25 us, the first pages, copies and products in turn.
+// What bounds it.  The products' warp: bf16, 64 x 8 rows of 8 x 4 heads x 128 behind 16384
+// tokens take 85 of 148 us with own tokens and joins, a pair of row tiles times 128 tokens
+// 4260 cycles, in which it is busy throughout.  A product of scores reads 8 KB of shared
+// memory, 64 cycles for 32 of mathematics; one of outputs, whose weights are in tensor memory,
+// 4 KB.  E4M3, 48 x 4 rows of 8 x 8 heads x 64 behind 20016: 67 of 104 us, the same; without
+// the exponentials, three quarters of the conversions or most copies 103 to 104, with half of
+// the weights 96.  32 x 1 rows behind 32768: 37 of 73 us, a tile's chain from scores to weights
+// to products, 3.6 TB/s.  4 x 1 behind 2048: 9 of 25 us, pages, copies and products in turn.
 #pragma once
 
 #include <climits>
