@@ -37,9 +37,10 @@
 // tokens take 85 of 148 us with own tokens and joins, a pair of row tiles times 128 tokens
 // 4260 cycles, in which it is busy throughout.  A product of scores reads 8 KB of shared
 // memory, 64 cycles for 32 of mathematics; one of outputs, whose weights are in tensor memory,
-// 4 KB.  E4M3, 48 x 4 rows of 8 x 8 heads x 64 behind 20016: 67 of 104 us, the same; without
-// the exponentials, three quarters of the conversions or most copies 103 to 104, with half of
-// the weights 96.  32 x 1 rows behind 32768: 37 of 73 us, a tile's chain from scores to weights
+// 4 KB.  E4M3, 48 x 4 rows of 8 x 8 heads x 64 behind 20016: 67 of 104 us, the chain of steps
+// between that warp and the lanes; without the exponentials, three quarters of the conversions
+// or most copies 103 to 104, with half of the weights 96, with a third buffer of scores or
+// with the queries in tensor memory 103.  32 x 1 rows behind 32768: 37 of 73 us, a tile's chain from scores to weights
 // to products, 3.6 TB/s.  4 x 1 behind 2048: 9 of 25 us, pages, copies and products in turn.
 #pragma once
 

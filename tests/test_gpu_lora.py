@@ -196,3 +196,14 @@ def test_nothing_to_do():
     assert binding.lora_add(**p).shape == (0, 100)
     p = problem([0, 1], 2, 16, 64, 0)
     assert binding.lora_add(**p).shape == (2, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [8, 16, 24, 32, 64, 96, 128])
+@pytest.mark.parametrize("N", [1, 31, 601, 604])
+def test_rows_of_any_width(N, R, dtype):
+    """Tiles of 16, 32 or 64 rows, whose columns are no whole pieces of 16 bytes."""
+    p = problem([0] * 130 + [-1] * 41 + [1] * 65 + [2] * 3 + [0] * 31, 3, R, 256, N, dtype, seed=R + N)
+    want = check(p)
+    got = p["base"].clone()
+    assert torch.equal(binding.lora_add(**{**p, "base": got}, out=got), want)

@@ -266,3 +266,28 @@ def test_nothing_to_do():
     assert out.shape == (2, 0, 4, 128)
     out = binding.shared_prefix_attention(queries(2, 3, 4, 128)[:0], s.k, s.v, s.prefix, s.table[:0], s.lengths[:0])
     assert out.shape == (0, 3, 4, 128)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [1, 3, 5, 7, 20, 100, 129])
+def test_pages_that_no_box_divides(page, D, dtype):
+    """Rows copied one by one, keys and values in orders of their own."""
+    s = Shared(-(-700 // page), [5, 17], 2, D, page, dtype, seed=page + D)
+    q = queries(2, 3, 6, D)
+    out, lse = check(q, s)
+    s.v = s.v.view(torch.uint8).permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3).view(dtype) if dtype == E4M3 else \
+        s.v.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+    assert s.v.stride() != s.k.stride()
+    again, lse2 = check(q, s)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+@pytest.mark.parametrize("Hkv,D", [(1, 64), (1, 128), (1, 256), (3, 128)])
+def test_a_row_in_parts_of_every_sm(Hkv, D, dtype):
+    """Few rows behind a long prefix, which lie in a part of each SM, and rows enough that many CTAs join them."""
+    s = Shared(170, [3, 9], Hkv, D, 128, dtype, seed=21)
+    check(queries(2, 2, 4 * Hkv, D), s)
+    s = Shared(170, [16] * 40, Hkv, D, 128, dtype, seed=22)
+    check(queries(40, 4, 2 * Hkv, D), s)
