@@ -7,14 +7,17 @@
 // The mathematics.  What orders the experts (logits, or scores with the bias) is put on a
 // scale of 2^23 steps between the row's least and greatest, with the expert's number, the
 // lowest first, in the 9 bits below: one unsigned key each, no two alike.  Every lane sorts
-// its own keys once; then k + 1 rounds take the largest of the lanes' first ones.  Neighbours
-// of that order that are nearer than the steps' and the scores' own errors (or than one
-// step, where logits are compared) may be in the wrong order, unless they are the same
-// logit with the same bias: then, in some tokens of a thousand, the warp does the token again
-// in 64 bits, one maximum after another.  The errors: a sigmoid from the approximate
-// exponential and reciprocal is off by 4 2^-24, a softmax by 24 2^-24 (exponentials 2 units in
-// the last place each, a sum of 512 in 31 + 5 steps), a key's own rounding is |key| 2^-24; so
-// two keys more than kGap (1 + |key|) apart are in their order, with kGap 2^-20 and 2^-18.
+// its own keys once; then k rounds take the largest of the lanes' first ones.  Keys nearer
+// than the steps' and the scores' own errors (or than one step, where logits are compared)
+// may be in the wrong order, unless they are the same logit with the same bias.  So the
+// chosen ones are held against their neighbours, and the last of them against every key that
+// is left that near to it, as of equals in 32 bits a better one may lie anywhere behind.
+// Where one of those pairs is not the same logit with the same bias, in some tokens of a
+// thousand, the warp does the token again in 64 bits, one maximum after another.  The errors:
+// a sigmoid from the approximate exponential and reciprocal is off by 4 2^-24, a softmax by
+// 24 2^-24 (exponentials 2 units in the last place each, a sum of 512 in 31 + 5 steps), a
+// key's own rounding is |key| 2^-24; so two keys more than kGap (1 + |key|) apart are in their
+// order, with kGap 2^-20 and 2^-18.
 //
 // What bounds it: instructions, 985 a token of 256 experts in 8 groups (62% of the issue
 // slots, 58% of the integer pipe): 16384 tokens 34 us, at a floor of 2.7.  One token: 5 us,
@@ -322,9 +325,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
     key[i] = open && i < l.mine ? step << 9 | (511u - (l.first + i)) : 0u;
   }
   sort_down(key);
-  uint32_t mine = 0, next = 0;
-  for (int j = 0; j <= a.k; ++j) {
-    next = warp_max(key[0]);
+  uint32_t mine = 0;
+  for (int j = 0; j < a.k; ++j) {
+    const uint32_t next = warp_max(key[0]);
     if (lane == j) mine = next;
     const bool taken = key[0] == next;
 #pragma unroll
@@ -334,12 +337,23 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   int expert = 511 - static_cast<int>(mine & 511u);
   float logit = lane < a.k ? logit_of(a, t, expert) : 0.f;
   {
-    // neighbours of the order, down to the first that is left out
-    const uint32_t after = __shfl_down_sync(0xffffffffu, mine, 1), below = lane == a.k - 1 ? next : after;
-    bool told = true;
-    if (lane < a.k && below != 0 && (mine >> 9) - (below >> 9) < margin) {
-      const int e = 511 - static_cast<int>(below & 511u);
-      told = logit_of(a, t, e) == logit && (!biased || a.bias[e] == a.bias[expert] || logit == -INFINITY);
+    const float its_bias = biased && lane < a.k ? a.bias[expert] : 0.f;
+    const auto same = [](float x, float b, float y, float c) { return x == y && (b == c || x == -INFINITY); };
+    // neighbours among the chosen ones
+    const uint32_t below = __shfl_down_sync(0xffffffffu, mine, 1);
+    const float x_below = __shfl_down_sync(0xffffffffu, logit, 1), b_below = __shfl_down_sync(0xffffffffu, its_bias, 1);
+    bool told = lane >= a.k - 1 || (mine >> 9) - (below >> 9) >= margin || same(logit, its_bias, x_below, b_below);
+    // the last of them, and what is left
+    const uint32_t last = __shfl_sync(0xffffffffu, mine, a.k - 1);
+    const auto near = [&](uint32_t k) { return k != 0u && (last >> 9) - (k >> 9) < margin; };
+    if (__any_sync(0xffffffffu, near(key[0]))) {
+      const float x_last = __shfl_sync(0xffffffffu, logit, a.k - 1), b_last = __shfl_sync(0xffffffffu, its_bias, a.k - 1);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (near(key[i])) {
+          const int e = 511 - static_cast<int>(key[i] & 511u);
+          told = told && same(x_last, b_last, logit_of(a, t, e), biased ? a.bias[e] : 0.f);
+        }
     }
     apart = __all_sync(0xffffffffu, told) && apart;
   }
