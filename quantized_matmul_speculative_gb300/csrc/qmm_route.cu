@@ -17,7 +17,7 @@
 // a sigmoid from the approximate exponential and reciprocal is off by 4 2^-24, a softmax by
 // 24 2^-24 (exponentials 2 units in the last place each, a sum of 512 in 31 + 5 steps), a
 // key's own rounding is |key| 2^-24; so two keys more than kGap (1 + |key|) apart are in their
-// order, with kGap 2^-20 and 2^-18.
+// order, with kGap 2^-20 and 2^-18.  Groups likewise, with the sizes of both terms of a worth.
 //
 // What bounds it: instructions, 985 a token of 256 experts in 8 groups (62% of the issue
 // slots, 58% of the integer pipe): 16384 tokens 34 us, at a floor of 2.7.  One token: 5 us,
@@ -93,9 +93,10 @@ __device__ __forceinline__ float logit_of(const RouteArgs& a, int64_t t, int e) 
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[t * a.ld + e]));
 }
 
-// The best one or two of v[0 .. PER - 1] and of the neighbouring lanes of a group.
+// The best one or two of v[0 .. PER - 1] and of the neighbouring lanes of a group; `size`: of these terms, as numbers
+// that cancel keep both their errors.
 template <class F, int PER>
-__device__ __forceinline__ F group_worth(const RouteArgs& a, const F (&v)[PER]) {
+__device__ __forceinline__ F group_worth(const RouteArgs& a, const F (&v)[PER], F& size) {
   F best = -F(INFINITY), second = -F(INFINITY);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -107,7 +108,9 @@ __device__ __forceinline__ F group_worth(const RouteArgs& a, const F (&v)[PER]) 
     second = b > best ? (best > c ? best : c) : (b > second ? b : second);
     best = b > best ? b : best;
   }
-  return a.group_best == 2 && second > -F(INFINITY) ? best + second : best;
+  const bool both = a.group_best == 2 && second > -F(INFINITY);
+  size = both ? fabs(best) + fabs(second) : fabs(best);
+  return both ? best + second : best;
 }
 
 // Whether this lane's group is open, from its groups' worths; `last` the least that is, `left` the best that is not.
@@ -217,7 +220,8 @@ __device__ __noinline__ int choose_exactly(const RouteArgs& a, int64_t t) {
     key[i] = i < l.mine ? ordered(v) : Key(0);
   }
   if (grouped) {
-    const Key of_group = ordered(group_worth(a, worth));  // (every lane takes part in it)
+    double size;
+    const Key of_group = ordered(group_worth(a, worth, size));  // (every lane takes part in it)
     Key last, left;
     if (!open_groups(a, l.real ? of_group : Key(0), last, left))
 #pragma unroll
@@ -298,11 +302,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   }
   bool apart = true, open = l.real;
   if (grouped) {
-    const uint32_t of_group = ordered(group_worth(a, worth));  // (every lane takes part in it)
+    float size;
+    const float mine = group_worth(a, worth, size);  // (every lane takes part in it)
     uint32_t last, left;
-    open = open_groups(a, l.real ? of_group : 0u, last, left);
-    const float hi = value_of(last), lo = value_of(left);
-    if (biased || by_sum) apart = hi - lo > 2.f * gap * (1.f + fabsf(hi)) || (hi == lo && hi == -INFINITY);
+    open = open_groups(a, l.real ? ordered(mine) : 0u, last, left);
+    const float hi = value_of(last), lo = value_of(left), between = 0.5f * hi + 0.5f * lo, off = gap * (1.f + size);
+    // every group on its side of what lies between the open and the others (-inf is exact; with +inf nothing is told)
+    if (biased || by_sum)
+      apart = open ? mine - off > between || (hi == -INFINITY && mine == hi) : !l.real || mine == -INFINITY || mine + off < between;
   }
   // the scale: 2 .. 2^23 - 2 from the least that is not masked by a very large negative number; 1 for -inf
   float hi = -INFINITY, lo = INFINITY;
@@ -355,7 +362,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
           told = told && same(x_last, b_last, logit_of(a, t, e), biased ? a.bias[e] : 0.f);
         }
     }
-    apart = __all_sync(0xffffffffu, told) && apart;
+    apart = __all_sync(0xffffffffu, told && apart);
   }
   if (!apart) {
     expert = choose_exactly<PER>(a, t);
