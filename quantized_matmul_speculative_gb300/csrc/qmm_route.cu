@@ -75,9 +75,9 @@ __device__ __forceinline__ F warp_sum(F v) {
   for (int s = 16; s > 0; s /= 2) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
-__device__ __forceinline__ float sigmoid_of(float x) {
-  const float e = expf(x < 0.f ? x : -x);
-  return (x < 0.f ? e : 1.f) / (1.f + e);
+// e^-by / (1 + e^-x), where by is x at least if x is negative, else 0.
+__device__ __forceinline__ float sigmoid_of(float x, float by) {
+  return (x < 0.f ? expf(x - by) : 1.f) / (1.f + expf(-fabsf(x)));
 }
 // The same within 4 2^-24, absolutely.
 __device__ __forceinline__ float sigmoid_near(float x) {
@@ -372,9 +372,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   const float best = warp_max(lane < a.k ? logit : -INFINITY);
   float w = 0.f;
   if (lane < a.k && logit != -INFINITY) {
-    // (sigmoids below 2^-43 are exponentials, whose ratios do not depend on the largest)
-    if (a.renormalize && (!a.sigmoid || best < -30.f)) w = expf(logit - best);
-    else w = a.sigmoid ? sigmoid_of(logit) : expf(logit - ref) / total;
+    // (of sigmoids the ratios count: all are taken e^-best times where best is negative, so that none is lost below 32 bits' range)
+    if (a.renormalize) w = a.sigmoid ? sigmoid_of(logit, fminf(best, 0.f)) : expf(logit - best);
+    else w = a.sigmoid ? sigmoid_of(logit, 0.f) : expf(logit - ref) / total;
   }
   if (a.renormalize) {
     const float sum = warp_sum(w);
