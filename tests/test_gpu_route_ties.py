@@ -118,3 +118,18 @@ def test_repeated_logits():
             for bias in (None, torch.zeros(E), 0.25 * torch.randint(0, 2, (E,), generator=g).float()):
                 check(x, k, scoring, bias)
                 check(x, k, scoring, bias, groups=8, top_groups=4)
+
+
+@pytest.mark.parametrize("offset", [-3e3, -4096.0, -5e3, -2e4, -1e9, 1e4, 1e9, 1e30])
+def test_rows_far_from_zero(offset):
+    """Of logits as large as the masked ones nothing is left out of the comparison."""
+    g = torch.Generator().manual_seed(3)
+    x = (20 * torch.randn(500, 64, generator=g).double() + offset).float()
+    x[::2, ::3] -= abs(offset)  # half of the rows in two parts
+    for scoring in ("softmax", "sigmoid"):
+        for k in (1, 8):
+            check(x, k, scoring)
+        check(x, 2, scoring, groups=8, top_groups=2, group_best=1)
+    check(x, 8, "softmax", (0.1 * torch.randn(64, generator=g)))
+    bias = (20 * torch.randn(64, generator=g).double() + offset).float()
+    check(torch.randn(500, 64, generator=g), 8, "sigmoid", bias)
