@@ -410,9 +410,8 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None,
                                 _handle(stream)), "qmm_kv_append")
 
 
-@functools.lru_cache(maxsize=256)
 def paged_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
-    """Bytes of workspace that :func:`paged_attention` needs for these sizes."""
+    """Bytes of workspace that :func:`paged_attention` needs for these sizes on the current device (it goes by the number of SMs)."""
     return int(lib().qmm_paged_attention_workspace(B, M, q_heads, heads, head_dim))
 
 
@@ -454,9 +453,8 @@ def rope_append(q, k_new, v_new, k_cache, v_cache, block_table, lengths, inv_fre
                    "qmm_rope_append")
 
 
-@functools.lru_cache(maxsize=256)
 def shared_prefix_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
-    """Bytes of workspace that :func:`shared_prefix_attention` needs for these sizes."""
+    """Bytes of workspace that :func:`shared_prefix_attention` needs for these sizes on the current device (it goes by the number of SMs)."""
     return int(lib().qmm_shared_prefix_attention_workspace(B, M, q_heads, heads, head_dim))
 
 
