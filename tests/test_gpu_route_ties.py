@@ -18,7 +18,8 @@ def chosen(x, k, scoring, bias=None, groups=1, top_groups=None, group_best=2):
     those that are equal in exact arithmetic, lie in the order of these roundings, unless their terms are the same."""
     x = x.double().cpu()
     T, E = x.shape
-    s = torch.softmax(x, -1) if scoring == "softmax" else 1 / (1 + torch.exp(-x))
+    near_0 = torch.exp(-x.abs())
+    s = torch.softmax(x, -1) if scoring == "softmax" else torch.where(x < 0, near_0, 1.0) / (1 + near_0)
     key = x if bias is None else s + bias.double().cpu()
     left_open = torch.zeros(T, dtype=torch.bool)
     if top_groups is not None and top_groups < groups:
