@@ -18,8 +18,8 @@
 // 8 (g / 2) + 2 j + g mod 2 of 32, so that a thread ends with 8 neighbouring columns.
 //
 // What bounds it: HBM for many adapters (64 x 4 rows, 48 of rank 64, 34816 x 5120: 51 us,
-// 4.7 TB/s), two or three launches and their loads' latency for few (4 rows of rank 16: 7.3
-// us) and short ones (6 x 700 rows of rank 16, 5120 x 17408, fp32: 26 us, 2.3 TB/s).
+// 4.7 TB/s), two or three launches and their loads' latency for few (4 rows of rank 16: 7 to
+// 8 us) and short ones (6 x 700 rows of rank 16, 5120 x 17408, fp32: 26 us, 2.3 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

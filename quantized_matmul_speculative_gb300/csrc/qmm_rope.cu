@@ -11,8 +11,8 @@
 // A row's angles are computed once for all its heads, while its elements are on their way.
 //
 // What bounds it: the copies, whose places depend on lengths and table: 2 x 4001 rows of
-// 32 + 16 heads x 128, 26 us, 5.0 TB/s; 128 x 16 rows into E4M3 13.3 us, 3.5 TB/s; 4 x 5 rows
-// 4.6 us, a launch and that chain.
+// 32 + 16 heads x 128, 26 us, 5.0 TB/s; 128 x 16 rows into E4M3 13.3 us, 3.5 TB/s (1.4
+// us more with scales that are no powers of two); 4 x 5 rows 4.6 us, a launch and that chain.
 #include <algorithm>
 #include <cmath>
 

@@ -7,12 +7,12 @@
 // The mathematics.  What orders the experts (logits, or scores with the bias) is put on a
 // scale of 2^23 steps between the row's greatest and its least that is not masked, with the
 // expert's number, the lowest first, in the 9 bits below: one unsigned key each, no two
-// alike.  Every lane sorts
-// its own keys once; then k rounds take the largest of the lanes' first ones.  Keys nearer
-// than the steps' and the scores' own errors (or than one step, where logits are compared)
-// may be in the wrong order, unless they are the same logit with the same bias.  So the
-// chosen ones are held against their neighbours, and the last of them against every key that
-// is left that near to it, as of equals in 32 bits a better one may lie anywhere behind.
+// alike.  Every lane sorts its own keys once; then k rounds take the largest of the lanes'
+// first ones.  Keys nearer than the steps' and the scores' own errors (or than one step,
+// where logits are compared) may be in the wrong order, unless they are the same logit with
+// the same bias.  So the chosen ones are held against their neighbours, and the last of them
+// against every key that is left that near to it, as of equals in 32 bits a better one may
+// lie anywhere behind.
 // Where one of those pairs is not the same logit with the same bias, in some tokens of a
 // thousand, the warp does the token again in 64 bits, one maximum after another.  The errors:
 // a sigmoid from the approximate exponential and reciprocal is off by 4 2^-24, a softmax by
@@ -20,9 +20,9 @@
 // key's own rounding is |key| 2^-24; so two keys more than kGap (1 + |key|) apart are in their
 // order, with kGap 2^-20 and 2^-18.  Groups likewise, with the sizes of both terms of a worth.
 //
-// What bounds it: instructions, 985 a token of 256 experts in 8 groups (62% of the issue
-// slots, 58% of the integer pipe): 16384 tokens 34 us, at a floor of 2.7.  One token: 5 us,
-// a launch and a chain.  As many lanes hold keys as there are experts, so that few experts
+// What bounds it: instructions, 974 a token of 256 experts in 8 groups (62% of the issue
+// slots, 57% of the integer pipe): 16384 tokens 33 to 37 us by the inputs, at a floor of 2.7.
+// One token: 5 us, a launch and a chain.  As many lanes hold keys as there are experts, so that few experts
 // cost much for their bytes (243398 tokens of 16: 135 us).
 #include <cfloat>
 #include <climits>
