@@ -411,7 +411,7 @@ def kv_append(k_new, v_new, k_cache, v_cache, block_table, lengths, q_lens=None,
 
 
 def paged_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
-    """Bytes of workspace that :func:`paged_attention` needs for these sizes on the current device (it goes by the number of SMs)."""
+    """Bytes of workspace that :func:`paged_attention` needs for these sizes on the current device, by its number of SMs."""
     return int(lib().qmm_paged_attention_workspace(B, M, q_heads, heads, head_dim))
 
 
@@ -454,7 +454,7 @@ def rope_append(q, k_new, v_new, k_cache, v_cache, block_table, lengths, inv_fre
 
 
 def shared_prefix_attention_workspace(B: int, M: int, q_heads: int, heads: int, head_dim: int) -> int:
-    """Bytes of workspace that :func:`shared_prefix_attention` needs for these sizes on the current device (it goes by the number of SMs)."""
+    """Bytes of workspace that :func:`shared_prefix_attention` needs for these sizes on the current device, by its number of SMs."""
     return int(lib().qmm_shared_prefix_attention_workspace(B, M, q_heads, heads, head_dim))
 
 
